@@ -77,7 +77,7 @@ extern "C" {
 /* ---- host-side return codes ------------------------------------------- */
 #define SMC_OK             0
 #define SMC_ERR_ARG       (-1)   /* NULL pointer, size out of range, bad shape */
-#define SMC_ERR_DTYPE     (-2)   /* dtype is neither SMC_F32 nor SMC_BF16      */
+#define SMC_ERR_DTYPE     (-2)   /* a dtype that the entry point does not take */
 #define SMC_ERR_WORKSPACE (-3)   /* workspace NULL, too small or misaligned    */
 #define SMC_ERR_LAUNCH    (-4)   /* a kernel launch was rejected by CUDA       */
 #define SMC_ERR_CUDA      (-5)   /* a CUDA runtime call failed                 */
@@ -93,6 +93,8 @@ extern "C" {
                                           negative or oversized token count      */
 #define SMC_DEV_TIMEOUT          0x80  /* a bounded wait for a bulk copy gave up;
                                           re-initialise the workspace            */
+#define SMC_DEV_BAD_ROWS         0x100 /* row offsets, a position or a path index out
+                                          of range (cache entry points)          */
 
 /* ---- limits ------------------------------------------------------------ */
 #define SMC_MAX_N  256        /* particles per prompt                           */
@@ -106,7 +108,8 @@ extern "C" {
 #define SMC_PURPOSE_RESIDUAL  3  /* stream b, position j (sps_verify)            */
 #define SMC_PURPOSE_RESAMPLE  4  /* stream b, position 0                         */
 
-typedef enum { SMC_F32 = 0, SMC_BF16 = 1 } smc_dtype;
+/* SMC_F16 is a type of the paged cache only: logits are SMC_F32 or SMC_BF16. */
+typedef enum { SMC_F32 = 0, SMC_BF16 = 1, SMC_F16 = 2 } smc_dtype;
 
 /* Shape and scalars of one step. */
 typedef struct {
@@ -383,6 +386,172 @@ int32_t smc_step_noalloc(const smc_params *p, const void *target_logits,
                          float *log_weights, int32_t *tokens_out, int32_t *ancestors,
                          float *ess, int32_t *resampled, const smc_kv *kv,
                          int32_t *status_bits, void *stream);
+
+/* ---- the paged cache's data --------------------------------------------
+ * The step and kv_blocktable_remap above move block tables only.  These entry
+ * points work on the keys and values behind the tables, as the pages' system
+ * needs around the step ([SMC] section 2, "Score & Bonus": one target forward
+ * over every particle's drafted tokens; "KV Cache 优化": shared prefixes, and
+ * the copy of a partially filled block that a remap hands to the caller in
+ * cow_pairs).  [SpS] section 4.1, "并行打分", scores the drafted tokens in one
+ * forward; a drafted tree generalises its chain.
+ *
+ * A sequence's *new* tokens are the last ones it holds: its token count
+ * (seq_len) includes them, as it does after kv_blocktable_remap's append.  New
+ * token i of sequence s sits at position seq_len[s] - n_new[s] + i of its
+ * table.  All tokens before the new ones are *committed*.
+ *
+ * The conventions at the top of this file hold, with these additions.
+ *   - The calls take strides in elements, so the cache may be token-major,
+ *     head-major or one layer of a larger array; only the head_dim axis must
+ *     be contiguous.  Offsets are 64-bit.
+ *   - One workspace of smc_cache_workspace_bytes() serves all of them on one
+ *     stream.  Its status word is read with smc_device_status.
+ *   - A table entry outside [0, blocks) or a token count that is negative, too
+ *     small for the new tokens or too large for the table sets
+ *     SMC_DEV_BAD_BLOCK; row offsets, positions and path indices out of range
+ *     set SMC_DEV_BAD_ROWS.  Nothing outside the arrays is read or written. */
+
+/* Keys and values of every layer.  Element (layer, block, token, head, d) of
+ * k, and of v, is at layer*layer_stride + block*block_stride +
+ * token*token_stride + head*head_stride + d. */
+typedef struct {
+  void *k, *v;              /* DEVICE                                            */
+  int64_t layer_stride, block_stride, token_stride, head_stride; /* elements     */
+  int32_t layers, blocks, block_size, kv_heads, head_dim;        /* each >= 1    */
+  int32_t dtype;            /* smc_dtype                                         */
+} smc_cache;
+
+/* The sequences of one call and their new tokens.  Rows of q, k, v, masks and
+ * outputs are the new tokens of sequence 0, then of sequence 1, and so on. */
+typedef struct {
+  const int32_t *tables;    /* DEVICE [S, T] block id per table slot             */
+  const int32_t *seq_len;   /* DEVICE [S] tokens held, the new ones included     */
+  const int32_t *row_start; /* DEVICE [S + 1] row of each sequence's first new
+                               token, ascending; rows past row_start[S] are not
+                               touched.  NULL: every sequence has max_new        */
+  int32_t S;                /* sequences, >= 1                                   */
+  int32_t T;                /* table slots per sequence, >= 1                    */
+  int32_t rows;             /* rows of the arrays (S * max_new without row_start) */
+  int32_t max_new;          /* most new tokens of a sequence,
+                               1..SMC_MAX_NEW                                    */
+  int32_t group;            /* sequences per prompt, consecutive (a divisor of S;
+                               1: unrelated).  Leading table slots that all of a
+                               prompt's sequences share are read once            */
+} smc_batch;
+
+#define SMC_MAX_NEW (1 << 16)
+
+/* Bytes of workspace for the entry points below: for any of them with `batch`
+ * and q_heads query heads; with batch NULL, for those that take no batch.
+ * Returns 0 when the shape is invalid. */
+size_t smc_cache_workspace_bytes(const smc_cache *cache, const smc_batch *batch,
+                                 int32_t q_heads);
+
+/* Arguments of smc_tree_attention that are not device arrays. */
+typedef struct {
+  int32_t q_heads;          /* a multiple of cache->kv_heads                     */
+  int32_t mask_words;       /* 32-bit words per mask row (0 without a mask)      */
+  float scale;              /* finite, > 0                                       */
+  int32_t reserved;         /* must be 0                                         */
+  int64_t q_row_stride, q_head_stride;     /* elements                           */
+  int64_t out_row_stride, out_head_stride; /* elements                           */
+} smc_attn_params;
+
+/* Attention of the new tokens over their sequences' caches, under a tree mask.
+ *
+ * q [rows, q_heads, head_dim] and out (the same) have the cache's dtype; lse
+ * [rows, q_heads] fp32 may be NULL.  mask [rows, mask_words] uint32, or NULL:
+ * bit j % 32 of word j / 32 of a row says that the row sees new token j of its
+ * own sequence (its own bit too, if it is to see itself); bits past the
+ * sequence's new tokens are ignored, and words past mask_words count as 0.
+ * Without a mask new token i sees new tokens 0..i (a chain).  Every row sees
+ * every committed token.  With z_j = scale * <q, k_j> over the visible tokens,
+ *   out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j).
+ * Query head h reads key head h / (q_heads / kv_heads).  A row that sees
+ * nothing gets out = 0 and lse = -inf.  Keys and values of tokens that a row
+ * does not see do not reach it, whatever they hold.
+ *
+ * The new tokens' keys and values must be in the cache already
+ * (smc_qk_norm_rope).  dtype SMC_BF16 or SMC_F16; head_dim a multiple of 8, at
+ * most 128; pointers and strides in multiples of 16 bytes.  Scores, statistics
+ * and sums are fp32; the weights are rounded to the cache's dtype for the
+ * product with v.  Equal inputs give equal bits. */
+int32_t smc_tree_attention(const smc_attn_params *p, const smc_cache *cache, int32_t layer,
+                           const smc_batch *batch, const void *q, const uint32_t *mask,
+                           void *out, float *lse, void *workspace, size_t ws_bytes,
+                           void *stream);
+
+/* Arguments of smc_qk_norm_rope that are not device arrays. */
+typedef struct {
+  int32_t q_heads;          /* >= 1                                              */
+  int32_t rot_dim;          /* leading dims rotated: even, 0..head_dim           */
+  int32_t max_pos;          /* rows of the rope table                            */
+  int32_t interleaved;      /* 0: dim i turns with i + rot_dim/2;
+                               1: dim 2i turns with 2i + 1                       */
+  float eps;                /* >= 0, finite                                      */
+  float weight_offset;      /* added to every norm weight (0, or 1 where weights
+                               are stored around 0)                              */
+  int64_t q_row_stride, q_head_stride;     /* elements                           */
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride;
+} smc_qk_params;
+
+/* Per-head norms of queries and keys, the position rotation, and the write of
+ * keys and values into the cache, in one pass over the new tokens.
+ *
+ * q [rows, q_heads, head_dim], k and v [rows, kv_heads, head_dim] and q_out
+ * (as q; it may be q itself) have the cache's dtype.  q_weight and k_weight
+ * [head_dim], of the same dtype, may be NULL: no norm of q, or of k.  rope
+ * [max_pos, rot_dim] fp32: rot_dim/2 cosines, then as many sines, of each
+ * position's angles.  positions [rows] int32, or NULL: each token's position
+ * in its table.  In fp32, rounded once:
+ *   y = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset);
+ *   (a, b) -> (a cos - b sin, a sin + b cos) over the rotated pairs.
+ * q_out gets the queries, the cache's slots of the new tokens the keys and the
+ * values (the values bit for bit).  head_dim at most 256; any cache dtype.  A
+ * row whose position is outside [0, max_pos) sets SMC_DEV_BAD_ROWS and is
+ * skipped.  A block that two sequences share must not hold new tokens of
+ * either (kv_blocktable_remap forks it, kv_copy_blocks copies it). */
+int32_t smc_qk_norm_rope(const smc_qk_params *p, const smc_cache *cache, int32_t layer,
+                         const smc_batch *batch, const void *q, const void *k, const void *v,
+                         const void *q_weight, const void *k_weight, const int32_t *positions,
+                         const float *rope, void *q_out, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/* Copies blocks, keys and values of every layer: pair i < counts[l] of list l
+ * copies block pairs[l, i, 0] to block pairs[l, i, 1].  pairs [lists,
+ * max_pairs, 2] int32 and counts [lists] int32 are a step's cow_pairs and
+ * n_cow (lists = B, max_pairs = N).  The destinations are distinct, and none is
+ * a source, as with the pairs of one remap.  A count outside [0, max_pairs]
+ * sets SMC_DEV_BAD_ROWS and its list is skipped; a block id out of range sets
+ * SMC_DEV_BAD_BLOCK and its pair is skipped.  Any dtype. */
+int32_t kv_copy_blocks(const smc_cache *cache, const int32_t *pairs, const int32_t *counts,
+                       int32_t lists, int32_t max_pairs, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/* Moves the accepted path of a drafted tree to the front of its sequence's new
+ * tokens, keys and values of every layer: new token path[s, i] goes to new
+ * token i for i < n_path[s].  path [S, max_path] int32 holds indices among the
+ * sequence's new tokens in strictly ascending order (a parent precedes its
+ * children); n_path [S] int32 in [0, max_path].  An index that is out of range
+ * or does not ascend sets SMC_DEV_BAD_ROWS and is skipped.  The token counts
+ * stay: kv_truncate gives back what the path leaves over. */
+int32_t kv_compact_tokens(const smc_cache *cache, const smc_batch *batch, const int32_t *path,
+                          const int32_t *n_path, int32_t max_path, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/* Shortens particles: particle (b, n) keeps its first new_len[b, n] tokens.
+ * Table slots past the blocks that hold them become -1, and each such
+ * reference subtracts 1 from its block's count; blocks that reach 0 are pushed
+ * on prompt b's free stack in ascending id order.  new_len [B, N] int32 (0
+ * frees a particle).  A new_len outside [0, seq_len], a block outside its
+ * prompt's pool or one with no reference left sets SMC_DEV_BAD_BLOCK; that
+ * particle, or that block, is left as it is.  p supplies B and N; the
+ * workspace is one of smc_workspace_bytes(p, kv). */
+int32_t kv_truncate(const smc_params *p, const smc_kv *kv, const int32_t *new_len,
+                    void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

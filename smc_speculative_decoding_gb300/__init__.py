@@ -14,6 +14,9 @@ from .binding import (  # noqa: F401
     smc_draft_sample,
     smc_kv_usage,
     smc_step_opts, SMC_F32, SMC_BF16,
+    SMC_F16, smc_cache, smc_batch, make_cache, make_batch, smc_cache_workspace_bytes,
+    alloc_cache_workspace, smc_tree_attention, smc_qk_norm_rope, kv_copy_blocks,
+    kv_compact_tokens, kv_truncate,
 )
 
 __all__ = [
@@ -24,4 +27,7 @@ __all__ = [
     "smc_selftest_bounded_wait",
     "smc_step_ex", "smc_draft_sample",
     "smc_kv_usage", "smc_step_opts", "SMC_F32", "SMC_BF16",
+    "SMC_F16", "smc_cache", "smc_batch", "make_cache", "make_batch", "smc_cache_workspace_bytes",
+    "alloc_cache_workspace", "smc_tree_attention", "smc_qk_norm_rope", "kv_copy_blocks",
+    "kv_compact_tokens", "kv_truncate",
 ]

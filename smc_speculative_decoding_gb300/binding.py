@@ -15,12 +15,13 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmcsd.so")
 
-SMC_F32, SMC_BF16 = 0, 1
+SMC_F32, SMC_BF16, SMC_F16 = 0, 1, 2
 
 # device status bits (smcsd.h)
 DEV_BITS = {
     0x01: "bad_token", 0x02: "nonfinite", 0x04: "empty_row", 0x08: "all_zero_weight",
     0x10: "pool_exhausted", 0x20: "table_overflow", 0x40: "bad_block", 0x80: "timeout",
+    0x100: "bad_rows",
 }
 
 
@@ -49,6 +50,38 @@ class smc_kv(ctypes.Structure):
 class smc_step_opts(ctypes.Structure):
     _fields_ = [("log_potential", ctypes.c_void_p), ("temperature", ctypes.c_float),
                 ("top_p", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)]
+
+
+class smc_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("layers", ctypes.c_int32),
+                ("blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class smc_batch(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("row_start", ctypes.c_void_p), ("S", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_new", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class smc_attn_params(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("mask_words", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class smc_qk_params(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("max_pos", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -84,6 +117,25 @@ _SIGS = {
                                           ctypes.c_size_t, ctypes.c_void_p]),
     "smc_kv_usage": (ctypes.c_int32, [ctypes.POINTER(smc_params), ctypes.POINTER(smc_kv),
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "smc_cache_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(smc_cache),
+                                                    ctypes.POINTER(smc_batch), ctypes.c_int32]),
+    "smc_tree_attention": (ctypes.c_int32, [ctypes.POINTER(smc_attn_params),
+                                            ctypes.POINTER(smc_cache), ctypes.c_int32,
+                                            ctypes.POINTER(smc_batch)] + [ctypes.c_void_p] * 4 +
+                           [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "smc_qk_norm_rope": (ctypes.c_int32, [ctypes.POINTER(smc_qk_params),
+                                          ctypes.POINTER(smc_cache), ctypes.c_int32,
+                                          ctypes.POINTER(smc_batch)] + [ctypes.c_void_p] * 8 +
+                         [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kv_copy_blocks": (ctypes.c_int32, [ctypes.POINTER(smc_cache), ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kv_compact_tokens": (ctypes.c_int32, [ctypes.POINTER(smc_cache), ctypes.POINTER(smc_batch),
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kv_truncate": (ctypes.c_int32, [ctypes.POINTER(smc_params), ctypes.POINTER(smc_kv),
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                     ctypes.c_void_p]),
 }
 
 
@@ -374,3 +426,165 @@ def smc_step_noalloc(params, target_logits, draft_logits, draft_tokens, log_weig
                                   ctypes.byref(kv) if kv is not None else None,
                                   _ptr(status_bits, "status_bits", torch.int32, 1),
                                   _stream(stream)))
+
+
+# ---- the paged cache's data ------------------------------------------------
+
+_CACHE_DTYPES = {torch.float32: SMC_F32, torch.bfloat16: SMC_BF16, torch.float16: SMC_F16}
+_CACHE_TORCH = {code: dtype for dtype, code in _CACHE_DTYPES.items()}
+
+
+def make_cache(k, v):
+    """smc_cache over keys and values [layers, blocks, block_size, kv_heads,
+    head_dim]: CUDA tensors of one dtype (fp32, bf16 or fp16), one shape and
+    one set of strides, the last of them 1 (a head-major cache, or a slice of
+    a larger one, is passed as a view).  The struct holds their addresses:
+    keep the tensors."""
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        if t.dim() != 5 or t.dtype not in _CACHE_DTYPES:
+            raise ValueError(f"{name} must be [layers, blocks, block_size, kv_heads, head_dim] "
+                             f"in fp32, bf16 or fp16, got {tuple(t.shape)} {t.dtype}")
+    if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        raise ValueError("k and v must have one shape, dtype and set of strides")
+    if k.numel() == 0 or (k.stride(4) != 1 and k.shape[4] > 1):
+        raise ValueError("k and v must not be empty and their last axis must be contiguous")
+    return smc_cache(k.data_ptr(), v.data_ptr(), *k.stride()[:4], *k.shape, _CACHE_DTYPES[k.dtype])
+
+
+def make_batch(tables, seq_len, max_new, row_start=None, rows=None, group=1):
+    """smc_batch over a call's sequences: tables [S, T] (or [B, N, T], as in
+    the KV state) and seq_len [S] int32, at most max_new new tokens each;
+    row_start [S + 1] int32 when their numbers differ, with `rows` rows in the
+    arrays (default S * max_new).  group: consecutive sequences of one prompt.
+    The struct holds the tensors' addresses: keep the tensors."""
+    S = seq_len.numel()
+    T = tables.shape[-1]
+    if rows is None:
+        rows = S * max_new
+    return smc_batch(_ptr(tables, "tables", torch.int32, S * T),
+                     _ptr(seq_len, "seq_len", torch.int32),
+                     None if row_start is None else _ptr(row_start, "row_start", torch.int32, S + 1),
+                     S, T, int(rows), int(max_new), int(group))
+
+
+def smc_cache_workspace_bytes(cache, batch=None, q_heads=0):
+    n = lib().smc_cache_workspace_bytes(
+        ctypes.byref(cache), None if batch is None else ctypes.byref(batch), int(q_heads))
+    if n == 0:
+        raise SmcError("smc_cache_workspace_bytes", -1, "invalid shape")
+    return n
+
+
+def alloc_cache_workspace(cache, batch=None, q_heads=0, device="cuda"):
+    """A zero-filled workspace for the cache entry points: with a batch and
+    q_heads for all of them, without for those that take no batch."""
+    return torch.zeros(smc_cache_workspace_bytes(cache, batch, q_heads), dtype=torch.uint8,
+                       device=device)
+
+
+def _rows(t, name, cache, rows, heads):
+    """A [rows, heads, head_dim] tensor of the cache's dtype: its pointer and
+    its row and head strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    shape = (rows, heads, cache.head_dim)
+    if t.shape != shape or t.dtype != _CACHE_TORCH[cache.dtype]:
+        raise ValueError(f"{name} must be {shape} in {_CACHE_TORCH[cache.dtype]}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+    row, head, dim = t.stride()
+    if dim != 1 and cache.head_dim > 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return t.data_ptr(), row, head
+
+
+def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=None, scale=None,
+                       stream=None):
+    """Attention of the new tokens q [rows, q_heads, head_dim] over their
+    sequences' caches into out; mask [rows, words] int32 of packed bits (None:
+    a chain), lse [rows, q_heads] fp32 (None: not wanted), scale (None:
+    head_dim ** -0.5).  See smc_tree_attention in smcsd.h."""
+    rows = batch.rows
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    heads = q.shape[1]
+    qp, q_row, q_head = _rows(q, "q", cache, rows, heads)
+    op, o_row, o_head = _rows(out, "out", cache, rows, heads)
+    words = 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] != rows:
+            raise ValueError(f"mask must be [{rows}, words], got {tuple(mask.shape)}")
+        words = mask.shape[1]
+    params = smc_attn_params(heads, words, cache.head_dim ** -0.5 if scale is None else scale, 0,
+                             q_row, q_head, o_row, o_head)
+    _check("smc_tree_attention", lib().smc_tree_attention(
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp,
+        None if mask is None else _ptr(mask, "mask", torch.int32), op,
+        None if lse is None else _ptr(lse, "lse", torch.float32, rows * heads),
+        _ptr(workspace, "workspace"), workspace.numel(), _stream(stream)))
+
+
+def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, positions=None,
+                     q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
+                     stream=None):
+    """Norms and rotation of the new tokens' q [rows, q_heads, head_dim] (into
+    q_out) and k [rows, kv_heads, head_dim] (into the cache, with v).  rope
+    [max_pos, rot_dim] fp32: cosines, then sines; positions [rows] int32
+    (None: the tokens' own); weights [head_dim] (None: no norm).  See
+    smc_qk_norm_rope in smcsd.h."""
+    rows = batch.rows
+    if q.dim() != 3 or rope.dim() != 2:
+        raise ValueError("q must be [rows, q_heads, head_dim] and rope [max_pos, rot_dim]")
+    heads, dtype = q.shape[1], _CACHE_TORCH[cache.dtype]
+    qp, q_row, q_head = _rows(q, "q", cache, rows, heads)
+    kp, k_row, k_head = _rows(k, "k", cache, rows, cache.kv_heads)
+    vp, v_row, v_head = _rows(v, "v", cache, rows, cache.kv_heads)
+    op, o_row, o_head = _rows(q_out, "q_out", cache, rows, heads)
+    params = smc_qk_params(heads, rope.shape[1], rope.shape[0], int(bool(interleaved)), eps,
+                           weight_offset, q_row, q_head, k_row, k_head, v_row, v_head, o_row,
+                           o_head)
+    _check("smc_qk_norm_rope", lib().smc_qk_norm_rope(
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp, kp, vp,
+        None if q_weight is None else _ptr(q_weight, "q_weight", dtype, cache.head_dim),
+        None if k_weight is None else _ptr(k_weight, "k_weight", dtype, cache.head_dim),
+        None if positions is None else _ptr(positions, "positions", torch.int32, rows),
+        _ptr(rope, "rope", torch.float32), op, _ptr(workspace, "workspace"), workspace.numel(),
+        _stream(stream)))
+
+
+def kv_copy_blocks(cache, pairs, counts, workspace, stream=None):
+    """Copies blocks pairs[l, i, 0] to pairs[l, i, 1], i < counts[l], in every
+    layer: a step's cow_pairs [B, N, 2] and n_cow [B]."""
+    if pairs.dim() != 3 or pairs.shape[2] != 2:
+        raise ValueError(f"pairs must be [lists, max_pairs, 2], got {tuple(pairs.shape)}")
+    lists, most = pairs.shape[:2]
+    _check("kv_copy_blocks", lib().kv_copy_blocks(
+        ctypes.byref(cache), _ptr(pairs, "pairs", torch.int32),
+        _ptr(counts, "counts", torch.int32, lists), lists, most, _ptr(workspace, "workspace"),
+        workspace.numel(), _stream(stream)))
+
+
+def kv_compact_tokens(cache, batch, path, n_path, workspace, stream=None):
+    """Moves new tokens path[s, i] (ascending), i < n_path[s], to new token i
+    of their sequence, in every layer; path [S, max_path], n_path [S] int32."""
+    if path.dim() != 2:
+        raise ValueError(f"path must be [S, max_path], got {tuple(path.shape)}")
+    _check("kv_compact_tokens", lib().kv_compact_tokens(
+        ctypes.byref(cache), ctypes.byref(batch),
+        _ptr(path, "path", torch.int32, batch.S * path.shape[1]),
+        _ptr(n_path, "n_path", torch.int32, batch.S), path.shape[1],
+        _ptr(workspace, "workspace"), workspace.numel(), _stream(stream)))
+
+
+def kv_truncate(params, kv, new_len, workspace, stream=None):
+    """Shortens every particle to new_len [B, N] int32 tokens and gives the
+    blocks past them back."""
+    _check("kv_truncate", lib().kv_truncate(
+        ctypes.byref(params), ctypes.byref(kv),
+        _ptr(new_len, "new_len", torch.int32, params.B * params.N), _ptr(workspace, "workspace"),
+        workspace.numel(), _stream(stream)))

@@ -155,6 +155,14 @@ static int32_t prepare_ws(const smc_params *p, const smc_kv *kv, void *workspace
   return SMC_OK;
 }
 
+int32_t prepare_kv_call(const smc_params *p, const smc_kv *kv, const int32_t *array,
+                        void *workspace, size_t ws_bytes, Workspace *ws) {
+  if (!p) return SMC_ERR_ARG;
+  if (p->dtype != SMC_F32 && p->dtype != SMC_BF16) return SMC_ERR_DTYPE;
+  if (!shape_ok(p) || !kv || !kv_ok(p, kv) || !array) return SMC_ERR_ARG;
+  return prepare_ws(p, kv, workspace, ws_bytes, ws);
+}
+
 }  // namespace smcsd
 
 using namespace smcsd;
@@ -167,8 +175,8 @@ const char *smc_strerror(int32_t code) {
   switch (code) {
     case SMC_OK: return "ok";
     case SMC_ERR_ARG: return "invalid argument (null pointer, size out of range or bad shape)";
-    case SMC_ERR_DTYPE: return "unsupported logit dtype";
-    case SMC_ERR_WORKSPACE: return "workspace null, misaligned or smaller than smc_workspace_bytes()";
+    case SMC_ERR_DTYPE: return "unsupported dtype";
+    case SMC_ERR_WORKSPACE: return "workspace null, misaligned or smaller than its size query says";
     case SMC_ERR_LAUNCH: return "kernel launch failed";
     case SMC_ERR_CUDA: return "CUDA runtime call failed";
     case SMC_DEV_BAD_TOKEN: return "device: drafted token outside [0, V)";
@@ -179,6 +187,7 @@ const char *smc_strerror(int32_t code) {
     case SMC_DEV_TABLE_OVERFLOW: return "device: block table too short";
     case SMC_DEV_BAD_BLOCK: return "device: block id outside its prompt's pool or bad KV state";
     case SMC_DEV_TIMEOUT: return "device: a bounded wait gave up; re-initialise the workspace";
+    case SMC_DEV_BAD_ROWS: return "device: row offset, position or path index out of range";
     default: return code > 0 ? "device: several status bits set" : "unknown error";
   }
 }

@@ -1,0 +1,245 @@
+// Blocks of the cache: copying them (kv_copy_blocks), moving a drafted tree's
+// accepted path to the front (kv_compact_tokens), and giving blocks back
+// (kv_truncate).  Declared in smcsd.h.
+#include "cache_common.cuh"
+
+namespace smcsd {
+
+constexpr int kPageThreads = 256;
+
+// A block seen as rows of contiguous elements: block b, row r (of `rows`, the
+// tokens and heads that are not contiguous with one another).
+struct BlockRows {
+  int32_t rows_outer, rows_inner;      // rows = outer * inner
+  int64_t outer_stride, inner_stride;  // elements
+  int32_t row_elems;
+};
+
+// Collapses (token, head, d) of one block into as few contiguous rows as its
+// strides allow.
+static BlockRows block_rows(const CacheArgs &c) {
+  BlockRows r{c.block_size, c.kv_heads, c.token_stride, c.head_stride, c.head_dim};
+  if (c.head_stride == c.head_dim || c.kv_heads == 1) {  // heads of a token lie side by side
+    r = {1, c.block_size, 0, c.token_stride, c.head_dim * c.kv_heads};
+    if (c.token_stride == r.row_elems) r = {1, 1, 0, 0, r.row_elems * c.block_size};
+  } else if (c.token_stride == c.head_dim || c.block_size == 1) {  // tokens of a head do
+    r = {1, c.kv_heads, 0, c.head_stride, c.head_dim * c.block_size};
+    if (c.head_stride == r.row_elems) r = {1, 1, 0, 0, r.row_elems * c.kv_heads};
+  }
+  return r;
+}
+
+template <typename U>
+__global__ void __launch_bounds__(kPageThreads)
+copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_t *counts,
+                   int max_pairs, int esz, unsigned *status) {
+  const int list = blockIdx.x / max_pairs, i = blockIdx.x % max_pairs;
+  const int n = counts[list];
+  if (n < 0 || n > max_pairs) {
+    if (threadIdx.x == 0) raise_status(status, SMC_DEV_BAD_ROWS);
+    return;
+  }
+  if (i >= n) return;
+  const int src = pairs[2 * static_cast<int64_t>(blockIdx.x)];
+  const int dst = pairs[2 * static_cast<int64_t>(blockIdx.x) + 1];
+  if (src < 0 || src >= c.blocks || dst < 0 || dst >= c.blocks) {
+    if (threadIdx.x == 0) raise_status(status, SMC_DEV_BAD_BLOCK);
+    return;
+  }
+  const int layer = blockIdx.y >> 1;
+  char *base = ((blockIdx.y & 1) ? c.v : c.k) + layer * c.layer_stride * esz;
+  const char *from = base + src * c.block_stride * esz;
+  char *to = base + dst * c.block_stride * esz;
+  const int per_row = static_cast<int>(static_cast<int64_t>(br.row_elems) * esz / sizeof(U));
+  const int rows = br.rows_outer * br.rows_inner;
+  for (int r = 0; r < rows; ++r) {
+    const int64_t off = ((r / br.rows_inner) * br.outer_stride +
+                         (r % br.rows_inner) * br.inner_stride) * esz;
+    for (int e = threadIdx.x; e < per_row; e += kPageThreads) {
+      reinterpret_cast<U *>(to + off)[e] = reinterpret_cast<const U *>(from + off)[e];
+    }
+  }
+}
+
+// Thread t owns column t of a token's (head, d) elements for the whole path.
+// A path ascends, so path[i] >= i: taken in order, no move overwrites a later
+// source, and no thread touches another's column.
+template <typename U>
+__global__ void __launch_bounds__(kPageThreads)
+compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32_t *n_path,
+                      int max_path, int esz, unsigned *status) {
+  const int s = blockIdx.x;
+  const SeqInfo si = seq_info(b, c.block_size, s);
+  const int n = n_path[s];
+  const bool reports = threadIdx.x == 0 && blockIdx.y == 0;
+  if (si.bits || n < 0 || n > max_path) {
+    if (reports) raise_status(status, si.bits | (n < 0 || n > max_path ? SMC_DEV_BAD_ROWS : 0));
+    return;
+  }
+  const int layer = blockIdx.y >> 1;
+  char *base = ((blockIdx.y & 1) ? c.v : c.k) + layer * c.layer_stride * esz;
+  const int per_head = static_cast<int>(static_cast<int64_t>(c.head_dim) * esz / sizeof(U));
+  const int cols = per_head * c.kv_heads;
+  const int first = si.len - si.n;
+  const int32_t *table = b.tables + static_cast<int64_t>(s) * b.T;
+  const int32_t *p = path + static_cast<int64_t>(s) * max_path;
+  for (int col = threadIdx.x; col < cols; col += kPageThreads) {
+    const int64_t in_token = (col / per_head) * c.head_stride * esz +
+                             static_cast<int64_t>(col % per_head) * sizeof(U);
+    int last = -1;
+    for (int i = 0; i < n; ++i) {
+      const int j = p[i];
+      if (j <= last || j >= si.n) {
+        if (reports) raise_status(status, SMC_DEV_BAD_ROWS);
+        continue;
+      }
+      last = j;
+      if (j == i) continue;
+      const int from = first + j, to = first + i;
+      const int fb = table[from / c.block_size], tb = table[to / c.block_size];
+      if (fb < 0 || fb >= c.blocks || tb < 0 || tb >= c.blocks) {
+        if (reports) raise_status(status, SMC_DEV_BAD_BLOCK);
+        continue;
+      }
+      const int64_t fo = fb * c.block_stride + (from % c.block_size) * c.token_stride;
+      const int64_t to_ = tb * c.block_stride + (to % c.block_size) * c.token_stride;
+      *reinterpret_cast<U *>(base + to_ * esz + in_token) =
+          *reinterpret_cast<const U *>(base + fo * esz + in_token);
+    }
+  }
+}
+
+// One CTA per prompt: references of the slots past the kept blocks are
+// dropped, freed blocks collected in the workspace's bitmap, then pushed in
+// ascending id order; the bitmap is left clear.
+__global__ void __launch_bounds__(kPageThreads)
+kv_truncate_kernel(int N, KvArgs kv, const int32_t *new_len, Workspace ws) {
+  __shared__ int s_warp[kPageThreads / 32];
+  __shared__ int s_top;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int words = (kv.P + 31) / 32;
+  unsigned *bitmap = ws.kv_bitmap + static_cast<int64_t>(b) * words;
+  const int base = b * kv.P;
+  for (int n = 0; n < N; ++n) {
+    const int64_t at = static_cast<int64_t>(b) * N + n;
+    const int len = kv.seq_len[at], keep = new_len[at];
+    if (keep < 0 || keep > len || len > static_cast<int64_t>(kv.T) * kv.block_size) {
+      if (tid == 0) raise_status(ws.status, SMC_DEV_BAD_BLOCK);
+      continue;
+    }
+    const int from = static_cast<int>((static_cast<int64_t>(keep) + kv.block_size - 1) / kv.block_size);
+    const int to = static_cast<int>((static_cast<int64_t>(len) + kv.block_size - 1) / kv.block_size);
+    for (int t = from + tid; t < to; t += kPageThreads) {
+      int32_t *slot = kv.tables + at * kv.T + t;
+      const int id = *slot;
+      if (id < base || id >= base + kv.P) {
+        raise_status(ws.status, SMC_DEV_BAD_BLOCK);
+        continue;
+      }
+      *slot = -1;
+      const int old = atomicSub(&kv.refcount[id], 1);
+      if (old <= 0) {
+        atomicAdd(&kv.refcount[id], 1);
+        raise_status(ws.status, SMC_DEV_BAD_BLOCK);
+      } else if (old == 1) {
+        atomicOr(&bitmap[(id - base) >> 5], 1u << ((id - base) & 31));
+      }
+    }
+    __syncthreads();  // every thread has read this particle's length
+    if (tid == 0) kv.seq_len[at] = keep;
+  }
+  if (tid == 0) s_top = kv.free_top[b];
+  __syncthreads();
+  for (int w0 = 0; w0 < words; w0 += kPageThreads) {
+    const int w = w0 + tid;
+    unsigned m = 0;
+    if (w < words) {
+      m = __ldcg(&bitmap[w]);
+      if (m) bitmap[w] = 0;
+    }
+    const int mine = __popc(m);
+    int incl = mine;
+    const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int before = s_top, total = 0;
+    for (int k = 0; k < kPageThreads / 32; ++k) {
+      if (k < warp) before += s_warp[k];
+      total += s_warp[k];
+    }
+    int at = before + incl - mine;
+    while (m) {
+      const int bit = __ffs(m) - 1;
+      m &= m - 1;
+      if (at >= 0 && at < kv.P) kv.free_list[static_cast<int64_t>(base) + at] = base + 32 * w + bit;
+      else raise_status(ws.status, SMC_DEV_BAD_BLOCK);
+      ++at;
+    }
+    __syncthreads();
+    if (tid == 0) s_top += total;
+    __syncthreads();
+  }
+  if (tid == 0) kv.free_top[b] = s_top;
+}
+
+// Widest access that every address of the cache is a multiple of.
+static int access_bytes(const CacheArgs &c) {
+  const int esz = dtype_bytes(c.dtype);
+  const uint64_t bits = reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) |
+                        static_cast<uint64_t>(c.layer_stride * esz) |
+                        static_cast<uint64_t>(c.block_stride * esz) |
+                        static_cast<uint64_t>(c.token_stride * esz) |
+                        static_cast<uint64_t>(c.head_stride * esz) |
+                        static_cast<uint64_t>(c.head_dim) * esz;
+  if (bits % 16 == 0) return 16;
+  return bits % 4 == 0 ? 4 : 2;
+}
+
+cudaError_t launch_copy_blocks(const CacheArgs &c, const int32_t *pairs, const int32_t *counts,
+                               int lists, int max_pairs, unsigned *status, cudaStream_t st) {
+  const dim3 grid(lists * max_pairs, 2 * c.layers);
+  const BlockRows br = block_rows(c);
+  const int esz = dtype_bytes(c.dtype);
+  switch (access_bytes(c)) {
+    case 16:
+      copy_blocks_kernel<uint4><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
+      break;
+    case 4:
+      copy_blocks_kernel<uint32_t><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
+      break;
+    default:
+      copy_blocks_kernel<uint16_t><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact_tokens(const CacheArgs &c, const BatchArgs &b, const int32_t *path,
+                                  const int32_t *n_path, int max_path, unsigned *status,
+                                  cudaStream_t st) {
+  const dim3 grid(b.S, 2 * c.layers);
+  const int esz = dtype_bytes(c.dtype);
+  switch (access_bytes(c)) {
+    case 16:
+      compact_tokens_kernel<uint4><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
+      break;
+    case 4:
+      compact_tokens_kernel<uint32_t><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
+      break;
+    default:
+      compact_tokens_kernel<uint16_t><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_truncate(int B, int N, const KvArgs &kv, const int32_t *new_len,
+                               const Workspace &ws, cudaStream_t st) {
+  kv_truncate_kernel<<<B, kPageThreads, 0, st>>>(N, kv, new_len, ws);
+  return cudaGetLastError();
+}
+
+}  // namespace smcsd

@@ -18,6 +18,11 @@ int32_t check_step_args(const smc_params *p, const void *target_logits,
                         const int32_t *ancestors, const float *ess, const int32_t *resampled,
                         const smc_kv *kv);
 
+// The checks of an entry point that takes a shape, a KV struct and one device
+// array, and the carve of its workspace: SMC_OK or the code it returns.
+int32_t prepare_kv_call(const smc_params *p, const smc_kv *kv, const int32_t *array,
+                        void *workspace, size_t ws_bytes, struct Workspace *ws);
+
 // Per-(row, chunk) partial of a vocabulary reduction: chunk max m, fast fp32
 // sum s of exp(l - m), and the float-float sum (shi, slo) of the sampling
 // weights exp(alpha (l - m)) (bonus rows only).

@@ -36,11 +36,15 @@ static bool batch_ok(const smc_batch *b) {
   return true;
 }
 
+// The stride of an axis of length 1 is never used: it counts as an aligned one.
+static int64_t stride_of(int64_t stride, int32_t length) { return length > 1 ? stride : 128; }
+
 static CacheArgs to_cache(const smc_cache *c, int layer) {
   const int64_t at = layer * c->layer_stride * dtype_bytes(c->dtype);
-  return {static_cast<char *>(c->k) + at, static_cast<char *>(c->v) + at, c->layer_stride,
-          c->block_stride, c->token_stride, c->head_stride, c->layers, c->blocks, c->block_size,
-          c->kv_heads, c->head_dim, c->dtype};
+  return {static_cast<char *>(c->k) + at, static_cast<char *>(c->v) + at,
+          stride_of(c->layer_stride, c->layers), stride_of(c->block_stride, c->blocks),
+          stride_of(c->token_stride, c->block_size), stride_of(c->head_stride, c->kv_heads),
+          c->layers, c->blocks, c->block_size, c->kv_heads, c->head_dim, c->dtype};
 }
 
 static BatchArgs to_batch(const smc_batch *b) {
@@ -91,8 +95,11 @@ int32_t smc_tree_attention(const smc_attn_params *p, const smc_cache *cache, int
   if (p->mask_words < 0 || (mask && p->mask_words < 1)) return SMC_ERR_ARG;
   if (cache->head_dim % 8 != 0 || cache->head_dim > 128) return SMC_ERR_ARG;
   const CacheArgs c = to_cache(cache, layer);
-  for (const int64_t stride : {c.block_stride, c.token_stride, c.head_stride, p->q_row_stride,
-                               p->q_head_stride, p->out_row_stride, p->out_head_stride}) {
+  const int rows = batch->rows;
+  for (const int64_t stride :
+       {c.block_stride, c.token_stride, c.head_stride, stride_of(p->q_row_stride, rows),
+        stride_of(p->q_head_stride, p->q_heads), stride_of(p->out_row_stride, rows),
+        stride_of(p->out_head_stride, p->q_heads)}) {
     if (stride < 0 || stride % 8 != 0) return SMC_ERR_ARG;
   }
   if (!multiple_of_16(c.k) || !multiple_of_16(c.v) || !multiple_of_16(q) || !multiple_of_16(out)) {

@@ -1,90 +1,1199 @@
 // Attention of each sequence's new tokens over its paged cache, under a tree
 // mask (smc_tree_attention in smcsd.h).
+//
+// Three kernels, chained by programmatic dependent launch:
+//   plan_kernel       lists the call's work in tiles of 128 tokens;
+//   attention_kernel  persistent, one CTA per SM, on the 5th-generation tensor
+//                     cores; every CTA takes an equal run of the tiles;
+//   combine_kernel    joins rows that several CTAs, or a shared and an own
+//                     part, contributed to.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "cache_common.cuh"
 
 namespace smcsd {
 
-constexpr int kAttnThreads = 256;
+// ---------------------------------------------------------------------------
+// Work.  An *entry* is a run of consecutive rows and a range of tokens that
+// they all attend: the own part of one sequence, or the part that the
+// sequences of a prompt share (their leading equal table slots).  Per key
+// head and per 256 rows (new token x query head of the key head) an entry
+// makes one *unit* of ceil(tokens / 128) tiles.  The units' tiles form one
+// line; CTA c takes tiles [c * per, (c + 1) * per) of it, so ragged lengths
+// load every SM alike.  A unit's first tiles' CTA owns the unit's result;
+// every later CTA of the unit has exactly one such continuation (its first
+// segment) and stores it in its own slot.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 128;        // tokens per tile
+constexpr int kUnitRows = 256;    // rows per unit: two tensor-core tiles of 128
+constexpr int kMaxCtas = 192;     // slots for continuations
+constexpr int kPlanThreads = 1024;
+constexpr uint32_t kWaitPolls = 1u << 17;  // each may suspend up to 20 us
 
-// One warp per (row, head): the online softmax, a token at a time.
-template <typename T>
-__global__ void __launch_bounds__(kAttnThreads) tree_attention_kernel(const AttnArgs a) {
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (unit >= static_cast<int64_t>(a.b.rows) * a.q_heads) return;
-  const int row = static_cast<int>(unit / a.q_heads), h = static_cast<int>(unit % a.q_heads);
-  const int s = seq_of_row(a.b, row);
-  if (s < 0) return;
-  const SeqInfo si = seq_info(a.b, a.c.block_size, s);
-  const int i = row - si.row0;
-  if (i < 0 || i >= si.n) {
-    if (lane == 0 && si.bits) raise_status(a.status, si.bits);
-    return;
+struct Entry {
+  int row0;    // first row
+  int tokens;  // rows of one query head
+  int seq;     // whose table
+  int kv0, kv1;
+  int ctx;     // tokens before ctx are seen by every row
+  int tiles;   // per unit
+  int flags;
+};
+constexpr int kShared = 1, kSolo = 2;  // a shared part; the rows have no other part
+
+struct PlanHeader {
+  unsigned ticket;  // plan CTAs done; returns to zero
+  int total, per;   // tiles, tiles per CTA
+};
+
+struct AttnWorkspace {
+  PlanHeader *head;
+  int *common;     // [groups] shared tokens
+  int *tile0;      // [entries + 1]
+  Entry *entries;  // shared parts of the groups (when group > 1), then the sequences
+  float *lse[2];   // own, shared: [rows * q_heads], log2
+  float *o[2];     // [rows * q_heads][head_dim], normalised
+  float *lse_c;    // [kMaxCtas][kUnitRows] continuations
+  float *o_c;      // [kMaxCtas][kUnitRows][head_dim]
+  int groups;      // 0 when group == 1
+  int n_entries;
+};
+
+static size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, char *base,
+                    AttnWorkspace *w) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return base + at;
+  };
+  AttnWorkspace t{};
+  const size_t rh = static_cast<size_t>(b.rows) * q_heads, D = c.head_dim;
+  t.groups = b.group > 1 ? b.S / b.group : 0;
+  t.n_entries = b.S + t.groups;
+  take(kCacheStatusBytes);
+  t.head = reinterpret_cast<PlanHeader *>(take(sizeof(PlanHeader)));
+  t.common = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
+  t.tile0 = reinterpret_cast<int *>(take(sizeof(int) * (static_cast<size_t>(t.n_entries) + 1)));
+  t.entries = reinterpret_cast<Entry *>(take(sizeof(Entry) * t.n_entries));
+  for (int k = 0; k < 2; ++k) {
+    const size_t n = k == 0 || t.groups ? rh : 0;
+    t.lse[k] = reinterpret_cast<float *>(take(sizeof(float) * n));
+    t.o[k] = reinterpret_cast<float *>(take(sizeof(float) * n * D));
   }
-  const int D = a.c.head_dim;
-  const T *q = reinterpret_cast<const T *>(a.q) + row * a.q_row + h * a.q_head;
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+  t.lse_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows));
+  t.o_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows * D));
+  if (w) *w = t;
+  return off;
+}
+
+size_t attention_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads) {
+  return carve(c, b, q_heads, nullptr, nullptr);
+}
+
+struct KernelArgs {
+  AttnArgs a;
+  AttnWorkspace w;
+  int rep;      // query heads per key head
+  int box;      // tokens per copied box (0: element copies)
+  float sc;     // scale * log2 e
+};
+
+// ---------------------------------------------------------------------------
+// plan_kernel: the tokens that each prompt's sequences share, then (the last
+// CTA to finish) the entries and the prefix of their tiles.
+// ---------------------------------------------------------------------------
+__device__ int block_scan_excl(int v, int *warps, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) qv[e] = lane + 32 * e < D ? to_f32(q[lane + 32 * e]) : 0.f;
-  const int kh = h / (a.q_heads / a.c.kv_heads);
-  const int32_t *table = a.b.tables + static_cast<int64_t>(s) * a.b.T;
-  const int ctx = si.len - si.n;
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < si.len; ++t) {
-    if (t >= ctx) {
-      const int j = t - ctx;
-      bool sees = j <= i;
-      if (a.mask) {
-        sees = (j >> 5) < a.mask_words &&
-               (a.mask[static_cast<int64_t>(row) * a.mask_words + (j >> 5)] >> (j & 31) & 1u);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int k = 0; k < kPlanThreads / 32; ++k) {
+    if (k < warp) before += warps[k];
+    all += warps[k];
+  }
+  __syncthreads();
+  *total = all;
+  return before + incl - v;
+}
+
+__device__ __forceinline__ int entry_tiles(const KernelArgs &k, int tokens, int kv0, int kv1,
+                                           int *per_unit) {
+  *per_unit = (kv1 - kv0 + kTile - 1) / kTile;
+  if (tokens <= 0 || kv1 <= kv0) return 0;
+  return *per_unit * k.a.c.kv_heads * ((tokens * k.rep + kUnitRows - 1) / kUnitRows);
+}
+
+__device__ int make_entry(const KernelArgs &k, int e, Entry *out) {
+  const BatchArgs &b = k.a.b;
+  const int bs = k.a.c.block_size;
+  Entry t{};
+  int tiles;
+  if (e < k.w.groups) {
+    const int s0 = e * b.group;
+    const int shared = __ldcg(&k.w.common[e]);
+    if (shared > 0) {  // every sequence is in order, so the rows are consecutive
+      const SeqInfo first = seq_info(b, bs, s0), last = seq_info(b, bs, s0 + b.group - 1);
+      t = {first.row0, last.row0 + last.n - first.row0, s0, 0, shared, shared, 0, kShared};
+    }
+    tiles = entry_tiles(k, t.tokens, 0, shared, &t.tiles);
+  } else {
+    const int s = e - k.w.groups;
+    const SeqInfo si = seq_info(b, bs, s);
+    if (si.bits) raise_status(k.a.status, si.bits);
+    const int shared = k.w.groups ? __ldcg(&k.w.common[s / b.group]) : 0;
+    t = {si.row0, si.n, s, shared, si.len, si.len - si.n, 0, shared ? 0 : kSolo};
+    tiles = entry_tiles(k, t.tokens, t.kv0, t.kv1, &t.tiles);
+  }
+  if (out) *out = t;
+  return tiles;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KernelArgs k, int ctas) {
+  __shared__ int warps[kPlanThreads / 32];
+  __shared__ int s_slots, s_limit, s_seqs, s_bad, s_ref;
+  __shared__ bool s_last;
+  const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const BatchArgs &b = k.a.b;
+  const int bs = k.a.c.block_size;
+  if (k.w.groups) {
+    const int s0 = blockIdx.x * b.group;
+    if (tid == 0) {
+      s_limit = 0x7fffffff;
+      s_seqs = s_bad = 0;
+      s_ref = 0x7fffffff;
+    }
+    __syncthreads();
+    for (int i = tid; i < b.group; i += kPlanThreads) {
+      const SeqInfo si = seq_info(b, bs, s0 + i);
+      if (si.bits) s_bad = 1;
+      if (si.n > 0) {
+        atomicMin(&s_limit, si.len - si.n);
+        atomicAdd(&s_seqs, 1);
+        atomicMin(&s_ref, s0 + i);
       }
-      if (!sees) continue;
     }
-    const int block = table[t / a.c.block_size];
-    if (block < 0 || block >= a.c.blocks) {
-      if (lane == 0) raise_status(a.status, SMC_DEV_BAD_BLOCK);
-      continue;
+    __syncthreads();
+    if (tid == 0) s_slots = s_seqs > 1 && !s_bad ? s_limit / bs : 0;
+    __syncthreads();
+    const int slots = s_slots;
+    if (slots > 0) {
+      const int32_t *ref = b.tables + static_cast<int64_t>(s_ref) * b.T;
+      int mine = slots;
+      for (int i = s_ref - s0 + 1; i < b.group; ++i) {
+        if (b.row_start && b.row_start[s0 + i] == b.row_start[s0 + i + 1]) continue;  // no rows
+        const int32_t *row = b.tables + static_cast<int64_t>(s0 + i) * b.T;
+        for (int t = tid; t < mine; t += kPlanThreads) {
+          if (row[t] != ref[t]) mine = t;
+        }
+      }
+      if (mine < slots) atomicMin(&s_slots, mine);
     }
-    const int64_t off = block * a.c.block_stride + (t % a.c.block_size) * a.c.token_stride +
-                        kh * a.c.head_stride;
-    const T *k = reinterpret_cast<const T *>(a.c.k) + off;
-    const T *v = reinterpret_cast<const T *>(a.c.v) + off;
-    float z = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (lane + 32 * e < D) z = fmaf(qv[e], to_f32(k[lane + 32 * e]), z);
+    __syncthreads();
+    if (tid == 0) {
+      const int64_t tokens = static_cast<int64_t>(s_slots) * bs;
+      k.w.common[blockIdx.x] = static_cast<int>(tokens / kTile * kTile);
+      __threadfence();
+      s_last = atomicAdd(&k.w.head->ticket, 1) + 1 == gridDim.x;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    z *= a.scale;
-    const float mn = fmaxf(m, z);
-    const float f = m == -INFINITY ? 0.f : __expf(m - mn), p = mn == -INFINITY ? 0.f : __expf(z - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (lane + 32 * e < D) acc[e] = fmaf(p, to_f32(v[lane + 32 * e]), acc[e] * f);
-    }
-    m = mn;
+    __syncthreads();
+    if (!s_last) return;
+    if (tid == 0) k.w.head->ticket = 0;
+    __threadfence();
   }
-  T *out = reinterpret_cast<T *>(a.out) + row * a.o_row + h * a.o_head;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (lane + 32 * e < D) out[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : acc[e] / l);
+  // the prefix of the tiles: thread t takes a run of entries
+  const int run = (k.w.n_entries + kPlanThreads - 1) / kPlanThreads;
+  const int e0 = min(tid * run, k.w.n_entries), e1 = min(e0 + run, k.w.n_entries);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) {
+    Entry t;
+    mine += make_entry(k, e, &t);
+    k.w.entries[e] = t;
   }
-  if (a.lse && lane == 0) a.lse[unit] = l == 0.f ? -INFINITY : m + logf(l);
+  int total;
+  int at = block_scan_excl(mine, warps, &total);
+  for (int e = e0; e < e1; ++e) {
+    k.w.tile0[e] = at;
+    const Entry &t = k.w.entries[e];
+    int unused;
+    at += entry_tiles(k, t.tokens, t.kv0, t.kv1, &unused);
+  }
+  if (tid == 0) {
+    k.w.tile0[k.w.n_entries] = total;
+    k.w.head->total = total;
+    k.w.head->per = max(1, (total + ctas - 1) / ctas);
+  }
 }
 
-size_t attention_workspace_bytes(const CacheArgs &, const BatchArgs &, int) {
-  return kCacheStatusBytes;
+// ---------------------------------------------------------------------------
+// Tensor-core and tensor-memory primitives (PTX for sm_103a).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_512(uint32_t *dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                   smem_addr(dst))
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_512(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#define SMC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                     "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define SMC_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), \
+                     "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 columns of the calling warp's 32 lanes: thread = lane, register = column.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : SMC_R8(r, 0), SMC_R8(r, 8), SMC_R8(r, 16), SMC_R8(r, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
+          SMC_I8(r, 0),
+      SMC_I8(r, 8), SMC_I8(r, 16), SMC_I8(r, 24), "r"(addr)
+      : "memory");
+}
+// Waits for the warp's loads.  The registers of a load count as written only
+// here, so that no use of them moves ahead of the wait.
+#define SMC_T8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
+                     "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_tie(uint32_t *r) {
+  asm volatile("" : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24));
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Shared-memory operand in 128-byte-swizzled rows of 64 elements: `lbo` bytes
+// between 64-element panels (of the contiguous axis, MN-major operands only),
+// 1024 bytes between groups of eight rows.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
+         static_cast<uint64_t>(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// kind::f16 with 128 rows, n columns, fp32 accumulators; b_mn: B is stored
+// with its n axis contiguous.
+__host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int d, int token,
+                                            int head, int block, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(token), "r"(head), "r"(block)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
 }
 
-cudaError_t launch_tree_attention(const AttnArgs &a, void *, cudaStream_t st) {
+template <typename T>
+struct Weights;
+template <>
+struct Weights<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
+  // weights are 2^(z - m), m at most kLazy below the running maximum
+  static constexpr float kOffset = 0.f;
+  static constexpr uint32_t kExpMask = 0x7f807f80u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+  }
+};
+template <>
+struct Weights<__half> {
+  static constexpr bool kBf16 = false;
+  // fp16 has 2^-24 .. 65504: weights are scaled by 2^7, so that with kLazy
+  // they stay below 2^15 and small ones keep 7 more bits
+  static constexpr float kOffset = 7.f;
+  static constexpr uint32_t kExpMask = 0x7c007c00u;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+  }
+};
+// The accumulators are rescaled only when the running maximum (log2) rises
+// by more than this; until then weights may reach 2^kLazy.
+constexpr float kLazy = 8.f;
+
+// ---------------------------------------------------------------------------
+// attention_kernel.  Warps 0-3 and 4-7: two softmax groups (thread = row of a
+// 128-row tile); warp 8: the thread that issues the matrix products; warp 9:
+// the copies.  Shared memory: Q (two row tiles) and a ring of K and V tiles.
+// Tensor memory: scores of either group (their weights overwrite them), and
+// either group's accumulator.
+//   Units of up to 128 rows: the groups take alternate tiles of the unit, each
+//   with its own running maximum, sum and accumulator, joined at the end.
+//   Larger units: each group has its own 128 rows; a tile of K and V serves
+//   both.
+// Group g's next scores are issued right behind its last product with V, so
+// one group's softmax runs beside the other's products.
+// ---------------------------------------------------------------------------
+constexpr int kAttnThreads = 320;
+constexpr int kRingBytes = 160 * 1024;
+
+template <int kHalves>  // 64-element panels of the head dim
+struct Geometry {
+  static constexpr int kTileBytes = kHalves * kTile * 128;
+  static constexpr int kSlots = kRingBytes / kTileBytes;
+  static constexpr int kQBytes = 2 * kTileBytes;
+  static constexpr int kTail = kQBytes + kRingBytes;
+};
+
+struct AttnTail {
+  uint64_t full[10], empty[10], q_full, scores[2], weights[2], o_full, stats, drained;
+  float2 stat[2][kTile];  // either group's (max, sum) of a row
+  uint32_t tmem;
+  unsigned nonfinite;     // segment number (from 1) of the last one with a non-finite value
+  volatile int abort;
+};
+
+// A CTA's walk over its tiles: one segment (part of a unit) at a time.
+struct Walk {
+  int x, x1, e;
+  Entry t;
+  int base;       // tile0[e]
+  int head, rt;   // unit
+  int i0, n;      // tiles [i0, i0 + n) of the unit
+  int rows;       // rows of the unit
+  __device__ __forceinline__ void start(const AttnWorkspace &w) {
+    const int per = __ldcg(&w.head->per), total = __ldcg(&w.head->total);
+    x = min(static_cast<int>(blockIdx.x) * per, total);
+    x1 = min(x + per, total);
+    if (x >= x1) return;
+    int lo = 0, hi = w.n_entries - 1;  // the last entry with tile0 <= x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldcg(&w.tile0[mid]) <= x) lo = mid; else hi = mid - 1;
+    }
+    e = lo;
+    load(w);
+  }
+  __device__ __forceinline__ void load(const AttnWorkspace &w) {
+    const int4 *p = reinterpret_cast<const int4 *>(&w.entries[e]);
+    const int4 a = __ldcg(p), b = __ldcg(p + 1);
+    t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    base = __ldcg(&w.tile0[e]);
+  }
+  __device__ __forceinline__ bool next(const KernelArgs &k) {
+    if (x >= x1) return false;
+    const int total_rows = t.tokens * k.rep;
+    int rts = (total_rows + kUnitRows - 1) / kUnitRows;
+    while (t.tiles * rts * k.a.c.kv_heads <= x - base || t.tokens <= 0) {
+      ++e;
+      load(k.w);
+      rts = (t.tokens * k.rep + kUnitRows - 1) / kUnitRows;
+    }
+    const int local = x - base, u = local / t.tiles;
+    i0 = local - u * t.tiles;
+    n = min(t.tiles - i0, x1 - x);
+    head = u / rts;
+    rt = u - head * rts;
+    rows = min(t.tokens * k.rep - rt * kUnitRows, kUnitRows);
+    x += n;
+    return true;
+  }
+};
+
+// Ring positions of a segment's n tiles, in the order of their use.
+__device__ __forceinline__ int pos_k(bool pair, int n, int i) {
+  return pair ? 2 * i : (i == 0 ? 0 : 2 * i - 1);
+}
+__device__ __forceinline__ int pos_v(bool pair, int n, int i) {
+  return pair ? 2 * i + 1 : (i + 1 < n ? 2 * i + 2 : 2 * n - 1);
+}
+
+// False when the wait gave up (it raised the status bit and the abort flag, at
+// which every other wait of the CTA gives up too).
+__device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_t parity,
+                                             unsigned *status) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (s->abort) return false;
+  }
+  s->abort = 1;
+  raise_status(status, SMC_DEV_TIMEOUT);
+  return false;
+}
+
+// The same for a whole warp: one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t parity,
+                                          unsigned *status) {
+  return __all_sync(0xffffffffu, guarded_wait(s, bar, parity, status));
+}
+
+// Bits of a row's view of new tokens j0 .. j0 + 31: 1 for committed tokens
+// (j < 0), the mask's bit or the chain's for new ones, 0 past them.
+__device__ __forceinline__ uint32_t view_bits(const uint32_t *mask, int words, int i, int n_new,
+                                              int j0) {
+  if (j0 + 32 <= 0) return 0xffffffffu;
+  if (j0 >= n_new) return 0u;
+  uint32_t bits;
+  if (mask) {
+    const int w = j0 >> 5;
+    const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? __ldg(mask + w) : 0u);
+    const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? __ldg(mask + w + 1) : 0u);
+    bits = __funnelshift_r(lo, hi, j0 & 31);
+  } else {
+    const int c = i - j0 + 1;  // new tokens 0..i
+    bits = c <= 0 ? 0u : (c >= 32 ? 0xffffffffu : (1u << c) - 1u);
+  }
+  const int left = n_new - j0;
+  if (left < 32) bits &= (1u << left) - 1u;
+  return bits;
+}
+
+// A new token that holds an infinity or NaN had it zeroed in the products, as
+// rows that do not see the token must not meet it; rows that see it get it
+// here: columns [col, col + 32) of v, of the new tokens in [t0, t1).
+template <typename T>
+__device__ __noinline__ void add_nonfinite(const KernelArgs &k, const Entry &t, int head, int row,
+                                           int i, int t0, int t1, int col, float *o) {
+  const uint32_t *mask = k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
+  const int32_t *table = k.a.b.tables + static_cast<int64_t>(t.seq) * k.a.b.T;
+  for (int at = max(t0, t.ctx); at < min(t1, t.kv1); ++at) {
+    if (!(view_bits(mask, k.a.mask_words, i, t.tokens, at - t.ctx) & 1u)) continue;
+    const int block = table[at / k.a.c.block_size];
+    if (block < 0 || block >= k.a.c.blocks) continue;
+    const T *v = reinterpret_cast<const T *>(k.a.c.v) + block * k.a.c.block_stride +
+                 (at % k.a.c.block_size) * k.a.c.token_stride + head * k.a.c.head_stride;
+    for (int d = 0; d < 32; ++d) {
+      if (col + d >= k.a.c.head_dim) break;
+      const float x = to_f32(v[col + d]);
+      if (!(fabsf(x) < INFINITY)) o[d] += x;
+    }
+  }
+}
+
+template <typename T, int kHalves, bool kTma>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v) {
+  using G = Geometry<kHalves>;
+  using Wt = Weights<T>;
+  extern __shared__ __align__(1024) char smem[];
+  char *const s_q = smem;
+  char *const s_ring = smem + G::kQBytes;
+  AttnTail *const s = reinterpret_cast<AttnTail *>(smem + G::kTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int D = k.a.c.head_dim;
+
+  if (tid == 0) {
+    for (int i = 0; i < G::kSlots; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 1);
+    }
+    mbar_init(&s->q_full, 8);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s->scores[g], 1);
+      mbar_init(&s->weights[g], 4);
+    }
+    mbar_init(&s->o_full, 1);
+    mbar_init(&s->stats, 8);
+    mbar_init(&s->drained, 1);
+    s->nonfinite = 0;
+    s->abort = (smem_addr(smem) & 1023u) != 0;  // the swizzle counts from 1 KB boundaries
+    mbar_init_fence();
+  }
+  if (warp == 8) tmem_alloc_512(&s->tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (s->abort) {
+    if (tid == 0) raise_status(k.a.status, SMC_DEV_TIMEOUT);
+  } else if (warp < 8) {
+    // ---- softmax groups ---------------------------------------------------
+    const int g = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;  // row of the group's tile
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t t_s = tmem + lanes + g * 128, t_o = tmem + lanes + 256 + g * 128;
+    Walk w;
+    w.start(k.w);
+    uint32_t seg = 0, ring = 0, phase = 0;
+    bool ok = true;
+    while (ok && w.next(k)) {
+      ++seg;
+      const bool pair = w.rows > kTile;
+      const int row_in_unit = pair ? g * kTile + r : r;
+      const bool live = row_in_unit < w.rows;
+      const bool warp_live = (pair ? g * kTile : 0) + wq * 32 < w.rows;
+      const int r_all = w.rt * kUnitRows + row_in_unit;
+      const int i_new = live ? r_all / k.rep : 0;  // new token of a sequence's own part
+      const int row = w.t.row0 + i_new;
+      const int qh = w.head * k.rep + (live ? r_all - i_new * k.rep : 0);
+      {  // Q: a row of either tile per thread; with one tile the groups split its columns
+        const T *q = reinterpret_cast<const T *>(k.a.q) + row * k.a.q_row + qh * k.a.q_head;
+        char *dst = s_q + (pair ? g * G::kTileBytes : 0) + r * 128;
+        const int c0 = pair ? 0 : g * 4 * kHalves, c1 = pair ? 8 * kHalves : c0 + 4 * kHalves;
+        if (warp_live) {
+          for (int c = c0; c < c1; ++c) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live && c * 8 < D) x = *reinterpret_cast<const uint4 *>(q + c * 8);
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kTile * 128) +
+                                       (((c & 7) ^ (r & 7)) << 4)) = x;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
+        const int t0 = w.t.kv0 + (w.i0 + i) * kTile;
+        if (!(ok = warp_wait(s, &s->scores[g], phase & 1u, k.a.status))) break;
+        ++phase;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t z[128];
+          tmem_ld32(t_s, z);
+          tmem_ld32(t_s + 32, z + 32);
+          tmem_ld32(t_s + 64, z + 64);
+          tmem_ld32(t_s + 96, z + 96);
+          tmem_wait_ld(z);
+          tmem_tie(z + 32);
+          tmem_tie(z + 64);
+          tmem_tie(z + 96);
+          if (t0 + kTile > w.t.ctx && !(w.t.flags & kShared)) {
+            const uint32_t *mask =
+                k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t see = view_bits(mask, k.a.mask_words, i_new, w.t.tokens,
+                                             t0 + 32 * b - w.t.ctx);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                if (!(see >> c & 1u)) z[32 * b + c] = 0xff800000u;
+              }
+            }
+            __syncwarp();
+          }
+          float mx[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) mx[b] = __uint_as_float(z[b]);
+#pragma unroll
+          for (int c = 4; c < 128; c += 4) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[c + b]));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k.sc;
+          const bool rise = top > m + kLazy || (first && top > m);
+          if (first) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, rise)) {
+            const float mn = rise ? top : m;
+            const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(t_o + c, o);
+            }
+            tmem_wait_st();
+          }
+          first = false;
+          const float sub = Wt::kOffset - (m == -INFINITY ? 0.f : m);
+          const unsigned long long sc2 = f2dup(k.sc), sub2 = f2dup(sub);
+          unsigned long long sum2 = f2dup(0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const unsigned long long y =
+                  fma2(f2pack(__uint_as_float(z[64 * h + 2 * c]),
+                              __uint_as_float(z[64 * h + 2 * c + 1])), sc2, sub2);
+              float a, b;
+              f2unpack(y, a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              sum2 = add2(sum2, f2pack(a, b));
+              p[c] = Wt::pack(a, b);
+            }
+            tmem_st32(t_s + 32 * h, p);
+          }
+          float sa, sb;
+          f2unpack(sum2, sa, sb);
+          l += sa + sb;
+          tmem_wait_st();
+        }
+        if (t0 + kTile > w.t.ctx && !(w.t.flags & kShared)) {
+          // the tile reaches past the committed tokens: V rows past the last
+          // token become 0 (they may hold anything), and so do infinities
+          // and NaN of new tokens, which add_nonfinite puts back
+          const uint32_t at = ring + pos_v(pair, w.n, i), slot = at % G::kSlots;
+          if (!(ok = warp_wait(s, &s->full[slot], at / G::kSlots & 1u, k.a.status))) break;
+          const int t = t0 + r;
+          if (t >= w.t.ctx) {
+            char *v = s_ring + slot * G::kTileBytes + r * 128;
+            bool found = false;
+#pragma unroll 4
+            for (int c = 0; c < 8 * kHalves; ++c) {
+              uint4 *at16 = reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) +
+                                                      (((c + lane) & 7) << 4));
+              uint4 x = make_uint4(0, 0, 0, 0);
+              bool change = t >= w.t.kv1;
+              if (!change) {
+                x = *at16;
+                uint32_t *words = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const uint32_t bad = __vcmpeq2(words[b] & Wt::kExpMask, Wt::kExpMask);
+                  if (bad) {
+                    words[b] &= ~bad;
+                    change = found = true;
+                  }
+                }
+              }
+              if (change) *at16 = x;
+            }
+            if (found) s->nonfinite = seg;
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->weights[g]);
+      }
+      if (!ok) break;
+      // ---- the unit's result -----------------------------------------------
+      s->stat[g][r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->stats);
+      ok = warp_wait(s, &s->o_full, (seg - 1) & 1u, k.a.status) &&
+           warp_wait(s, &s->stats, (seg - 1) & 1u, k.a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const bool bad = s->nonfinite == seg;
+      const bool two = !pair && w.n > 1;
+      float f0 = 1.f, f1 = 0.f;
+      if (!pair) {
+        const float2 s0 = s->stat[0][r], s1 = s->stat[1][r];
+        m = fmaxf(s0.x, s1.x);
+        f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
+        f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
+        l = s0.y * f0 + s1.y * f1;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      f0 *= inv;
+      f1 *= inv;
+      const float lse2 = l == 0.f ? -INFINITY : m - Wt::kOffset + log2f(l);
+      const bool whole = (w.t.flags & kSolo) && w.n == w.t.tiles;
+      const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
+      const int64_t cont = static_cast<int64_t>(blockIdx.x) * kUnitRows + row_in_unit;
+      const bool base = w.i0 == 0;
+      const int kind = w.t.flags & kShared;
+      if (live && (pair || g == 0)) {
+        if (whole) {
+          if (k.a.lse) k.a.lse[rh] = lse2 * 0.69314718055994531f;
+        } else if (base) {
+          k.w.lse[kind][rh] = lse2;
+        } else {
+          k.w.lse_c[cont] = lse2;
+        }
+      }
+      if (warp_live) {
+        const uint32_t t_a = tmem + lanes + 256 + (pair ? g * 128 : 0);
+        const int half_cols = 32 * kHalves;
+        const int c_begin = pair ? 0 : g * half_cols, c_end = pair ? 2 * half_cols : c_begin + half_cols;
+#pragma unroll 1
+        for (int c = c_begin; c < c_end; c += 32) {
+          if (c >= D) break;
+          uint32_t x[32], y[32];
+          tmem_ld32(t_a + c, x);
+          if (two) tmem_ld32(t_a + 128 + c, y);
+          tmem_wait_ld(x);
+          if (two) tmem_tie(y);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            o[e] = __uint_as_float(x[e]) * f0;
+            if (two) o[e] = fmaf(__uint_as_float(y[e]), f1, o[e]);
+          }
+          if (live && bad) {
+            const int t0 = w.t.kv0 + w.i0 * kTile;
+            add_nonfinite<T>(k, w.t, w.head, row, i_new, t0, t0 + w.n * kTile, c, o);
+          }
+          if (live && whole) {
+            T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              if (c + e < D) {
+                *reinterpret_cast<uint4 *>(dst + e) =
+                    make_uint4(Wt::pack(o[e], o[e + 1]), Wt::pack(o[e + 2], o[e + 3]),
+                               Wt::pack(o[e + 4], o[e + 5]), Wt::pack(o[e + 6], o[e + 7]));
+              }
+            }
+          } else if (live) {
+            float *dst = (base ? k.w.o[kind] + rh * D : k.w.o_c + cont * D) + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              if (c + e < D) {
+                *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+      ring += 2 * w.n;
+    }
+  } else if (warp == 8) {
+    // ---- matrix products ----------------------------------------------------
+    if (lane == 0) {
+      Walk w;
+      w.start(k.w);
+      const uint32_t id_qk = instr_desc(Wt::kBf16, kTile, false);
+      const uint32_t id_pv = instr_desc(Wt::kBf16, (D + 15) / 16 * 16, true);
+      const int k_steps = (D + 15) / 16;
+      uint32_t seg = 0, ring = 0, ph[2] = {0, 0};
+      bool ok = true;
+      const uint32_t q_addr = smem_addr(s_q), ring_addr = smem_addr(s_ring);
+      auto wait_full = [&](uint32_t at) {
+        return guarded_wait(s, &s->full[at % G::kSlots], at / G::kSlots & 1u, k.a.status);
+      };
+      auto release = [&](uint32_t at) { tc_commit(&s->empty[at % G::kSlots]); };
+      auto scores = [&](int g, int q_tile, uint32_t at) {
+        const uint32_t ka = ring_addr + (at % G::kSlots) * G::kTileBytes;
+        const uint32_t qa = q_addr + q_tile * G::kTileBytes;
+        for (int c = 0; c < k_steps; ++c) {
+          const uint32_t off = (c >> 2) * (kTile * 128) + (c & 3) * 32;
+          mma_ss(tmem + g * 128, smem_desc(qa + off, 16), smem_desc(ka + off, 16), id_qk, c > 0);
+        }
+        tc_commit(&s->scores[g]);
+      };
+      auto values = [&](int g, uint32_t at, bool more) {
+        const uint32_t va = ring_addr + (at % G::kSlots) * G::kTileBytes;
+        for (int c = 0; c < kTile / 16; ++c) {
+          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + c * 8,
+                 smem_desc(va + c * 2048, kTile * 128), id_pv, more || c > 0);
+        }
+      };
+      while (ok && w.next(k)) {
+        const bool pair = w.rows > kTile;
+        const int n = w.n;
+        if (!(ok = guarded_wait(s, &s->q_full, seg & 1u, k.a.status))) break;
+        ++seg;
+        tc_fence_after();
+        auto at_k = [&](int i) { return ring + pos_k(pair, n, i); };
+        auto at_v = [&](int i) { return ring + pos_v(pair, n, i); };
+        if (pair) {
+          if (!(ok = wait_full(at_k(0)))) break;
+          scores(0, 0, at_k(0));
+          scores(1, 1, at_k(0));
+          release(at_k(0));
+          for (int i = 0; ok && i < n; ++i) {
+            for (int g = 0; ok && g < 2; ++g) {
+              ok = guarded_wait(s, &s->weights[g], ph[g]++ & 1u, k.a.status) &&
+                   (g == 1 || wait_full(at_v(i)));
+              if (!ok) break;
+              tc_fence_after();
+              values(g, at_v(i), i > 0);
+              if (g == 1) release(at_v(i));
+              if (i + 1 < n) {
+                if (g == 0 && !(ok = wait_full(at_k(i + 1)))) break;
+                scores(g, g, at_k(i + 1));
+                if (g == 1) release(at_k(i + 1));
+              }
+            }
+          }
+        } else {
+          for (int i = 0; ok && i < n && i < 2; ++i) {
+            if (!(ok = wait_full(at_k(i)))) break;
+            scores(i, 0, at_k(i));
+            release(at_k(i));
+          }
+          for (int i = 0; ok && i < n; ++i) {
+            const int g = i & 1;
+            ok = guarded_wait(s, &s->weights[g], ph[g]++ & 1u, k.a.status) && wait_full(at_v(i));
+            if (!ok) break;
+            tc_fence_after();
+            values(g, at_v(i), i > 1);
+            release(at_v(i));
+            if (i + 2 < n) {
+              if (!(ok = wait_full(at_k(i + 2)))) break;
+              scores(g, 0, at_k(i + 2));
+              release(at_k(i + 2));
+            }
+          }
+        }
+        if (!ok) break;
+        tc_commit(&s->o_full);
+        ring += 2 * n;
+      }
+      tc_commit(&s->drained);  // nothing of this CTA runs on when it ends
+      if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(k.a.status, SMC_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ---- copies ---------------------------------------------------------------
+    Walk w;
+    w.start(k.w);
+    const CacheArgs &c = k.a.c;
+    const int bs = c.block_size;
+    uint32_t at = 0;
+    bool ok = true;
+    unsigned bits = 0;
+    auto block_of = [&](const int32_t *table, int t) {
+      int id = table[t / bs];
+      if (id < 0 || id >= c.blocks) {
+        bits |= SMC_DEV_BAD_BLOCK;
+        id = 0;
+      }
+      return id;
+    };
+    while (ok && w.next(k)) {
+      const bool pair = w.rows > kTile;
+      const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.t.seq) * k.a.b.T;
+      for (int j = 0; ok && j < 2 * w.n; ++j) {
+        // position j holds K of tile i or V of tile i
+        const bool is_k = pair ? !(j & 1) : j == 0 || ((j & 1) && j < 2 * w.n - 1);
+        const int i = pair ? j >> 1 : (is_k ? (j + 1) >> 1 : (j == 2 * w.n - 1 ? w.n - 1 : (j >> 1) - 1));
+        const int t0 = w.t.kv0 + (w.i0 + i) * kTile, t1 = min(t0 + kTile, w.t.kv1);
+        const uint32_t slot = at % G::kSlots;
+        char *dst = s_ring + slot * G::kTileBytes;
+        if constexpr (kTma) {
+          const int boxes = (t1 - t0 + k.box - 1) / k.box;
+          const int b = lane / kHalves, half = lane % kHalves;
+          const bool mine = b < boxes;
+          const int t = t0 + b * k.box;
+          const int block = mine ? block_of(table, t) : 0;
+          if (at >= static_cast<uint32_t>(G::kSlots) &&
+              !(ok = warp_wait(s, &s->empty[slot], (at / G::kSlots - 1) & 1u, k.a.status))) {
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], boxes * kHalves * k.box * 128);
+          __syncwarp();
+          if (mine) {
+            tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, is_k ? &map_k : &map_v,
+                        half * 64, t % bs, w.head, block, &s->full[slot]);
+          }
+        } else {
+          if (at >= static_cast<uint32_t>(G::kSlots) &&
+              !(ok = warp_wait(s, &s->empty[slot], (at / G::kSlots - 1) & 1u, k.a.status))) {
+            break;
+          }
+          const char *src = is_k ? c.k : c.v;
+          const uint32_t d0 = smem_addr(dst);
+          constexpr int kChunks = 8 * kHalves;
+          const int ch = lane % kChunks;
+          const bool take = ch * 8 < D;
+          for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
+            const int t = t0 + r;
+            const int64_t off = block_of(table, t) * c.block_stride + (t % bs) * c.token_stride +
+                                w.head * c.head_stride + (take ? ch * 8 : 0);
+            cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       src + off * 2, take);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (at > 0) {  // the position before this one has arrived
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->full[(at - 1) % G::kSlots]);
+          }
+        }
+        ++at;
+      }
+    }
+    if constexpr (kTma) {
+      // every copy has landed before the CTA ends
+      for (uint32_t a = at > static_cast<uint32_t>(G::kSlots) ? at - G::kSlots : 0; a < at; ++a) {
+        mbar_wait(&s->full[a % G::kSlots], a / G::kSlots & 1u, kWaitPolls);
+      }
+    } else {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (at > 0) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->full[(at - 1) % G::kSlots]);
+      }
+    }
+    if (bits) raise_status(k.a.status, bits);
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free_512(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// combine_kernel: a warp per (row, query head).  Each part p has a
+// log-sum-exp L_p (log2) and a normalised result o_p:
+//   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
+// Rows that one CTA finished alone were written by it.
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const KernelArgs k) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rh = static_cast<int64_t>(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rh >= static_cast<int64_t>(k.a.b.rows) * k.a.q_heads) return;
+  const int row = static_cast<int>(rh / k.a.q_heads), qh = static_cast<int>(rh % k.a.q_heads);
+  const int seq = seq_of_row(k.a.b, row);
+  if (seq < 0) return;
+  const int D = k.a.c.head_dim, per = __ldcg(&k.w.head->per);
+  const int head = qh / k.rep;
+  struct Part { int first, count, slot0; bool any; } part[2];
+  bool whole = false;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    part[p] = {0, 0, 0, false};
+    if (p == 1 && !k.w.groups) continue;
+    const int e = p == 0 ? k.w.groups + seq : seq / k.a.b.group;
+    const int4 *at = reinterpret_cast<const int4 *>(&k.w.entries[e]);
+    const int4 a = __ldcg(at), b = __ldcg(at + 1);
+    const Entry t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (p == 0 && (row < t.row0 || row >= t.row0 + t.tokens)) return;  // a sequence out of order
+    if (t.tiles <= 0 || t.tokens <= 0) continue;
+    const int r_all = (row - t.row0) * k.rep + qh - head * k.rep;
+    const int rts = (t.tokens * k.rep + kUnitRows - 1) / kUnitRows;
+    const int x0 = __ldcg(&k.w.tile0[e]) + (head * rts + r_all / kUnitRows) * t.tiles;
+    const int c0 = x0 / per, c1 = (x0 + t.tiles - 1) / per;
+    part[p] = {c0, c1 - c0, r_all % kUnitRows, true};
+    if (p == 0) whole = (t.flags & kSolo) && c0 == c1;
+  }
+  if (whole) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (!part[p].any) continue;
+    top = fmaxf(top, __ldcg(&k.w.lse[p][rh]));
+    for (int j = lane; j < part[p].count; j += 32) {
+      top = fmaxf(top, __ldcg(&k.w.lse_c[(part[p].first + 1 + j) * kUnitRows + part[p].slot0]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const bool live = 4 * lane < D;
+  auto add = [&](float lse, const float *o) {
+    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
+    sum += f;
+    if (live) {
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(o) + lane);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (!part[p].any) continue;
+    add(__ldcg(&k.w.lse[p][rh]), k.w.o[p] + rh * D);
+#pragma unroll 4
+    for (int j = 0; j < part[p].count; ++j) {
+      const int64_t slot = static_cast<int64_t>(part[p].first + 1 + j) * kUnitRows + part[p].slot0;
+      add(__ldcg(&k.w.lse_c[slot]), k.w.o_c + slot * D);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (live) {
+    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(Weights<T>::pack(acc.x * inv, acc.y * inv), Weights<T>::pack(acc.z * inv, acc.w * inv));
+  }
+  if (k.a.lse && lane == 0) {
+    k.a.lse[rh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launch.
+// ---------------------------------------------------------------------------
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+static EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// [blocks][kv_heads][block_size][head_dim] in boxes of 64 elements x `box`
+// tokens; columns past head_dim read as 0.
+static bool make_map(CUtensorMap *map, const CacheArgs &c, void *base, int box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.block_size),
+                              static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.blocks)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride) * 2,
+                                 static_cast<cuuint64_t>(c.head_stride) * 2,
+                                 static_cast<cuuint64_t>(c.block_stride) * 2};
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return fn(map, c.dtype == SMC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            4, base, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static cudaError_t launch_pdl(const void *fn, unsigned grid, unsigned block, size_t dyn, void **args,
+                              cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <typename T>
+static const void *attention_fn(bool wide, bool tma) {
+  if (wide) {
+    return tma ? reinterpret_cast<const void *>(attention_kernel<T, 2, true>)
+               : reinterpret_cast<const void *>(attention_kernel<T, 2, false>);
+  }
+  return tma ? reinterpret_cast<const void *>(attention_kernel<T, 1, true>)
+             : reinterpret_cast<const void *>(attention_kernel<T, 1, false>);
+}
+
+constexpr size_t kAttnSmem = Geometry<2>::kTail + sizeof(AttnTail);
+static_assert(Geometry<1>::kTail <= Geometry<2>::kTail && kAttnSmem <= 227 * 1024, "shared memory");
+static_assert(Geometry<1>::kSlots <= 10 && Geometry<2>::kSlots >= 4, "ring");
+
+static cudaError_t configure(int *sms) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int slot = dev < kMaxDev ? dev : kMaxDev - 1;
+  *sms = dev < kMaxDev ? known[slot].load(std::memory_order_acquire) : 0;
+  if (*sms) return cudaSuccess;
+  for (const bool wide : {false, true}) {
+    for (const bool tma : {false, true}) {
+      for (const void *fn : {attention_fn<__nv_bfloat16>(wide, tma), attention_fn<__half>(wide, tma)}) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kAttnSmem));
+        if (e != cudaSuccess) return e;
+      }
+    }
+  }
+  int n = 0;
+  e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  *sms = n < kMaxCtas ? n : kMaxCtas;
+  if (dev < kMaxDev) known[slot].store(*sms, std::memory_order_release);
+  return cudaSuccess;
+}
+
+cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream_t st) {
+  if (a.b.rows == 0) return cudaSuccess;
+  int sms = 0;
+  cudaError_t e = configure(&sms);
+  if (e != cudaSuccess) return e;
+  KernelArgs k{};
+  k.a = a;
+  carve(a.c, a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
+  k.rep = a.q_heads / a.c.kv_heads;
+  k.sc = a.scale * 1.4426950408889634f;
+  // a box is a run of tokens inside one block and one tile; the swizzle
+  // repeats every eight rows, so a box starts on a multiple of eight
+  int box = 128;
+  while (a.c.block_size % box) box >>= 1;
+  CUtensorMap map_k{}, map_v{};
+  const bool tma = box >= 8 && make_map(&map_k, a.c, a.c.k, box) && make_map(&map_v, a.c, a.c.v, box);
+  k.box = box;
+  // no more CTAs than tiles there can be
+  const int64_t most = (static_cast<int64_t>(a.b.T) * a.c.block_size + kTile - 1) / kTile *
+                       a.c.kv_heads * a.b.S *
+                       ((static_cast<int64_t>(a.b.max_new) * k.rep + kUnitRows - 1) / kUnitRows);
+  int ctas = most < sms ? static_cast<int>(most) : sms;
+  plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const bool bf16 = a.c.dtype == SMC_BF16, wide = a.c.head_dim > 64;
+  void *args[] = {&k, &map_k, &map_v};
+  e = launch_pdl(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
+                 ctas, kAttnThreads, kAttnSmem, args, st);
+  if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.b.rows) * a.q_heads;
-  if (units == 0) return cudaSuccess;
-  const unsigned grid = static_cast<unsigned>((units + kAttnThreads / 32 - 1) / (kAttnThreads / 32));
-  if (a.c.dtype == SMC_BF16) tree_attention_kernel<__nv_bfloat16><<<grid, kAttnThreads, 0, st>>>(a);
-  else tree_attention_kernel<__half><<<grid, kAttnThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  void *cargs[] = {&k};
+  return launch_pdl(bf16 ? reinterpret_cast<const void *>(combine_kernel<__nv_bfloat16>)
+                         : reinterpret_cast<const void *>(combine_kernel<__half>),
+                    static_cast<unsigned>((units + kCombineThreads / 32 - 1) / (kCombineThreads / 32)),
+                    kCombineThreads, 0, cargs, st);
 }
 
 }  // namespace smcsd

@@ -2,7 +2,7 @@
 // mask (smc_tree_attention in smcsd.h).
 //
 // Three kernels, chained by programmatic dependent launch:
-//   plan_kernel       lists the call's work in tiles of 128 tokens;
+//   plan_kernel       lists the call's work in tiles of 64 tokens;
 //   attention_kernel  persistent, one CTA per SM, on the 5th-generation tensor
 //                     cores; every CTA takes an equal run of the tiles;
 //   combine_kernel    joins rows that several CTAs, or a shared and an own
@@ -20,13 +20,14 @@ namespace smcsd {
 // they all attend: the own part of one sequence, or the part that the
 // sequences of a prompt share (their leading equal table slots).  Per key
 // head and per 256 rows (new token x query head of the key head) an entry
-// makes one *unit* of ceil(tokens / 128) tiles.  The units' tiles form one
+// makes one *unit* of ceil(tokens / 64) tiles.  The units' tiles form one
 // line; CTA c takes tiles [c * per, (c + 1) * per) of it, so ragged lengths
 // load every SM alike.  A unit's first tiles' CTA owns the unit's result;
 // every later CTA of the unit has exactly one such continuation (its first
 // segment) and stores it in its own slot.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128;        // tokens per tile
+constexpr int kTile = 64;         // tokens per tile
+constexpr int kRows = 128;        // rows of a tensor-core tile
 constexpr int kUnitRows = 256;    // rows per unit: two tensor-core tiles of 128
 constexpr int kMaxCtas = 192;     // slots for continuations
 constexpr int kPlanThreads = 1024;
@@ -97,7 +98,8 @@ struct KernelArgs {
   AttnArgs a;
   AttnWorkspace w;
   int rep;      // query heads per key head
-  int box;      // tokens per copied box (0: element copies)
+  int box;      // tokens per copied box
+  uint32_t magic, shift;  // t / block_size == umulhi(t, magic) >> shift
   float sc;     // scale * log2 e
 };
 
@@ -157,7 +159,7 @@ __device__ int make_entry(const KernelArgs &k, int e, Entry *out) {
   return tiles;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KernelArgs k, int ctas) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ KernelArgs k, int ctas) {
   __shared__ int warps[kPlanThreads / 32];
   __shared__ int s_slots, s_limit, s_seqs, s_bad, s_ref;
   __shared__ bool s_last;
@@ -258,23 +260,42 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
           smem_addr(bar))
       : "memory");
 }
+// Shared-memory operand in 128-byte-swizzled rows of 64 elements: `lbo` bytes
+// between 64-element panels (of the contiguous axis, MN-major operands only),
+// 1024 bytes between groups of eight rows.  Only the low word of a descriptor
+// varies.  The products take it as 32 bits and are issued by an elected
+// thread: with 64-bit descriptors in an unrolled `lane == 0` branch the
+// compiled code used wrong addresses for all but the first step.
+constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;  // version, swizzle
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lbo) {  // low word
+  return (addr & 0x3ffffu) >> 4 | (lbo >> 4) << 16;
+}
 // D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
 }
 #define SMC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
                      "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
@@ -311,13 +332,6 @@ __device__ __forceinline__ void tmem_tie(uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// Shared-memory operand in 128-byte-swizzled rows of 64 elements: `lbo` bytes
-// between 64-element panels (of the contiguous axis, MN-major operands only),
-// 1024 bytes between groups of eight rows.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
-         static_cast<uint64_t>(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 // kind::f16 with 128 rows, n columns, fp32 accumulators; b_mn: B is stored
 // with its n axis contiguous.
@@ -374,14 +388,15 @@ constexpr float kLazy = 8.f;
 // attention_kernel.  Warps 0-3 and 4-7: two softmax groups (thread = row of a
 // 128-row tile); warp 8: the thread that issues the matrix products; warp 9:
 // the copies.  Shared memory: Q (two row tiles) and a ring of K and V tiles.
-// Tensor memory: scores of either group (their weights overwrite them), and
-// either group's accumulator.
+// Tensor memory: two score buffers of 64 columns per group (the weights
+// overwrite the scores) and either group's accumulator.
 //   Units of up to 128 rows: the groups take alternate tiles of the unit, each
 //   with its own running maximum, sum and accumulator, joined at the end.
 //   Larger units: each group has its own 128 rows; a tile of K and V serves
 //   both.
-// Group g's next scores are issued right behind its last product with V, so
-// one group's softmax runs beside the other's products.
+// Scores run two of a group's tiles ahead of its softmax (kLead tiles of the
+// unit), so that neither a group nor the ring waits for a product's latency:
+// K tiles leave the ring as they come, and only V waits for its weights.
 // ---------------------------------------------------------------------------
 constexpr int kAttnThreads = 320;
 constexpr int kRingBytes = 160 * 1024;
@@ -390,13 +405,14 @@ template <int kHalves>  // 64-element panels of the head dim
 struct Geometry {
   static constexpr int kTileBytes = kHalves * kTile * 128;
   static constexpr int kSlots = kRingBytes / kTileBytes;
-  static constexpr int kQBytes = 2 * kTileBytes;
+  static constexpr int kQTile = kHalves * kRows * 128;
+  static constexpr int kQBytes = 2 * kQTile;
   static constexpr int kTail = kQBytes + kRingBytes;
 };
 
 struct AttnTail {
-  uint64_t full[10], empty[10], q_full, scores[2], weights[2], o_full, stats, drained;
-  float2 stat[2][kTile];  // either group's (max, sum) of a row
+  uint64_t full[20], empty[20], q_full, scores[2][2], weights[2][2], added[2], o_full, stats, drained;
+  float2 stat[2][kRows];  // either group's (max, sum) of a row
   uint32_t tmem;
   unsigned nonfinite;     // segment number (from 1) of the last one with a non-finite value
   volatile int abort;
@@ -449,12 +465,12 @@ struct Walk {
   }
 };
 
-// Ring positions of a segment's n tiles, in the order of their use.
-__device__ __forceinline__ int pos_k(bool pair, int n, int i) {
-  return pair ? 2 * i : (i == 0 ? 0 : 2 * i - 1);
-}
-__device__ __forceinline__ int pos_v(bool pair, int n, int i) {
-  return pair ? 2 * i + 1 : (i + 1 < n ? 2 * i + 2 : 2 * n - 1);
+// Ring positions of a segment's n tiles, in the order of their use: K of the
+// first `lead` tiles, then V of tile i and K of tile i + lead in turn.
+__device__ __forceinline__ int lead_of(bool pair) { return pair ? 2 : 4; }
+__device__ __forceinline__ int pos_k(int lead, int i) { return i < lead ? i : 2 * i + 1 - lead; }
+__device__ __forceinline__ int pos_v(int lead, int n, int i) {
+  return i + lead < n ? lead + 2 * i : n + i;
 }
 
 // False when the wait gave up (it raised the status bit and the abort flag, at
@@ -470,10 +486,28 @@ __device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_
   return false;
 }
 
-// The same for a whole warp: one answer for all its lanes.
+// The same for a whole warp, in step: every lane polls and takes the same
+// branch, so that the warp is converged for the .aligned instructions that
+// follow.
 __device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t parity,
                                           unsigned *status) {
-  return __all_sync(0xffffffffu, guarded_wait(s, bar, parity, status));
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, s->abort)) return false;
+  }
+  s->abort = 1;
+  raise_status(status, SMC_DEV_TIMEOUT);
+  return false;
+}
+// One arrival for a warp (lane 0's), by predicate and not by a branch, for
+// the same reason.  What the other lanes did before is ordered by __syncwarp.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lane)
+      : "memory");
 }
 
 // Bits of a row's view of new tokens j0 .. j0 + 31: 1 for committed tokens
@@ -501,12 +535,13 @@ __device__ __forceinline__ uint32_t view_bits(const uint32_t *mask, int words, i
 // rows that do not see the token must not meet it; rows that see it get it
 // here: columns [col, col + 32) of v, of the new tokens in [t0, t1).
 template <typename T>
-__device__ __noinline__ void add_nonfinite(const KernelArgs &k, const Entry &t, int head, int row,
-                                           int i, int t0, int t1, int col, float *o) {
+__device__ __noinline__ void add_nonfinite(const KernelArgs &k, int seq, int ctx, int n_new,
+                                           int head, int row, int i, int t0, int t1, int col,
+                                           float *o) {
   const uint32_t *mask = k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
-  const int32_t *table = k.a.b.tables + static_cast<int64_t>(t.seq) * k.a.b.T;
-  for (int at = max(t0, t.ctx); at < min(t1, t.kv1); ++at) {
-    if (!(view_bits(mask, k.a.mask_words, i, t.tokens, at - t.ctx) & 1u)) continue;
+  const int32_t *table = k.a.b.tables + static_cast<int64_t>(seq) * k.a.b.T;
+  for (int at = max(t0, ctx); at < t1; ++at) {
+    if (!(view_bits(mask, k.a.mask_words, i, n_new, at - ctx) & 1u)) continue;
     const int block = table[at / k.a.c.block_size];
     if (block < 0 || block >= k.a.c.blocks) continue;
     const T *v = reinterpret_cast<const T *>(k.a.c.v) + block * k.a.c.block_stride +
@@ -521,7 +556,7 @@ __device__ __noinline__ void add_nonfinite(const KernelArgs &k, const Entry &t, 
 
 template <typename T, int kHalves, bool kTma>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
+attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
   using G = Geometry<kHalves>;
   using Wt = Weights<T>;
@@ -539,8 +574,11 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
     }
     mbar_init(&s->q_full, 8);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&s->scores[g], 1);
-      mbar_init(&s->weights[g], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s->scores[g][b], 1);
+        mbar_init(&s->weights[g][b], 4);
+      }
+      mbar_init(&s->added[g], 1);
     }
     mbar_init(&s->o_full, 1);
     mbar_init(&s->stats, 8);
@@ -564,59 +602,59 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
     const int g = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;  // row of the group's tile
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t t_s = tmem + lanes + g * 128, t_o = tmem + lanes + 256 + g * 128;
+    const uint32_t t_o = tmem + lanes + 256 + g * 128;
     Walk w;
     w.start(k.w);
-    uint32_t seg = 0, ring = 0, phase = 0;
+    uint32_t seg = 0, ring = 0, turn = 0;  // turn: tiles of this group so far
     bool ok = true;
     while (ok && w.next(k)) {
       ++seg;
-      const bool pair = w.rows > kTile;
-      const int row_in_unit = pair ? g * kTile + r : r;
+      const bool pair = w.rows > kRows;
+      const int row_in_unit = pair ? g * kRows + r : r;
       const bool live = row_in_unit < w.rows;
-      const bool warp_live = (pair ? g * kTile : 0) + wq * 32 < w.rows;
+      const bool warp_live = (pair ? g * kRows : 0) + wq * 32 < w.rows;
       const int r_all = w.rt * kUnitRows + row_in_unit;
       const int i_new = live ? r_all / k.rep : 0;  // new token of a sequence's own part
       const int row = w.t.row0 + i_new;
       const int qh = w.head * k.rep + (live ? r_all - i_new * k.rep : 0);
       {  // Q: a row of either tile per thread; with one tile the groups split its columns
         const T *q = reinterpret_cast<const T *>(k.a.q) + row * k.a.q_row + qh * k.a.q_head;
-        char *dst = s_q + (pair ? g * G::kTileBytes : 0) + r * 128;
+        char *dst = s_q + (pair ? g * G::kQTile : 0) + r * 128;
         const int c0 = pair ? 0 : g * 4 * kHalves, c1 = pair ? 8 * kHalves : c0 + 4 * kHalves;
         if (warp_live) {
           for (int c = c0; c < c1; ++c) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (live && c * 8 < D) x = *reinterpret_cast<const uint4 *>(q + c * 8);
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kTile * 128) +
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kRows * 128) +
                                        (((c & 7) ^ (r & 7)) << 4)) = x;
           }
         }
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s->q_full);
+        warp_arrive(&s->q_full, lane);
       }
+      const int lead = lead_of(pair);
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
         const int t0 = w.t.kv0 + (w.i0 + i) * kTile;
-        if (!(ok = warp_wait(s, &s->scores[g], phase & 1u, k.a.status))) break;
-        ++phase;
+        const uint32_t buf = turn & 1u;
+        const uint32_t t_s = tmem + lanes + g * 128 + buf * 64;
+        if (!(ok = warp_wait(s, &s->scores[g][buf], turn >> 1 & 1u, k.a.status))) break;
+        ++turn;
         tc_fence_after();
+        const bool edge = t0 + kTile > w.t.ctx && !(w.t.flags & kShared);
         if (warp_live) {
-          uint32_t z[128];
+          uint32_t z[64];
+          __syncwarp();
           tmem_ld32(t_s, z);
           tmem_ld32(t_s + 32, z + 32);
-          tmem_ld32(t_s + 64, z + 64);
-          tmem_ld32(t_s + 96, z + 96);
           tmem_wait_ld(z);
           tmem_tie(z + 32);
-          tmem_tie(z + 64);
-          tmem_tie(z + 96);
-          if (t0 + kTile > w.t.ctx && !(w.t.flags & kShared)) {
+          if (edge) {
             const uint32_t *mask =
                 k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
               const uint32_t see = view_bits(mask, k.a.mask_words, i_new, w.t.tokens,
                                              t0 + 32 * b - w.t.ctx);
 #pragma unroll
@@ -630,7 +668,7 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
           for (int b = 0; b < 4; ++b) mx[b] = __uint_as_float(z[b]);
 #pragma unroll
-          for (int c = 4; c < 128; c += 4) {
+          for (int c = 4; c < 64; c += 4) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[c + b]));
           }
@@ -639,6 +677,9 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           if (first) {
             m = top;
           } else if (__any_sync(0xffffffffu, rise)) {
+            // the group's last product has been added (turn counts this tile)
+            if (!(ok = warp_wait(s, &s->added[g], (turn - 2) & 1u, k.a.status))) break;
+            tc_fence_after();
             const float mn = rise ? top : m;
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
             l *= f;
@@ -658,40 +699,38 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           const float sub = Wt::kOffset - (m == -INFINITY ? 0.f : m);
           const unsigned long long sc2 = f2dup(k.sc), sub2 = f2dup(sub);
           unsigned long long sum2 = f2dup(0.f);
+          uint32_t p[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const unsigned long long y =
-                  fma2(f2pack(__uint_as_float(z[64 * h + 2 * c]),
-                              __uint_as_float(z[64 * h + 2 * c + 1])), sc2, sub2);
-              float a, b;
-              f2unpack(y, a, b);
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-              sum2 = add2(sum2, f2pack(a, b));
-              p[c] = Wt::pack(a, b);
-            }
-            tmem_st32(t_s + 32 * h, p);
+          for (int c = 0; c < 32; ++c) {
+            const unsigned long long y = fma2(
+                f2pack(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1])), sc2, sub2);
+            float a, b;
+            f2unpack(y, a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum2 = add2(sum2, f2pack(a, b));
+            p[c] = Wt::pack(a, b);
           }
+          __syncwarp();
+          tmem_st32(t_s, p);
           float sa, sb;
           f2unpack(sum2, sa, sb);
           l += sa + sb;
           tmem_wait_st();
         }
-        if (t0 + kTile > w.t.ctx && !(w.t.flags & kShared)) {
+        if (edge) {
           // the tile reaches past the committed tokens: V rows past the last
           // token become 0 (they may hold anything), and so do infinities
           // and NaN of new tokens, which add_nonfinite puts back
-          const uint32_t at = ring + pos_v(pair, w.n, i), slot = at % G::kSlots;
+          const uint32_t at = ring + pos_v(lead, w.n, i), slot = at % G::kSlots;
           if (!(ok = warp_wait(s, &s->full[slot], at / G::kSlots & 1u, k.a.status))) break;
-          const int t = t0 + r;
+          const int t = t0 + (r & (kTile - 1));
           if (t >= w.t.ctx) {
-            char *v = s_ring + slot * G::kTileBytes + r * 128;
+            char *v = s_ring + slot * G::kTileBytes + (r & (kTile - 1)) * 128;
             bool found = false;
+            const int c0 = (r / kTile) * 4 * kHalves;
 #pragma unroll 4
-            for (int c = 0; c < 8 * kHalves; ++c) {
+            for (int c = c0; c < c0 + 4 * kHalves; ++c) {
               uint4 *at16 = reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) +
                                                       (((c + lane) & 7) << 4));
               uint4 x = make_uint4(0, 0, 0, 0);
@@ -715,14 +754,12 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s->weights[g]);
+        warp_arrive(&s->weights[g][buf], lane);
       }
       if (!ok) break;
       // ---- the unit's result -----------------------------------------------
       s->stat[g][r] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s->stats);
+      warp_arrive(&s->stats, lane);
       ok = warp_wait(s, &s->o_full, (seg - 1) & 1u, k.a.status) &&
            warp_wait(s, &s->stats, (seg - 1) & 1u, k.a.status);
       if (!ok) break;
@@ -755,6 +792,7 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           k.w.lse_c[cont] = lse2;
         }
       }
+      __syncwarp();
       if (warp_live) {
         const uint32_t t_a = tmem + lanes + 256 + (pair ? g * 128 : 0);
         const int half_cols = 32 * kHalves;
@@ -775,7 +813,8 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           }
           if (live && bad) {
             const int t0 = w.t.kv0 + w.i0 * kTile;
-            add_nonfinite<T>(k, w.t, w.head, row, i_new, t0, t0 + w.n * kTile, c, o);
+            add_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0,
+                             min(t0 + w.n * kTile, w.t.kv1), c, o);
           }
           if (live && whole) {
             T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + c;
@@ -804,86 +843,94 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
     }
   } else if (warp == 8) {
     // ---- matrix products ----------------------------------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       Walk w;
       w.start(k.w);
       const uint32_t id_qk = instr_desc(Wt::kBf16, kTile, false);
       const uint32_t id_pv = instr_desc(Wt::kBf16, (D + 15) / 16 * 16, true);
       const int k_steps = (D + 15) / 16;
-      uint32_t seg = 0, ring = 0, ph[2] = {0, 0};
+      // descriptors of the first bytes; a step's offset is added to the address field
+      const uint32_t q0 = smem_desc(smem_addr(s_q), 16), k0 = smem_desc(smem_addr(s_ring), 16);
+      const uint32_t v0 = smem_desc(smem_addr(s_ring), kTile * 128);
+      uint32_t seg = 0;
+      uint32_t slot = 0, lap = 0;  // the ring position to be used next: positions are used in order
+      uint32_t asked[2] = {0, 0}, given[2] = {0, 0};  // tiles of either group: scores, values
       bool ok = true;
-      const uint32_t q_addr = smem_addr(s_q), ring_addr = smem_addr(s_ring);
-      auto wait_full = [&](uint32_t at) {
-        return guarded_wait(s, &s->full[at % G::kSlots], at / G::kSlots & 1u, k.a.status);
+      auto wait_full = [&](uint32_t at, uint32_t parity) {
+        return guarded_wait(s, &s->full[at], parity, k.a.status);
       };
-      auto release = [&](uint32_t at) { tc_commit(&s->empty[at % G::kSlots]); };
-      auto scores = [&](int g, int q_tile, uint32_t at) {
-        const uint32_t ka = ring_addr + (at % G::kSlots) * G::kTileBytes;
-        const uint32_t qa = q_addr + q_tile * G::kTileBytes;
-        for (int c = 0; c < k_steps; ++c) {
-          const uint32_t off = (c >> 2) * (kTile * 128) + (c & 3) * 32;
-          mma_ss(tmem + g * 128, smem_desc(qa + off, 16), smem_desc(ka + off, 16), id_qk, c > 0);
+      auto advance = [&] {
+        if (++slot == G::kSlots) {
+          slot = 0;
+          lap ^= 1;
         }
-        tc_commit(&s->scores[g]);
+      };
+      auto scores = [&](int g, int q_tile, uint32_t at) {
+        const uint32_t buf = asked[g]++ & 1u;
+        const uint32_t ka = k0 + at * (G::kTileBytes >> 4), qa = q0 + q_tile * (G::kQTile >> 4);
+        const uint32_t d = tmem + g * 128 + buf * 64;
+#pragma unroll
+        for (int c = 0; c < 4 * kHalves; ++c) {
+          if (c < k_steps) {
+            mma_ss(d, qa + ((c >> 2) * (kRows * 128) + (c & 3) * 32) / 16,
+                   ka + ((c >> 2) * (kTile * 128) + (c & 3) * 32) / 16, id_qk, c > 0);
+          }
+        }
+        tc_commit(&s->scores[g][buf]);
+      };
+      auto wait_weights = [&](int g) {
+        return guarded_wait(s, &s->weights[g][given[g] & 1u], given[g] >> 1 & 1u, k.a.status);
       };
       auto values = [&](int g, uint32_t at, bool more) {
-        const uint32_t va = ring_addr + (at % G::kSlots) * G::kTileBytes;
+        const uint32_t buf = given[g]++ & 1u;
+        const uint32_t va = v0 + at * (G::kTileBytes >> 4);
+        const uint32_t p = tmem + g * 128 + buf * 64;
+#pragma unroll
         for (int c = 0; c < kTile / 16; ++c) {
-          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + c * 8,
-                 smem_desc(va + c * 2048, kTile * 128), id_pv, more || c > 0);
+          mma_ts(tmem + 256 + g * 128, p + c * 8, va + c * 2048 / 16, id_pv, more || c > 0);
         }
+        tc_commit(&s->added[g]);
       };
       while (ok && w.next(k)) {
-        const bool pair = w.rows > kTile;
-        const int n = w.n;
+        const bool pair = w.rows > kRows;
+        const int n = w.n, lead = lead_of(pair);
         if (!(ok = guarded_wait(s, &s->q_full, seg & 1u, k.a.status))) break;
         ++seg;
         tc_fence_after();
-        auto at_k = [&](int i) { return ring + pos_k(pair, n, i); };
-        auto at_v = [&](int i) { return ring + pos_v(pair, n, i); };
-        if (pair) {
-          if (!(ok = wait_full(at_k(0)))) break;
-          scores(0, 0, at_k(0));
-          scores(1, 1, at_k(0));
-          release(at_k(0));
-          for (int i = 0; ok && i < n; ++i) {
-            for (int g = 0; ok && g < 2; ++g) {
-              ok = guarded_wait(s, &s->weights[g], ph[g]++ & 1u, k.a.status) &&
-                   (g == 1 || wait_full(at_v(i)));
-              if (!ok) break;
-              tc_fence_after();
-              values(g, at_v(i), i > 0);
-              if (g == 1) release(at_v(i));
-              if (i + 1 < n) {
-                if (g == 0 && !(ok = wait_full(at_k(i + 1)))) break;
-                scores(g, g, at_k(i + 1));
-                if (g == 1) release(at_k(i + 1));
-              }
-            }
+        for (int j = 0; ok && j < n && j < lead; ++j) {
+          if (!(ok = wait_full(slot, lap))) break;
+          if (pair) {
+            scores(0, 0, slot);
+            scores(1, 1, slot);
+          } else {
+            scores(j & 1, 0, slot);
           }
-        } else {
-          for (int i = 0; ok && i < n && i < 2; ++i) {
-            if (!(ok = wait_full(at_k(i)))) break;
-            scores(i, 0, at_k(i));
-            release(at_k(i));
-          }
-          for (int i = 0; ok && i < n; ++i) {
-            const int g = i & 1;
-            ok = guarded_wait(s, &s->weights[g], ph[g]++ & 1u, k.a.status) && wait_full(at_v(i));
-            if (!ok) break;
+          tc_commit(&s->empty[slot]);
+          advance();
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          // V of tile i, then (unless the tiles run out) K of tile i + lead
+          const bool ask = i + lead < n;
+          const uint32_t at = slot, at_lap = lap;
+          advance();
+          const uint32_t next = slot, next_lap = lap;
+          if (ask) advance();
+          for (int g = pair ? 0 : i & 1, end = pair ? 2 : g + 1; ok && g < end; ++g) {
+            const bool fresh = !pair || g == 0;  // the first use of either tile
+            const bool last = !pair || g == 1;
+            if (!(ok = (!fresh || wait_full(at, at_lap)) && wait_weights(g))) break;
             tc_fence_after();
-            values(g, at_v(i), i > 1);
-            release(at_v(i));
-            if (i + 2 < n) {
-              if (!(ok = wait_full(at_k(i + 2)))) break;
-              scores(g, 0, at_k(i + 2));
-              release(at_k(i + 2));
+            values(g, at, i >= (pair ? 1 : 2));
+            if (last) tc_commit(&s->empty[at]);
+            if (ask) {
+              if (fresh && !(ok = wait_full(next, next_lap))) break;
+              scores(g, pair ? g : 0, next);
+              if (last) tc_commit(&s->empty[next]);
             }
           }
         }
         if (!ok) break;
         tc_commit(&s->o_full);
-        ring += 2 * n;
       }
       tc_commit(&s->drained);  // nothing of this CTA runs on when it ends
       if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(k.a.status, SMC_DEV_TIMEOUT);
@@ -894,47 +941,67 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
     Walk w;
     w.start(k.w);
     const CacheArgs &c = k.a.c;
-    const int bs = c.block_size;
-    uint32_t at = 0;
+    const uint32_t bs = c.block_size;
+    uint32_t at = 0, slot = 0, lap = 1;  // lap: parity of the slot's release before its last use
     bool ok = true;
     unsigned bits = 0;
-    auto block_of = [&](const int32_t *table, int t) {
-      int id = table[t / bs];
+    // (block, first token) of a box or token t of the sequence
+    auto place = [&](const int32_t *table, uint32_t t) {
+      const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
+      int id = table[b];
       if (id < 0 || id >= c.blocks) {
         bits |= SMC_DEV_BAD_BLOCK;
         id = 0;
       }
-      return id;
+      return make_int2(id, t - b * bs);
     };
     while (ok && w.next(k)) {
-      const bool pair = w.rows > kTile;
+      const int lead = lead_of(w.rows > kRows);
       const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.t.seq) * k.a.b.T;
+      const int tok0 = w.t.kv0 + w.i0 * kTile, tok1 = min(tok0 + w.n * kTile, w.t.kv1);
+      // the places of 32 boxes, one per lane, for K and (behind it) for V
+      const int per_tile = kTma ? kTile / k.box : 0;
+      int2 ahead_k = make_int2(0, 0), ahead_v = make_int2(0, 0);
+      int from_k = -64, from_v = -64;
       for (int j = 0; ok && j < 2 * w.n; ++j) {
         // position j holds K of tile i or V of tile i
-        const bool is_k = pair ? !(j & 1) : j == 0 || ((j & 1) && j < 2 * w.n - 1);
-        const int i = pair ? j >> 1 : (is_k ? (j + 1) >> 1 : (j == 2 * w.n - 1 ? w.n - 1 : (j >> 1) - 1));
-        const int t0 = w.t.kv0 + (w.i0 + i) * kTile, t1 = min(t0 + kTile, w.t.kv1);
-        const uint32_t slot = at % G::kSlots;
+        const int past = j - lead, paired = 2 * (w.n - lead);
+        const bool is_k = j < min(lead, w.n) || (past < paired && (past & 1));
+        const int i = j < min(lead, w.n) ? j
+                      : past < paired    ? (past >> 1) + (is_k ? lead : 0)
+                                         : j - w.n;
+        const int t0 = tok0 + i * kTile, t1 = min(t0 + kTile, tok1);
         char *dst = s_ring + slot * G::kTileBytes;
         if constexpr (kTma) {
           const int boxes = (t1 - t0 + k.box - 1) / k.box;
           const int b = lane / kHalves, half = lane % kHalves;
-          const bool mine = b < boxes;
-          const int t = t0 + b * k.box;
-          const int block = mine ? block_of(table, t) : 0;
+          int block, token;
+          auto locate = [&](int2 &cached, int &from) {
+            const int first = i * per_tile;
+            if (first < from || first + per_tile > from + 32) {
+              from = first;
+              const int t = tok0 + (first + lane) * k.box;
+              if (t < tok1) cached = place(table, t);
+            }
+            const int src = (first - from + b) & 31;
+            block = __shfl_sync(0xffffffffu, cached.x, src);
+            token = __shfl_sync(0xffffffffu, cached.y, src);
+          };
+          if (is_k) locate(ahead_k, from_k);
+          else locate(ahead_v, from_v);
           if (at >= static_cast<uint32_t>(G::kSlots) &&
-              !(ok = warp_wait(s, &s->empty[slot], (at / G::kSlots - 1) & 1u, k.a.status))) {
+              !(ok = warp_wait(s, &s->empty[slot], lap, k.a.status))) {
             break;
           }
           if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], boxes * kHalves * k.box * 128);
           __syncwarp();
-          if (mine) {
+          if (b < boxes) {
             tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, is_k ? &map_k : &map_v,
-                        half * 64, t % bs, w.head, block, &s->full[slot]);
+                        half * 64, token, w.head, block, &s->full[slot]);
           }
         } else {
           if (at >= static_cast<uint32_t>(G::kSlots) &&
-              !(ok = warp_wait(s, &s->empty[slot], (at / G::kSlots - 1) & 1u, k.a.status))) {
+              !(ok = warp_wait(s, &s->empty[slot], lap, k.a.status))) {
             break;
           }
           const char *src = is_k ? c.k : c.v;
@@ -943,8 +1010,8 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           const int ch = lane % kChunks;
           const bool take = ch * 8 < D;
           for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
-            const int t = t0 + r;
-            const int64_t off = block_of(table, t) * c.block_stride + (t % bs) * c.token_stride +
+            const int2 at_block = place(table, t0 + r);
+            const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
                                 w.head * c.head_stride + (take ? ch * 8 : 0);
             cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
                        src + off * 2, take);
@@ -958,6 +1025,10 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
           }
         }
         ++at;
+        if (++slot == G::kSlots) {
+          slot = 0;
+          lap ^= 1;
+        }
       }
     }
     if constexpr (kTma) {
@@ -991,7 +1062,7 @@ attention_kernel(const KernelArgs k, const __grid_constant__ CUtensorMap map_k,
 constexpr int kCombineThreads = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const KernelArgs k) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ KernelArgs k) {
   const int lane = threadIdx.x & 31;
   const int64_t rh = static_cast<int64_t>(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1131,7 +1202,7 @@ static const void *attention_fn(bool wide, bool tma) {
 
 constexpr size_t kAttnSmem = Geometry<2>::kTail + sizeof(AttnTail);
 static_assert(Geometry<1>::kTail <= Geometry<2>::kTail && kAttnSmem <= 227 * 1024, "shared memory");
-static_assert(Geometry<1>::kSlots <= 10 && Geometry<2>::kSlots >= 4, "ring");
+static_assert(Geometry<1>::kSlots <= 20 && Geometry<2>::kSlots >= 8, "ring");
 
 static cudaError_t configure(int *sms) {
   constexpr int kMaxDev = 64;
@@ -1169,9 +1240,16 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   carve(a.c, a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
   k.rep = a.q_heads / a.c.kv_heads;
   k.sc = a.scale * 1.4426950408889634f;
+  // with 2^s the power of two at or above the block size, 2^(31 + s) / size
+  // rounded up divides every t < 2^31 exactly
+  const uint64_t bs = a.c.block_size;
+  uint32_t log2 = 0;
+  while ((1ull << log2) < bs) ++log2;
+  k.magic = static_cast<uint32_t>(((1ull << (31 + log2)) + bs - 1) / bs);
+  k.shift = log2 ? log2 - 1 : 0;
   // a box is a run of tokens inside one block and one tile; the swizzle
   // repeats every eight rows, so a box starts on a multiple of eight
-  int box = 128;
+  int box = kTile;
   while (a.c.block_size % box) box >>= 1;
   CUtensorMap map_k{}, map_v{};
   const bool tma = box >= 8 && make_map(&map_k, a.c, a.c.k, box) && make_map(&map_v, a.c, a.c.v, box);

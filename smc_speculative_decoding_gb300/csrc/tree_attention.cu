@@ -386,32 +386,37 @@ constexpr float kLazy = 8.f;
 
 // ---------------------------------------------------------------------------
 // attention_kernel.  Warps 0-3 and 4-7: two softmax groups (thread = row of a
-// 128-row tile); warp 8: the thread that issues the matrix products; warp 9:
-// the copies.  Shared memory: Q (two row tiles) and a ring of K and V tiles.
+// 128-row tile); warps 8 and 9: the threads that issue either group's matrix
+// products; warps 10 and 11: the copies of K and of V.  Shared memory: Q (two row tiles) and a ring of K and V tiles.
 // Tensor memory: two score buffers of 64 columns per group (the weights
 // overwrite the scores) and either group's accumulator.
 //   Units of up to 128 rows: the groups take alternate tiles of the unit, each
 //   with its own running maximum, sum and accumulator, joined at the end.
 //   Larger units: each group has its own 128 rows; a tile of K and V serves
 //   both.
-// Scores run two of a group's tiles ahead of its softmax (kLead tiles of the
-// unit), so that neither a group nor the ring waits for a product's latency:
-// K tiles leave the ring as they come, and only V waits for its weights.
+// Scores run two of a group's tiles ahead of its products with V, so that
+// neither a group nor its ring waits for a product's latency: K tiles leave
+// their ring as they come, and only V waits for its weights.  K and V have a
+// ring each, so that each slot's barriers are followed by one copying warp.
 // ---------------------------------------------------------------------------
-constexpr int kAttnThreads = 320;
+constexpr int kAttnThreads = 384;
 constexpr int kRingBytes = 160 * 1024;
 
 template <int kHalves>  // 64-element panels of the head dim
 struct Geometry {
   static constexpr int kTileBytes = kHalves * kTile * 128;
-  static constexpr int kSlots = kRingBytes / kTileBytes;
+  // Slots of K and of V: V waits for its weights, K does not.  Both even: with
+  // alternate tiles a slot is then always the same group's, whose waits see
+  // every turn of its barriers (a wait two turns behind would pass at once).
+  static constexpr int kSlotsK = 4 * (2 / kHalves), kSlotsV = 6 * (2 / kHalves);
   static constexpr int kQTile = kHalves * kRows * 128;
   static constexpr int kQBytes = 2 * kQTile;
   static constexpr int kTail = kQBytes + kRingBytes;
 };
 
 struct AttnTail {
-  uint64_t full[20], empty[20], q_full, scores[2][2], weights[2][2], added[2], o_full, stats, drained;
+  uint64_t full[2][12], empty[2][12];  // K, V
+  uint64_t q_full, scores[2][2], weights[2][2], added[2], o_full[2], stats, drained[2];
   float2 stat[2][kRows];  // either group's (max, sum) of a row
   uint32_t tmem;
   unsigned nonfinite;     // segment number (from 1) of the last one with a non-finite value
@@ -465,13 +470,18 @@ struct Walk {
   }
 };
 
-// Ring positions of a segment's n tiles, in the order of their use: K of the
-// first `lead` tiles, then V of tile i and K of tile i + lead in turn.
-__device__ __forceinline__ int lead_of(bool pair) { return pair ? 2 : 4; }
-__device__ __forceinline__ int pos_k(int lead, int i) { return i < lead ? i : 2 * i + 1 - lead; }
-__device__ __forceinline__ int pos_v(int lead, int n, int i) {
-  return i + lead < n ? lead + 2 * i : n + i;
-}
+// The slot of a CTA's tile number `t` in either ring, and the parity of the
+// slot's barriers for it.
+template <int kSlots>
+struct Slot {
+  uint32_t at, parity;
+  __device__ __forceinline__ explicit Slot(uint32_t t) {
+    static_assert(kSlots % 2 == 0, "see Geometry");
+    const uint32_t lap = t / kSlots;
+    at = t - lap * kSlots;
+    parity = lap & 1u;
+  }
+};
 
 // False when the wait gave up (it raised the status bit and the abort flag, at
 // which every other wait of the CTA gives up too).
@@ -554,6 +564,115 @@ __device__ __noinline__ void add_nonfinite(const KernelArgs &k, int seq, int ctx
   }
 }
 
+// One copying warp: every tile of the CTA's segments, of K or of V, into its
+// ring.
+template <int kHalves, bool kTma, int kSlots>
+__device__ __forceinline__ void copy_tiles(const KernelArgs &k, const CUtensorMap *map,
+                                           const char *src, char *ring, uint64_t *full,
+                                           uint64_t *empty, AttnTail *s) {
+  using G = Geometry<kHalves>;
+  const int lane = threadIdx.x & 31;
+  const int D = k.a.c.head_dim;
+  Walk w;
+  w.start(k.w);
+  const CacheArgs &c = k.a.c;
+  const uint32_t bs = c.block_size;
+  uint32_t tiles = 0, filled = 0;  // tiles of the CTA before the segment, tiles begun
+  bool ok = true;
+  unsigned bits = 0;
+  // (block, token in it) of token t of the sequence
+  auto place = [&](const int32_t *table, uint32_t t) {
+    const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
+    int id = table[b];
+    if (id < 0 || id >= c.blocks) {
+      bits |= SMC_DEV_BAD_BLOCK;
+      id = 0;
+    }
+    return make_int2(id, t - b * bs);
+  };
+  while (ok && w.next(k)) {
+    const bool pair = w.rows > kRows;
+    const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.t.seq) * k.a.b.T;
+    const int tok0 = w.t.kv0 + w.i0 * kTile, tok1 = min(tok0 + w.n * kTile, w.t.kv1);
+    const int per_tile = kTile / k.box;
+    int2 ahead = make_int2(0, 0);  // the place of box `from` + lane
+    int from = -64;
+    int unseen = -1;  // the slot whose element copies may still be under way
+    for (int i = 0; i < w.n; ++i) {
+      const int t0 = tok0 + i * kTile, t1 = min(t0 + kTile, tok1);
+      const Slot<kSlots> slot(tiles + i);
+      char *dst = ring + slot.at * G::kTileBytes;
+      if constexpr (kTma) {
+        const int first = i * per_tile;
+        if (first + per_tile > from + 32) {
+          from = first;
+          const int t = t0 + lane * k.box;
+          if (t < tok1) ahead = place(table, t);
+        }
+      }
+      if (tiles + i >= kSlots &&
+          !(ok = warp_wait(s, &empty[slot.at], slot.parity ^ 1u, k.a.status))) {
+        break;
+      }
+      if (!pair) warp_arrive(&empty[slot.at], lane);  // one group uses it
+      ++filled;
+      if constexpr (kTma) {
+        const int boxes = (t1 - t0 + k.box - 1) / k.box;
+        const int at = i * per_tile - from;
+        if (elect_one()) mbar_arrive_expect_tx(&full[slot.at], boxes * kHalves * k.box * 128);
+        __syncwarp();
+        for (int b = 0; b < boxes; ++b) {
+          const int block = __shfl_sync(0xffffffffu, ahead.x, at + b);
+          const int token = __shfl_sync(0xffffffffu, ahead.y, at + b);
+          if (elect_one()) {
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half) {
+              tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token,
+                          w.head, block, &full[slot.at]);
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        const uint32_t d0 = smem_addr(dst);
+        constexpr int kChunks = 8 * kHalves;
+        const int ch = lane % kChunks;
+        const bool take = ch * 8 < D;
+        for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
+          const int2 at_block = place(table, t0 + r);
+          const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
+                              w.head * c.head_stride + (take ? ch * 8 : 0);
+          cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                     src + off * 2, take);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (unseen >= 0) {  // the tile before this one has arrived
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          fence_proxy_async_smem();
+          warp_arrive(&full[unseen], lane);
+        }
+        unseen = slot.at;
+      }
+    }
+    if constexpr (!kTma) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (unseen >= 0) {
+        fence_proxy_async_smem();
+        warp_arrive(&full[unseen], lane);
+      }
+    }
+    tiles += w.n;
+  }
+  if constexpr (kTma) {
+    // every copy has landed before the CTA ends, also when it gave up
+    for (uint32_t t = filled > kSlots ? filled - kSlots : 0; t < filled; ++t) {
+      const Slot<kSlots> slot(t);
+      mbar_wait(&full[slot.at], slot.parity, kWaitPolls);
+    }
+  }
+  if (bits) raise_status(k.a.status, bits);
+}
+
 template <typename T, int kHalves, bool kTma>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ CUtensorMap map_k,
@@ -562,15 +681,17 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   using Wt = Weights<T>;
   extern __shared__ __align__(1024) char smem[];
   char *const s_q = smem;
-  char *const s_ring = smem + G::kQBytes;
+  char *const s_k = smem + G::kQBytes, *const s_v = s_k + G::kSlotsK * G::kTileBytes;
   AttnTail *const s = reinterpret_cast<AttnTail *>(smem + G::kTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = k.a.c.head_dim;
 
   if (tid == 0) {
-    for (int i = 0; i < G::kSlots; ++i) {
-      mbar_init(&s->full[i], 1);
-      mbar_init(&s->empty[i], 1);
+    for (int v = 0; v < 2; ++v) {
+      for (int i = 0; i < (v ? G::kSlotsV : G::kSlotsK); ++i) {
+        mbar_init(&s->full[v][i], 1);
+        mbar_init(&s->empty[v][i], 2);  // both groups, or one and the copying warp
+      }
     }
     mbar_init(&s->q_full, 8);
     for (int g = 0; g < 2; ++g) {
@@ -579,10 +700,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         mbar_init(&s->weights[g][b], 4);
       }
       mbar_init(&s->added[g], 1);
+      mbar_init(&s->o_full[g], 1);
+      mbar_init(&s->drained[g], 1);
     }
-    mbar_init(&s->o_full, 1);
     mbar_init(&s->stats, 8);
-    mbar_init(&s->drained, 1);
     s->nonfinite = 0;
     s->abort = (smem_addr(smem) & 1023u) != 0;  // the swizzle counts from 1 KB boundaries
     mbar_init_fence();
@@ -605,7 +726,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     const uint32_t t_o = tmem + lanes + 256 + g * 128;
     Walk w;
     w.start(k.w);
-    uint32_t seg = 0, ring = 0, turn = 0;  // turn: tiles of this group so far
+    uint32_t seg = 0, tiles = 0, turn = 0;  // tiles of the CTA, of this group so far
     bool ok = true;
     while (ok && w.next(k)) {
       ++seg;
@@ -632,7 +753,6 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         fence_proxy_async_smem();
         warp_arrive(&s->q_full, lane);
       }
-      const int lead = lead_of(pair);
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
@@ -677,8 +797,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           if (first) {
             m = top;
           } else if (__any_sync(0xffffffffu, rise)) {
-            // the group's last product has been added (turn counts this tile)
-            if (!(ok = warp_wait(s, &s->added[g], (turn - 2) & 1u, k.a.status))) break;
+            // the product with V of the group's last tile (number turn - 2) is done
+            if (!(ok = warp_wait(s, &s->added[g], turn & 1u, k.a.status))) break;
             tc_fence_after();
             const float mn = rise ? top : m;
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
@@ -722,11 +842,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           // the tile reaches past the committed tokens: V rows past the last
           // token become 0 (they may hold anything), and so do infinities
           // and NaN of new tokens, which add_nonfinite puts back
-          const uint32_t at = ring + pos_v(lead, w.n, i), slot = at % G::kSlots;
-          if (!(ok = warp_wait(s, &s->full[slot], at / G::kSlots & 1u, k.a.status))) break;
+          const Slot<G::kSlotsV> slot(tiles + i);
+          if (!(ok = warp_wait(s, &s->full[1][slot.at], slot.parity, k.a.status))) break;
           const int t = t0 + (r & (kTile - 1));
           if (t >= w.t.ctx) {
-            char *v = s_ring + slot * G::kTileBytes + (r & (kTile - 1)) * 128;
+            char *v = s_v + slot.at * G::kTileBytes + (r & (kTile - 1)) * 128;
             bool found = false;
             const int c0 = (r / kTile) * 4 * kHalves;
 #pragma unroll 4
@@ -760,8 +880,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       // ---- the unit's result -----------------------------------------------
       s->stat[g][r] = make_float2(m, l);
       warp_arrive(&s->stats, lane);
-      ok = warp_wait(s, &s->o_full, (seg - 1) & 1u, k.a.status) &&
-           warp_wait(s, &s->stats, (seg - 1) & 1u, k.a.status);
+      ok = warp_wait(s, &s->o_full[g], (seg - 1) & 1u, k.a.status) &&
+           (pair || (warp_wait(s, &s->o_full[1 - g], (seg - 1) & 1u, k.a.status) &&
+                     warp_wait(s, &s->stats, (seg - 1) & 1u, k.a.status)));
       if (!ok) break;
       tc_fence_after();
       const bool bad = s->nonfinite == seg;
@@ -839,10 +960,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         }
         tc_fence_before();
       }
-      ring += 2 * w.n;
+      tiles += w.n;
     }
-  } else if (warp == 8) {
-    // ---- matrix products ----------------------------------------------------
+  } else if (warp < 10) {
+    // ---- matrix products: warp 8 for group 0, warp 9 for group 1 --------------
+    const int g = warp - 8;
     if (elect_one()) {
       Walk w;
       w.start(k.w);
@@ -850,201 +972,68 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       const uint32_t id_pv = instr_desc(Wt::kBf16, (D + 15) / 16 * 16, true);
       const int k_steps = (D + 15) / 16;
       // descriptors of the first bytes; a step's offset is added to the address field
-      const uint32_t q0 = smem_desc(smem_addr(s_q), 16), k0 = smem_desc(smem_addr(s_ring), 16);
-      const uint32_t v0 = smem_desc(smem_addr(s_ring), kTile * 128);
-      uint32_t seg = 0;
-      uint32_t slot = 0, lap = 0;  // the ring position to be used next: positions are used in order
-      uint32_t asked[2] = {0, 0}, given[2] = {0, 0};  // tiles of either group: scores, values
+      const uint32_t q0 = smem_desc(smem_addr(s_q), 16), k0 = smem_desc(smem_addr(s_k), 16);
+      const uint32_t v0 = smem_desc(smem_addr(s_v), kTile * 128);
+      const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
+      uint32_t seg = 0, tiles = 0;
+      uint32_t asked = 0, given = 0;  // tiles of the group so far: scores, products with V
       bool ok = true;
-      auto wait_full = [&](uint32_t at, uint32_t parity) {
-        return guarded_wait(s, &s->full[at], parity, k.a.status);
-      };
-      auto advance = [&] {
-        if (++slot == G::kSlots) {
-          slot = 0;
-          lap ^= 1;
-        }
-      };
-      auto scores = [&](int g, int q_tile, uint32_t at) {
-        const uint32_t buf = asked[g]++ & 1u;
-        const uint32_t ka = k0 + at * (G::kTileBytes >> 4), qa = q0 + q_tile * (G::kQTile >> 4);
-        const uint32_t d = tmem + g * 128 + buf * 64;
-#pragma unroll
-        for (int c = 0; c < 4 * kHalves; ++c) {
-          if (c < k_steps) {
-            mma_ss(d, qa + ((c >> 2) * (kRows * 128) + (c & 3) * 32) / 16,
-                   ka + ((c >> 2) * (kTile * 128) + (c & 3) * 32) / 16, id_qk, c > 0);
-          }
-        }
-        tc_commit(&s->scores[g][buf]);
-      };
-      auto wait_weights = [&](int g) {
-        return guarded_wait(s, &s->weights[g][given[g] & 1u], given[g] >> 1 & 1u, k.a.status);
-      };
-      auto values = [&](int g, uint32_t at, bool more) {
-        const uint32_t buf = given[g]++ & 1u;
-        const uint32_t va = v0 + at * (G::kTileBytes >> 4);
-        const uint32_t p = tmem + g * 128 + buf * 64;
-#pragma unroll
-        for (int c = 0; c < kTile / 16; ++c) {
-          mma_ts(tmem + 256 + g * 128, p + c * 8, va + c * 2048 / 16, id_pv, more || c > 0);
-        }
-        tc_commit(&s->added[g]);
-      };
       while (ok && w.next(k)) {
         const bool pair = w.rows > kRows;
-        const int n = w.n, lead = lead_of(pair);
+        const int n = w.n, step = pair ? 1 : 2;
+        const uint32_t qa = q0 + (pair ? g * (G::kQTile >> 4) : 0);
+        // scores of tile i, once its K is there
+        auto scores = [&](int i) {
+          const Slot<G::kSlotsK> slot(tiles + i);
+          if (!guarded_wait(s, &s->full[0][slot.at], slot.parity, k.a.status)) return false;
+          const uint32_t buf = asked++ & 1u, ka = k0 + slot.at * (G::kTileBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < 4 * kHalves; ++c) {
+            if (c < k_steps) {
+              mma_ss(t_s + buf * 64, qa + ((c >> 2) * (kRows * 128) + (c & 3) * 32) / 16,
+                     ka + ((c >> 2) * (kTile * 128) + (c & 3) * 32) / 16, id_qk, c > 0);
+            }
+          }
+          tc_commit(&s->scores[g][buf]);
+          tc_commit(&s->empty[0][slot.at]);
+          return true;
+        };
         if (!(ok = guarded_wait(s, &s->q_full, seg & 1u, k.a.status))) break;
         ++seg;
         tc_fence_after();
-        for (int j = 0; ok && j < n && j < lead; ++j) {
-          if (!(ok = wait_full(slot, lap))) break;
-          if (pair) {
-            scores(0, 0, slot);
-            scores(1, 1, slot);
-          } else {
-            scores(j & 1, 0, slot);
+        const int first = pair ? 0 : g;
+        for (int i = first; ok && i < n && i < 2 * step; i += step) ok = scores(i);
+        for (int i = first; ok && i < n; i += step) {
+          const Slot<G::kSlotsV> slot(tiles + i);
+          const uint32_t buf = given & 1u, va = v0 + slot.at * (G::kTileBytes >> 4);
+          ok = guarded_wait(s, &s->full[1][slot.at], slot.parity, k.a.status) &&
+               guarded_wait(s, &s->weights[g][buf], given >> 1 & 1u, k.a.status);
+          if (!ok) break;
+          ++given;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kTile / 16; ++c) {
+            mma_ts(t_o, t_s + buf * 64 + c * 8, va + c * 2048 / 16, id_pv, i >= step || c > 0);
           }
-          tc_commit(&s->empty[slot]);
-          advance();
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          // V of tile i, then (unless the tiles run out) K of tile i + lead
-          const bool ask = i + lead < n;
-          const uint32_t at = slot, at_lap = lap;
-          advance();
-          const uint32_t next = slot, next_lap = lap;
-          if (ask) advance();
-          for (int g = pair ? 0 : i & 1, end = pair ? 2 : g + 1; ok && g < end; ++g) {
-            const bool fresh = !pair || g == 0;  // the first use of either tile
-            const bool last = !pair || g == 1;
-            if (!(ok = (!fresh || wait_full(at, at_lap)) && wait_weights(g))) break;
-            tc_fence_after();
-            values(g, at, i >= (pair ? 1 : 2));
-            if (last) tc_commit(&s->empty[at]);
-            if (ask) {
-              if (fresh && !(ok = wait_full(next, next_lap))) break;
-              scores(g, pair ? g : 0, next);
-              if (last) tc_commit(&s->empty[next]);
-            }
-          }
+          tc_commit(&s->added[g]);
+          tc_commit(&s->empty[1][slot.at]);
+          if (i + 2 * step < n) ok = scores(i + 2 * step);
         }
         if (!ok) break;
-        tc_commit(&s->o_full);
+        tc_commit(&s->o_full[g]);
+        tiles += n;
       }
-      tc_commit(&s->drained);  // nothing of this CTA runs on when it ends
-      if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(k.a.status, SMC_DEV_TIMEOUT);
+      tc_commit(&s->drained[g]);  // nothing of this CTA runs on when it ends
+      if (!mbar_wait(&s->drained[g], 0, kWaitPolls)) raise_status(k.a.status, SMC_DEV_TIMEOUT);
     }
     __syncwarp();
   } else {
-    // ---- copies ---------------------------------------------------------------
-    Walk w;
-    w.start(k.w);
-    const CacheArgs &c = k.a.c;
-    const uint32_t bs = c.block_size;
-    uint32_t at = 0, slot = 0, lap = 1;  // lap: parity of the slot's release before its last use
-    bool ok = true;
-    unsigned bits = 0;
-    // (block, first token) of a box or token t of the sequence
-    auto place = [&](const int32_t *table, uint32_t t) {
-      const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
-      int id = table[b];
-      if (id < 0 || id >= c.blocks) {
-        bits |= SMC_DEV_BAD_BLOCK;
-        id = 0;
-      }
-      return make_int2(id, t - b * bs);
-    };
-    while (ok && w.next(k)) {
-      const int lead = lead_of(w.rows > kRows);
-      const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.t.seq) * k.a.b.T;
-      const int tok0 = w.t.kv0 + w.i0 * kTile, tok1 = min(tok0 + w.n * kTile, w.t.kv1);
-      // the places of 32 boxes, one per lane, for K and (behind it) for V
-      const int per_tile = kTma ? kTile / k.box : 0;
-      int2 ahead_k = make_int2(0, 0), ahead_v = make_int2(0, 0);
-      int from_k = -64, from_v = -64;
-      for (int j = 0; ok && j < 2 * w.n; ++j) {
-        // position j holds K of tile i or V of tile i
-        const int past = j - lead, paired = 2 * (w.n - lead);
-        const bool is_k = j < min(lead, w.n) || (past < paired && (past & 1));
-        const int i = j < min(lead, w.n) ? j
-                      : past < paired    ? (past >> 1) + (is_k ? lead : 0)
-                                         : j - w.n;
-        const int t0 = tok0 + i * kTile, t1 = min(t0 + kTile, tok1);
-        char *dst = s_ring + slot * G::kTileBytes;
-        if constexpr (kTma) {
-          const int boxes = (t1 - t0 + k.box - 1) / k.box;
-          const int b = lane / kHalves, half = lane % kHalves;
-          int block, token;
-          auto locate = [&](int2 &cached, int &from) {
-            const int first = i * per_tile;
-            if (first < from || first + per_tile > from + 32) {
-              from = first;
-              const int t = tok0 + (first + lane) * k.box;
-              if (t < tok1) cached = place(table, t);
-            }
-            const int src = (first - from + b) & 31;
-            block = __shfl_sync(0xffffffffu, cached.x, src);
-            token = __shfl_sync(0xffffffffu, cached.y, src);
-          };
-          if (is_k) locate(ahead_k, from_k);
-          else locate(ahead_v, from_v);
-          if (at >= static_cast<uint32_t>(G::kSlots) &&
-              !(ok = warp_wait(s, &s->empty[slot], lap, k.a.status))) {
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], boxes * kHalves * k.box * 128);
-          __syncwarp();
-          if (b < boxes) {
-            tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, is_k ? &map_k : &map_v,
-                        half * 64, token, w.head, block, &s->full[slot]);
-          }
-        } else {
-          if (at >= static_cast<uint32_t>(G::kSlots) &&
-              !(ok = warp_wait(s, &s->empty[slot], lap, k.a.status))) {
-            break;
-          }
-          const char *src = is_k ? c.k : c.v;
-          const uint32_t d0 = smem_addr(dst);
-          constexpr int kChunks = 8 * kHalves;
-          const int ch = lane % kChunks;
-          const bool take = ch * 8 < D;
-          for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
-            const int2 at_block = place(table, t0 + r);
-            const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
-                                w.head * c.head_stride + (take ? ch * 8 : 0);
-            cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       src + off * 2, take);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (at > 0) {  // the position before this one has arrived
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s->full[(at - 1) % G::kSlots]);
-          }
-        }
-        ++at;
-        if (++slot == G::kSlots) {
-          slot = 0;
-          lap ^= 1;
-        }
-      }
-    }
-    if constexpr (kTma) {
-      // every copy has landed before the CTA ends
-      for (uint32_t a = at > static_cast<uint32_t>(G::kSlots) ? at - G::kSlots : 0; a < at; ++a) {
-        mbar_wait(&s->full[a % G::kSlots], a / G::kSlots & 1u, kWaitPolls);
-      }
+    // ---- copies -----------------------------------------------------------------
+    if (warp == 10) {
+      copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s);
     } else {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (at > 0) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s->full[(at - 1) % G::kSlots]);
-      }
+      copy_tiles<kHalves, kTma, G::kSlotsV>(k, &map_v, k.a.c.v, s_v, s->full[1], s->empty[1], s);
     }
-    if (bits) raise_status(k.a.status, bits);
   }
   __syncthreads();
   if (warp == 8) {
@@ -1202,7 +1191,9 @@ static const void *attention_fn(bool wide, bool tma) {
 
 constexpr size_t kAttnSmem = Geometry<2>::kTail + sizeof(AttnTail);
 static_assert(Geometry<1>::kTail <= Geometry<2>::kTail && kAttnSmem <= 227 * 1024, "shared memory");
-static_assert(Geometry<1>::kSlots <= 20 && Geometry<2>::kSlots >= 8, "ring");
+static_assert(Geometry<1>::kSlotsV <= 12 &&
+              (Geometry<2>::kSlotsK + Geometry<2>::kSlotsV) * Geometry<2>::kTileBytes == kRingBytes,
+              "rings");
 
 static cudaError_t configure(int *sms) {
   constexpr int kMaxDev = 64;

@@ -434,6 +434,23 @@ _CACHE_DTYPES = {torch.float32: SMC_F32, torch.bfloat16: SMC_BF16, torch.float16
 _CACHE_TORCH = {code: dtype for dtype, code in _CACHE_DTYPES.items()}
 
 
+def _addr(t, name, dtype, numel=None):
+    """The address of a contiguous CUDA tensor, for the calls of a decoding
+    loop: the checks of _ptr, the common case in one expression."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        return t.data_ptr()
+    return _ptr(t, name, dtype, numel).value
+
+
+def _raw_stream(stream, tensor):
+    """The stream's handle; without one, the current stream of the tensor's
+    device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def make_cache(k, v):
     """smc_cache over keys and values [layers, blocks, block_size, kv_heads,
     head_dim]: CUDA tensors of one dtype (fp32, bf16 or fp16), one shape and
@@ -524,9 +541,9 @@ def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=No
                              q_row, q_head, o_row, o_head)
     _check("smc_tree_attention", lib().smc_tree_attention(
         ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp,
-        None if mask is None else _ptr(mask, "mask", torch.int32), op,
-        None if lse is None else _ptr(lse, "lse", torch.float32, rows * heads),
-        _ptr(workspace, "workspace"), workspace.numel(), _stream(stream)))
+        None if mask is None else _addr(mask, "mask", torch.int32), op,
+        None if lse is None else _addr(lse, "lse", torch.float32, rows * heads),
+        _addr(workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(stream, workspace)))
 
 
 def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, positions=None,
@@ -550,11 +567,11 @@ def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, posit
                            o_head)
     _check("smc_qk_norm_rope", lib().smc_qk_norm_rope(
         ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp, kp, vp,
-        None if q_weight is None else _ptr(q_weight, "q_weight", dtype, cache.head_dim),
-        None if k_weight is None else _ptr(k_weight, "k_weight", dtype, cache.head_dim),
-        None if positions is None else _ptr(positions, "positions", torch.int32, rows),
-        _ptr(rope, "rope", torch.float32), op, _ptr(workspace, "workspace"), workspace.numel(),
-        _stream(stream)))
+        None if q_weight is None else _addr(q_weight, "q_weight", dtype, cache.head_dim),
+        None if k_weight is None else _addr(k_weight, "k_weight", dtype, cache.head_dim),
+        None if positions is None else _addr(positions, "positions", torch.int32, rows),
+        _addr(rope, "rope", torch.float32), op, _addr(workspace, "workspace", torch.uint8), workspace.numel(),
+        _raw_stream(stream, workspace)))
 
 
 def kv_copy_blocks(cache, pairs, counts, workspace, stream=None):
@@ -564,9 +581,9 @@ def kv_copy_blocks(cache, pairs, counts, workspace, stream=None):
         raise ValueError(f"pairs must be [lists, max_pairs, 2], got {tuple(pairs.shape)}")
     lists, most = pairs.shape[:2]
     _check("kv_copy_blocks", lib().kv_copy_blocks(
-        ctypes.byref(cache), _ptr(pairs, "pairs", torch.int32),
-        _ptr(counts, "counts", torch.int32, lists), lists, most, _ptr(workspace, "workspace"),
-        workspace.numel(), _stream(stream)))
+        ctypes.byref(cache), _addr(pairs, "pairs", torch.int32),
+        _addr(counts, "counts", torch.int32, lists), lists, most, _addr(workspace, "workspace", torch.uint8),
+        workspace.numel(), _raw_stream(stream, workspace)))
 
 
 def kv_compact_tokens(cache, batch, path, n_path, workspace, stream=None):
@@ -576,9 +593,9 @@ def kv_compact_tokens(cache, batch, path, n_path, workspace, stream=None):
         raise ValueError(f"path must be [S, max_path], got {tuple(path.shape)}")
     _check("kv_compact_tokens", lib().kv_compact_tokens(
         ctypes.byref(cache), ctypes.byref(batch),
-        _ptr(path, "path", torch.int32, batch.S * path.shape[1]),
-        _ptr(n_path, "n_path", torch.int32, batch.S), path.shape[1],
-        _ptr(workspace, "workspace"), workspace.numel(), _stream(stream)))
+        _addr(path, "path", torch.int32, batch.S * path.shape[1]),
+        _addr(n_path, "n_path", torch.int32, batch.S), path.shape[1],
+        _addr(workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(stream, workspace)))
 
 
 def kv_truncate(params, kv, new_len, workspace, stream=None):
@@ -586,5 +603,5 @@ def kv_truncate(params, kv, new_len, workspace, stream=None):
     blocks past them back."""
     _check("kv_truncate", lib().kv_truncate(
         ctypes.byref(params), ctypes.byref(kv),
-        _ptr(new_len, "new_len", torch.int32, params.B * params.N), _ptr(workspace, "workspace"),
-        workspace.numel(), _stream(stream)))
+        _addr(new_len, "new_len", torch.int32, params.B * params.N), _addr(workspace, "workspace", torch.uint8),
+        workspace.numel(), _raw_stream(stream, workspace)))

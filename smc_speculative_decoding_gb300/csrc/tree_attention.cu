@@ -5,7 +5,8 @@
 //   plan_kernel       lists the call's work in tiles of 64 tokens;
 //   attention_kernel  persistent, one CTA per SM, on the 5th-generation tensor
 //                     cores; every CTA takes an equal run of the tiles;
-//   combine_kernel    joins rows that several CTAs, or a shared and an own
+//   join_cut_units_kernel, or with shared parts join_shared_kernel,
+//                     joins the rows that several CTAs, or a shared and an own
 //                     part, contributed to.
 #include <cuda.h>
 
@@ -44,6 +45,12 @@ struct Entry {
 };
 constexpr int kShared = 1, kSolo = 2;  // a shared part; the rows have no other part
 
+// The unit that the boundary before a CTA is the first to cut.
+struct Cut {
+  int row0, rows, head, more;  // first row, rows of the unit (0: no such unit), key head,
+  int rt, pad[3];              // continuations, row tile
+};
+
 struct PlanHeader {
   unsigned ticket;  // plan CTAs done; returns to zero
   int total, per;   // tiles, tiles per CTA
@@ -56,6 +63,7 @@ struct AttnWorkspace {
   Entry *entries;  // shared parts of the groups (when group > 1), then the sequences
   float *lse[2];   // own, shared: [rows * q_heads], log2
   float *o[2];     // [rows * q_heads][head_dim], normalised
+  Cut *cuts;       // [kMaxCtas]
   float *lse_c;    // [kMaxCtas][kUnitRows] continuations
   float *o_c;      // [kMaxCtas][kUnitRows][head_dim]
   int groups;      // 0 when group == 1
@@ -84,6 +92,7 @@ static size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, char *b
     t.lse[k] = reinterpret_cast<float *>(take(sizeof(float) * n));
     t.o[k] = reinterpret_cast<float *>(take(sizeof(float) * n * D));
   }
+  t.cuts = reinterpret_cast<Cut *>(take(sizeof(Cut) * kMaxCtas));
   t.lse_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows));
   t.o_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows * D));
   if (w) *w = t;
@@ -188,14 +197,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) s_slots = s_seqs > 1 && !s_bad ? s_limit / bs : 0;
     __syncthreads();
     const int slots = s_slots;
-    if (slots > 0) {
+    if (slots > 0) {  // a warp per sequence, against the first one that has rows
       const int32_t *ref = b.tables + static_cast<int64_t>(s_ref) * b.T;
       int mine = slots;
-      for (int i = s_ref - s0 + 1; i < b.group; ++i) {
+      for (int i = s_ref - s0 + 1 + (tid >> 5); i < b.group; i += kPlanThreads / 32) {
         if (b.row_start && b.row_start[s0 + i] == b.row_start[s0 + i + 1]) continue;  // no rows
         const int32_t *row = b.tables + static_cast<int64_t>(s0 + i) * b.T;
-        for (int t = tid; t < mine; t += kPlanThreads) {
-          if (row[t] != ref[t]) mine = t;
+#pragma unroll 4
+        for (int t = tid & 31; t < slots; t += 32) {
+          if (row[t] != ref[t]) mine = min(mine, t);
         }
       }
       if (mine < slots) atomicMin(&s_slots, mine);
@@ -350,6 +360,13 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(take ? 16 : 0)
+               : "memory");
+}
+
+// Eight words to a 32-byte boundary, one whole sector a thread.
+__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                : "memory");
 }
 
@@ -542,25 +559,27 @@ __device__ __forceinline__ uint32_t view_bits(const uint32_t *mask, int words, i
 }
 
 // A new token that holds an infinity or NaN had it zeroed in the products, as
-// rows that do not see the token must not meet it; rows that see it get it
-// here: columns [col, col + 32) of v, of the new tokens in [t0, t1).
-template <typename T>
-__device__ __noinline__ void add_nonfinite(const KernelArgs &k, int seq, int ctx, int n_new,
-                                           int head, int row, int i, int t0, int t1, int col,
-                                           float *o) {
+// rows that do not see the token must not meet it.  Rows that see it get it
+// here: columns [c0, c1) of the row's result whose visible new tokens in
+// [t0, t1) hold such values become the sum of these.
+template <typename T, typename Out>
+__device__ __noinline__ void patch_nonfinite(const KernelArgs &k, int seq, int ctx, int n_new,
+                                             int head, int row, int i, int t0, int t1, int c0,
+                                             int c1, Out *o) {
   const uint32_t *mask = k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
   const int32_t *table = k.a.b.tables + static_cast<int64_t>(seq) * k.a.b.T;
-  for (int at = max(t0, ctx); at < t1; ++at) {
-    if (!(view_bits(mask, k.a.mask_words, i, n_new, at - ctx) & 1u)) continue;
-    const int block = table[at / k.a.c.block_size];
-    if (block < 0 || block >= k.a.c.blocks) continue;
-    const T *v = reinterpret_cast<const T *>(k.a.c.v) + block * k.a.c.block_stride +
-                 (at % k.a.c.block_size) * k.a.c.token_stride + head * k.a.c.head_stride;
-    for (int d = 0; d < 32; ++d) {
-      if (col + d >= k.a.c.head_dim) break;
-      const float x = to_f32(v[col + d]);
-      if (!(fabsf(x) < INFINITY)) o[d] += x;
+  for (int d = c0; d < c1; ++d) {
+    float sum = 0.f;
+    for (int at = max(t0, ctx); at < t1; ++at) {
+      if (!(view_bits(mask, k.a.mask_words, i, n_new, at - ctx) & 1u)) continue;
+      const int block = table[at / k.a.c.block_size];
+      if (block < 0 || block >= k.a.c.blocks) continue;
+      const T *v = reinterpret_cast<const T *>(k.a.c.v) + block * k.a.c.block_stride +
+                   (at % k.a.c.block_size) * k.a.c.token_stride + head * k.a.c.head_stride;
+      const float x = to_f32(v[d]);
+      if (!(fabsf(x) < INFINITY)) sum += x;
     }
+    if (sum != 0.f) o[d] = from_f32<Out>(sum);
   }
 }
 
@@ -727,8 +746,18 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     Walk w;
     w.start(k.w);
     uint32_t seg = 0, tiles = 0, turn = 0;  // tiles of the CTA, of this group so far
-    bool ok = true;
-    while (ok && w.next(k)) {
+    bool ok = true, more = w.next(k);
+    if (tid == 0 && !k.w.groups) {
+      const int per = __ldcg(&k.w.head->per);
+      const bool cut = more && w.i0 > 0 && w.i0 <= per;
+      const int first = static_cast<int>(blockIdx.x) * per;
+      int4 *to = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
+      to[0] = cut ? make_int4(w.t.row0, w.rows, w.head,
+                              (first - w.i0 + w.t.tiles - 1) / per - static_cast<int>(blockIdx.x) + 1)
+                  : make_int4(0, 0, 0, 0);
+      to[1] = make_int4(w.rt, 0, 0, 0);
+    }
+    while (ok && more) {
       ++seg;
       const bool pair = w.rows > kRows;
       const int row_in_unit = pair ? g * kRows + r : r;
@@ -743,16 +772,25 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         char *dst = s_q + (pair ? g * G::kQTile : 0) + r * 128;
         const int c0 = pair ? 0 : g * 4 * kHalves, c1 = pair ? 8 * kHalves : c0 + 4 * kHalves;
         if (warp_live) {
-          for (int c = c0; c < c1; ++c) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live && c * 8 < D) x = *reinterpret_cast<const uint4 *>(q + c * 8);
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kRows * 128) +
-                                       (((c & 7) ^ (r & 7)) << 4)) = x;
+          for (int c = c0; c < c1; c += 4 * kHalves) {  // loads first: one latency a batch
+            uint4 x[4 * kHalves];
+#pragma unroll
+            for (int e = 0; e < 4 * kHalves; ++e) {
+              x[e] = make_uint4(0, 0, 0, 0);
+              if (live && (c + e) * 8 < D) x[e] = *reinterpret_cast<const uint4 *>(q + (c + e) * 8);
+            }
+#pragma unroll
+            for (int e = 0; e < 4 * kHalves; ++e) {
+              *reinterpret_cast<uint4 *>(dst + ((c + e) >> 3) * (kRows * 128) +
+                                         ((((c + e) & 7) ^ (r & 7)) << 4)) = x[e];
+            }
           }
         }
         fence_proxy_async_smem();
         warp_arrive(&s->q_full, lane);
       }
+      Walk ahead = w;  // found while the first scores are under way
+      more = ahead.next(k);
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
@@ -788,10 +826,14 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
 #pragma unroll
           for (int b = 0; b < 4; ++b) mx[b] = __uint_as_float(z[b]);
 #pragma unroll
-          for (int c = 4; c < 64; c += 4) {
+          for (int c = 4; c < 60; c += 8) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[c + b]));
+            for (int b = 0; b < 4; ++b) {
+              mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(z[c + b])), __uint_as_float(z[c + 4 + b]));
+            }
           }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[60 + b]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k.sc;
           const bool rise = top > m + kLazy || (first && top > m);
           if (first) {
@@ -818,7 +860,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           first = false;
           const float sub = Wt::kOffset - (m == -INFINITY ? 0.f : m);
           const unsigned long long sc2 = f2dup(k.sc), sub2 = f2dup(sub);
-          unsigned long long sum2 = f2dup(0.f);
+          unsigned long long sum2[2] = {f2dup(0.f), f2dup(0.f)};
           uint32_t p[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -828,13 +870,13 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             f2unpack(y, a, b);
             a = fast_exp2(a);
             b = fast_exp2(b);
-            sum2 = add2(sum2, f2pack(a, b));
+            sum2[c & 1] = add2(sum2[c & 1], f2pack(a, b));
             p[c] = Wt::pack(a, b);
           }
           __syncwarp();
           tmem_st32(t_s, p);
           float sa, sb;
-          f2unpack(sum2, sa, sb);
+          f2unpack(add2(sum2[0], sum2[1]), sa, sb);
           l += sa + sb;
           tmem_wait_st();
         }
@@ -914,45 +956,47 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         }
       }
       __syncwarp();
+      const int half_cols = 32 * kHalves;
+      const int c_begin = pair ? 0 : g * half_cols;
+      const int c_end = min(pair ? 2 * half_cols : c_begin + half_cols, D);
+      T *const out = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head;
+      float *const part = base ? k.w.o[kind] + rh * D : k.w.o_c + cont * D;
       if (warp_live) {
         const uint32_t t_a = tmem + lanes + 256 + (pair ? g * 128 : 0);
-        const int half_cols = 32 * kHalves;
-        const int c_begin = pair ? 0 : g * half_cols, c_end = pair ? 2 * half_cols : c_begin + half_cols;
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
-          if (c >= D) break;
           uint32_t x[32], y[32];
           tmem_ld32(t_a + c, x);
           if (two) tmem_ld32(t_a + 128 + c, y);
           tmem_wait_ld(x);
-          if (two) tmem_tie(y);
-          float o[32];
+          if (two) {
+            tmem_tie(y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            o[e] = __uint_as_float(x[e]) * f0;
-            if (two) o[e] = fmaf(__uint_as_float(y[e]), f1, o[e]);
-          }
-          if (live && bad) {
-            const int t0 = w.t.kv0 + w.i0 * kTile;
-            add_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0,
-                             min(t0 + w.n * kTile, w.t.kv1), c, o);
-          }
-          if (live && whole) {
-            T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              if (c + e < D) {
-                *reinterpret_cast<uint4 *>(dst + e) =
-                    make_uint4(Wt::pack(o[e], o[e + 1]), Wt::pack(o[e + 2], o[e + 3]),
-                               Wt::pack(o[e + 4], o[e + 5]), Wt::pack(o[e + 6], o[e + 7]));
-              }
+            for (int e = 0; e < 32; ++e) {
+              x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f1, __uint_as_float(x[e]) * f0));
             }
-          } else if (live) {
-            float *dst = (base ? k.w.o[kind] + rh * D : k.w.o_c + cont * D) + c;
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              if (c + e < D) {
-                *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f0);
+          }
+          if (live) {
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                if (c + e < D) {
+                  uint4 v;
+                  uint32_t *words = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    words[j] = Wt::pack(__uint_as_float(x[e + 2 * j]), __uint_as_float(x[e + 2 * j + 1]));
+                  }
+                  *reinterpret_cast<uint4 *>(out + c + e) = v;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                if (c + e < D) store_32_bytes(part + c + e, x + e);
               }
             }
           }
@@ -960,7 +1004,17 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         }
         tc_fence_before();
       }
+      if (bad && live) {
+        const int t0 = w.t.kv0 + w.i0 * kTile, t1 = min(t0 + w.n * kTile, w.t.kv1);
+        if (whole) {
+          patch_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0, t1, c_begin, c_end, out);
+        } else {
+          patch_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0, t1, c_begin, c_end, part);
+        }
+      }
+      __syncwarp();
       tiles += w.n;
+      w = ahead;
     }
   } else if (warp < 10) {
     // ---- matrix products: warp 8 for group 0, warp 9 for group 1 --------------
@@ -1043,87 +1097,183 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------------------
-// combine_kernel: a warp per (row, query head).  Each part p has a
-// log-sum-exp L_p (log2) and a normalised result o_p:
+// Joining a row's parts: each part p has a log-sum-exp L_p (log2) and a
+// normalised result o_p;
 //   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
-// Rows that one CTA finished alone were written by it.
+// The parts of a unit are the owner's and one continuation for each of `more`
+// CTAs from `cta` + 1 on, at row `slot` of their slots.  A warp joins a row.
 // ---------------------------------------------------------------------------
-constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = 8;
 
-template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ KernelArgs k) {
+struct Parts {
+  bool any;
+  int cta, more, slot;
+};
+
+// kUnits units of each of kBatch rows, whose loads are under way together.
+template <typename T, int kUnits, int kBatch>
+__device__ __forceinline__ void join_rows(const KernelArgs &k, const Parts (&part)[kBatch][kUnits],
+                                          const int64_t (&rh)[kBatch], const int (&row)[kBatch],
+                                          const int (&qh)[kBatch]) {
   const int lane = threadIdx.x & 31;
-  const int64_t rh = static_cast<int64_t>(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (rh >= static_cast<int64_t>(k.a.b.rows) * k.a.q_heads) return;
-  const int row = static_cast<int>(rh / k.a.q_heads), qh = static_cast<int>(rh % k.a.q_heads);
-  const int seq = seq_of_row(k.a.b, row);
-  if (seq < 0) return;
-  const int D = k.a.c.head_dim, per = __ldcg(&k.w.head->per);
-  const int head = qh / k.rep;
-  struct Part { int first, count, slot0; bool any; } part[2];
-  bool whole = false;
+  const int D = k.a.c.head_dim;
+  const bool live = 4 * lane < D;
+  auto load = [&](const float *o) {
+    return live ? __ldcg(reinterpret_cast<const float4 *>(o) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float own[kBatch][kUnits], top[kBatch];
+  float4 first[kBatch][kUnits];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    part[p] = {0, 0, 0, false};
-    if (p == 1 && !k.w.groups) continue;
-    const int e = p == 0 ? k.w.groups + seq : seq / k.a.b.group;
-    const int4 *at = reinterpret_cast<const int4 *>(&k.w.entries[e]);
-    const int4 a = __ldcg(at), b = __ldcg(at + 1);
-    const Entry t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (p == 0 && (row < t.row0 || row >= t.row0 + t.tokens)) return;  // a sequence out of order
-    if (t.tiles <= 0 || t.tokens <= 0) continue;
-    const int r_all = (row - t.row0) * k.rep + qh - head * k.rep;
-    const int rts = (t.tokens * k.rep + kUnitRows - 1) / kUnitRows;
-    const int x0 = __ldcg(&k.w.tile0[e]) + (head * rts + r_all / kUnitRows) * t.tiles;
-    const int c0 = x0 / per, c1 = (x0 + t.tiles - 1) / per;
-    part[p] = {c0, c1 - c0, r_all % kUnitRows, true};
-    if (p == 0) whole = (t.flags & kSolo) && c0 == c1;
-  }
-  if (whole) return;
-  float top = -INFINITY;
+  for (int b = 0; b < kBatch; ++b) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    if (!part[p].any) continue;
-    top = fmaxf(top, __ldcg(&k.w.lse[p][rh]));
-    for (int j = lane; j < part[p].count; j += 32) {
-      top = fmaxf(top, __ldcg(&k.w.lse_c[(part[p].first + 1 + j) * kUnitRows + part[p].slot0]));
+    for (int p = 0; p < kUnits; ++p) {
+      own[b][p] = part[b][p].any ? __ldcg(&k.w.lse[p][rh[b]]) : -INFINITY;
+      first[b][p] = part[b][p].any ? load(k.w.o[p] + rh[b] * D) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  const bool live = 4 * lane < D;
-  auto add = [&](float lse, const float *o) {
-    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
-    sum += f;
-    if (live) {
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(o) + lane);
+  for (int b = 0; b < kBatch; ++b) {
+    top[b] = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < kUnits; ++p) {
+      top[b] = fmaxf(top[b], own[b][p]);
+      for (int j = lane; j < part[b][p].more; j += 32) {
+        top[b] = fmaxf(top[b], __ldcg(&k.w.lse_c[(part[b][p].cta + 1 + j) * kUnitRows + part[b][p].slot]));
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
+  }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    bool any = false;
+    auto add = [&](float lse, float4 x) {
+      const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top[b]);
+      sum += f;
       acc.x = fmaf(f, x.x, acc.x);
       acc.y = fmaf(f, x.y, acc.y);
       acc.z = fmaf(f, x.z, acc.z);
       acc.w = fmaf(f, x.w, acc.w);
-    }
-  };
+    };
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    if (!part[p].any) continue;
-    add(__ldcg(&k.w.lse[p][rh]), k.w.o[p] + rh * D);
-#pragma unroll 4
-    for (int j = 0; j < part[p].count; ++j) {
-      const int64_t slot = static_cast<int64_t>(part[p].first + 1 + j) * kUnitRows + part[p].slot0;
-      add(__ldcg(&k.w.lse_c[slot]), k.w.o_c + slot * D);
+    for (int p = 0; p < kUnits; ++p) {
+      const Parts &u = part[b][p];
+      if (!u.any) continue;
+      any = true;
+      add(own[b][p], first[b][p]);
+      const int64_t slot0 = static_cast<int64_t>(u.cta + 1) * kUnitRows + u.slot;
+      for (int j = 0; j < u.more; j += 4) {  // four loads under way at a time
+        float l[4];
+        float4 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = j + e < u.more;
+          const int64_t slot = slot0 + static_cast<int64_t>(j + e) * kUnitRows;
+          l[e] = in ? __ldcg(&k.w.lse_c[slot]) : -INFINITY;
+          x[e] = in ? load(k.w.o_c + slot * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add(l[e], x[e]);
+      }
+    }
+    if (!any) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (live) {
+      T *dst = reinterpret_cast<T *>(k.a.out) + row[b] * k.a.o_row + qh[b] * k.a.o_head + 4 * lane;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(acc.x * inv, acc.y * inv),
+                                                   Weights<T>::pack(acc.z * inv, acc.w * inv));
+    }
+    if (k.a.lse && lane == 0) {
+      k.a.lse[rh[b]] = sum == 0.f ? -INFINITY : (top[b] + log2f(sum)) * 0.69314718055994531f;
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (live) {
-    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(Weights<T>::pack(acc.x * inv, acc.y * inv), Weights<T>::pack(acc.z * inv, acc.w * inv));
+}
+
+__device__ __forceinline__ Entry load_entry(const AttnWorkspace &w, int e) {
+  const int4 *p = reinterpret_cast<const int4 *>(&w.entries[e]);
+  const int4 a = __ldcg(p), b = __ldcg(p + 1);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+constexpr int kJoinBatch = 4;
+
+// Without shared parts only the units that a CTA's range cuts have parts to
+// join: CTA (c, chunk) takes 32 rows of the unit that the boundary between
+// CTAs c and c + 1 is the first to cut (CTA c + 1 left its record), four rows
+// a warp.
+template <typename T>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+join_cut_units_kernel(const __grid_constant__ KernelArgs k) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int cta = blockIdx.x;
+  const int4 *cut = reinterpret_cast<const int4 *>(&k.w.cuts[cta + 1]);
+  const int4 c = __ldcg(cut);  // row0, rows, head, more
+  const int rt = __ldcg(cut + 1).x;
+  const int slot0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * kJoinBatch;
+  if (slot0 >= c.y) return;
+  Parts part[kJoinBatch][1];
+  int64_t rh[kJoinBatch];
+  int row[kJoinBatch], qh[kJoinBatch];
+#pragma unroll
+  for (int b = 0; b < kJoinBatch; ++b) {
+    const int slot = slot0 + b, r = rt * kUnitRows + slot, i = r / k.rep;
+    row[b] = c.x + i;
+    qh[b] = c.z * k.rep + r - i * k.rep;
+    rh[b] = static_cast<int64_t>(row[b]) * k.a.q_heads + qh[b];
+    const bool in = slot < c.y;
+    part[b][0] = {in, cta, in ? c.w : 0, slot};
   }
-  if (k.a.lse && lane == 0) {
-    k.a.lse[rh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  join_rows<T, 1, kJoinBatch>(k, part, rh, row, qh);
+}
+
+// With shared parts every row has two units: a CTA per row, four heads a warp
+// at a time.
+template <typename T>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+join_shared_kernel(const __grid_constant__ KernelArgs k) {
+  const int guess = min(static_cast<int>(blockIdx.x) / k.a.b.max_new, k.a.b.S - 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r0 = blockIdx.x;
+  int seq = guess;  // right when every sequence has max_new rows
+  if (k.a.b.row_start && !(k.a.b.row_start[guess] <= r0 && r0 < k.a.b.row_start[guess + 1])) {
+    seq = seq_of_row(k.a.b, r0);
+  }
+  if (seq < 0) return;
+  const int e[2] = {k.w.groups + seq, seq / k.a.b.group};
+  const int per = __ldcg(&k.w.head->per);
+  const Entry t[2] = {load_entry(k.w, e[0]), load_entry(k.w, e[1])};
+  const int tile0[2] = {__ldcg(&k.w.tile0[e[0]]), __ldcg(&k.w.tile0[e[1]])};
+  if (r0 < t[0].row0 || r0 >= t[0].row0 + t[0].tokens) return;  // a sequence out of order
+  for (int q0 = (threadIdx.x >> 5) * kJoinBatch; q0 < k.a.q_heads; q0 += kCombineWarps * kJoinBatch) {
+    Parts part[kJoinBatch][2];
+    int64_t rh[kJoinBatch];
+    int row[kJoinBatch], qh[kJoinBatch];
+#pragma unroll
+    for (int b = 0; b < kJoinBatch; ++b) {
+      row[b] = r0;
+      qh[b] = q0 + b;
+      const int head = qh[b] / k.rep;
+      rh[b] = static_cast<int64_t>(r0) * k.a.q_heads + qh[b];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        part[b][p] = {qh[b] < k.a.q_heads && t[p].tiles > 0 && t[p].tokens > 0, 0, 0, 0};
+        if (!part[b][p].any) continue;
+        const int r = (r0 - t[p].row0) * k.rep + qh[b] - head * k.rep;
+        const int rts = (t[p].tokens * k.rep + kUnitRows - 1) / kUnitRows;
+        const int x0 = tile0[p] + (head * rts + r / kUnitRows) * t[p].tiles;
+        part[b][p].cta = x0 / per;
+        part[b][p].more = (x0 + t[p].tiles - 1) / per - part[b][p].cta;
+        part[b][p].slot = r % kUnitRows;
+      }
+      // a row that one CTA finished alone was written by it
+      if ((t[0].flags & kSolo) && part[b][0].more == 0) part[b][0].any = part[b][1].any = false;
+    }
+    join_rows<T, 2, kJoinBatch>(k, part, rh, row, qh);
   }
 }
 
@@ -1164,10 +1314,10 @@ static bool make_map(CUtensorMap *map, const CacheArgs &c, void *base, int box) 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static cudaError_t launch_pdl(const void *fn, unsigned grid, unsigned block, size_t dyn, void **args,
+static cudaError_t launch_pdl(const void *fn, dim3 grid, unsigned block, size_t dyn, void **args,
                               cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = dyn;
   cfg.stream = st;
@@ -1255,14 +1405,21 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   const bool bf16 = a.c.dtype == SMC_BF16, wide = a.c.head_dim > 64;
   void *args[] = {&k, &map_k, &map_v};
   e = launch_pdl(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
-                 ctas, kAttnThreads, kAttnSmem, args, st);
+                 dim3(ctas), kAttnThreads, kAttnSmem, args, st);
   if (e != cudaSuccess) return e;
-  const int64_t units = static_cast<int64_t>(a.b.rows) * a.q_heads;
   void *cargs[] = {&k};
-  return launch_pdl(bf16 ? reinterpret_cast<const void *>(combine_kernel<__nv_bfloat16>)
-                         : reinterpret_cast<const void *>(combine_kernel<__half>),
-                    static_cast<unsigned>((units + kCombineThreads / 32 - 1) / (kCombineThreads / 32)),
-                    kCombineThreads, 0, cargs, st);
+  if (k.w.groups) {
+    return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_shared_kernel<__nv_bfloat16>)
+                           : reinterpret_cast<const void *>(join_shared_kernel<__half>),
+                      dim3(a.b.rows), 32 * kCombineWarps, 0, cargs, st);
+  }
+  if (ctas == 1) return cudaSuccess;  // nothing is cut
+  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * k.rep;
+  constexpr int kChunk = kCombineWarps * kJoinBatch;
+  const int chunks = static_cast<int>(((most_rows < kUnitRows ? most_rows : kUnitRows) + kChunk - 1) / kChunk);
+  return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
+                         : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
+                    dim3(ctas - 1, chunks), 32 * kCombineWarps, 0, cargs, st);
 }
 
 }  // namespace smcsd

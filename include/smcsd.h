@@ -450,7 +450,7 @@ size_t smc_cache_workspace_bytes(const smc_cache *cache, const smc_batch *batch,
 
 /* Arguments of smc_tree_attention that are not device arrays. */
 typedef struct {
-  int32_t q_heads;          /* a multiple of cache->kv_heads                     */
+  int32_t q_heads;          /* a multiple of cache->kv_heads, at most 128 times it */
   int32_t mask_words;       /* 32-bit words per mask row (0 without a mask)      */
   float scale;              /* finite, > 0                                       */
   int32_t reserved;         /* must be 0                                         */

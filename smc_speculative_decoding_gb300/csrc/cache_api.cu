@@ -54,6 +54,7 @@ static BatchArgs to_batch(const smc_batch *b) {
 static bool attention_shape_ok(const smc_cache *c, const smc_batch *b, int q_heads) {
   return q_heads >= 1 && q_heads <= (1 << 16) && q_heads % c->kv_heads == 0 &&
          static_cast<double>(b->rows) * q_heads < 2147483647.0 &&
+         q_heads / c->kv_heads <= 128 &&
          static_cast<double>(b->max_new) * b->group * (q_heads / c->kv_heads) < 1073741824.0;
 }
 
@@ -102,6 +103,8 @@ int32_t smc_tree_attention(const smc_attn_params *p, const smc_cache *cache, int
         stride_of(p->out_head_stride, p->q_heads)}) {
     if (stride < 0 || stride % 8 != 0) return SMC_ERR_ARG;
   }
+  // an axis is not a broadcast one
+  if (stride_of(p->q_row_stride, rows) == 0 || stride_of(p->q_head_stride, p->q_heads) == 0) return SMC_ERR_ARG;
   if (!multiple_of_16(c.k) || !multiple_of_16(c.v) || !multiple_of_16(q) || !multiple_of_16(out)) {
     return SMC_ERR_ARG;
   }
@@ -117,8 +120,8 @@ int32_t smc_tree_attention(const smc_attn_params *p, const smc_cache *cache, int
   a.q_heads = p->q_heads;
   a.mask_words = p->mask_words;
   a.scale = p->scale;
-  a.q_row = p->q_row_stride;
-  a.q_head = p->q_head_stride;
+  a.q_row = stride_of(p->q_row_stride, rows);
+  a.q_head = stride_of(p->q_head_stride, p->q_heads);
   a.o_row = p->out_row_stride;
   a.o_head = p->out_head_stride;
   a.status = static_cast<unsigned *>(workspace);

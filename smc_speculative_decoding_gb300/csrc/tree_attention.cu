@@ -20,8 +20,9 @@ namespace smcsd {
 // Work.  An *entry* is a run of consecutive rows and a range of tokens that
 // they all attend: the own part of one sequence, or the part that the
 // sequences of a prompt share (their leading equal table slots).  Per key
-// head and per 256 rows (new token x query head of the key head) an entry
-// makes one *unit* of ceil(tokens / 64) tiles.  The units' tiles form one
+// head and per two row tiles an entry makes one *unit* of ceil(tokens / 64)
+// tiles.  A row tile is floor(128 / rep) new tokens times the rep query heads
+// of the key head, so a tile starts on a token.  The units' tiles form one
 // line; CTA c takes tiles [c * per, (c + 1) * per) of it, so ragged lengths
 // load every SM alike.  A unit's first tiles' CTA owns the unit's result;
 // every later CTA of the unit has exactly one such continuation (its first
@@ -29,7 +30,7 @@ namespace smcsd {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;         // tokens per tile
 constexpr int kRows = 128;        // rows of a tensor-core tile
-constexpr int kUnitRows = 256;    // rows per unit: two tensor-core tiles of 128
+constexpr int kUnitRows = 256;    // most rows of a unit: two tensor-core tiles of 128
 constexpr int kMaxCtas = 192;     // slots for continuations
 constexpr int kPlanThreads = 1024;
 constexpr uint32_t kWaitPolls = 1u << 17;  // each may suspend up to 20 us
@@ -48,7 +49,7 @@ constexpr int kShared = 1, kSolo = 2;  // a shared part; the rows have no other 
 // The unit that the boundary before a CTA is the first to cut.
 struct Cut {
   int row0, rows, head, more;  // first row, rows of the unit (0: no such unit), key head,
-  int rt, pad[3];              // continuations, row tile
+  int flags, pad[3];           // continuations; the entry's flags
 };
 
 struct PlanHeader {
@@ -106,7 +107,9 @@ size_t attention_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_h
 struct KernelArgs {
   AttnArgs a;
   AttnWorkspace w;
-  int rep;      // query heads per key head
+  int rep;      // query heads per key head, at most 128
+  int tile_tokens;  // new tokens of a row tile: floor(128 / rep)
+  int q_box;    // new tokens of a copied box of Q
   int box;      // tokens per copied box
   uint32_t magic, shift;  // t / block_size == umulhi(t, magic) >> shift
   float sc;     // scale * log2 e
@@ -136,11 +139,16 @@ __device__ int block_scan_excl(int v, int *warps, int *total) {
   return before + incl - v;
 }
 
+// Units of one key head: row tiles of an entry, two by two.
+__device__ __forceinline__ int unit_tiles(const KernelArgs &k, int tokens) {
+  return (tokens + 2 * k.tile_tokens - 1) / (2 * k.tile_tokens);
+}
+
 __device__ __forceinline__ int entry_tiles(const KernelArgs &k, int tokens, int kv0, int kv1,
                                            int *per_unit) {
   *per_unit = (kv1 - kv0 + kTile - 1) / kTile;
   if (tokens <= 0 || kv1 <= kv0) return 0;
-  return *per_unit * k.a.c.kv_heads * ((tokens * k.rep + kUnitRows - 1) / kUnitRows);
+  return *per_unit * k.a.c.kv_heads * unit_tiles(k, tokens);
 }
 
 __device__ int make_entry(const KernelArgs &k, int e, Entry *out) {
@@ -357,6 +365,14 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
       "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(token), "r"(head), "r"(block)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int d, int head,
+                                            int row, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(head), "r"(row)
+      : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(take ? 16 : 0)
@@ -403,40 +419,59 @@ constexpr float kLazy = 8.f;
 
 // ---------------------------------------------------------------------------
 // attention_kernel.  Warps 0-3 and 4-7: two softmax groups (thread = row of a
-// 128-row tile); warps 8 and 9: the threads that issue either group's matrix
-// products; warps 10 and 11: the copies of K and of V.  Shared memory: Q (two row tiles) and a ring of K and V tiles.
-// Tensor memory: two score buffers of 64 columns per group (the weights
-// overwrite the scores) and either group's accumulator.
-//   Units of up to 128 rows: the groups take alternate tiles of the unit, each
+// row tile); warps 8 and 9: the threads that issue either group's matrix
+// products; warp 10 finds the CTA's segments (parts of units) for all and
+// copies K; warp 11 copies Q and V.  Shared memory: two Q tiles and a ring
+// each of K and V tiles.  Tensor memory: two score buffers of 64 columns per
+// group (the weights overwrite the scores) and either group's accumulator.
+//   Units of one row tile: the groups take alternate tiles of the unit, each
 //   with its own running maximum, sum and accumulator, joined at the end.
-//   Larger units: each group has its own 128 rows; a tile of K and V serves
+//   Units of two: each group has its own row tile; a tile of K and V serves
 //   both.
-// Scores run two of a group's tiles ahead of its products with V, so that
-// neither a group nor its ring waits for a product's latency: K tiles leave
-// their ring as they come, and only V waits for its weights.  K and V have a
-// ring each, so that each slot's barriers are followed by one copying warp.
+// Scores run two of a group's tiles ahead of its products with V, and into the
+// next segment while the last one's result is written, so that neither a group
+// nor its ring waits for a product's latency: K tiles leave their ring as they
+// come, and only V waits for its weights.
+//   Every wait is on a barrier all of whose turns the waiting thread follows:
+// a slot is one group's for good (see Geometry), and before both groups use a
+// tile, all earlier tiles are done with.
 // ---------------------------------------------------------------------------
 constexpr int kAttnThreads = 384;
 constexpr int kRingBytes = 160 * 1024;
+constexpr int kSegs = 4;  // segments found ahead
 
 template <int kHalves>  // 64-element panels of the head dim
 struct Geometry {
   static constexpr int kTileBytes = kHalves * kTile * 128;
-  // Slots of K and of V: V waits for its weights, K does not.  Both even: with
-  // alternate tiles a slot is then always the same group's, whose waits see
-  // every turn of its barriers (a wait two turns behind would pass at once).
+  // Slots of K and of V: V waits for its weights, K does not.  Tile i of a
+  // segment takes one of group i % 2's half of the slots (the even or the odd
+  // ones) in turn.
   static constexpr int kSlotsK = 4 * (2 / kHalves), kSlotsV = 6 * (2 / kHalves);
   static constexpr int kQTile = kHalves * kRows * 128;
   static constexpr int kQBytes = 2 * kQTile;
   static constexpr int kTail = kQBytes + kRingBytes;
 };
 
+struct Seg {
+  int row0, rows;  // first row of the unit, rows of it
+  int i0;          // new token of the first row (own parts)
+  int seq, head;
+  int t0, n;       // first token, tiles
+  int ctx, kv1;    // tokens before ctx are seen by all; end of the entry's tokens
+  int n_new;       // new tokens of the sequence (own parts)
+  int flags, pad;
+};
+constexpr int kWhole = 4, kBase = 8, kEnd = 16;  // with kShared: final result, first tiles, none left
+
 struct AttnTail {
   uint64_t full[2][12], empty[2][12];  // K, V
-  uint64_t q_full, scores[2][2], weights[2][2], added[2], o_full[2], stats, drained[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t q_full[2], q_free[2], scores[2][2], weights[2][2], added[2], o_full[2], o_free, stats;
+  uint64_t drained[2];
+  Seg seg[kSegs];
   float2 stat[2][kRows];  // either group's (max, sum) of a row
   uint32_t tmem;
-  unsigned nonfinite;     // segment number (from 1) of the last one with a non-finite value
+  unsigned nonfinite[2];  // segment number (from 1) of the last odd or even one with such a value
   volatile int abort;
 };
 
@@ -447,6 +482,7 @@ struct Walk {
   int base;       // tile0[e]
   int head, rt;   // unit
   int i0, n;      // tiles [i0, i0 + n) of the unit
+  int tokens0;    // new token of the unit's first row
   int rows;       // rows of the unit
   __device__ __forceinline__ void start(const AttnWorkspace &w) {
     const int per = __ldcg(&w.head->per), total = __ldcg(&w.head->total);
@@ -469,34 +505,44 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const KernelArgs &k) {
     if (x >= x1) return false;
-    const int total_rows = t.tokens * k.rep;
-    int rts = (total_rows + kUnitRows - 1) / kUnitRows;
+    int rts = unit_tiles(k, t.tokens);
     while (t.tiles * rts * k.a.c.kv_heads <= x - base || t.tokens <= 0) {
       ++e;
       load(k.w);
-      rts = (t.tokens * k.rep + kUnitRows - 1) / kUnitRows;
+      rts = unit_tiles(k, t.tokens);
     }
     const int local = x - base, u = local / t.tiles;
     i0 = local - u * t.tiles;
     n = min(t.tiles - i0, x1 - x);
     head = u / rts;
     rt = u - head * rts;
-    rows = min(t.tokens * k.rep - rt * kUnitRows, kUnitRows);
+    tokens0 = rt * 2 * k.tile_tokens;
+    rows = min(t.tokens - tokens0, 2 * k.tile_tokens) * k.rep;
     x += n;
     return true;
   }
 };
 
-// The slot of a CTA's tile number `t` in either ring, and the parity of the
-// slot's barriers for it.
+// A ring's slots, tile by tile: the slot of tile i of the current segment, and
+// the parity of the slot's barriers for it.
 template <int kSlots>
-struct Slot {
-  uint32_t at, parity;
-  __device__ __forceinline__ explicit Slot(uint32_t t) {
-    static_assert(kSlots % 2 == 0, "see Geometry");
-    const uint32_t lap = t / kSlots;
-    at = t - lap * kSlots;
-    parity = lap & 1u;
+struct Ring {
+  static constexpr uint32_t kHalf = kSlots / 2;
+  uint32_t done[2] = {0, 0};  // tiles of either half before the segment
+  uint32_t used[2] = {0, 0};  // tiles of either half that were begun (copying warps)
+  uint32_t at, parity, turn;
+  __device__ __forceinline__ void tile(int i) {
+    const uint32_t half = i & 1u, c = (half ? done[1] : done[0]) + (i >> 1);
+    turn = c / kHalf;
+    at = half + 2 * (c - turn * kHalf);
+    parity = turn & 1u;
+  }
+  __device__ __forceinline__ void begin(int i) {
+    if (i & 1) used[1] = done[1] + (i >> 1) + 1; else used[0] = done[0] + (i >> 1) + 1;
+  }
+  __device__ __forceinline__ void next_segment(int n) {
+    done[0] += (n + 1) >> 1;
+    done[1] += n >> 1;
   }
 };
 
@@ -583,119 +629,122 @@ __device__ __noinline__ void patch_nonfinite(const KernelArgs &k, int seq, int c
   }
 }
 
-// One copying warp: every tile of the CTA's segments, of K or of V, into its
-// ring.
+// Segment number `seg` (from 0) as warp 10 left it.  False when the wait gave
+// up or no segment is left.
+__device__ __forceinline__ bool take_segment(AttnTail *s, uint32_t seg, Seg *to, unsigned *status) {
+  if (!warp_wait(s, &s->seg_full[seg % kSegs], seg / kSegs & 1u, status)) return false;
+  const int4 *from = reinterpret_cast<const int4 *>(&s->seg[seg % kSegs]);
+  const int4 a = from[0], b = from[1], c = from[2];
+  *to = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  return !(to->flags & kEnd);
+}
+
+// Copies the tiles of one segment, of K or of V, into their ring.
 template <int kHalves, bool kTma, int kSlots>
-__device__ __forceinline__ void copy_tiles(const KernelArgs &k, const CUtensorMap *map,
-                                           const char *src, char *ring, uint64_t *full,
-                                           uint64_t *empty, AttnTail *s) {
+__device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMap *map, const char *src,
+                                           char *slots, uint64_t *full, uint64_t *empty, AttnTail *s,
+                                           Ring<kSlots> &ring, const Seg &seg, bool pair,
+                                           unsigned *bits) {
   using G = Geometry<kHalves>;
   const int lane = threadIdx.x & 31;
-  const int D = k.a.c.head_dim;
-  Walk w;
-  w.start(k.w);
   const CacheArgs &c = k.a.c;
   const uint32_t bs = c.block_size;
-  uint32_t tiles = 0, filled = 0;  // tiles of the CTA before the segment, tiles begun
-  bool ok = true;
-  unsigned bits = 0;
+  const int32_t *table = k.a.b.tables + static_cast<int64_t>(seg.seq) * k.a.b.T;
+  const int end = min(seg.t0 + seg.n * kTile, seg.kv1), per_tile = kTile / k.box;
   // (block, token in it) of token t of the sequence
-  auto place = [&](const int32_t *table, uint32_t t) {
+  auto place = [&](uint32_t t) {
     const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
     int id = table[b];
     if (id < 0 || id >= c.blocks) {
-      bits |= SMC_DEV_BAD_BLOCK;
+      *bits |= SMC_DEV_BAD_BLOCK;
       id = 0;
     }
     return make_int2(id, t - b * bs);
   };
-  while (ok && w.next(k)) {
-    const bool pair = w.rows > kRows;
-    const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.t.seq) * k.a.b.T;
-    const int tok0 = w.t.kv0 + w.i0 * kTile, tok1 = min(tok0 + w.n * kTile, w.t.kv1);
-    const int per_tile = kTile / k.box;
-    int2 ahead = make_int2(0, 0);  // the place of box `from` + lane
-    int from = -64;
-    int unseen = -1;  // the slot whose element copies may still be under way
-    for (int i = 0; i < w.n; ++i) {
-      const int t0 = tok0 + i * kTile, t1 = min(t0 + kTile, tok1);
-      const Slot<kSlots> slot(tiles + i);
-      char *dst = ring + slot.at * G::kTileBytes;
-      if constexpr (kTma) {
-        const int first = i * per_tile;
-        if (first + per_tile > from + 32) {
-          from = first;
-          const int t = t0 + lane * k.box;
-          if (t < tok1) ahead = place(table, t);
-        }
-      }
-      if (tiles + i >= kSlots &&
-          !(ok = warp_wait(s, &empty[slot.at], slot.parity ^ 1u, k.a.status))) {
-        break;
-      }
-      if (!pair) warp_arrive(&empty[slot.at], lane);  // one group uses it
-      ++filled;
-      if constexpr (kTma) {
-        const int boxes = (t1 - t0 + k.box - 1) / k.box;
-        const int at = i * per_tile - from;
-        if (elect_one()) mbar_arrive_expect_tx(&full[slot.at], boxes * kHalves * k.box * 128);
-        __syncwarp();
-        for (int b = 0; b < boxes; ++b) {
-          const int block = __shfl_sync(0xffffffffu, ahead.x, at + b);
-          const int token = __shfl_sync(0xffffffffu, ahead.y, at + b);
-          if (elect_one()) {
-#pragma unroll
-            for (int half = 0; half < kHalves; ++half) {
-              tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token,
-                          w.head, block, &full[slot.at]);
-            }
-          }
-          __syncwarp();
-        }
-      } else {
-        const uint32_t d0 = smem_addr(dst);
-        constexpr int kChunks = 8 * kHalves;
-        const int ch = lane % kChunks;
-        const bool take = ch * 8 < D;
-        for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
-          const int2 at_block = place(table, t0 + r);
-          const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
-                              w.head * c.head_stride + (take ? ch * 8 : 0);
-          cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                     src + off * 2, take);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (unseen >= 0) {  // the tile before this one has arrived
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          fence_proxy_async_smem();
-          warp_arrive(&full[unseen], lane);
-        }
-        unseen = slot.at;
+  int2 ahead = make_int2(0, 0);  // the place of box `from` + lane
+  int from = -64;
+  int unseen = -1;  // the slot whose element copies may still be under way
+  bool ok = true;
+  for (int i = 0; i < seg.n; ++i) {
+    const int t0 = seg.t0 + i * kTile, t1 = min(t0 + kTile, end);
+    ring.tile(i);
+    char *dst = slots + ring.at * G::kTileBytes;
+    if constexpr (kTma) {
+      if ((i + 1) * per_tile > from + 32) {
+        from = i * per_tile;
+        const int t = t0 + lane * k.box;
+        if (t < end) ahead = place(t);
       }
     }
-    if constexpr (!kTma) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (unseen >= 0) {
+    if (ring.turn > 0 && !(ok = warp_wait(s, &empty[ring.at], ring.parity ^ 1u, k.a.status))) break;
+    if (!pair) warp_arrive(&empty[ring.at], lane);  // one group uses it
+    ring.begin(i);
+    if constexpr (kTma) {
+      const int boxes = (t1 - t0 + k.box - 1) / k.box;
+      const int at = i * per_tile - from;
+      if (elect_one()) mbar_arrive_expect_tx(&full[ring.at], boxes * kHalves * k.box * 128);
+      __syncwarp();
+      for (int b = 0; b < boxes; ++b) {
+        const int block = __shfl_sync(0xffffffffu, ahead.x, at + b);
+        const int token = __shfl_sync(0xffffffffu, ahead.y, at + b);
+        if (elect_one()) {
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token, seg.head,
+                        block, &full[ring.at]);
+          }
+        }
+        __syncwarp();
+      }
+    } else {
+      const uint32_t d0 = smem_addr(dst);
+      constexpr int kChunks = 8 * kHalves;
+      const int ch = lane % kChunks;
+      const bool take = ch * 8 < c.head_dim;
+      for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
+        const int2 at_block = place(t0 + r);
+        const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
+                            seg.head * c.head_stride + (take ? ch * 8 : 0);
+        cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   src + off * 2, take);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (unseen >= 0) {  // the tile before this one has arrived
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         fence_proxy_async_smem();
         warp_arrive(&full[unseen], lane);
       }
-    }
-    tiles += w.n;
-  }
-  if constexpr (kTma) {
-    // every copy has landed before the CTA ends, also when it gave up
-    for (uint32_t t = filled > kSlots ? filled - kSlots : 0; t < filled; ++t) {
-      const Slot<kSlots> slot(t);
-      mbar_wait(&full[slot.at], slot.parity, kWaitPolls);
+      unseen = ring.at;
     }
   }
-  if (bits) raise_status(k.a.status, bits);
+  if constexpr (!kTma) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (unseen >= 0) {
+      fence_proxy_async_smem();
+      warp_arrive(&full[unseen], lane);
+    }
+  }
+  return ok;
+}
+
+// Waits until the last copy into each of a ring's slots has landed: a CTA that
+// gave up may have left some under way.
+template <int kSlots>
+__device__ __forceinline__ void wait_landed(uint64_t *full, const Ring<kSlots> &ring) {
+  constexpr uint32_t kHalf = Ring<kSlots>::kHalf;
+  for (uint32_t half = 0; half < 2; ++half) {
+    const uint32_t end = half ? ring.used[1] : ring.used[0];
+    for (uint32_t c = end > kHalf ? end - kHalf : 0; c < end; ++c) {
+      const uint32_t turn = c / kHalf;
+      mbar_wait(&full[half + 2 * (c - turn * kHalf)], turn & 1u, 1u << 12);
+    }
+  }
 }
 
 template <typename T, int kHalves, bool kTma>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v) {
+attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ CUtensorMap map_q,
+                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using G = Geometry<kHalves>;
   using Wt = Weights<T>;
   extern __shared__ __align__(1024) char smem[];
@@ -704,6 +753,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   AttnTail *const s = reinterpret_cast<AttnTail *>(smem + G::kTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = k.a.c.head_dim;
+  const int tile_rows = k.tile_tokens * k.rep;
+  unsigned *const status = k.a.status;
 
   if (tid == 0) {
     for (int v = 0; v < 2; ++v) {
@@ -712,8 +763,13 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         mbar_init(&s->empty[v][i], 2);  // both groups, or one and the copying warp
       }
     }
-    mbar_init(&s->q_full, 8);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&s->seg_full[i], 1);
+      mbar_init(&s->seg_empty[i], 11);  // every warp but the one that fills it
+    }
     for (int g = 0; g < 2; ++g) {
+      mbar_init(&s->q_full[g], 1);
+      mbar_init(&s->q_free[g], 2);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s->scores[g][b], 1);
         mbar_init(&s->weights[g][b], 4);
@@ -722,8 +778,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       mbar_init(&s->o_full[g], 1);
       mbar_init(&s->drained[g], 1);
     }
+    mbar_init(&s->o_free, 8);
     mbar_init(&s->stats, 8);
-    s->nonfinite = 0;
+    s->nonfinite[0] = s->nonfinite[1] = 0;
     s->abort = (smem_addr(smem) & 1023u) != 0;  // the swizzle counts from 1 KB boundaries
     mbar_init_fence();
   }
@@ -736,71 +793,38 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (s->abort) {
-    if (tid == 0) raise_status(k.a.status, SMC_DEV_TIMEOUT);
+    if (tid == 0) raise_status(status, SMC_DEV_TIMEOUT);
   } else if (warp < 8) {
     // ---- softmax groups ---------------------------------------------------
     const int g = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;  // row of the group's tile
+    const int r_tok = r / k.rep, r_head = r - r_tok * k.rep;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t t_o = tmem + lanes + 256 + g * 128;
-    Walk w;
-    w.start(k.w);
-    uint32_t seg = 0, tiles = 0, turn = 0;  // tiles of the CTA, of this group so far
-    bool ok = true, more = w.next(k);
-    if (tid == 0 && !k.w.groups) {
-      const int per = __ldcg(&k.w.head->per);
-      const bool cut = more && w.i0 > 0 && w.i0 <= per;
-      const int first = static_cast<int>(blockIdx.x) * per;
-      int4 *to = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
-      to[0] = cut ? make_int4(w.t.row0, w.rows, w.head,
-                              (first - w.i0 + w.t.tiles - 1) / per - static_cast<int>(blockIdx.x) + 1)
-                  : make_int4(0, 0, 0, 0);
-      to[1] = make_int4(w.rt, 0, 0, 0);
-    }
-    while (ok && more) {
+    uint32_t seg = 0, turn = 0;  // segments, and tiles of this group so far
+    Ring<G::kSlotsV> ring;
+    bool ok = true;
+    Seg w;
+    while (ok && take_segment(s, seg, &w, status)) {
+      warp_arrive(&s->seg_empty[seg % kSegs], lane);
       ++seg;
-      const bool pair = w.rows > kRows;
-      const int row_in_unit = pair ? g * kRows + r : r;
-      const bool live = row_in_unit < w.rows;
-      const bool warp_live = (pair ? g * kRows : 0) + wq * 32 < w.rows;
-      const int r_all = w.rt * kUnitRows + row_in_unit;
-      const int i_new = live ? r_all / k.rep : 0;  // new token of a sequence's own part
-      const int row = w.t.row0 + i_new;
-      const int qh = w.head * k.rep + (live ? r_all - i_new * k.rep : 0);
-      {  // Q: a row of either tile per thread; with one tile the groups split its columns
-        const T *q = reinterpret_cast<const T *>(k.a.q) + row * k.a.q_row + qh * k.a.q_head;
-        char *dst = s_q + (pair ? g * G::kQTile : 0) + r * 128;
-        const int c0 = pair ? 0 : g * 4 * kHalves, c1 = pair ? 8 * kHalves : c0 + 4 * kHalves;
-        if (warp_live) {
-          for (int c = c0; c < c1; c += 4 * kHalves) {  // loads first: one latency a batch
-            uint4 x[4 * kHalves];
-#pragma unroll
-            for (int e = 0; e < 4 * kHalves; ++e) {
-              x[e] = make_uint4(0, 0, 0, 0);
-              if (live && (c + e) * 8 < D) x[e] = *reinterpret_cast<const uint4 *>(q + (c + e) * 8);
-            }
-#pragma unroll
-            for (int e = 0; e < 4 * kHalves; ++e) {
-              *reinterpret_cast<uint4 *>(dst + ((c + e) >> 3) * (kRows * 128) +
-                                         ((((c + e) & 7) ^ (r & 7)) << 4)) = x[e];
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        warp_arrive(&s->q_full, lane);
-      }
-      Walk ahead = w;  // found while the first scores are under way
-      more = ahead.next(k);
+      const bool pair = w.rows > tile_rows;
+      const int rows = pair ? (g == 0 ? tile_rows : w.rows - tile_rows) : w.rows;  // of this group
+      const bool live = r < rows, warp_live = wq * 32 < rows;
+      const int tok = (pair && g ? k.tile_tokens : 0) + (live ? r_tok : 0);
+      const int i_new = w.i0 + tok;  // new token of a sequence's own part
+      const int row = w.row0 + tok, qh = w.head * k.rep + (live ? r_head : 0);
+      const bool own = !(w.flags & kShared);
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
-        const int t0 = w.t.kv0 + (w.i0 + i) * kTile;
+        const int t0 = w.t0 + i * kTile;
         const uint32_t buf = turn & 1u;
         const uint32_t t_s = tmem + lanes + g * 128 + buf * 64;
-        if (!(ok = warp_wait(s, &s->scores[g][buf], turn >> 1 & 1u, k.a.status))) break;
+        if (!(ok = warp_wait(s, &s->scores[g][buf], turn >> 1 & 1u, status))) break;
         ++turn;
         tc_fence_after();
-        const bool edge = t0 + kTile > w.t.ctx && !(w.t.flags & kShared);
+        const bool edge = own && t0 + kTile > w.ctx;
         if (warp_live) {
           uint32_t z[64];
           __syncwarp();
@@ -813,8 +837,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
                 k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              const uint32_t see = view_bits(mask, k.a.mask_words, i_new, w.t.tokens,
-                                             t0 + 32 * b - w.t.ctx);
+              const uint32_t see = view_bits(mask, k.a.mask_words, i_new, w.n_new, t0 + 32 * b - w.ctx);
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
                 if (!(see >> c & 1u)) z[32 * b + c] = 0xff800000u;
@@ -835,12 +858,12 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
 #pragma unroll
           for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[60 + b]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k.sc;
-          const bool rise = top > m + kLazy || (first && top > m);
+          const bool rise = top > m + kLazy;
           if (first) {
             m = top;
           } else if (__any_sync(0xffffffffu, rise)) {
             // the product with V of the group's last tile (number turn - 2) is done
-            if (!(ok = warp_wait(s, &s->added[g], turn & 1u, k.a.status))) break;
+            if (!(ok = warp_wait(s, &s->added[g], turn & 1u, status))) break;
             tc_fence_after();
             const float mn = rise ? top : m;
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
@@ -883,12 +906,12 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         if (edge) {
           // the tile reaches past the committed tokens: V rows past the last
           // token become 0 (they may hold anything), and so do infinities
-          // and NaN of new tokens, which add_nonfinite puts back
-          const Slot<G::kSlotsV> slot(tiles + i);
-          if (!(ok = warp_wait(s, &s->full[1][slot.at], slot.parity, k.a.status))) break;
+          // and NaN of new tokens, which patch_nonfinite puts back
+          ring.tile(i);
+          if (!(ok = warp_wait(s, &s->full[1][ring.at], ring.parity, status))) break;
           const int t = t0 + (r & (kTile - 1));
-          if (t >= w.t.ctx) {
-            char *v = s_v + slot.at * G::kTileBytes + (r & (kTile - 1)) * 128;
+          if (t >= w.ctx) {
+            char *v = s_v + ring.at * G::kTileBytes + (r & (kTile - 1)) * 128;
             bool found = false;
             const int c0 = (r / kTile) * 4 * kHalves;
 #pragma unroll 4
@@ -896,7 +919,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
               uint4 *at16 = reinterpret_cast<uint4 *>(v + (c >> 3) * (kTile * 128) +
                                                       (((c + lane) & 7) << 4));
               uint4 x = make_uint4(0, 0, 0, 0);
-              bool change = t >= w.t.kv1;
+              bool change = t >= w.kv1;
               if (!change) {
                 x = *at16;
                 uint32_t *words = reinterpret_cast<uint32_t *>(&x);
@@ -911,7 +934,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
               }
               if (change) *at16 = x;
             }
-            if (found) s->nonfinite = seg;
+            if (found) s->nonfinite[seg & 1u] = seg;
           }
           fence_proxy_async_smem();
         }
@@ -919,15 +942,16 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         warp_arrive(&s->weights[g][buf], lane);
       }
       if (!ok) break;
+      ring.next_segment(w.n);
       // ---- the unit's result -----------------------------------------------
-      s->stat[g][r] = make_float2(m, l);
-      warp_arrive(&s->stats, lane);
-      ok = warp_wait(s, &s->o_full[g], (seg - 1) & 1u, k.a.status) &&
-           (pair || (warp_wait(s, &s->o_full[1 - g], (seg - 1) & 1u, k.a.status) &&
-                     warp_wait(s, &s->stats, (seg - 1) & 1u, k.a.status)));
+      const uint32_t par = (seg - 1) & 1u;
+      ok = warp_wait(s, &s->o_full[g], par, status) && (pair || warp_wait(s, &s->o_full[1 - g], par, status));
       if (!ok) break;
       tc_fence_after();
-      const bool bad = s->nonfinite == seg;
+      s->stat[g][r] = make_float2(m, l);
+      warp_arrive(&s->stats, lane);
+      if (!pair && !(ok = warp_wait(s, &s->stats, par, status))) break;
+      const bool bad = s->nonfinite[seg & 1u] == seg;
       const bool two = !pair && w.n > 1;
       float f0 = 1.f, f1 = 0.f;
       if (!pair) {
@@ -940,13 +964,12 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       const float inv = l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
       f1 *= inv;
-      const float lse2 = l == 0.f ? -INFINITY : m - Wt::kOffset + log2f(l);
-      const bool whole = (w.t.flags & kSolo) && w.n == w.t.tiles;
+      const bool whole = w.flags & kWhole, base = w.flags & kBase;
+      const int kind = own ? 0 : 1;
       const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
-      const int64_t cont = static_cast<int64_t>(blockIdx.x) * kUnitRows + row_in_unit;
-      const bool base = w.i0 == 0;
-      const int kind = w.t.flags & kShared;
+      const int64_t cont = static_cast<int64_t>(blockIdx.x) * kUnitRows + (pair && g ? tile_rows : 0) + r;
       if (live && (pair || g == 0)) {
+        const float lse2 = l == 0.f ? -INFINITY : m - Wt::kOffset + log2f(l);
         if (whole) {
           if (k.a.lse) k.a.lse[rh] = lse2 * 0.69314718055994531f;
         } else if (base) {
@@ -979,6 +1002,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f0);
           }
+          if (c + 32 >= c_end) {  // the accumulators may be written again
+            tc_fence_before();
+            warp_arrive(&s->o_free, lane);
+          }
           if (live) {
             if (whole) {
 #pragma unroll
@@ -1002,45 +1029,48 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           }
           __syncwarp();
         }
-        tc_fence_before();
       }
+      if (!warp_live || c_begin >= c_end) warp_arrive(&s->o_free, lane);
       if (bad && live) {
-        const int t0 = w.t.kv0 + w.i0 * kTile, t1 = min(t0 + w.n * kTile, w.t.kv1);
+        const int t1 = min(w.t0 + w.n * kTile, w.kv1);
         if (whole) {
-          patch_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0, t1, c_begin, c_end, out);
+          patch_nonfinite<T>(k, w.seq, w.ctx, w.n_new, w.head, row, i_new, w.t0, t1, c_begin, c_end, out);
         } else {
-          patch_nonfinite<T>(k, w.t.seq, w.t.ctx, w.t.tokens, w.head, row, i_new, t0, t1, c_begin, c_end, part);
+          patch_nonfinite<T>(k, w.seq, w.ctx, w.n_new, w.head, row, i_new, w.t0, t1, c_begin, c_end, part);
         }
       }
       __syncwarp();
-      tiles += w.n;
-      w = ahead;
     }
   } else if (warp < 10) {
     // ---- matrix products: warp 8 for group 0, warp 9 for group 1 --------------
     const int g = warp - 8;
-    if (elect_one()) {
-      Walk w;
-      w.start(k.w);
-      const uint32_t id_qk = instr_desc(Wt::kBf16, kTile, false);
-      const uint32_t id_pv = instr_desc(Wt::kBf16, (D + 15) / 16 * 16, true);
-      const int k_steps = (D + 15) / 16;
-      // descriptors of the first bytes; a step's offset is added to the address field
-      const uint32_t q0 = smem_desc(smem_addr(s_q), 16), k0 = smem_desc(smem_addr(s_k), 16);
-      const uint32_t v0 = smem_desc(smem_addr(s_v), kTile * 128);
-      const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
-      uint32_t seg = 0, tiles = 0;
-      uint32_t asked = 0, given = 0;  // tiles of the group so far: scores, products with V
-      bool ok = true;
-      while (ok && w.next(k)) {
-        const bool pair = w.rows > kRows;
-        const int n = w.n, step = pair ? 1 : 2;
-        const uint32_t qa = q0 + (pair ? g * (G::kQTile >> 4) : 0);
-        // scores of tile i, once its K is there
+    const uint32_t id_qk = instr_desc(Wt::kBf16, kTile, false);
+    const uint32_t id_pv = instr_desc(Wt::kBf16, (D + 15) / 16 * 16, true);
+    const int k_steps = (D + 15) / 16;
+    // descriptors of the first bytes; a step's offset is added to the address field
+    const uint32_t q0 = smem_desc(smem_addr(s_q), 16), k0 = smem_desc(smem_addr(s_k), 16);
+    const uint32_t v0 = smem_desc(smem_addr(s_v), kTile * 128);
+    const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
+    uint32_t seg = 0, q_turn = 0;           // segments and Q tiles so far
+    uint32_t asked = 0, given = 0;          // tiles of the group so far: scores, products with V
+    Ring<G::kSlotsK> ring_k;
+    Ring<G::kSlotsV> ring_v;
+    bool ok = true;
+    Seg w;
+    while (ok && take_segment(s, seg, &w, status)) {
+      warp_arrive(&s->seg_empty[seg % kSegs], lane);
+      const bool pair = w.rows > tile_rows;
+      const int n = w.n, step = pair ? 1 : 2, first = pair ? 0 : g;
+      const uint32_t q_at = q_turn + (pair ? g : 0), q_other = q_turn + 1 - g;
+      q_turn += pair ? 2 : 1;
+      if (elect_one()) {
+        const uint32_t qa = q0 + (q_at & 1u) * (G::kQTile >> 4);
+        // scores of tile i, once its K is there; after the last one Q is free
         auto scores = [&](int i) {
-          const Slot<G::kSlotsK> slot(tiles + i);
-          if (!guarded_wait(s, &s->full[0][slot.at], slot.parity, k.a.status)) return false;
-          const uint32_t buf = asked++ & 1u, ka = k0 + slot.at * (G::kTileBytes >> 4);
+          ring_k.tile(i);
+          if (!guarded_wait(s, &s->full[0][ring_k.at], ring_k.parity, status)) return false;
+          const uint32_t buf = asked & 1u, ka = k0 + ring_k.at * (G::kTileBytes >> 4);
+          ++asked;
 #pragma unroll
           for (int c = 0; c < 4 * kHalves; ++c) {
             if (c < k_steps) {
@@ -1049,19 +1079,28 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             }
           }
           tc_commit(&s->scores[g][buf]);
-          tc_commit(&s->empty[0][slot.at]);
+          tc_commit(&s->empty[0][ring_k.at]);
           return true;
         };
-        if (!(ok = guarded_wait(s, &s->q_full, seg & 1u, k.a.status))) break;
-        ++seg;
-        tc_fence_after();
-        const int first = pair ? 0 : g;
-        for (int i = first; ok && i < n && i < 2 * step; i += step) ok = scores(i);
+        auto free_q = [&] {
+          tc_commit(&s->q_free[q_at & 1u]);
+          if (pair) tc_commit(&s->q_free[q_other & 1u]);
+        };
+        // both tiles of a pair, as both issuing threads free both
+        ok = guarded_wait(s, &s->q_full[q_at & 1u], q_at >> 1 & 1u, status) &&
+             (!pair || guarded_wait(s, &s->q_full[q_other & 1u], q_other >> 1 & 1u, status));
+        if (ok) {
+          tc_fence_after();
+          for (int i = first; ok && i < n && i < 2 * step; i += step) ok = scores(i);
+          if (first + 2 * step >= n) free_q();
+        }
+        // the last segment's result has been read
+        if (ok && seg > 0) ok = guarded_wait(s, &s->o_free, (seg - 1) & 1u, status);
         for (int i = first; ok && i < n; i += step) {
-          const Slot<G::kSlotsV> slot(tiles + i);
-          const uint32_t buf = given & 1u, va = v0 + slot.at * (G::kTileBytes >> 4);
-          ok = guarded_wait(s, &s->full[1][slot.at], slot.parity, k.a.status) &&
-               guarded_wait(s, &s->weights[g][buf], given >> 1 & 1u, k.a.status);
+          ring_v.tile(i);
+          const uint32_t buf = given & 1u, va = v0 + ring_v.at * (G::kTileBytes >> 4);
+          ok = guarded_wait(s, &s->full[1][ring_v.at], ring_v.parity, status) &&
+               guarded_wait(s, &s->weights[g][buf], given >> 1 & 1u, status);
           if (!ok) break;
           ++given;
           tc_fence_after();
@@ -1070,24 +1109,107 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             mma_ts(t_o, t_s + buf * 64 + c * 8, va + c * 2048 / 16, id_pv, i >= step || c > 0);
           }
           tc_commit(&s->added[g]);
-          tc_commit(&s->empty[1][slot.at]);
-          if (i + 2 * step < n) ok = scores(i + 2 * step);
+          tc_commit(&s->empty[1][ring_v.at]);
+          if (i + 2 * step < n) {
+            ok = scores(i + 2 * step);
+            if (i + 3 * step >= n) free_q();
+          }
         }
-        if (!ok) break;
-        tc_commit(&s->o_full[g]);
-        tiles += n;
+        if (ok) tc_commit(&s->o_full[g]);
       }
+      // what the elected lane counted, for whichever is elected next
+      ok = __all_sync(0xffffffffu, ok);
+      asked = __reduce_max_sync(0xffffffffu, asked);
+      given = __reduce_max_sync(0xffffffffu, given);
+      ring_k.next_segment(n);
+      ring_v.next_segment(n);
+      ++seg;
+    }
+    if (elect_one()) {
       tc_commit(&s->drained[g]);  // nothing of this CTA runs on when it ends
-      if (!mbar_wait(&s->drained[g], 0, kWaitPolls)) raise_status(k.a.status, SMC_DEV_TIMEOUT);
+      if (!mbar_wait(&s->drained[g], 0, kWaitPolls)) raise_status(status, SMC_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else {
-    // ---- copies -----------------------------------------------------------------
-    if (warp == 10) {
-      copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s);
-    } else {
-      copy_tiles<kHalves, kTma, G::kSlotsV>(k, &map_v, k.a.c.v, s_v, s->full[1], s->empty[1], s);
+  } else if (warp == 10) {
+    // ---- segments, K ------------------------------------------------------------
+    Walk w;
+    w.start(k.w);
+    Ring<G::kSlotsK> ring;
+    unsigned bits = 0;
+    bool ok = true;
+    const int per = __ldcg(&k.w.head->per), first = static_cast<int>(blockIdx.x) * per;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const bool more = w.next(k);
+      if (seg == 0 && lane == 0) {
+        const bool cut = more && w.i0 > 0 && w.i0 <= per;
+        int4 *to = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
+        to[0] = cut ? make_int4(w.t.row0 + w.tokens0, w.rows, w.head,
+                                (first - w.i0 + w.t.tiles - 1) / per - static_cast<int>(blockIdx.x) + 1)
+                    : make_int4(0, 0, 0, 0);
+        to[1] = make_int4(more ? w.t.flags : 0, 0, 0, 0);
+      }
+      Seg t{};
+      t.flags = kEnd;
+      if (more) {
+        t = {w.t.row0 + w.tokens0, w.rows, w.tokens0, w.t.seq, w.head, w.t.kv0 + w.i0 * kTile, w.n,
+             w.t.ctx, w.t.kv1, w.t.tokens, 0, 0};
+        t.flags = (w.t.flags & kShared) | ((w.t.flags & kSolo) && w.n == w.t.tiles ? kWhole : 0) |
+                  (w.i0 == 0 ? kBase : 0);
+      }
+      if (seg >= kSegs &&
+          !(ok = warp_wait(s, &s->seg_empty[seg % kSegs], (seg / kSegs - 1) & 1u, status))) {
+        break;
+      }
+      if (lane == 0) {
+        int4 *to = reinterpret_cast<int4 *>(&s->seg[seg % kSegs]);
+        to[0] = make_int4(t.row0, t.rows, t.i0, t.seq);
+        to[1] = make_int4(t.head, t.t0, t.n, t.ctx);
+        to[2] = make_int4(t.kv1, t.n_new, t.flags, 0);
+      }
+      warp_arrive(&s->seg_full[seg % kSegs], lane);
+      if (!more) break;
+      ok = copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s, ring,
+                                                 t, t.rows > tile_rows, &bits);
+      if (ok) ring.next_segment(t.n);
     }
+    if (kTma && s->abort) wait_landed(s->full[0], ring);
+    if (bits) raise_status(status, bits);
+  } else {
+    // ---- Q and V ----------------------------------------------------------------
+    Ring<G::kSlotsV> ring;
+    uint32_t seg = 0, q_turn = 0;
+    unsigned bits = 0;
+    bool ok = true;
+    Seg w;
+    while (ok && take_segment(s, seg, &w, status)) {
+      warp_arrive(&s->seg_empty[seg % kSegs], lane);
+      ++seg;
+      const bool pair = w.rows > tile_rows;
+      for (int j = 0; ok && j < (pair ? 2 : 1); ++j, ++q_turn) {
+        const uint32_t at = q_turn & 1u;
+        if (q_turn >= 2 && !(ok = warp_wait(s, &s->q_free[at], ((q_turn >> 1) - 1) & 1u, status))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&s->q_full[at], kHalves * k.q_box * k.rep * 128);
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            tma_load_3d(s_q + at * G::kQTile + half * (kRows * 128), &map_q, half * 64, w.head * k.rep,
+                        w.row0 + j * k.tile_tokens, &s->q_full[at]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      ok = copy_tiles<kHalves, kTma, G::kSlotsV>(k, &map_v, k.a.c.v, s_v, s->full[1], s->empty[1], s, ring,
+                                                 w, pair, &bits);
+      if (ok) ring.next_segment(w.n);
+    }
+    if (s->abort) {
+      if (kTma) wait_landed(s->full[1], ring);
+      for (uint32_t q = q_turn > 2 ? q_turn - 2 : 0; q < q_turn; ++q) {
+        mbar_wait(&s->q_full[q & 1u], q >> 1 & 1u, 1u << 12);
+      }
+    }
+    if (bits) raise_status(status, bits);
   }
   __syncthreads();
   if (warp == 8) {
@@ -1100,180 +1222,144 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
 // Joining a row's parts: each part p has a log-sum-exp L_p (log2) and a
 // normalised result o_p;
 //   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
-// The parts of a unit are the owner's and one continuation for each of `more`
-// CTAs from `cta` + 1 on, at row `slot` of their slots.  A warp joins a row.
+// A warp joins a row, with as many parts' loads under way as it can.
 // ---------------------------------------------------------------------------
-constexpr int kCombineWarps = 8;
+constexpr int kJoinWarps = 8;
 
-struct Parts {
-  bool any;
-  int cta, more, slot;
+struct Joined {
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void raise(float to) {
+    const float f = top == -INFINITY ? 0.f : fast_exp2(top - to);
+    sum *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+    top = to;
+  }
+  __device__ __forceinline__ void add(float lse, float4 x) {  // lse <= top
+    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
+    sum += f;
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  __device__ __forceinline__ float lse2() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
+  __device__ __forceinline__ float4 result() const {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
 };
 
-// kUnits units of each of kBatch rows, whose loads are under way together.
-template <typename T, int kUnits, int kBatch>
-__device__ __forceinline__ void join_rows(const KernelArgs &k, const Parts (&part)[kBatch][kUnits],
-                                          const int64_t (&rh)[kBatch], const int (&row)[kBatch],
-                                          const int (&qh)[kBatch]) {
-  const int lane = threadIdx.x & 31;
-  const int D = k.a.c.head_dim;
-  const bool live = 4 * lane < D;
-  auto load = [&](const float *o) {
-    return live ? __ldcg(reinterpret_cast<const float4 *>(o) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  float own[kBatch][kUnits], top[kBatch];
-  float4 first[kBatch][kUnits];
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-#pragma unroll
-    for (int p = 0; p < kUnits; ++p) {
-      own[b][p] = part[b][p].any ? __ldcg(&k.w.lse[p][rh[b]]) : -INFINITY;
-      first[b][p] = part[b][p].any ? load(k.w.o[p] + rh[b] * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    top[b] = -INFINITY;
-#pragma unroll
-    for (int p = 0; p < kUnits; ++p) {
-      top[b] = fmaxf(top[b], own[b][p]);
-      for (int j = lane; j < part[b][p].more; j += 32) {
-        top[b] = fmaxf(top[b], __ldcg(&k.w.lse_c[(part[b][p].cta + 1 + j) * kUnitRows + part[b][p].slot]));
-      }
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
-  }
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    bool any = false;
-    auto add = [&](float lse, float4 x) {
-      const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top[b]);
-      sum += f;
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
-    };
-#pragma unroll
-    for (int p = 0; p < kUnits; ++p) {
-      const Parts &u = part[b][p];
-      if (!u.any) continue;
-      any = true;
-      add(own[b][p], first[b][p]);
-      const int64_t slot0 = static_cast<int64_t>(u.cta + 1) * kUnitRows + u.slot;
-      for (int j = 0; j < u.more; j += 4) {  // four loads under way at a time
-        float l[4];
-        float4 x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool in = j + e < u.more;
-          const int64_t slot = slot0 + static_cast<int64_t>(j + e) * kUnitRows;
-          l[e] = in ? __ldcg(&k.w.lse_c[slot]) : -INFINITY;
-          x[e] = in ? load(k.w.o_c + slot * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) add(l[e], x[e]);
-      }
-    }
-    if (!any) continue;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (live) {
-      T *dst = reinterpret_cast<T *>(k.a.out) + row[b] * k.a.o_row + qh[b] * k.a.o_head + 4 * lane;
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(acc.x * inv, acc.y * inv),
-                                                   Weights<T>::pack(acc.z * inv, acc.w * inv));
-    }
-    if (k.a.lse && lane == 0) {
-      k.a.lse[rh[b]] = sum == 0.f ? -INFINITY : (top[b] + log2f(sum)) * 0.69314718055994531f;
-    }
-  }
+__device__ __forceinline__ float4 load_part(const float *o, bool live) {
+  return live ? __ldcg(reinterpret_cast<const float4 *>(o) + (threadIdx.x & 31))
+              : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-__device__ __forceinline__ Entry load_entry(const AttnWorkspace &w, int e) {
-  const int4 *p = reinterpret_cast<const int4 *>(&w.entries[e]);
-  const int4 a = __ldcg(p), b = __ldcg(p + 1);
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-
-constexpr int kJoinBatch = 4;
-
-// Without shared parts only the units that a CTA's range cuts have parts to
-// join: CTA (c, chunk) takes 32 rows of the unit that the boundary between
-// CTAs c and c + 1 is the first to cut (CTA c + 1 left its record), four rows
-// a warp.
 template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+__device__ __forceinline__ void write_row(const KernelArgs &k, int64_t rh, int row, int qh, const Joined &j) {
+  const int lane = threadIdx.x & 31;
+  const float4 x = j.result();
+  if (4 * lane < k.a.c.head_dim) {
+    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(x.x, x.y), Weights<T>::pack(x.z, x.w));
+  }
+  if (k.a.lse && lane == 0) k.a.lse[rh] = j.lse2() * 0.69314718055994531f;
+}
+
+// The units that a CTA's range cuts: CTA (c, chunk) takes eight rows of the
+// unit that the boundary between CTAs c and c + 1 is the first to cut (CTA
+// c + 1 left its record): its owner's part and a continuation each of CTAs
+// c + 1 .. c + more.  Rows that have another unit too get their joined part
+// back for join_shared_kernel.
+template <typename T>
+__global__ void __launch_bounds__(32 * kJoinWarps)
 join_cut_units_kernel(const __grid_constant__ KernelArgs k) {
+  // the last kernel of a call lets nothing start before it has ended
+  if (k.w.groups) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int cta = blockIdx.x;
+  const int cta = blockIdx.x, lane = threadIdx.x & 31;
   const int4 *cut = reinterpret_cast<const int4 *>(&k.w.cuts[cta + 1]);
   const int4 c = __ldcg(cut);  // row0, rows, head, more
-  const int rt = __ldcg(cut + 1).x;
-  const int slot0 = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * kJoinBatch;
-  if (slot0 >= c.y) return;
-  Parts part[kJoinBatch][1];
-  int64_t rh[kJoinBatch];
-  int row[kJoinBatch], qh[kJoinBatch];
+  const int flags = __ldcg(cut + 1).x;
+  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (slot >= c.y) return;
+  const int D = k.a.c.head_dim, i = slot / k.rep, row = c.x + i, qh = c.z * k.rep + slot - i * k.rep;
+  const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
+  const bool live = 4 * lane < D;
+  const int kind = flags & kShared;
+  Joined j;
+  float l = __ldcg(&k.w.lse[kind][rh]);
+  float4 x = load_part(k.w.o[kind] + rh * D, live);
+  const int64_t slot0 = static_cast<int64_t>(cta + 1) * kUnitRows + slot;
+  constexpr int kBatch = 8;
+  for (int p = 0; p < c.w; p += kBatch) {
+    float ls[kBatch];
+    float4 xs[kBatch];
+    float top = fmaxf(j.top, l);
 #pragma unroll
-  for (int b = 0; b < kJoinBatch; ++b) {
-    const int slot = slot0 + b, r = rt * kUnitRows + slot, i = r / k.rep;
-    row[b] = c.x + i;
-    qh[b] = c.z * k.rep + r - i * k.rep;
-    rh[b] = static_cast<int64_t>(row[b]) * k.a.q_heads + qh[b];
-    const bool in = slot < c.y;
-    part[b][0] = {in, cta, in ? c.w : 0, slot};
+    for (int e = 0; e < kBatch; ++e) {
+      const int64_t at = slot0 + static_cast<int64_t>(p + e) * kUnitRows;
+      const bool in = p + e < c.w;
+      ls[e] = in ? __ldcg(&k.w.lse_c[at]) : -INFINITY;
+      xs[e] = load_part(k.w.o_c + at * D, live && in);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) top = fmaxf(top, ls[e]);
+    j.raise(top);
+    j.add(l, x);
+    l = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) j.add(ls[e], xs[e]);
   }
-  join_rows<T, 1, kJoinBatch>(k, part, rh, row, qh);
+  if (flags & kSolo) {
+    write_row<T>(k, rh, row, qh, j);
+  } else {
+    const float4 y = j.result();
+    if (live) reinterpret_cast<float4 *>(k.w.o[kind] + rh * D)[lane] = y;
+    if (lane == 0) k.w.lse[kind][rh] = j.lse2();
+  }
 }
 
-// With shared parts every row has two units: a CTA per row, four heads a warp
-// at a time.
+// The rows of prompts with a shared part: its result and the own part's.  A
+// CTA per row, four heads a warp at a time.
+constexpr int kJoinHeads = 4;
 template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 join_shared_kernel(const __grid_constant__ KernelArgs k) {
-  const int guess = min(static_cast<int>(blockIdx.x) / k.a.b.max_new, k.a.b.S - 1);
+  const BatchArgs &b = k.a.b;
+  const int row = blockIdx.x;
+  int seq = min(row / b.max_new, b.S - 1);  // right when every sequence has max_new rows
+  if (b.row_start && !(b.row_start[seq] <= row && row < b.row_start[seq + 1])) seq = seq_of_row(b, row);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r0 = blockIdx.x;
-  int seq = guess;  // right when every sequence has max_new rows
-  if (k.a.b.row_start && !(k.a.b.row_start[guess] <= r0 && r0 < k.a.b.row_start[guess + 1])) {
-    seq = seq_of_row(k.a.b, r0);
-  }
-  if (seq < 0) return;
-  const int e[2] = {k.w.groups + seq, seq / k.a.b.group};
-  const int per = __ldcg(&k.w.head->per);
-  const Entry t[2] = {load_entry(k.w, e[0]), load_entry(k.w, e[1])};
-  const int tile0[2] = {__ldcg(&k.w.tile0[e[0]]), __ldcg(&k.w.tile0[e[1]])};
-  if (r0 < t[0].row0 || r0 >= t[0].row0 + t[0].tokens) return;  // a sequence out of order
-  for (int q0 = (threadIdx.x >> 5) * kJoinBatch; q0 < k.a.q_heads; q0 += kCombineWarps * kJoinBatch) {
-    Parts part[kJoinBatch][2];
-    int64_t rh[kJoinBatch];
-    int row[kJoinBatch], qh[kJoinBatch];
+  // without a shared part the row is written already; its rows are in order with one
+  if (seq < 0 || __ldcg(&k.w.common[seq / b.group]) == 0) return;
+  const int D = k.a.c.head_dim, lane = threadIdx.x & 31;
+  const bool live = 4 * lane < D;
+  for (int q0 = (threadIdx.x >> 5) * kJoinHeads; q0 < k.a.q_heads; q0 += kJoinWarps * kJoinHeads) {
+    float l[kJoinHeads][2];
+    float4 x[kJoinHeads][2];
 #pragma unroll
-    for (int b = 0; b < kJoinBatch; ++b) {
-      row[b] = r0;
-      qh[b] = q0 + b;
-      const int head = qh[b] / k.rep;
-      rh[b] = static_cast<int64_t>(r0) * k.a.q_heads + qh[b];
+    for (int e = 0; e < kJoinHeads; ++e) {
+      const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + q0 + e;
+      const bool in = q0 + e < k.a.q_heads;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        part[b][p] = {qh[b] < k.a.q_heads && t[p].tiles > 0 && t[p].tokens > 0, 0, 0, 0};
-        if (!part[b][p].any) continue;
-        const int r = (r0 - t[p].row0) * k.rep + qh[b] - head * k.rep;
-        const int rts = (t[p].tokens * k.rep + kUnitRows - 1) / kUnitRows;
-        const int x0 = tile0[p] + (head * rts + r / kUnitRows) * t[p].tiles;
-        part[b][p].cta = x0 / per;
-        part[b][p].more = (x0 + t[p].tiles - 1) / per - part[b][p].cta;
-        part[b][p].slot = r % kUnitRows;
+        l[e][p] = in ? __ldcg(&k.w.lse[p][rh]) : -INFINITY;
+        x[e][p] = load_part(k.w.o[p] + rh * D, live && in);
       }
-      // a row that one CTA finished alone was written by it
-      if ((t[0].flags & kSolo) && part[b][0].more == 0) part[b][0].any = part[b][1].any = false;
     }
-    join_rows<T, 2, kJoinBatch>(k, part, rh, row, qh);
+#pragma unroll
+    for (int e = 0; e < kJoinHeads; ++e) {
+      if (q0 + e >= k.a.q_heads) break;
+      Joined j;
+      j.top = fmaxf(l[e][0], l[e][1]);
+      j.add(l[e][0], x[e][0]);
+      j.add(l[e][1], x[e][1]);
+      write_row<T>(k, static_cast<int64_t>(row) * k.a.q_heads + q0 + e, row, q0 + e, j);
+    }
   }
 }
 
@@ -1294,6 +1380,23 @@ static EncodeFn encode_fn() {
     return reinterpret_cast<EncodeFn>(p);
   }();
   return fn;
+}
+
+// [rows][q_heads][head_dim] in boxes of 64 elements x the heads of a key head x
+// a row tile's tokens; rows past the last read as 0.
+static bool make_q_map(CUtensorMap *map, const KernelArgs &k) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const AttnArgs &a = k.a;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.head_dim), static_cast<cuuint64_t>(a.q_heads),
+                              static_cast<cuuint64_t>(a.b.rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.q_head) * 2, static_cast<cuuint64_t>(a.q_row) * 2};
+  const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(k.rep), static_cast<cuuint32_t>(k.q_box)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return fn(map, a.c.dtype == SMC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            3, const_cast<char *>(a.q), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [blocks][kv_heads][block_size][head_dim] in boxes of 64 elements x `box`
@@ -1380,6 +1483,8 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   k.a = a;
   carve(a.c, a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
   k.rep = a.q_heads / a.c.kv_heads;
+  k.tile_tokens = kRows / k.rep;
+  k.q_box = a.b.rows < k.tile_tokens ? a.b.rows : k.tile_tokens;
   k.sc = a.scale * 1.4426950408889634f;
   // with 2^s the power of two at or above the block size, 2^(31 + s) / size
   // rounded up divides every t < 2^31 exactly
@@ -1392,34 +1497,34 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   // repeats every eight rows, so a box starts on a multiple of eight
   int box = kTile;
   while (a.c.block_size % box) box >>= 1;
-  CUtensorMap map_k{}, map_v{};
+  CUtensorMap map_q{}, map_k{}, map_v{};
+  if (!make_q_map(&map_q, k)) return cudaErrorInvalidValue;
   const bool tma = box >= 8 && make_map(&map_k, a.c, a.c.k, box) && make_map(&map_v, a.c, a.c.v, box);
   k.box = box;
   // no more CTAs than tiles there can be
-  const int64_t most = (static_cast<int64_t>(a.b.T) * a.c.block_size + kTile - 1) / kTile *
-                       a.c.kv_heads * a.b.S *
-                       ((static_cast<int64_t>(a.b.max_new) * k.rep + kUnitRows - 1) / kUnitRows);
-  int ctas = most < sms ? static_cast<int>(most) : sms;
+  const int64_t units = a.b.S * ((static_cast<int64_t>(a.b.max_new) + 2 * k.tile_tokens - 1) / (2 * k.tile_tokens));
+  const int64_t most = (static_cast<int64_t>(a.b.T) * a.c.block_size + kTile - 1) / kTile * a.c.kv_heads * units;
+  const int ctas = most < sms ? static_cast<int>(most) : sms;
   plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const bool bf16 = a.c.dtype == SMC_BF16, wide = a.c.head_dim > 64;
-  void *args[] = {&k, &map_k, &map_v};
+  void *args[] = {&k, &map_q, &map_k, &map_v};
   e = launch_pdl(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
                  dim3(ctas), kAttnThreads, kAttnSmem, args, st);
   if (e != cudaSuccess) return e;
-  void *cargs[] = {&k};
-  if (k.w.groups) {
-    return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_shared_kernel<__nv_bfloat16>)
-                           : reinterpret_cast<const void *>(join_shared_kernel<__half>),
-                      dim3(a.b.rows), 32 * kCombineWarps, 0, cargs, st);
+  void *jargs[] = {&k};
+  if (ctas > 1) {  // else nothing is cut
+    const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * a.b.group * k.rep;
+    const int rows = static_cast<int>(most_rows < kUnitRows ? most_rows : kUnitRows);
+    e = launch_pdl(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
+                        : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
+                   dim3(ctas - 1, (rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, jargs, st);
+    if (e != cudaSuccess) return e;
   }
-  if (ctas == 1) return cudaSuccess;  // nothing is cut
-  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * k.rep;
-  constexpr int kChunk = kCombineWarps * kJoinBatch;
-  const int chunks = static_cast<int>(((most_rows < kUnitRows ? most_rows : kUnitRows) + kChunk - 1) / kChunk);
-  return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
-                         : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
-                    dim3(ctas - 1, chunks), 32 * kCombineWarps, 0, cargs, st);
+  if (!k.w.groups) return cudaSuccess;
+  return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_shared_kernel<__nv_bfloat16>)
+                         : reinterpret_cast<const void *>(join_shared_kernel<__half>),
+                    dim3(a.b.rows), 32 * kJoinWarps, 0, jargs, st);
 }
 
 }  // namespace smcsd

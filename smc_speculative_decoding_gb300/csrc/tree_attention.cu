@@ -422,16 +422,18 @@ constexpr float kLazy = 8.f;
 // row tile); warps 8 and 9: the threads that issue either group's matrix
 // products; warp 10 finds the CTA's segments (parts of units) for all and
 // copies K; warp 11 copies Q and V.  Shared memory: two Q tiles and a ring
-// each of K and V tiles.  Tensor memory: two score buffers of 64 columns per
-// group (the weights overwrite the scores) and either group's accumulator.
+// each of K and V tiles.  Tensor memory, per group: a tile's scores (64
+// columns), two tiles' weights (32 each) and the accumulator (128).
 //   Units of one row tile: the groups take alternate tiles of the unit, each
 //   with its own running maximum, sum and accumulator, joined at the end.
 //   Units of two: each group has its own row tile; a tile of K and V serves
 //   both.
-// Scores run two of a group's tiles ahead of its products with V, and into the
-// next segment while the last one's result is written, so that neither a group
-// nor its ring waits for a product's latency: K tiles leave their ring as they
-// come, and only V waits for its weights.
+// A group takes its scores to registers at once, so the next tile's scores are
+// computed beside its softmax (and the next segment's beside the write of a
+// result), and the product with V of one tile beside the softmax of the next:
+// a group waits for no product's latency.  With the weights in place of the
+// scores, and the next scores behind the product with V, a tile of 256 rows
+// took 2700 cycles, of which 1100 were that wait.
 //   Every wait is on a barrier all of whose turns the waiting thread follows:
 // a slot is one group's for good (see Geometry), and before both groups use a
 // tile, all earlier tiles are done with.
@@ -446,7 +448,7 @@ struct Geometry {
   // Slots of K and of V: V waits for its weights, K does not.  Tile i of a
   // segment takes one of group i % 2's half of the slots (the even or the odd
   // ones) in turn.
-  static constexpr int kSlotsK = 4 * (2 / kHalves), kSlotsV = 6 * (2 / kHalves);
+  static constexpr int kSlotsK = 6 * (2 / kHalves), kSlotsV = 4 * (2 / kHalves);
   static constexpr int kQTile = kHalves * kRows * 128;
   static constexpr int kQBytes = 2 * kQTile;
   static constexpr int kTail = kQBytes + kRingBytes;
@@ -466,7 +468,7 @@ constexpr int kWhole = 4, kBase = 8, kEnd = 16;  // with kShared: final result, 
 struct AttnTail {
   uint64_t full[2][12], empty[2][12];  // K, V
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full[2], q_free[2], scores[2][2], weights[2][2], added[2], o_full[2], o_free, stats;
+  uint64_t q_full[2], q_free[2], scores[2], s_free[2], weights[2][2], o_full[2], o_free, stats;
   uint64_t drained[2];
   Seg seg[kSegs];
   float2 stat[2][kRows];  // either group's (max, sum) of a row
@@ -523,33 +525,40 @@ struct Walk {
   }
 };
 
-// A ring's slots, tile by tile: the slot of tile i of the current segment, and
-// the parity of the slot's barriers for it.
+// A ring's slots, tile by tile.  Either half of the slots (the even and the odd
+// ones) is used in turn; `pos` and `parity` are the half's next slot and the
+// parity of that slot's barriers.
 template <int kSlots>
 struct Ring {
   static constexpr uint32_t kHalf = kSlots / 2;
-  uint32_t done[2] = {0, 0};  // tiles of either half before the segment
-  uint32_t used[2] = {0, 0};  // tiles of either half that were begun (copying warps)
-  uint32_t at, parity, turn;
-  __device__ __forceinline__ void tile(int i) {
-    const uint32_t half = i & 1u, c = (half ? done[1] : done[0]) + (i >> 1);
-    turn = c / kHalf;
-    at = half + 2 * (c - turn * kHalf);
-    parity = turn & 1u;
+  uint32_t pos[2] = {0, 0}, parity[2] = {0, 0};
+  __device__ __forceinline__ uint32_t at(bool odd) const {
+    return odd ? 2 * pos[1] + 1 : 2 * pos[0];
   }
-  __device__ __forceinline__ void begin(int i) {
-    if (i & 1) used[1] = done[1] + (i >> 1) + 1; else used[0] = done[0] + (i >> 1) + 1;
+  __device__ __forceinline__ uint32_t par(bool odd) const { return odd ? parity[1] : parity[0]; }
+  __device__ __forceinline__ void step(bool odd) {
+    uint32_t &p = odd ? pos[1] : pos[0], &q = odd ? parity[1] : parity[0];
+    if (++p == kHalf) {
+      p = 0;
+      q ^= 1u;
+    }
   }
-  __device__ __forceinline__ void next_segment(int n) {
-    done[0] += (n + 1) >> 1;
-    done[1] += n >> 1;
+  // past n tiles of one half that this thread does not use
+  __device__ __forceinline__ void skip(bool odd, uint32_t n) {
+    uint32_t &p = odd ? pos[1] : pos[0], &q = odd ? parity[1] : parity[0];
+    p += n;
+    const uint32_t turns = p / kHalf;
+    p -= turns * kHalf;
+    q ^= turns & 1u;
   }
 };
 
-// False when the wait gave up (it raised the status bit and the abort flag, at
-// which every other wait of the CTA gives up too).
-__device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_t parity,
-                                             unsigned *status) {
+// Waits.  Every one is bounded, and gives up for the whole CTA: the one that
+// ran out raises the status bit and the abort flag, at which the others end.
+// What is done when a barrier has already completed is kept to a few
+// instructions: each role's code runs once a tile, after other roles' code has
+// displaced it from the instruction cache, and is paid for by its length.
+__device__ __noinline__ bool wait_slowly(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (s->abort) return false;
@@ -558,12 +567,13 @@ __device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_
   raise_status(status, SMC_DEV_TIMEOUT);
   return false;
 }
-
+__device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+  return mbar_try_wait(bar, parity) || wait_slowly(s, bar, parity, status);
+}
 // The same for a whole warp, in step: every lane polls and takes the same
 // branch, so that the warp is converged for the .aligned instructions that
 // follow.
-__device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t parity,
-                                          unsigned *status) {
+__device__ __noinline__ bool warp_wait_slowly(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, s->abort)) return false;
@@ -571,6 +581,9 @@ __device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t p
   s->abort = 1;
   raise_status(status, SMC_DEV_TIMEOUT);
   return false;
+}
+__device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_slowly(s, bar, parity, status);
 }
 // One arrival for a warp (lane 0's), by predicate and not by a branch, for
 // the same reason.  What the other lanes did before is ordered by __syncwarp.
@@ -644,7 +657,7 @@ template <int kHalves, bool kTma, int kSlots>
 __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMap *map, const char *src,
                                            char *slots, uint64_t *full, uint64_t *empty, AttnTail *s,
                                            Ring<kSlots> &ring, const Seg &seg, bool pair,
-                                           unsigned *bits) {
+                                           unsigned *bits, uint32_t *filled, uint32_t *parities) {
   using G = Geometry<kHalves>;
   const int lane = threadIdx.x & 31;
   const CacheArgs &c = k.a.c;
@@ -667,8 +680,9 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
   bool ok = true;
   for (int i = 0; i < seg.n; ++i) {
     const int t0 = seg.t0 + i * kTile, t1 = min(t0 + kTile, end);
-    ring.tile(i);
-    char *dst = slots + ring.at * G::kTileBytes;
+    const bool odd = i & 1;
+    const uint32_t slot = ring.at(odd);
+    char *dst = slots + slot * G::kTileBytes;
     if constexpr (kTma) {
       if ((i + 1) * per_tile > from + 32) {
         from = i * per_tile;
@@ -676,13 +690,16 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
         if (t < end) ahead = place(t);
       }
     }
-    if (ring.turn > 0 && !(ok = warp_wait(s, &empty[ring.at], ring.parity ^ 1u, k.a.status))) break;
-    if (!pair) warp_arrive(&empty[ring.at], lane);  // one group uses it
-    ring.begin(i);
+    // (the first turn of a fresh barrier passes for the one before it)
+    if (!(ok = warp_wait(s, &empty[slot], ring.par(odd) ^ 1u, k.a.status))) break;
+    if (!pair) warp_arrive(&empty[slot], lane);  // one group uses it
+    *filled |= 1u << slot;
+    *parities = (*parities & ~(1u << slot)) | ring.par(odd) << slot;
+    ring.step(odd);
     if constexpr (kTma) {
       const int boxes = (t1 - t0 + k.box - 1) / k.box;
       const int at = i * per_tile - from;
-      if (elect_one()) mbar_arrive_expect_tx(&full[ring.at], boxes * kHalves * k.box * 128);
+      if (elect_one()) mbar_arrive_expect_tx(&full[slot], boxes * kHalves * k.box * 128);
       __syncwarp();
       for (int b = 0; b < boxes; ++b) {
         const int block = __shfl_sync(0xffffffffu, ahead.x, at + b);
@@ -691,7 +708,7 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {
             tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token, seg.head,
-                        block, &full[ring.at]);
+                        block, &full[slot]);
           }
         }
         __syncwarp();
@@ -714,7 +731,7 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
         fence_proxy_async_smem();
         warp_arrive(&full[unseen], lane);
       }
-      unseen = ring.at;
+      unseen = slot;
     }
   }
   if constexpr (!kTma) {
@@ -729,15 +746,9 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
 
 // Waits until the last copy into each of a ring's slots has landed: a CTA that
 // gave up may have left some under way.
-template <int kSlots>
-__device__ __forceinline__ void wait_landed(uint64_t *full, const Ring<kSlots> &ring) {
-  constexpr uint32_t kHalf = Ring<kSlots>::kHalf;
-  for (uint32_t half = 0; half < 2; ++half) {
-    const uint32_t end = half ? ring.used[1] : ring.used[0];
-    for (uint32_t c = end > kHalf ? end - kHalf : 0; c < end; ++c) {
-      const uint32_t turn = c / kHalf;
-      mbar_wait(&full[half + 2 * (c - turn * kHalf)], turn & 1u, 1u << 12);
-    }
+__device__ __noinline__ void wait_landed(uint64_t *full, uint32_t filled, uint32_t parities) {
+  for (uint32_t slot = 0; slot < 12; ++slot) {
+    if (filled >> slot & 1u) mbar_wait(&full[slot], parities >> slot & 1u, 1u << 12);
   }
 }
 
@@ -770,11 +781,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s->q_full[g], 1);
       mbar_init(&s->q_free[g], 2);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&s->scores[g][b], 1);
-        mbar_init(&s->weights[g][b], 4);
-      }
-      mbar_init(&s->added[g], 1);
+      for (int b = 0; b < 2; ++b) mbar_init(&s->weights[g][b], 4);
+      mbar_init(&s->scores[g], 1);
+      mbar_init(&s->s_free[g], 4);
       mbar_init(&s->o_full[g], 1);
       mbar_init(&s->drained[g], 1);
     }
@@ -800,9 +809,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     const int r = wq * 32 + lane;  // row of the group's tile
     const int r_tok = r / k.rep, r_head = r - r_tok * k.rep;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t t_o = tmem + lanes + 256 + g * 128;
+    const uint32_t t_s = tmem + lanes + g * 128, t_o = tmem + lanes + 256 + g * 128;
     uint32_t seg = 0, turn = 0;  // segments, and tiles of this group so far
-    Ring<G::kSlotsV> ring;
+    Ring<G::kSlotsV> ring_v;
     bool ok = true;
     Seg w;
     while (ok && take_segment(s, seg, &w, status)) {
@@ -816,22 +825,28 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       const int row = w.row0 + tok, qh = w.head * k.rep + (live ? r_head : 0);
       const bool own = !(w.flags & kShared);
       float m = -INFINITY, l = 0.f;
-      bool first = true;
+      // the releases of the V slots of the group's last tile and the one before
+      uint64_t *last = nullptr, *before = nullptr;
+      uint32_t last_par = 0, before_par = 0;
       for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
         const int t0 = w.t0 + i * kTile;
         const uint32_t buf = turn & 1u;
-        const uint32_t t_s = tmem + lanes + g * 128 + buf * 64;
-        if (!(ok = warp_wait(s, &s->scores[g][buf], turn >> 1 & 1u, status))) break;
+        if (!(ok = warp_wait(s, &s->scores[g], buf, status))) break;
         ++turn;
         tc_fence_after();
         const bool edge = own && t0 + kTile > w.ctx;
+        uint32_t z[64];
         if (warp_live) {
-          uint32_t z[64];
           __syncwarp();
           tmem_ld32(t_s, z);
           tmem_ld32(t_s + 32, z + 32);
           tmem_wait_ld(z);
           tmem_tie(z + 32);
+        }
+        tc_fence_before();
+        warp_arrive(&s->s_free[g], lane);
+        const bool odd = i & 1;
+        if (warp_live) {
           if (edge) {
             const uint32_t *mask =
                 k.a.mask ? k.a.mask + static_cast<int64_t>(row) * k.a.mask_words : nullptr;
@@ -859,11 +874,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           for (int b = 0; b < 4; ++b) mx[b] = fmaxf(mx[b], __uint_as_float(z[60 + b]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * k.sc;
           const bool rise = top > m + kLazy;
-          if (first) {
+          if (!last) {
             m = top;
           } else if (__any_sync(0xffffffffu, rise)) {
-            // the product with V of the group's last tile (number turn - 2) is done
-            if (!(ok = warp_wait(s, &s->added[g], turn & 1u, status))) break;
+            // the last product with V is in the accumulator when its slot is free
+            if (!(ok = warp_wait(s, last, last_par, status))) break;
             tc_fence_after();
             const float mn = rise ? top : m;
             const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
@@ -880,7 +895,6 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             }
             tmem_wait_st();
           }
-          first = false;
           const float sub = Wt::kOffset - (m == -INFINITY ? 0.f : m);
           const unsigned long long sc2 = f2dup(k.sc), sub2 = f2dup(sub);
           unsigned long long sum2[2] = {f2dup(0.f), f2dup(0.f)};
@@ -896,8 +910,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             sum2[c & 1] = add2(sum2[c & 1], f2pack(a, b));
             p[c] = Wt::pack(a, b);
           }
+          // the product with V of the tile before the last, which had these columns, is done
+          if (before && !(ok = warp_wait(s, before, before_par, status))) break;
+          tc_fence_after();
           __syncwarp();
-          tmem_st32(t_s, p);
+          tmem_st32(t_s + 64 + 32 * buf, p);
           float sa, sb;
           f2unpack(add2(sum2[0], sum2[1]), sa, sb);
           l += sa + sb;
@@ -907,11 +924,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           // the tile reaches past the committed tokens: V rows past the last
           // token become 0 (they may hold anything), and so do infinities
           // and NaN of new tokens, which patch_nonfinite puts back
-          ring.tile(i);
-          if (!(ok = warp_wait(s, &s->full[1][ring.at], ring.parity, status))) break;
+          if (!(ok = warp_wait(s, &s->full[1][ring_v.at(odd)], ring_v.par(odd), status))) break;
           const int t = t0 + (r & (kTile - 1));
           if (t >= w.ctx) {
-            char *v = s_v + ring.at * G::kTileBytes + (r & (kTile - 1)) * 128;
+            char *v = s_v + ring_v.at(odd) * G::kTileBytes + (r & (kTile - 1)) * 128;
             bool found = false;
             const int c0 = (r / kTile) * 4 * kHalves;
 #pragma unroll 4
@@ -940,9 +956,14 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         }
         tc_fence_before();
         warp_arrive(&s->weights[g][buf], lane);
+        before = last;
+        before_par = last_par;
+        last = &s->empty[1][ring_v.at(odd)];
+        last_par = ring_v.par(odd);
+        ring_v.step(odd);
       }
       if (!ok) break;
-      ring.next_segment(w.n);
+      if (!pair) ring_v.skip(g == 0, (w.n + g) >> 1);  // the other group's tiles
       // ---- the unit's result -----------------------------------------------
       const uint32_t par = (seg - 1) & 1u;
       ok = warp_wait(s, &s->o_full[g], par, status) && (pair || warp_wait(s, &s->o_full[1 - g], par, status));
@@ -1052,7 +1073,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     const uint32_t v0 = smem_desc(smem_addr(s_v), kTile * 128);
     const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128;
     uint32_t seg = 0, q_turn = 0;           // segments and Q tiles so far
-    uint32_t asked = 0, given = 0;          // tiles of the group so far: scores, products with V
+    uint32_t tiles = 0, asked = 0, given = 0;  // tiles of the group so far: scores, products with V
     Ring<G::kSlotsK> ring_k;
     Ring<G::kSlotsV> ring_v;
     bool ok = true;
@@ -1061,68 +1082,81 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       warp_arrive(&s->seg_empty[seg % kSegs], lane);
       const bool pair = w.rows > tile_rows;
       const int n = w.n, step = pair ? 1 : 2, first = pair ? 0 : g;
+      const Ring<G::kSlotsK> k_before = ring_k;
+      const Ring<G::kSlotsV> v_before = ring_v;
       const uint32_t q_at = q_turn + (pair ? g : 0), q_other = q_turn + 1 - g;
       q_turn += pair ? 2 : 1;
       if (elect_one()) {
         const uint32_t qa = q0 + (q_at & 1u) * (G::kQTile >> 4);
-        // scores of tile i, once its K is there; after the last one Q is free
+        // scores of tile i, once the last ones are taken and its K is there
         auto scores = [&](int i) {
-          ring_k.tile(i);
-          if (!guarded_wait(s, &s->full[0][ring_k.at], ring_k.parity, status)) return false;
-          const uint32_t buf = asked & 1u, ka = k0 + ring_k.at * (G::kTileBytes >> 4);
+          const bool odd = i & 1;
+          const uint32_t at = ring_k.at(odd);
+          // (the first turn of a fresh barrier passes for the one before it)
+          if (!guarded_wait(s, &s->s_free[g], ~asked & 1u, status) ||
+              !guarded_wait(s, &s->full[0][at], ring_k.par(odd), status)) {
+            return false;
+          }
           ++asked;
+          ring_k.step(odd);
+          tc_fence_after();
+          const uint32_t ka = k0 + at * (G::kTileBytes >> 4);
 #pragma unroll
           for (int c = 0; c < 4 * kHalves; ++c) {
             if (c < k_steps) {
-              mma_ss(t_s + buf * 64, qa + ((c >> 2) * (kRows * 128) + (c & 3) * 32) / 16,
+              mma_ss(t_s, qa + ((c >> 2) * (kRows * 128) + (c & 3) * 32) / 16,
                      ka + ((c >> 2) * (kTile * 128) + (c & 3) * 32) / 16, id_qk, c > 0);
             }
           }
-          tc_commit(&s->scores[g][buf]);
-          tc_commit(&s->empty[0][ring_k.at]);
+          tc_commit(&s->scores[g]);
+          tc_commit(&s->empty[0][at]);
           return true;
         };
-        auto free_q = [&] {
+        auto free_q = [&] {  // after the segment's last scores
           tc_commit(&s->q_free[q_at & 1u]);
           if (pair) tc_commit(&s->q_free[q_other & 1u]);
         };
         // both tiles of a pair, as both issuing threads free both
         ok = guarded_wait(s, &s->q_full[q_at & 1u], q_at >> 1 & 1u, status) &&
              (!pair || guarded_wait(s, &s->q_full[q_other & 1u], q_other >> 1 & 1u, status));
-        if (ok) {
-          tc_fence_after();
-          for (int i = first; ok && i < n && i < 2 * step; i += step) ok = scores(i);
-          if (first + 2 * step >= n) free_q();
-        }
-        // the last segment's result has been read
-        if (ok && seg > 0) ok = guarded_wait(s, &s->o_free, (seg - 1) & 1u, status);
+        if (ok && first < n) ok = scores(first);
+        if (ok && first + step >= n) free_q();
         for (int i = first; ok && i < n; i += step) {
-          ring_v.tile(i);
-          const uint32_t buf = given & 1u, va = v0 + ring_v.at * (G::kTileBytes >> 4);
-          ok = guarded_wait(s, &s->full[1][ring_v.at], ring_v.parity, status) &&
+          if (i + step < n) {
+            if (!(ok = scores(i + step))) break;
+            if (i + 2 * step >= n) free_q();
+          }
+          // the last segment's result has been read
+          if (i == first && seg > 0 && !(ok = guarded_wait(s, &s->o_free, (seg - 1) & 1u, status))) break;
+          const bool odd = i & 1;
+          const uint32_t at = ring_v.at(odd);
+          const uint32_t buf = given & 1u, va = v0 + at * (G::kTileBytes >> 4);
+          ok = guarded_wait(s, &s->full[1][at], ring_v.par(odd), status) &&
                guarded_wait(s, &s->weights[g][buf], given >> 1 & 1u, status);
           if (!ok) break;
           ++given;
+          ring_v.step(odd);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kTile / 16; ++c) {
-            mma_ts(t_o, t_s + buf * 64 + c * 8, va + c * 2048 / 16, id_pv, i >= step || c > 0);
+            mma_ts(t_o, t_s + 64 + 32 * buf + c * 8, va + c * 2048 / 16, id_pv, i >= step || c > 0);
           }
-          tc_commit(&s->added[g]);
-          tc_commit(&s->empty[1][ring_v.at]);
-          if (i + 2 * step < n) {
-            ok = scores(i + 2 * step);
-            if (i + 3 * step >= n) free_q();
-          }
+          tc_commit(&s->empty[1][at]);
         }
+        // a group without tiles keeps the others' pace
+        if (ok && first >= n && seg > 0) ok = guarded_wait(s, &s->o_free, (seg - 1) & 1u, status);
         if (ok) tc_commit(&s->o_full[g]);
       }
-      // what the elected lane counted, for whichever is elected next
+      // what the elected lane counted, for all: its tiles, and the other group's
       ok = __all_sync(0xffffffffu, ok);
-      asked = __reduce_max_sync(0xffffffffu, asked);
-      given = __reduce_max_sync(0xffffffffu, given);
-      ring_k.next_segment(n);
-      ring_v.next_segment(n);
+      const uint32_t mine = pair ? n : (n + 1 - g) >> 1;
+      asked = given = tiles += mine;
+      ring_k = k_before;
+      ring_v = v_before;
+      ring_k.skip(false, (n + 1) >> 1);
+      ring_k.skip(true, n >> 1);
+      ring_v.skip(false, (n + 1) >> 1);
+      ring_v.skip(true, n >> 1);
       ++seg;
     }
     if (elect_one()) {
@@ -1136,6 +1170,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     w.start(k.w);
     Ring<G::kSlotsK> ring;
     unsigned bits = 0;
+    uint32_t filled = 0, parities = 0;
     bool ok = true;
     const int per = __ldcg(&k.w.head->per), first = static_cast<int>(blockIdx.x) * per;
     for (uint32_t seg = 0; ok; ++seg) {
@@ -1169,16 +1204,16 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       warp_arrive(&s->seg_full[seg % kSegs], lane);
       if (!more) break;
       ok = copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s, ring,
-                                                 t, t.rows > tile_rows, &bits);
-      if (ok) ring.next_segment(t.n);
+                                                 t, t.rows > tile_rows, &bits, &filled, &parities);
     }
-    if (kTma && s->abort) wait_landed(s->full[0], ring);
+    if (kTma && s->abort) wait_landed(s->full[0], filled, parities);
     if (bits) raise_status(status, bits);
   } else {
     // ---- Q and V ----------------------------------------------------------------
     Ring<G::kSlotsV> ring;
     uint32_t seg = 0, q_turn = 0;
     unsigned bits = 0;
+    uint32_t filled = 0, parities = 0;
     bool ok = true;
     Seg w;
     while (ok && take_segment(s, seg, &w, status)) {
@@ -1200,11 +1235,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       }
       if (!ok) break;
       ok = copy_tiles<kHalves, kTma, G::kSlotsV>(k, &map_v, k.a.c.v, s_v, s->full[1], s->empty[1], s, ring,
-                                                 w, pair, &bits);
-      if (ok) ring.next_segment(w.n);
+                                                 w, pair, &bits, &filled, &parities);
     }
     if (s->abort) {
-      if (kTma) wait_landed(s->full[1], ring);
+      if (kTma) wait_landed(s->full[1], filled, parities);
       for (uint32_t q = q_turn > 2 ? q_turn - 2 : 0; q < q_turn; ++q) {
         mbar_wait(&s->q_full[q & 1u], q >> 1 & 1u, 1u << 12);
       }

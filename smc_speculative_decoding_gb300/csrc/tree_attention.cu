@@ -59,6 +59,7 @@ struct PlanHeader {
 
 struct AttnWorkspace {
   PlanHeader *head;
+  unsigned *tickets;  // [kMaxCtas] parts stored of the unit that a CTA's end cuts; return to zero
   int *common;     // [groups] shared tokens
   int *tile0;      // [entries + 1]
   Entry *entries;  // shared parts of the groups (when group > 1), then the sequences
@@ -85,6 +86,7 @@ static size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, char *b
   t.n_entries = b.S + t.groups;
   take(kCacheStatusBytes);
   t.head = reinterpret_cast<PlanHeader *>(take(sizeof(PlanHeader)));
+  t.tickets = reinterpret_cast<unsigned *>(take(sizeof(unsigned) * kMaxCtas));
   t.common = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
   t.tile0 = reinterpret_cast<int *>(take(sizeof(int) * (static_cast<size_t>(t.n_entries) + 1)));
   t.entries = reinterpret_cast<Entry *>(take(sizeof(Entry) * t.n_entries));
@@ -110,6 +112,8 @@ struct KernelArgs {
   int rep;      // query heads per key head, at most 128
   int tile_tokens;  // new tokens of a row tile: floor(128 / rep)
   int q_box;    // new tokens of a copied box of Q
+  int planned;      // plan_kernel has run (else each CTA finds its own work)
+  int join_inside;  // the last CTA of a cut unit joins its parts
   int box;      // tokens per copied box
   uint32_t magic, shift;  // t / block_size == umulhi(t, magic) >> shift
   float sc;     // scale * log2 e
@@ -461,57 +465,109 @@ struct Seg {
   int t0, n;       // first token, tiles
   int ctx, kv1;    // tokens before ctx are seen by all; end of the entry's tokens
   int n_new;       // new tokens of the sequence (own parts)
-  int flags, pad;
+  int flags;
+  int join;        // of a cut unit: the owner CTA, and continuations << 16
 };
 constexpr int kWhole = 4, kBase = 8, kEnd = 16;  // with kShared: final result, first tiles, none left
 
 struct AttnTail {
   uint64_t full[2][12], empty[2][12];  // K, V
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full[2], q_free[2], scores[2], s_free[2], weights[2][2], o_full[2], o_free, stats;
+  uint64_t q_full[2], q_free[2], scores[2], s_free[2], weights[2][2], o_full[2], o_free, stats, stored, counted;
   uint64_t drained[2];
   Seg seg[kSegs];
   float2 stat[2][kRows];  // either group's (max, sum) of a row
   uint32_t tmem;
   unsigned nonfinite[2];  // segment number (from 1) of the last odd or even one with such a value
   volatile int abort;
+  int joins;              // this CTA stored the last part of the unit
 };
 
-// A CTA's walk over its tiles: one segment (part of a unit) at a time.
+// A CTA's walk over its tiles: one segment (part of a unit) at a time.  All
+// lanes of a warp walk together.
 struct Walk {
-  int x, x1, e;
+  int x, x1, per, e;
   Entry t;
-  int base;       // tile0[e]
+  int base;       // tiles before entry e
   int head, rt;   // unit
   int i0, n;      // tiles [i0, i0 + n) of the unit
   int tokens0;    // new token of the unit's first row
   int rows;       // rows of the unit
-  __device__ __forceinline__ void start(const AttnWorkspace &w) {
-    const int per = __ldcg(&w.head->per), total = __ldcg(&w.head->total);
-    x = min(static_cast<int>(blockIdx.x) * per, total);
-    x1 = min(x + per, total);
-    if (x >= x1) return;
-    int lo = 0, hi = w.n_entries - 1;  // the last entry with tile0 <= x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldcg(&w.tile0[mid]) <= x) lo = mid; else hi = mid - 1;
-    }
-    e = lo;
-    load(w);
+
+  __device__ __forceinline__ int sequence_tiles(const KernelArgs &k, int e, unsigned *bits) {
+    if (e >= k.w.n_entries) return 0;
+    const SeqInfo si = seq_info(k.a.b, k.a.c.block_size, e);
+    *bits |= si.bits;
+    int unused;
+    return entry_tiles(k, si.n, 0, si.len, &unused);
   }
-  __device__ __forceinline__ void load(const AttnWorkspace &w) {
-    const int4 *p = reinterpret_cast<const int4 *>(&w.entries[e]);
-    const int4 a = __ldcg(p), b = __ldcg(p + 1);
-    t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    base = __ldcg(&w.tile0[e]);
+  __device__ __forceinline__ void start(const KernelArgs &k) {
+    const int lane = threadIdx.x & 31;
+    if (k.planned) {
+      per = __ldcg(&k.w.head->per);
+      const int total = __ldcg(&k.w.head->total);
+      x = min(static_cast<int>(blockIdx.x) * per, total);
+      x1 = min(x + per, total);
+      if (x >= x1) return;
+      int lo = 0, hi = k.w.n_entries - 1;  // the last entry with tile0 <= x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldcg(&k.w.tile0[mid]) <= x) lo = mid; else hi = mid - 1;
+      }
+      e = lo;
+    } else {
+      // the entries are the sequences: a lane each, 32 at a time
+      unsigned bits = 0;
+      int total = 0, mine = 0;
+      for (int s0 = 0; s0 < k.w.n_entries; s0 += 32) total += mine = sequence_tiles(k, s0 + lane, &bits);
+      total = __reduce_add_sync(0xffffffffu, total);
+      if (bits && blockIdx.x == 0) raise_status(k.a.status, bits);
+      per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+      x = min(static_cast<int>(blockIdx.x) * per, total);
+      x1 = min(x + per, total);
+      if (x >= x1) return;
+      base = 0;
+      for (int s0 = 0;; s0 += 32) {
+        if (k.w.n_entries > 32) mine = sequence_tiles(k, s0 + lane, &bits);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > x);
+        if (past) {
+          const int first = __ffs(past) - 1;
+          e = s0 + first;
+          base += __shfl_sync(0xffffffffu, incl - mine, first);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    load(k);
+  }
+  __device__ __forceinline__ void load(const KernelArgs &k) {
+    if (k.planned) {
+      const int4 *p = reinterpret_cast<const int4 *>(&k.w.entries[e]);
+      const int4 a = __ldcg(p), b = __ldcg(p + 1);
+      t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      base = __ldcg(&k.w.tile0[e]);
+    } else {
+      const SeqInfo si = seq_info(k.a.b, k.a.c.block_size, e);
+      t = {si.row0, si.n, e, 0, si.len, si.len - si.n, (si.len + kTile - 1) / kTile, kSolo};
+    }
   }
   __device__ __forceinline__ bool next(const KernelArgs &k) {
     if (x >= x1) return false;
-    int rts = unit_tiles(k, t.tokens);
-    while (t.tiles * rts * k.a.c.kv_heads <= x - base || t.tokens <= 0) {
-      ++e;
-      load(k.w);
+    int rts, unused;
+    for (;;) {
       rts = unit_tiles(k, t.tokens);
+      const int tiles = entry_tiles(k, t.tokens, t.kv0, t.kv1, &unused);
+      if (x - base < tiles) break;
+      base += tiles;
+      ++e;
+      load(k);
     }
     const int local = x - base, u = local / t.tiles;
     i0 = local - u * t.tiles;
@@ -640,6 +696,90 @@ __device__ __noinline__ void patch_nonfinite(const KernelArgs &k, int seq, int c
     }
     if (sum != 0.f) o[d] = from_f32<Out>(sum);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Joining a row's parts: each part p has a log-sum-exp L_p (log2) and a
+// normalised result o_p;
+//   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
+// A warp joins a row, with as many parts' loads under way as it can.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+struct Joined {
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void raise(float to) {
+    const float f = top == -INFINITY ? 0.f : fast_exp2(top - to);
+    sum *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+    top = to;
+  }
+  __device__ __forceinline__ void add(float lse, float4 x) {  // lse <= top
+    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
+    sum += f;
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  __device__ __forceinline__ float lse2() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
+  __device__ __forceinline__ float4 result() const {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+};
+
+__device__ __forceinline__ float4 load_part(const float *o, bool live) {
+  return live ? __ldcg(reinterpret_cast<const float4 *>(o) + (threadIdx.x & 31))
+              : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <typename T>
+__device__ __forceinline__ void write_row(const KernelArgs &k, int64_t rh, int row, int qh, const Joined &j) {
+  const int lane = threadIdx.x & 31;
+  const float4 x = j.result();
+  if (4 * lane < k.a.c.head_dim) {
+    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(x.x, x.y), Weights<T>::pack(x.z, x.w));
+  }
+  if (k.a.lse && lane == 0) k.a.lse[rh] = j.lse2() * 0.69314718055994531f;
+}
+
+// A row of a cut unit: its owner's part, and a continuation each of CTAs
+// cta + 1 .. cta + more at row `slot` of their slots.
+__device__ __forceinline__ Joined join_parts(const KernelArgs &k, int kind, int64_t rh, int cta, int more,
+                                             int slot) {
+  const int D = k.a.c.head_dim;
+  const bool live = 4 * static_cast<int>(threadIdx.x & 31) < D;
+  Joined j;
+  float l = __ldcg(&k.w.lse[kind][rh]);
+  float4 x = load_part(k.w.o[kind] + rh * D, live);
+  const int64_t slot0 = static_cast<int64_t>(cta + 1) * kUnitRows + slot;
+  constexpr int kBatch = 8;
+  for (int p = 0; p < more; p += kBatch) {
+    float ls[kBatch];
+    float4 xs[kBatch];
+    float top = fmaxf(j.top, l);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int64_t at = slot0 + static_cast<int64_t>(p + e) * kUnitRows;
+      const bool in = p + e < more;
+      ls[e] = in ? __ldcg(&k.w.lse_c[at]) : -INFINITY;
+      xs[e] = load_part(k.w.o_c + at * D, live && in);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) top = fmaxf(top, ls[e]);
+    j.raise(top);
+    j.add(l, x);
+    l = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) j.add(ls[e], xs[e]);
+  }
+  return j;
 }
 
 // Segment number `seg` (from 0) as warp 10 left it.  False when the wait gave
@@ -789,6 +929,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     }
     mbar_init(&s->o_free, 8);
     mbar_init(&s->stats, 8);
+    mbar_init(&s->stored, 8);
+    mbar_init(&s->counted, 1);
     s->nonfinite[0] = s->nonfinite[1] = 0;
     s->abort = (smem_addr(smem) & 1023u) != 0;  // the swizzle counts from 1 KB boundaries
     mbar_init_fence();
@@ -810,7 +952,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     const int r_tok = r / k.rep, r_head = r - r_tok * k.rep;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t t_s = tmem + lanes + g * 128, t_o = tmem + lanes + 256 + g * 128;
-    uint32_t seg = 0, turn = 0;  // segments, and tiles of this group so far
+    uint32_t seg = 0, turn = 0, cuts = 0;  // segments, tiles of this group, cut units so far
     Ring<G::kSlotsV> ring_v;
     bool ok = true;
     Seg w;
@@ -1061,6 +1203,32 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         }
       }
       __syncwarp();
+      if (k.join_inside && !whole) {
+        // the CTA that stores a cut unit's last part joins them, in their order
+        const int owner = w.join & 0xffff, more = w.join >> 16;
+        __threadfence();
+        warp_arrive(&s->stored, lane);
+        if (warp == 0) {
+          if (!(ok = warp_wait(s, &s->stored, cuts & 1u, status))) break;
+          if (lane == 0) {
+            const bool all = atomicAdd(&k.w.tickets[owner], 1u) == static_cast<unsigned>(more);
+            if (all) k.w.tickets[owner] = 0;
+            s->joins = all;
+            __threadfence();
+          }
+          warp_arrive(&s->counted, lane);
+        }
+        if (!(ok = warp_wait(s, &s->counted, cuts & 1u, status))) break;
+        ++cuts;
+        if (s->joins) {
+          for (int slot = warp; slot < w.rows; slot += 8) {
+            const int tok_in = slot / k.rep, head = w.head * k.rep + slot - tok_in * k.rep;
+            const int64_t to = static_cast<int64_t>(w.row0 + tok_in) * k.a.q_heads + head;
+            write_row<T>(k, to, w.row0 + tok_in, head, join_parts(k, 0, to, owner, more, slot));
+          }
+        }
+        __syncwarp();
+      }
     }
   } else if (warp < 10) {
     // ---- matrix products: warp 8 for group 0, warp 9 for group 1 --------------
@@ -1167,15 +1335,15 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   } else if (warp == 10) {
     // ---- segments, K ------------------------------------------------------------
     Walk w;
-    w.start(k.w);
+    w.start(k);
     Ring<G::kSlotsK> ring;
     unsigned bits = 0;
     uint32_t filled = 0, parities = 0;
     bool ok = true;
-    const int per = __ldcg(&k.w.head->per), first = static_cast<int>(blockIdx.x) * per;
+    const int per = w.per, first = static_cast<int>(blockIdx.x) * per;
     for (uint32_t seg = 0; ok; ++seg) {
       const bool more = w.next(k);
-      if (seg == 0 && lane == 0) {
+      if (seg == 0 && lane == 0 && !k.join_inside) {
         const bool cut = more && w.i0 > 0 && w.i0 <= per;
         int4 *to = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
         to[0] = cut ? make_int4(w.t.row0 + w.tokens0, w.rows, w.head,
@@ -1190,6 +1358,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
              w.t.ctx, w.t.kv1, w.t.tokens, 0, 0};
         t.flags = (w.t.flags & kShared) | ((w.t.flags & kSolo) && w.n == w.t.tiles ? kWhole : 0) |
                   (w.i0 == 0 ? kBase : 0);
+        if (k.join_inside && !(t.flags & kWhole)) {
+          const int unit0 = w.x - w.n - w.i0, owner = unit0 / per;
+          t.join = owner | (((unit0 + w.t.tiles - 1) / per - owner) << 16);
+        }
       }
       if (seg >= kSegs &&
           !(ok = warp_wait(s, &s->seg_empty[seg % kSegs], (seg / kSegs - 1) & 1u, status))) {
@@ -1199,7 +1371,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         int4 *to = reinterpret_cast<int4 *>(&s->seg[seg % kSegs]);
         to[0] = make_int4(t.row0, t.rows, t.i0, t.seq);
         to[1] = make_int4(t.head, t.t0, t.n, t.ctx);
-        to[2] = make_int4(t.kv1, t.n_new, t.flags, 0);
+        to[2] = make_int4(t.kv1, t.n_new, t.flags, t.join);
       }
       warp_arrive(&s->seg_full[seg % kSegs], lane);
       if (!more) break;
@@ -1252,57 +1424,6 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   }
 }
 
-// ---------------------------------------------------------------------------
-// Joining a row's parts: each part p has a log-sum-exp L_p (log2) and a
-// normalised result o_p;
-//   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
-// A warp joins a row, with as many parts' loads under way as it can.
-// ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
-
-struct Joined {
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void raise(float to) {
-    const float f = top == -INFINITY ? 0.f : fast_exp2(top - to);
-    sum *= f;
-    acc.x *= f;
-    acc.y *= f;
-    acc.z *= f;
-    acc.w *= f;
-    top = to;
-  }
-  __device__ __forceinline__ void add(float lse, float4 x) {  // lse <= top
-    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
-    sum += f;
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
-  }
-  __device__ __forceinline__ float lse2() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
-  __device__ __forceinline__ float4 result() const {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  }
-};
-
-__device__ __forceinline__ float4 load_part(const float *o, bool live) {
-  return live ? __ldcg(reinterpret_cast<const float4 *>(o) + (threadIdx.x & 31))
-              : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
-template <typename T>
-__device__ __forceinline__ void write_row(const KernelArgs &k, int64_t rh, int row, int qh, const Joined &j) {
-  const int lane = threadIdx.x & 31;
-  const float4 x = j.result();
-  if (4 * lane < k.a.c.head_dim) {
-    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(x.x, x.y), Weights<T>::pack(x.z, x.w));
-  }
-  if (k.a.lse && lane == 0) k.a.lse[rh] = j.lse2() * 0.69314718055994531f;
-}
-
 // The units that a CTA's range cuts: CTA (c, chunk) takes eight rows of the
 // unit that the boundary between CTAs c and c + 1 is the first to cut (CTA
 // c + 1 left its record): its owner's part and a continuation each of CTAs
@@ -1324,30 +1445,7 @@ join_cut_units_kernel(const __grid_constant__ KernelArgs k) {
   const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
   const bool live = 4 * lane < D;
   const int kind = flags & kShared;
-  Joined j;
-  float l = __ldcg(&k.w.lse[kind][rh]);
-  float4 x = load_part(k.w.o[kind] + rh * D, live);
-  const int64_t slot0 = static_cast<int64_t>(cta + 1) * kUnitRows + slot;
-  constexpr int kBatch = 8;
-  for (int p = 0; p < c.w; p += kBatch) {
-    float ls[kBatch];
-    float4 xs[kBatch];
-    float top = fmaxf(j.top, l);
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int64_t at = slot0 + static_cast<int64_t>(p + e) * kUnitRows;
-      const bool in = p + e < c.w;
-      ls[e] = in ? __ldcg(&k.w.lse_c[at]) : -INFINITY;
-      xs[e] = load_part(k.w.o_c + at * D, live && in);
-    }
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) top = fmaxf(top, ls[e]);
-    j.raise(top);
-    j.add(l, x);
-    l = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) j.add(ls[e], xs[e]);
-  }
+  const Joined j = join_parts(k, kind, rh, cta, c.w, slot);
   if (flags & kSolo) {
     write_row<T>(k, rh, row, qh, j);
   } else {
@@ -1452,7 +1550,7 @@ static bool make_map(CUtensorMap *map, const CacheArgs &c, void *base, int box) 
 }
 
 static cudaError_t launch_pdl(const void *fn, dim3 grid, unsigned block, size_t dyn, void **args,
-                              cudaStream_t st) {
+                              cudaStream_t st, bool early = true) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
@@ -1462,7 +1560,7 @@ static cudaError_t launch_pdl(const void *fn, dim3 grid, unsigned block, size_t 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;  // else the call's first kernel, in plain stream order
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -1539,20 +1637,29 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   const int64_t units = a.b.S * ((static_cast<int64_t>(a.b.max_new) + 2 * k.tile_tokens - 1) / (2 * k.tile_tokens));
   const int64_t most = (static_cast<int64_t>(a.b.T) * a.c.block_size + kTile - 1) / kTile * a.c.kv_heads * units;
   const int ctas = most < sms ? static_cast<int>(most) : sms;
-  plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // Up to 256 sequences, each CTA counts the tiles itself: a few loads a lane,
+  // against a launch of about 4 us.  Shared parts need the tables compared.
+  k.planned = k.w.groups > 0 || a.b.S > 256;
+  // Few rows: the last CTA of a cut unit joins its parts (at most ctas of each
+  // row, here under 1 MB), against another launch of about 4 us.  More rows
+  // take a kernel that spreads them over the machine.
+  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * a.b.group * k.rep;
+  const int unit_rows = static_cast<int>(most_rows < kUnitRows ? most_rows : kUnitRows);
+  k.join_inside = !k.w.groups && unit_rows * ctas <= 2048;
+  if (k.planned) {
+    plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   const bool bf16 = a.c.dtype == SMC_BF16, wide = a.c.head_dim > 64;
   void *args[] = {&k, &map_q, &map_k, &map_v};
   e = launch_pdl(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
-                 dim3(ctas), kAttnThreads, kAttnSmem, args, st);
+                 dim3(ctas), kAttnThreads, kAttnSmem, args, st, k.planned);
   if (e != cudaSuccess) return e;
   void *jargs[] = {&k};
-  if (ctas > 1) {  // else nothing is cut
-    const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * a.b.group * k.rep;
-    const int rows = static_cast<int>(most_rows < kUnitRows ? most_rows : kUnitRows);
+  if (ctas > 1 && !k.join_inside) {  // with one CTA nothing is cut
     e = launch_pdl(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
                         : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
-                   dim3(ctas - 1, (rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, jargs, st);
+                   dim3(ctas - 1, (unit_rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, jargs, st);
     if (e != cudaSuccess) return e;
   }
   if (!k.w.groups) return cudaSuccess;

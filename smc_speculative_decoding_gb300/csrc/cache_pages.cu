@@ -6,6 +6,7 @@
 namespace smcsd {
 
 constexpr int kPageThreads = 256;
+constexpr int kInFlight = 8;  // loads of a thread under way before their stores
 
 // A block seen as rows of contiguous elements: block b, row r (of `rows`, the
 // tokens and heads that are not contiguous with one another).
@@ -55,25 +56,46 @@ copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_
   for (int r = 0; r < rows; ++r) {
     const int64_t off = ((r / br.rows_inner) * br.outer_stride +
                          (r % br.rows_inner) * br.inner_stride) * esz;
-    for (int e = threadIdx.x; e < per_row; e += kPageThreads) {
-      reinterpret_cast<U *>(to + off)[e] = reinterpret_cast<const U *>(from + off)[e];
+    const U *src_row = reinterpret_cast<const U *>(from + off);
+    U *dst_row = reinterpret_cast<U *>(to + off);
+    for (int e0 = threadIdx.x; e0 < per_row; e0 += kInFlight * kPageThreads) {
+      U x[kInFlight];
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        const int e = e0 + i * kPageThreads;
+        if (e < per_row) x[i] = src_row[e];
+      }
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        const int e = e0 + i * kPageThreads;
+        if (e < per_row) dst_row[e] = x[i];
+      }
     }
   }
 }
 
 // Thread t owns column t of a token's (head, d) elements for the whole path.
-// A path ascends, so path[i] >= i: taken in order, no move overwrites a later
-// source, and no thread touches another's column.
+// A path ascends, so path[i] >= i: taken in order, with a batch's loads before
+// its stores, no move overwrites a later source, and no thread touches
+// another's column.  The places of 64 moves at a time are found by as many
+// threads; a CTA's time is then three dependent loads (the path, the blocks,
+// the first batch) and the bytes'.
+constexpr int kMoves = 64;
+
 template <typename U>
 __global__ void __launch_bounds__(kPageThreads)
 compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32_t *n_path,
                       int max_path, int esz, unsigned *status) {
-  const int s = blockIdx.x;
+  __shared__ int64_t s_from[kMoves], s_to[kMoves];
+  __shared__ int s_before[kMoves / 32 + 1], s_last;
+  const int s = blockIdx.x, tid = threadIdx.x;
+  const int32_t *p = path + static_cast<int64_t>(s) * max_path;
+  int mine = tid < kMoves && tid < max_path ? p[tid] : -1;
   const SeqInfo si = seq_info(b, c.block_size, s);
   const int n = n_path[s];
-  const bool reports = threadIdx.x == 0 && blockIdx.y == 0;
+  const bool reports = blockIdx.y == 0;
   if (si.bits || n < 0 || n > max_path) {
-    if (reports) raise_status(status, si.bits | (n < 0 || n > max_path ? SMC_DEV_BAD_ROWS : 0));
+    if (reports && tid == 0) raise_status(status, si.bits | (n < 0 || n > max_path ? SMC_DEV_BAD_ROWS : 0));
     return;
   }
   const int layer = blockIdx.y >> 1;
@@ -82,29 +104,62 @@ compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32
   const int cols = per_head * c.kv_heads;
   const int first = si.len - si.n;
   const int32_t *table = b.tables + static_cast<int64_t>(s) * b.T;
-  const int32_t *p = path + static_cast<int64_t>(s) * max_path;
-  for (int col = threadIdx.x; col < cols; col += kPageThreads) {
-    const int64_t in_token = (col / per_head) * c.head_stride * esz +
-                             static_cast<int64_t>(col % per_head) * sizeof(U);
-    int last = -1;
-    for (int i = 0; i < n; ++i) {
-      const int j = p[i];
-      if (j <= last || j >= si.n) {
-        if (reports) raise_status(status, SMC_DEV_BAD_ROWS);
-        continue;
+  if (tid == 0) s_last = -1;
+  for (int i0 = 0; i0 < n; i0 += kMoves) {
+    __syncthreads();  // the last moves' places have been read; s_last is set
+    if (tid < kMoves) {
+      const int i = i0 + tid, lane = tid & 31;
+      if (i0 > 0) mine = i < n ? p[i] : -1;
+      // an index counts when it is past every counting one before it: a
+      // running maximum over the warp, the warps and the moves before
+      const bool in = i < n && mine >= 0 && mine < si.n;
+      int top = in ? mine : -1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, up);
       }
-      last = j;
-      if (j == i) continue;
-      const int from = first + j, to = first + i;
-      const int fb = table[from / c.block_size], tb = table[to / c.block_size];
-      if (fb < 0 || fb >= c.blocks || tb < 0 || tb >= c.blocks) {
-        if (reports) raise_status(status, SMC_DEV_BAD_BLOCK);
-        continue;
+      if (lane == 31) s_before[tid >> 5] = top;
+      int before = __shfl_up_sync(0xffffffffu, top, 1);
+      if (lane == 0) before = -1;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      before = max(before, s_last);
+      for (int w = 0; w < (tid >> 5); ++w) before = max(before, s_before[w]);
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (tid == kMoves - 1) s_last = max(before, in ? mine : -1);
+      int64_t from = -1, to = -1;
+      const bool good = in && mine > before;
+      unsigned bits = i < n && !good ? SMC_DEV_BAD_ROWS : 0;
+      if (good && mine != i) {
+        const int ft = first + mine, tt = first + i;
+        const int fb = table[ft / c.block_size], tb = table[tt / c.block_size];
+        if (fb < 0 || fb >= c.blocks || tb < 0 || tb >= c.blocks) {
+          bits |= SMC_DEV_BAD_BLOCK;
+        } else {
+          from = (fb * c.block_stride + (ft % c.block_size) * c.token_stride) * esz;
+          to = (tb * c.block_stride + (tt % c.block_size) * c.token_stride) * esz;
+        }
       }
-      const int64_t fo = fb * c.block_stride + (from % c.block_size) * c.token_stride;
-      const int64_t to_ = tb * c.block_stride + (to % c.block_size) * c.token_stride;
-      *reinterpret_cast<U *>(base + to_ * esz + in_token) =
-          *reinterpret_cast<const U *>(base + fo * esz + in_token);
+      if (bits && reports) raise_status(status, bits);
+      s_from[tid] = from;
+      s_to[tid] = to;
+    }
+    __syncthreads();
+    const int moves = min(n - i0, kMoves);
+    for (int col = tid; col < cols; col += blockDim.x) {
+      char *column = base + (col / per_head) * c.head_stride * esz +
+                     static_cast<int64_t>(col % per_head) * sizeof(U);
+      for (int j = 0; j < moves; j += kInFlight) {
+        U x[kInFlight];
+#pragma unroll
+        for (int e = 0; e < kInFlight; ++e) {
+          if (j + e < moves && s_from[j + e] >= 0) x[e] = *reinterpret_cast<const U *>(column + s_from[j + e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kInFlight; ++e) {
+          if (j + e < moves && s_from[j + e] >= 0) *reinterpret_cast<U *>(column + s_to[j + e]) = x[e];
+        }
+      }
     }
   }
 }
@@ -222,16 +277,16 @@ cudaError_t launch_compact_tokens(const CacheArgs &c, const BatchArgs &b, const 
                                   const int32_t *n_path, int max_path, unsigned *status,
                                   cudaStream_t st) {
   const dim3 grid(b.S, 2 * c.layers);
-  const int esz = dtype_bytes(c.dtype);
-  switch (access_bytes(c)) {
-    case 16:
-      compact_tokens_kernel<uint4><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
-      break;
-    case 4:
-      compact_tokens_kernel<uint32_t><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
-      break;
-    default:
-      compact_tokens_kernel<uint16_t><<<grid, kPageThreads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
+  const int esz = dtype_bytes(c.dtype), width = access_bytes(c);
+  // a thread per column, as far as a CTA goes; at least those that find places
+  const int64_t cols = static_cast<int64_t>(c.kv_heads) * c.head_dim * esz / width;
+  const int threads = cols >= kPageThreads ? kPageThreads
+                      : cols > kMoves      ? static_cast<int>((cols + 31) / 32 * 32)
+                                           : kMoves;
+  switch (width) {
+    case 16: compact_tokens_kernel<uint4><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status); break;
+    case 4: compact_tokens_kernel<uint32_t><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status); break;
+    default: compact_tokens_kernel<uint16_t><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
   }
   return cudaGetLastError();
 }

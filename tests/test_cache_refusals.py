@@ -81,7 +81,8 @@ def test_bad_batches(lib, kw):
     dict(out=None), dict(layer=-1), dict(layer=2), dict(q=PTR + 2), dict(out=PTR + 8), dict(q_row_stride=1001),
     dict(q_head_stride=4), dict(out_row_stride=-8), dict(out_head_stride=129), dict(cache=_cache(head_dim=136)),
     dict(cache=_cache(head_dim=20)), dict(cache=_cache(token_stride=260)), dict(cache=_cache(k=PTR + 2)),
-    dict(cache=_cache(layer_stride=4), layer=1)])
+    dict(cache=_cache(layer_stride=4), layer=1), dict(q_row_stride=0), dict(q_head_stride=0),
+    dict(q_heads=258)])
 def test_bad_attention_arguments(lib, kw):
     assert _attn(lib, **kw) == ARG
 

@@ -106,6 +106,56 @@ def test_attention_shared_prefix(group, shared, ctx, new, mask):
     _check_attention(c, out, lse, ws)
 
 
+def _check_like_double(c, out, lse):
+    """Against torch in 64 bits on padded tensors: for shapes that the loops
+    of the reference would take long over."""
+    S, T, rep = len(c.ctx), c.tables.shape[1] * c.block, c.heads // c.kv_heads
+    at = torch.arange(T, device="cuda")[None].expand(S, -1)
+    slot = c.tables.long().clamp(min=0).gather(1, at // c.block)
+    k, v = (x[c.layer][slot, at % c.block].double() for x in (c.k, c.v))
+    held = at < c.seq_len[:, None]
+    for b in range(S):
+        r0, r1, n = int(c.starts[b]), int(c.starts[b + 1]), c.lengths[b]
+        if r0 == r1:
+            continue
+        q = c.q[r0:r1].double().unflatten(1, (c.kv_heads, rep))
+        z = torch.einsum("rhgd,thd->rhgt", q, k[b, :n]) * c.scale
+        sees = torch.zeros((r1 - r0, n), dtype=torch.bool, device="cuda")
+        sees[:, :c.ctx[b]] = True
+        for r in range(r0, r1):
+            cols = list(range(r - r0 + 1)) if c.seen is None else c.seen[r]
+            sees[r - r0, [c.ctx[b] + j for j in cols]] = True
+        z = z.masked_fill(~sees[:, None, None], -math.inf)
+        p = torch.softmax(z, -1)
+        want = torch.einsum("rhgt,thd->rhgd", p, v[b, :n])
+        mag = torch.einsum("rhgt,thd->rhgd", p, v[b, :n].abs())
+        u = torch.finfo(c.dtype).eps / 2
+        got = out[r0:r1].double().unflatten(1, (c.kv_heads, rep))
+        # weights and result rounded once each, fp32 scores and sums
+        assert ((got - want).abs() <= 1.01 * u * (mag + want.abs()) + 1e-3 * u * mag + 2.0 ** -17 * mag).all()
+        got = lse[r0:r1].double().unflatten(1, (c.kv_heads, rep))
+        assert ((got - torch.logsumexp(z, -1)).abs() <= 1e-5).all()
+
+
+@pytest.mark.parametrize("ctx,new,kw", [
+    ([3000, 9000, 500, 0, 6400, 77], [5, 64, 1, 30, 128, 2], dict(mask="tree", heads=32, kv_heads=8)),
+    ([20000, 100], [8, 8], dict(mask="tree", heads=64, kv_heads=8, block=64)),
+    ([1500] * 40, [16] * 40, dict(heads=16, kv_heads=4, block=32)),
+    ([900, 1100, 1300, 700] * 12, [5] * 48, dict(heads=16, kv_heads=4, group=4, shared=640)),
+    ([130] * 400, [1] * 400, dict(heads=8, kv_heads=2)),           # more sequences than one CTA counts
+    ([3000] * 3, [40] * 3, dict(heads=12, kv_heads=4, dim=64, mask="tree")),
+    ([2500, 40], [30, 30], dict(heads=24, kv_heads=1, dim=96, block=20, mask="tree")),  # odd blocks: element copies
+    ([5000], [2], dict(heads=128, kv_heads=1)),                     # as many heads as a row tile holds
+])
+def test_attention_of_larger_batches(ctx, new, kw):
+    c = CacheCase(ctx, new, poison=False, **kw)
+    out, lse, ws = _attend(c)
+    assert smcsd.smc_device_status(ws) == 0
+    _check_like_double(c, out, lse)
+    again, lse2, _ = _attend(c, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_of_many_sequences():
     rng = np.random.default_rng(3)
     ctx, new = rng.integers(0, 300, 300).tolist(), rng.integers(0, 4, 300).tolist()
@@ -317,6 +367,31 @@ def test_qk_in_place_far_positions_and_bad_rows():
     assert smcsd.status_names(smcsd.smc_device_status(ws, clear=True)) == ["bad_block"]
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,norm_q,norm_k", [
+    (32, 8, 128, True, False), (32, 8, 128, False, True), (71, 1, 64, True, True), (3, 3, 96, False, True),
+    (64, 64, 128, True, True), (1, 1, 8, True, True), (100, 4, 256, True, False)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_qk_heads_and_one_norm(heads, kv_heads, dim, norm_q, norm_k, dtype):
+    c = CacheCase([20, 3, 64, 0], [4, 4, 1, 3], heads=heads, kv_heads=kv_heads, dim=dim, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    q, k, v = (torch.randn((c.rows, n, dim), generator=g, device="cuda").to(dtype) for n in (heads, kv_heads, kv_heads))
+    w = (torch.randn(dim, generator=g, device="cuda") * 0.2 + 1).to(dtype)
+    table = rope_table(100, dim)
+    own = torch.cat([torch.arange(a, a + m) for a, m in zip(c.ctx, c.new)]).to(torch.int32).cuda()
+    cache, batch = c.cache(smcsd), c.batch(smcsd)
+    ws = smcsd.alloc_cache_workspace(cache)
+    out = torch.empty_like(q)
+    smcsd.smc_qk_norm_rope(cache, 0, batch, q, k, v, table, out, ws, q_weight=w if norm_q else None,
+                           k_weight=w if norm_k else None)
+    assert smcsd.smc_device_status(ws) == 0
+    at = [(c.tables[s, p // c.block], p % c.block) for s in range(4) for p in range(c.ctx[s], c.lengths[s])]
+    stored = torch.stack([c.k[0, b, o] for b, o in at])
+    for got, x, normed in ((out, q, norm_q), (stored, k, norm_k)):
+        ref, tol = qk_reference(x, w if normed else None, table, own, dim, False, 1e-6, 0.0)
+        assert ((got.double() - ref).abs() <= tol).all()
+    assert torch.equal(torch.stack([c.v[0, b, o] for b, o in at]), v)
+
+
 def test_qk_rows_of_zeros_and_infinities():
     """A zero row has no direction: eps keeps it 0; a row with an infinity is
     NaN, as its formula is."""
@@ -397,6 +472,34 @@ def test_compact_tokens(dim, block, kw, dtype):
     smcsd.kv_compact_tokens(cache, c.batch(smcsd), padded, n_path, ws)
     assert smcsd.smc_device_status(ws) == 0
     assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+
+
+def test_compact_of_long_paths():
+    """Paths longer than the moves that one pass places."""
+    rng = np.random.default_rng(8)
+    new = [300, 200]
+    c = CacheCase([5, 31], new, dim=64, layers=2, block=16)
+    path = [sorted(rng.choice(300, 190, replace=False).tolist()), sorted(rng.choice(200, 65, replace=False).tolist())]
+    n_path = torch.tensor([len(p) for p in path], dtype=torch.int32, device="cuda")
+    padded = torch.tensor([p + [0] * (200 - len(p)) for p in path], dtype=torch.int32, device="cuda")
+    before = c.k.clone(), c.v.clone()
+    want = c.k.clone(), c.v.clone()
+    for s, p in enumerate(path):
+        for i, j in enumerate(p):
+            a, b = c.ctx[s] + j, c.ctx[s] + i
+            for w, old in zip(want, before):
+                w[:, c.tables[s, b // 16], b % 16] = old[:, c.tables[s, a // 16], a % 16]
+    cache = c.cache(smcsd)
+    ws = smcsd.alloc_cache_workspace(cache)
+    smcsd.kv_compact_tokens(cache, c.batch(smcsd), padded, n_path, ws)
+    assert smcsd.smc_device_status(ws) == 0
+    assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+    # a bad index deep in a path is reported, whichever pass it falls in
+    for at in (3, 63, 64, 70, 189):
+        bad = padded.clone()
+        bad[0, at] = bad[0, at - 1]
+        smcsd.kv_compact_tokens(cache, c.batch(smcsd), bad, n_path, ws)
+        assert smcsd.status_names(smcsd.smc_device_status(ws, clear=True)) == ["bad_rows"], at
 
 
 def test_compact_reports_bad_paths():

@@ -455,8 +455,7 @@ def make_cache(k, v):
     """smc_cache over keys and values [layers, blocks, block_size, kv_heads,
     head_dim]: CUDA tensors of one dtype (fp32, bf16 or fp16), one shape and
     one set of strides, the last of them 1 (a head-major cache, or a slice of
-    a larger one, is passed as a view).  The struct holds their addresses:
-    keep the tensors."""
+    a larger one, is passed as a view).  The struct keeps the tensors alive."""
     for name, t in (("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -469,7 +468,9 @@ def make_cache(k, v):
         raise ValueError("k and v must have one shape, dtype and set of strides")
     if k.numel() == 0 or (k.stride(4) != 1 and k.shape[4] > 1):
         raise ValueError("k and v must not be empty and their last axis must be contiguous")
-    return smc_cache(k.data_ptr(), v.data_ptr(), *k.stride()[:4], *k.shape, _CACHE_DTYPES[k.dtype])
+    cache = smc_cache(k.data_ptr(), v.data_ptr(), *k.stride()[:4], *k.shape, _CACHE_DTYPES[k.dtype])
+    cache.tensors = (k, v)
+    return cache
 
 
 def make_batch(tables, seq_len, max_new, row_start=None, rows=None, group=1):
@@ -477,15 +478,17 @@ def make_batch(tables, seq_len, max_new, row_start=None, rows=None, group=1):
     the KV state) and seq_len [S] int32, at most max_new new tokens each;
     row_start [S + 1] int32 when their numbers differ, with `rows` rows in the
     arrays (default S * max_new).  group: consecutive sequences of one prompt.
-    The struct holds the tensors' addresses: keep the tensors."""
+    The struct keeps the tensors alive."""
     S = seq_len.numel()
     T = tables.shape[-1]
     if rows is None:
         rows = S * max_new
-    return smc_batch(_ptr(tables, "tables", torch.int32, S * T),
-                     _ptr(seq_len, "seq_len", torch.int32),
-                     None if row_start is None else _ptr(row_start, "row_start", torch.int32, S + 1),
-                     S, T, int(rows), int(max_new), int(group))
+    batch = smc_batch(_ptr(tables, "tables", torch.int32, S * T),
+                      _ptr(seq_len, "seq_len", torch.int32),
+                      None if row_start is None else _ptr(row_start, "row_start", torch.int32, S + 1),
+                      S, T, int(rows), int(max_new), int(group))
+    batch.tensors = (tables, seq_len, row_start)
+    return batch
 
 
 def smc_cache_workspace_bytes(cache, batch=None, q_heads=0):

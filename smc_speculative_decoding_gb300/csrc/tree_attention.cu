@@ -369,6 +369,9 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
       "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(token), "r"(head), "r"(block)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int d, int head,
                                             int row, uint64_t *bar) {
   asm volatile(
@@ -936,6 +939,13 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     mbar_init_fence();
   }
   if (warp == 8) tmem_alloc_512(&s->tmem);
+  if (warp == 9 && elect_one()) {
+    prefetch_map(&map_q);
+    if (kTma) {
+      prefetch_map(&map_k);
+      prefetch_map(&map_v);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1206,11 +1216,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       if (k.join_inside && !whole) {
         // the CTA that stores a cut unit's last part joins them, in their order
         const int owner = w.join & 0xffff, more = w.join >> 16;
-        __threadfence();
         warp_arrive(&s->stored, lane);
         if (warp == 0) {
           if (!(ok = warp_wait(s, &s->stored, cuts & 1u, status))) break;
           if (lane == 0) {
+            __threadfence();  // what the CTA stored, ahead of the count
             const bool all = atomicAdd(&k.w.tickets[owner], 1u) == static_cast<unsigned>(more);
             if (all) k.w.tickets[owner] = 0;
             s->joins = all;
@@ -1613,7 +1623,12 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   if (e != cudaSuccess) return e;
   KernelArgs k{};
   k.a = a;
-  carve(a.c, a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
+  // Reading shared blocks once takes two more kernels and a second part of
+  // every row, about 15 us.  While all the sequences' tables hold less than
+  // what the L2 cache does, reading them again costs less than that.
+  const double table_bytes = static_cast<double>(a.b.S) * a.b.T * a.c.block_size * a.c.kv_heads * a.c.head_dim * 4;
+  if (table_bytes < 96e6) k.a.b.group = 1;
+  carve(a.c, k.a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
   k.rep = a.q_heads / a.c.kv_heads;
   k.tile_tokens = kRows / k.rep;
   k.q_box = a.b.rows < k.tile_tokens ? a.b.rows : k.tile_tokens;
@@ -1640,12 +1655,13 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   // Up to 256 sequences, each CTA counts the tiles itself: a few loads a lane,
   // against a launch of about 4 us.  Shared parts need the tables compared.
   k.planned = k.w.groups > 0 || a.b.S > 256;
-  // Few rows: the last CTA of a cut unit joins its parts (at most ctas of each
-  // row, here under 1 MB), against another launch of about 4 us.  More rows
-  // take a kernel that spreads them over the machine.
-  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * a.b.group * k.rep;
+  // Few parts: the last CTA of a cut unit joins them, against another launch
+  // of about 4 us; a CTA takes about 8 us for 1344 parts (64 rows of 21), so
+  // more of them take a kernel that spreads them over the machine.  A unit
+  // spans at most 1 / kv_heads of the line, as its sequence has as many.
+  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * k.a.b.group * k.rep;
   const int unit_rows = static_cast<int>(most_rows < kUnitRows ? most_rows : kUnitRows);
-  k.join_inside = !k.w.groups && unit_rows * ctas <= 2048;
+  k.join_inside = !k.w.groups && unit_rows * (ctas / a.c.kv_heads + 2) <= 1024;
   if (k.planned) {
     plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

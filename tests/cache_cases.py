@@ -31,7 +31,7 @@ class CacheCase:
 
     def __init__(self, ctx, new, heads=8, kv_heads=2, dim=128, block=16, dtype=torch.bfloat16,
                  order="nhd", layers=1, layer=0, group=1, shared=0, mask="chain", seed=0,
-                 device="cuda", poison=False, strided=False, max_new=None, sigma=1.0):
+                 device="cuda", poison=False, strided=False, max_new=None, sigma=1.0, slots=0):
         g = torch.Generator().manual_seed(seed)
         self.ctx, self.new, self.lengths = ctx, new, [a + b for a, b in zip(ctx, new)]
         self.heads, self.kv_heads, self.dim, self.block = heads, kv_heads, dim, block
@@ -40,7 +40,7 @@ class CacheCase:
         S = len(ctx)
         need = [-(-n // block) for n in self.lengths]
         common = shared // block
-        T = max(1, max(need)) + 1
+        T = max(max(need) + 1, 2, slots)
         count = sum(need) + 3
         order_ids = torch.randperm(count, generator=g).tolist()
         tables = torch.full((S, T), -1, dtype=torch.int32)

@@ -98,12 +98,24 @@ def test_attention_memory_orders(order, strided, block):
     (8, 640, [650] * 8 + [700] * 8, [17] * 16),     # more rows than one tile over the shared part
     (3, 0, [50, 60, 70], [2, 2, 2]),
     (2, 384, [384, 384], [1, 0]),
+    (4, 256, [300, 290, 280, 310, 0, 5, 0, 1], [0, 3, 0, 2, 1, 1, 0, 2]),  # one prompt shares nothing
+    (2, 1024, [1100, 1030], [30, 35]),
 ])
 @pytest.mark.parametrize("mask", ["chain", "tree"])
-def test_attention_shared_prefix(group, shared, ctx, new, mask):
-    c = CacheCase(ctx, new, group=group, shared=shared, heads=8, kv_heads=2, mask=mask, poison=True)
+@pytest.mark.parametrize("slots", [0, 3100])  # tables as large as those whose shared blocks are read once
+def test_attention_shared_prefix(group, shared, ctx, new, mask, slots):
+    shared = min([shared] + [c for c in ctx if shared and c >= shared]) if shared else 0
+    ctx = [max(c, shared) if i // group == 0 else c for i, c in enumerate(ctx)]
+    one = any(c < shared for c in ctx)
+    c = CacheCase(ctx, new, group=group, shared=0 if one else shared, heads=8, kv_heads=2, mask=mask, poison=True,
+                  slots=slots)
+    if one:  # only the first prompt's sequences share their leading blocks
+        n = shared // c.block
+        c.tables[1:group, :n] = c.tables[:1, :n]
     out, lse, ws = _attend(c)
     _check_attention(c, out, lse, ws)
+    again, lse2, _ = _attend(c, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
 def _check_like_double(c, out, lse):
@@ -142,6 +154,8 @@ def _check_like_double(c, out, lse):
     ([20000, 100], [8, 8], dict(mask="tree", heads=64, kv_heads=8, block=64)),
     ([1500] * 40, [16] * 40, dict(heads=16, kv_heads=4, block=32)),
     ([900, 1100, 1300, 700] * 12, [5] * 48, dict(heads=16, kv_heads=4, group=4, shared=640)),
+    ([900, 1100, 1300, 700] * 12, [5] * 48, dict(heads=16, kv_heads=4, group=4, shared=640, slots=400)),
+    ([700] * 48, [70] * 48, dict(heads=16, kv_heads=4, group=16, shared=512, slots=400, mask="tree")),
     ([130] * 400, [1] * 400, dict(heads=8, kv_heads=2)),           # more sequences than one CTA counts
     ([3000] * 3, [40] * 3, dict(heads=12, kv_heads=4, dim=64, mask="tree")),
     ([2500, 40], [30, 30], dict(heads=24, kv_heads=1, dim=96, block=20, mask="tree")),  # odd blocks: element copies

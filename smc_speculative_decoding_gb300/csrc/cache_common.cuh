@@ -10,6 +10,11 @@
 
 namespace smcsd {
 
+// The kernels ahead in the stream have ended and their writes are visible.
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
 template <>

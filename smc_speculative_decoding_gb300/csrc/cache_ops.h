@@ -53,6 +53,13 @@ struct AttnArgs {
   unsigned *status;
 };
 
+// Launches with programmatic stream serialisation: a kernel's CTAs may start
+// while the kernel ahead of it in the stream drains, and wait for it in full
+// (wait_for_stream) before they touch global memory.  About 3 us of a small
+// attention call that follows another.
+cudaError_t launch_early(const void *fn, dim3 grid, unsigned block, size_t dyn, void **args,
+                         cudaStream_t st);
+
 // Workspace of the cache entry points: the status word first (256 bytes).
 constexpr size_t kCacheStatusBytes = 256;
 size_t attention_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads);

@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kPageThreads)
 copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_t *counts,
                    int max_pairs, int esz, unsigned *status) {
   const int list = blockIdx.x / max_pairs, i = blockIdx.x % max_pairs;
+  wait_for_stream();
   const int n = counts[list];
   if (n < 0 || n > max_pairs) {
     if (threadIdx.x == 0) raise_status(status, SMC_DEV_BAD_ROWS);
@@ -89,6 +90,7 @@ compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32
   __shared__ int64_t s_from[kMoves], s_to[kMoves];
   __shared__ int s_before[kMoves / 32 + 1], s_last;
   const int s = blockIdx.x, tid = threadIdx.x;
+  wait_for_stream();
   const int32_t *p = path + static_cast<int64_t>(s) * max_path;
   int mine = tid < kMoves && tid < max_path ? p[tid] : -1;
   const SeqInfo si = seq_info(b, c.block_size, s);
@@ -257,38 +259,34 @@ static int access_bytes(const CacheArgs &c) {
 
 cudaError_t launch_copy_blocks(const CacheArgs &c, const int32_t *pairs, const int32_t *counts,
                                int lists, int max_pairs, unsigned *status, cudaStream_t st) {
-  const dim3 grid(lists * max_pairs, 2 * c.layers);
-  const BlockRows br = block_rows(c);
-  const int esz = dtype_bytes(c.dtype);
-  switch (access_bytes(c)) {
-    case 16:
-      copy_blocks_kernel<uint4><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
-      break;
-    case 4:
-      copy_blocks_kernel<uint32_t><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
-      break;
-    default:
-      copy_blocks_kernel<uint16_t><<<grid, kPageThreads, 0, st>>>(c, br, pairs, counts, max_pairs, esz, status);
-  }
-  return cudaGetLastError();
+  CacheArgs cache = c;
+  BlockRows rows = block_rows(c);
+  int esz = dtype_bytes(c.dtype);
+  const int width = access_bytes(c);
+  const void *fn = width == 16  ? reinterpret_cast<const void *>(copy_blocks_kernel<uint4>)
+                   : width == 4 ? reinterpret_cast<const void *>(copy_blocks_kernel<uint32_t>)
+                                : reinterpret_cast<const void *>(copy_blocks_kernel<uint16_t>);
+  void *args[] = {&cache, &rows, &pairs, &counts, &max_pairs, &esz, &status};
+  return launch_early(fn, dim3(lists * max_pairs, 2 * c.layers), kPageThreads, 0, args, st);
 }
 
 cudaError_t launch_compact_tokens(const CacheArgs &c, const BatchArgs &b, const int32_t *path,
                                   const int32_t *n_path, int max_path, unsigned *status,
                                   cudaStream_t st) {
-  const dim3 grid(b.S, 2 * c.layers);
-  const int esz = dtype_bytes(c.dtype), width = access_bytes(c);
+  CacheArgs cache = c;
+  BatchArgs batch = b;
+  int esz = dtype_bytes(c.dtype);
+  const int width = access_bytes(c);
   // a thread per column, as far as a CTA goes; at least those that find places
   const int64_t cols = static_cast<int64_t>(c.kv_heads) * c.head_dim * esz / width;
   const int threads = cols >= kPageThreads ? kPageThreads
                       : cols > kMoves      ? static_cast<int>((cols + 31) / 32 * 32)
                                            : kMoves;
-  switch (width) {
-    case 16: compact_tokens_kernel<uint4><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status); break;
-    case 4: compact_tokens_kernel<uint32_t><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status); break;
-    default: compact_tokens_kernel<uint16_t><<<grid, threads, 0, st>>>(c, b, path, n_path, max_path, esz, status);
-  }
-  return cudaGetLastError();
+  const void *fn = width == 16  ? reinterpret_cast<const void *>(compact_tokens_kernel<uint4>)
+                   : width == 4 ? reinterpret_cast<const void *>(compact_tokens_kernel<uint32_t>)
+                                : reinterpret_cast<const void *>(compact_tokens_kernel<uint16_t>);
+  void *args[] = {&cache, &batch, &path, &n_path, &max_path, &esz, &status};
+  return launch_early(fn, dim3(b.S, 2 * c.layers), threads, 0, args, st);
 }
 
 cudaError_t launch_kv_truncate(int B, int N, const KvArgs &kv, const int32_t *new_len,

@@ -10,8 +10,9 @@ constexpr int kQkMaxPerLane = 8;  // head_dim <= 256 over 32 lanes
 // Any sizes, strides and alignment: one CTA per row; a warp per head, each lane
 // elements lane, lane + 32, ...
 template <typename T>
-__global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_constant__ QkArgs a) {
   const int row = blockIdx.x;
+  wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = seq_of_row(a.b, row);
   if (s < 0) return;
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kQkThreads, 16) qk_vectors_kernel(const __grid
   };
   // k's heads start at the first group, v's at the last one
   const int v0 = groups - 1 - group;
+  wait_for_stream();
   uint4 rq[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) rq[i] = fetch(a.q, a.q_row, a.q_head, a.q_heads, group + i * groups);
@@ -357,36 +359,33 @@ static bool vectors_ok(const QkArgs &a) {
 }
 
 template <typename T, bool kInter>
-static void launch_vectors(const QkArgs &a, cudaStream_t st) {
+static cudaError_t launch_vectors(const QkArgs &a, cudaStream_t st) {
   const int vectors = a.c.head_dim * static_cast<int>(sizeof(T)) / 16, heads = a.q_heads + 2 * a.c.kv_heads;
   const int lanes = vectors <= 8 ? 8 : vectors <= 16 ? 16 : 32;
   // no more threads than heads to start on
   const int threads = heads * lanes < kQkThreads ? (heads * lanes + 31) / 32 * 32 : kQkThreads;
-  switch (lanes) {
-    case 8: qk_vectors_kernel<T, 8, kInter><<<a.b.rows, threads, 0, st>>>(a); break;
-    case 16: qk_vectors_kernel<T, 16, kInter><<<a.b.rows, threads, 0, st>>>(a); break;
-    default: qk_vectors_kernel<T, 32, kInter><<<a.b.rows, threads, 0, st>>>(a); break;
-  }
+  const void *fn = lanes == 8    ? reinterpret_cast<const void *>(qk_vectors_kernel<T, 8, kInter>)
+                   : lanes == 16 ? reinterpret_cast<const void *>(qk_vectors_kernel<T, 16, kInter>)
+                                 : reinterpret_cast<const void *>(qk_vectors_kernel<T, 32, kInter>);
+  void *args[] = {const_cast<QkArgs *>(&a)};
+  return launch_early(fn, dim3(a.b.rows), threads, 0, args, st);
 }
 
 cudaError_t launch_qk_norm_rope(const QkArgs &a, cudaStream_t st) {
   if (a.b.rows == 0) return cudaSuccess;
   if (vectors_ok(a)) {
     switch (a.c.dtype) {
-      case SMC_F32: a.interleaved ? launch_vectors<float, true>(a, st) : launch_vectors<float, false>(a, st); break;
+      case SMC_F32: return a.interleaved ? launch_vectors<float, true>(a, st) : launch_vectors<float, false>(a, st);
       case SMC_BF16:
-        a.interleaved ? launch_vectors<__nv_bfloat16, true>(a, st) : launch_vectors<__nv_bfloat16, false>(a, st);
-        break;
-      default: a.interleaved ? launch_vectors<__half, true>(a, st) : launch_vectors<__half, false>(a, st); break;
+        return a.interleaved ? launch_vectors<__nv_bfloat16, true>(a, st) : launch_vectors<__nv_bfloat16, false>(a, st);
+      default: return a.interleaved ? launch_vectors<__half, true>(a, st) : launch_vectors<__half, false>(a, st);
     }
-    return cudaGetLastError();
   }
-  switch (a.c.dtype) {
-    case SMC_F32: qk_rows_kernel<float><<<a.b.rows, kQkThreads, 0, st>>>(a); break;
-    case SMC_BF16: qk_rows_kernel<__nv_bfloat16><<<a.b.rows, kQkThreads, 0, st>>>(a); break;
-    default: qk_rows_kernel<__half><<<a.b.rows, kQkThreads, 0, st>>>(a); break;
-  }
-  return cudaGetLastError();
+  const void *fn = a.c.dtype == SMC_F32    ? reinterpret_cast<const void *>(qk_rows_kernel<float>)
+                   : a.c.dtype == SMC_BF16 ? reinterpret_cast<const void *>(qk_rows_kernel<__nv_bfloat16>)
+                                           : reinterpret_cast<const void *>(qk_rows_kernel<__half>);
+  void *args[] = {const_cast<QkArgs *>(&a)};
+  return launch_early(fn, dim3(a.b.rows), kQkThreads, 0, args, st);
 }
 
 }  // namespace smcsd

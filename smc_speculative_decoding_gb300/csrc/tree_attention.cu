@@ -113,6 +113,7 @@ struct KernelArgs {
   int tile_tokens;  // new tokens of a row tile: floor(128 / rep)
   int q_box;    // new tokens of a copied box of Q
   int planned;      // plan_kernel has run (else each CTA finds its own work)
+  int more_kernels; // joins follow (a call's last kernel lets nothing start before its end)
   int join_inside;  // the last CTA of a cut unit joins its parts
   int box;      // tokens per copied box
   uint32_t magic, shift;  // t / block_size == umulhi(t, magic) >> shift
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ bool s_last;
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
   const BatchArgs &b = k.a.b;
   const int bs = k.a.c.block_size;
   if (k.w.groups) {
@@ -950,8 +952,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s->tmem;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
+  if (k.more_kernels) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (s->abort) {
     if (tid == 0) raise_status(status, SMC_DEV_TIMEOUT);
@@ -1444,7 +1446,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 join_cut_units_kernel(const __grid_constant__ KernelArgs k) {
   // the last kernel of a call lets nothing start before it has ended
   if (k.w.groups) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const int cta = blockIdx.x, lane = threadIdx.x & 31;
   const int4 *cut = reinterpret_cast<const int4 *>(&k.w.cuts[cta + 1]);
   const int4 c = __ldcg(cut);  // row0, rows, head, more
@@ -1473,9 +1475,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 join_shared_kernel(const __grid_constant__ KernelArgs k) {
   const BatchArgs &b = k.a.b;
   const int row = blockIdx.x;
+  wait_for_stream();
   int seq = min(row / b.max_new, b.S - 1);  // right when every sequence has max_new rows
   if (b.row_start && !(b.row_start[seq] <= row && row < b.row_start[seq + 1])) seq = seq_of_row(b, row);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // without a shared part the row is written already; its rows are in order with one
   if (seq < 0 || __ldcg(&k.w.common[seq / b.group]) == 0) return;
   const int D = k.a.c.head_dim, lane = threadIdx.x & 31;
@@ -1557,21 +1559,6 @@ static bool make_map(CUtensorMap *map, const CacheArgs &c, void *base, int box) 
             4, base, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-static cudaError_t launch_pdl(const void *fn, dim3 grid, unsigned block, size_t dyn, void **args,
-                              cudaStream_t st, bool early = true) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = dyn;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;  // else the call's first kernel, in plain stream order
-  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 template <typename T>
@@ -1662,24 +1649,28 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * k.a.b.group * k.rep;
   const int unit_rows = static_cast<int>(most_rows < kUnitRows ? most_rows : kUnitRows);
   k.join_inside = !k.w.groups && unit_rows * (ctas / a.c.kv_heads + 2) <= 1024;
+  k.more_kernels = k.w.groups > 0 || (ctas > 1 && !k.join_inside);
   if (k.planned) {
-    plan_kernel<<<k.w.groups ? k.w.groups : 1, kPlanThreads, 0, st>>>(k, ctas);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    int n = ctas;
+    void *pargs[] = {&k, &n};
+    e = launch_early(reinterpret_cast<const void *>(plan_kernel), dim3(k.w.groups ? k.w.groups : 1), kPlanThreads,
+                     0, pargs, st);
+    if (e != cudaSuccess) return e;
   }
   const bool bf16 = a.c.dtype == SMC_BF16, wide = a.c.head_dim > 64;
   void *args[] = {&k, &map_q, &map_k, &map_v};
-  e = launch_pdl(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
-                 dim3(ctas), kAttnThreads, kAttnSmem, args, st, k.planned);
+  e = launch_early(bf16 ? attention_fn<__nv_bfloat16>(wide, tma) : attention_fn<__half>(wide, tma),
+                 dim3(ctas), kAttnThreads, kAttnSmem, args, st);
   if (e != cudaSuccess) return e;
   void *jargs[] = {&k};
   if (ctas > 1 && !k.join_inside) {  // with one CTA nothing is cut
-    e = launch_pdl(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
+    e = launch_early(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
                         : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
                    dim3(ctas - 1, (unit_rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, jargs, st);
     if (e != cudaSuccess) return e;
   }
   if (!k.w.groups) return cudaSuccess;
-  return launch_pdl(bf16 ? reinterpret_cast<const void *>(join_shared_kernel<__nv_bfloat16>)
+  return launch_early(bf16 ? reinterpret_cast<const void *>(join_shared_kernel<__nv_bfloat16>)
                          : reinterpret_cast<const void *>(join_shared_kernel<__half>),
                     dim3(a.b.rows), 32 * kJoinWarps, 0, jargs, st);
 }

@@ -506,21 +506,20 @@ def alloc_cache_workspace(cache, batch=None, q_heads=0, device="cuda"):
                        device=device)
 
 
-def _rows(t, name, cache, rows, heads):
-    """A [rows, heads, head_dim] tensor of the cache's dtype: its pointer and
-    its row and head strides."""
+def _rows(t, name, dtype, shape):
+    """A [rows, heads, head_dim] CUDA tensor of the cache's dtype, its last
+    axis contiguous: its address and its row and head strides."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape:
+        row, head, dim = t.stride()
+        if dim == 1 or shape[2] == 1:
+            return t.data_ptr(), row, head
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    shape = (rows, heads, cache.head_dim)
-    if t.shape != shape or t.dtype != _CACHE_TORCH[cache.dtype]:
-        raise ValueError(f"{name} must be {shape} in {_CACHE_TORCH[cache.dtype]}, "
-                         f"got {tuple(t.shape)} {t.dtype}")
-    row, head, dim = t.stride()
-    if dim != 1 and cache.head_dim > 1:
-        raise ValueError(f"{name}'s last axis must be contiguous")
-    return t.data_ptr(), row, head
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {shape} in {dtype}, got {tuple(t.shape)} {t.dtype}")
+    raise ValueError(f"{name}'s last axis must be contiguous")
 
 
 def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=None, scale=None,
@@ -529,20 +528,21 @@ def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=No
     sequences' caches into out; mask [rows, words] int32 of packed bits (None:
     a chain), lse [rows, q_heads] fp32 (None: not wanted), scale (None:
     head_dim ** -0.5).  See smc_tree_attention in smcsd.h."""
-    rows = batch.rows
+    rows, dim, dtype = batch.rows, cache.head_dim, _CACHE_TORCH[cache.dtype]
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     heads = q.shape[1]
-    qp, q_row, q_head = _rows(q, "q", cache, rows, heads)
-    op, o_row, o_head = _rows(out, "out", cache, rows, heads)
+    shape = (rows, heads, dim)
+    qp, q_row, q_head = _rows(q, "q", dtype, shape)
+    op, o_row, o_head = _rows(out, "out", dtype, shape)
     words = 0
     if mask is not None:
         if mask.dim() != 2 or mask.shape[0] != rows:
             raise ValueError(f"mask must be [{rows}, words], got {tuple(mask.shape)}")
         words = mask.shape[1]
-    params = smc_attn_params(heads, words, cache.head_dim ** -0.5 if scale is None else scale, 0,
+    params = smc_attn_params(heads, words, dim ** -0.5 if scale is None else scale, 0,
                              q_row, q_head, o_row, o_head)
-    _check("smc_tree_attention", lib().smc_tree_attention(
+    _check("smc_tree_attention", (_lib or lib()).smc_tree_attention(
         ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp,
         None if mask is None else _addr(mask, "mask", torch.int32), op,
         None if lse is None else _addr(lse, "lse", torch.float32, rows * heads),
@@ -557,21 +557,22 @@ def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, posit
     [max_pos, rot_dim] fp32: cosines, then sines; positions [rows] int32
     (None: the tokens' own); weights [head_dim] (None: no norm).  See
     smc_qk_norm_rope in smcsd.h."""
-    rows = batch.rows
+    rows, dim, dtype = batch.rows, cache.head_dim, _CACHE_TORCH[cache.dtype]
     if q.dim() != 3 or rope.dim() != 2:
         raise ValueError("q must be [rows, q_heads, head_dim] and rope [max_pos, rot_dim]")
-    heads, dtype = q.shape[1], _CACHE_TORCH[cache.dtype]
-    qp, q_row, q_head = _rows(q, "q", cache, rows, heads)
-    kp, k_row, k_head = _rows(k, "k", cache, rows, cache.kv_heads)
-    vp, v_row, v_head = _rows(v, "v", cache, rows, cache.kv_heads)
-    op, o_row, o_head = _rows(q_out, "q_out", cache, rows, heads)
-    params = smc_qk_params(heads, rope.shape[1], rope.shape[0], int(bool(interleaved)), eps,
-                           weight_offset, q_row, q_head, k_row, k_head, v_row, v_head, o_row,
-                           o_head)
-    _check("smc_qk_norm_rope", lib().smc_qk_norm_rope(
+    heads = q.shape[1]
+    shape, kv_shape = (rows, heads, dim), (rows, cache.kv_heads, dim)
+    qp, q_row, q_head = _rows(q, "q", dtype, shape)
+    kp, k_row, k_head = _rows(k, "k", dtype, kv_shape)
+    vp, v_row, v_head = _rows(v, "v", dtype, kv_shape)
+    op, o_row, o_head = _rows(q_out, "q_out", dtype, shape)
+    max_pos, rot = rope.shape
+    params = smc_qk_params(heads, rot, max_pos, 1 if interleaved else 0, eps, weight_offset, q_row,
+                           q_head, k_row, k_head, v_row, v_head, o_row, o_head)
+    _check("smc_qk_norm_rope", (_lib or lib()).smc_qk_norm_rope(
         ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp, kp, vp,
-        None if q_weight is None else _addr(q_weight, "q_weight", dtype, cache.head_dim),
-        None if k_weight is None else _addr(k_weight, "k_weight", dtype, cache.head_dim),
+        None if q_weight is None else _addr(q_weight, "q_weight", dtype, dim),
+        None if k_weight is None else _addr(k_weight, "k_weight", dtype, dim),
         None if positions is None else _addr(positions, "positions", torch.int32, rows),
         _addr(rope, "rope", torch.float32), op, _addr(workspace, "workspace", torch.uint8), workspace.numel(),
         _raw_stream(stream, workspace)))
@@ -583,7 +584,7 @@ def kv_copy_blocks(cache, pairs, counts, workspace, stream=None):
     if pairs.dim() != 3 or pairs.shape[2] != 2:
         raise ValueError(f"pairs must be [lists, max_pairs, 2], got {tuple(pairs.shape)}")
     lists, most = pairs.shape[:2]
-    _check("kv_copy_blocks", lib().kv_copy_blocks(
+    _check("kv_copy_blocks", (_lib or lib()).kv_copy_blocks(
         ctypes.byref(cache), _addr(pairs, "pairs", torch.int32),
         _addr(counts, "counts", torch.int32, lists), lists, most, _addr(workspace, "workspace", torch.uint8),
         workspace.numel(), _raw_stream(stream, workspace)))
@@ -594,7 +595,7 @@ def kv_compact_tokens(cache, batch, path, n_path, workspace, stream=None):
     of their sequence, in every layer; path [S, max_path], n_path [S] int32."""
     if path.dim() != 2:
         raise ValueError(f"path must be [S, max_path], got {tuple(path.shape)}")
-    _check("kv_compact_tokens", lib().kv_compact_tokens(
+    _check("kv_compact_tokens", (_lib or lib()).kv_compact_tokens(
         ctypes.byref(cache), ctypes.byref(batch),
         _addr(path, "path", torch.int32, batch.S * path.shape[1]),
         _addr(n_path, "n_path", torch.int32, batch.S), path.shape[1],
@@ -604,7 +605,7 @@ def kv_compact_tokens(cache, batch, path, n_path, workspace, stream=None):
 def kv_truncate(params, kv, new_len, workspace, stream=None):
     """Shortens every particle to new_len [B, N] int32 tokens and gives the
     blocks past them back."""
-    _check("kv_truncate", lib().kv_truncate(
+    _check("kv_truncate", (_lib or lib()).kv_truncate(
         ctypes.byref(params), ctypes.byref(kv),
         _addr(new_len, "new_len", torch.int32, params.B * params.N), _addr(workspace, "workspace", torch.uint8),
         workspace.numel(), _raw_stream(stream, workspace)))

@@ -407,6 +407,8 @@ int32_t smc_step_noalloc(const smc_params *p, const void *target_logits,
  *     be contiguous.  Offsets are 64-bit.
  *   - One workspace of smc_cache_workspace_bytes() serves all of them on one
  *     stream.  Its status word is read with smc_device_status.
+ *   - The entry points that touch keys and values wait for the kernel ahead of
+ *     them in the stream in full, whenever it lets its dependents start.
  *   - A table entry outside [0, blocks) or a token count that is negative, too
  *     small for the new tokens or too large for the table sets
  *     SMC_DEV_BAD_BLOCK; row offsets, positions and path indices out of range
@@ -436,8 +438,10 @@ typedef struct {
   int32_t max_new;          /* most new tokens of a sequence,
                                1..SMC_MAX_NEW                                    */
   int32_t group;            /* sequences per prompt, consecutive (a divisor of S;
-                               1: unrelated).  Leading table slots that all of a
-                               prompt's sequences share are read once            */
+                               1: unrelated).  Leading blocks that all of a
+                               prompt's sequences share are read once (where the
+                               tables hold more than the L2 cache does); the
+                               result is that of group 1 up to rounding          */
 } smc_batch;
 
 #define SMC_MAX_NEW (1 << 16)
@@ -473,7 +477,7 @@ typedef struct {
  * does not see do not reach it, whatever they hold.
  *
  * The new tokens' keys and values must be in the cache already
- * (smc_qk_norm_rope).  dtype SMC_BF16 or SMC_F16; head_dim a multiple of 8, at
+ * (smc_qk_norm_rope); out must not overlap q.  dtype SMC_BF16 or SMC_F16; head_dim a multiple of 8, at
  * most 128; pointers and strides in multiples of 16 bytes.  Scores, statistics
  * and sums are fp32; the weights are rounded to the cache's dtype for the
  * product with v.  Equal inputs give equal bits. */

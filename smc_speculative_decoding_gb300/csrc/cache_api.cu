@@ -52,7 +52,11 @@ static BatchArgs to_batch(const smc_batch *b) {
 }
 
 static bool attention_shape_ok(const smc_cache *c, const smc_batch *b, int q_heads) {
-  return q_heads >= 1 && q_heads <= (1 << 16) && q_heads % c->kv_heads == 0 &&
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % c->kv_heads != 0) return false;
+  // tiles of 64 tokens and at least one row of a key head, counted in 32 bits
+  const double tiles = (static_cast<double>(b->T) * c->block_size / 64 + 1) * c->kv_heads * b->S *
+                       (static_cast<double>(b->max_new) * (q_heads / c->kv_heads) / 128 + 1);
+  return tiles < 536870912.0 &&
          static_cast<double>(b->rows) * q_heads < 2147483647.0 &&
          q_heads / c->kv_heads <= 128 &&
          static_cast<double>(b->max_new) * b->group * (q_heads / c->kv_heads) < 1073741824.0;

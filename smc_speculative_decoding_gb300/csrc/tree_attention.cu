@@ -908,16 +908,28 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
         __syncwarp();
       }
     } else {
-      const uint32_t d0 = smem_addr(dst);
-      constexpr int kChunks = 8 * kHalves;
-      const int ch = lane % kChunks;
+      // lane l finds rows l and l + 32; a copy's lanes take their rows' places
+      constexpr int kChunks = 8 * kHalves, kStep = 32 / kChunks;
+      const int ch = lane % kChunks, r0 = lane / kChunks;
       const bool take = ch * 8 < c.head_dim;
-      for (int r = lane / kChunks; r < t1 - t0; r += 32 / kChunks) {
-        const int2 at_block = place(t0 + r);
-        const int64_t off = at_block.x * c.block_stride + at_block.y * c.token_stride +
-                            seg.head * c.head_stride + (take ? ch * 8 : 0);
-        cp_async16(d0 + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                   src + off * 2, take);
+      int64_t off[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (t0 + lane + 32 * e < t1) {
+          const int2 at_block = place(t0 + lane + 32 * e);
+          off[e] = (at_block.x * c.block_stride + at_block.y * c.token_stride + seg.head * c.head_stride) * 2;
+        }
+      }
+      const char *column = src + (take ? ch * 16 : 0);
+      const uint32_t d0 = smem_addr(dst) + (ch >> 3) * (kTile * 128);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll 8
+        for (int r = r0; r < 32; r += kStep) {
+          const int64_t from_row = __shfl_sync(0xffffffffu, off[e], r);
+          const int row = r + 32 * e;
+          if (t0 + row < t1) cp_async16(d0 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), column + from_row, take);
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (unseen >= 0) {  // the tile before this one has arrived

@@ -343,6 +343,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
       SMC_I8(r, 8), SMC_I8(r, 16), SMC_I8(r, 24), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::SMC_I8(r, 0),
+      SMC_I8(r, 8), "r"(addr)
+      : "memory");
+}
 // Waits for the warp's loads.  The registers of a load count as written only
 // here, so that no use of them moves ahead of the wait.
 #define SMC_T8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
@@ -1055,9 +1062,16 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           __syncwarp();
           tmem_ld32(t_s, z);
           tmem_ld32(t_s + 32, z + 32);
+        }
+        // beside the load: the product with V of the tile before the last, which
+        // had this tile's weight columns, is done
+        ok = !before || warp_wait(s, before, before_par, status);
+        tc_fence_after();
+        if (warp_live) {
           tmem_wait_ld(z);
           tmem_tie(z + 32);
         }
+        if (!ok) break;
         tc_fence_before();
         warp_arrive(&s->s_free[g], lane);
         const bool odd = i & 1;
@@ -1116,6 +1130,10 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           uint32_t p[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
+            if (c == 16) {  // half the weights: fewer live registers
+              __syncwarp();
+              tmem_st16(t_s + 64 + 32 * buf, p);
+            }
             const unsigned long long y = fma2(
                 f2pack(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1])), sc2, sub2);
             float a, b;
@@ -1125,11 +1143,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             sum2[c & 1] = add2(sum2[c & 1], f2pack(a, b));
             p[c] = Wt::pack(a, b);
           }
-          // the product with V of the tile before the last, which had these columns, is done
-          if (before && !(ok = warp_wait(s, before, before_par, status))) break;
-          tc_fence_after();
           __syncwarp();
-          tmem_st32(t_s + 64 + 32 * buf, p);
+          tmem_st16(t_s + 64 + 32 * buf + 16, p + 16);
           float sa, sb;
           f2unpack(add2(sum2[0], sum2[1]), sa, sb);
           l += sa + sb;

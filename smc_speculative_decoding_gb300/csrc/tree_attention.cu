@@ -442,6 +442,12 @@ constexpr float kLazy = 8.f;
 // columns), two tiles' weights (32 each) and the accumulator (128).
 //   Units of one row tile: the groups take alternate tiles of the unit, each
 //   with its own running maximum, sum and accumulator, joined at the end.
+//   Two such units about as long, one after the other: a group each, so that
+//   their ends overlap and nothing is joined.  With 20 of the tile's 128 rows
+//   in use a tile takes the one softmax warp 2900 cycles and a segment's end
+//   10000, whatever its length: 256 sequences of 300 to 640 own tokens took 382
+//   us one by one and 273 so; 256 of one token and 100 to 1024 tokens 276 and
+//   197; 512 of 150 to 300 tokens 375 and 260.
 //   Units of two: each group has its own row tile; a tile of K and V serves
 //   both.
 // A group takes its scores to registers at once, so the next tile's scores are
@@ -457,6 +463,10 @@ constexpr float kLazy = 8.f;
 constexpr int kAttnThreads = 384;
 constexpr int kRingBytes = 160 * 1024;
 constexpr int kSegs = 4;  // segments found ahead
+// Two segments go side by side where their tiles differ by at most this: the
+// serving workload 315, 323 and 332 us at 1, 3 and 8 in their first form,
+// batches of 8k tokens 270, 270 and 294 us at 3, 8 and 64.
+constexpr int kTwoGap = 3;
 
 template <int kHalves>  // 64-element panels of the head dim
 struct Geometry {
@@ -478,16 +488,17 @@ struct Seg {
   int ctx, kv1;    // tokens before ctx are seen by all; end of the entry's tokens
   int n_new;       // new tokens of the sequence (own parts)
   int flags;
-  int join;        // of a cut unit: the owner CTA, and continuations << 16
+  int join;        // of a cut unit: the owner CTA, and continuations << 16; with kTwo the other's tiles
 };
-constexpr int kWhole = 4, kBase = 8, kEnd = 16;  // with kShared: final result, first tiles, none left
+// with kShared: final result, first tiles, none left, two segments side by side
+constexpr int kWhole = 4, kBase = 8, kEnd = 16, kTwo = 32;
 
 struct AttnTail {
   uint64_t full[2][12], empty[2][12];  // K, V
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t q_full[2], q_free[2], scores[2], s_free[2], weights[2][2], o_full[2], o_free, stats, stored, counted;
   uint64_t drained[2];
-  Seg seg[kSegs];
+  Seg seg[kSegs][2];  // either group's
   float2 stat[2][kRows];  // either group's (max, sum) of a row
   uint32_t tmem;
   unsigned nonfinite[2];  // segment number (from 1) of the last odd or even one with such a value
@@ -843,54 +854,63 @@ __device__ __forceinline__ Joined join_parts(const KernelArgs &k, int kind, int6
   return j;
 }
 
-// Segment number `seg` (from 0) as warp 10 left it.  False when the wait gave
+// Segment number `seg` (from 0) of a group as warp 10 left it.  False when the wait gave
 // up or no segment is left.
-__device__ __forceinline__ bool take_segment(AttnTail *s, uint32_t seg, Seg *to, unsigned *status) {
+__device__ __forceinline__ bool take_segment(AttnTail *s, uint32_t seg, int g, Seg *to, unsigned *status) {
   if (!warp_wait(s, &s->seg_full[seg % kSegs], seg / kSegs & 1u, status)) return false;
-  const int4 *from = reinterpret_cast<const int4 *>(&s->seg[seg % kSegs]);
+  const int4 *from = reinterpret_cast<const int4 *>(&s->seg[seg % kSegs][g]);
   const int4 a = from[0], b = from[1], c = from[2];
   *to = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
   return !(to->flags & kEnd);
 }
 
-// Copies the tiles of one segment, of K or of V, into their ring.
+// Copies the tiles of a segment, of K or of V, into their ring; with kTwo those
+// of two segments, in turn.  `seg` is where warp 10 left either group's.
 template <int kHalves, bool kTma, int kSlots>
 __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMap *map, const char *src,
                                            char *slots, uint64_t *full, uint64_t *empty, AttnTail *s,
-                                           Ring<kSlots> &ring, const Seg &seg, bool pair,
+                                           Ring<kSlots> &ring, const Seg *seg, bool pair,
                                            unsigned *bits, uint32_t *filled, uint32_t *parities) {
   using G = Geometry<kHalves>;
   const int lane = threadIdx.x & 31;
   const CacheArgs &c = k.a.c;
   const uint32_t bs = c.block_size;
-  const int32_t *table = k.a.b.tables + static_cast<int64_t>(seg.seq) * k.a.b.T;
-  const int end = min(seg.t0 + seg.n * kTile, seg.kv1), per_tile = kTile / k.box;
-  // (block, token in it) of token t of the sequence
-  auto place = [&](uint32_t t) {
+  const int per_tile = kTile / k.box;
+  const bool two = seg->flags & kTwo;
+  // (block, token in it) of token t of a segment's sequence
+  auto place = [&](const Seg *of, uint32_t t) {
     const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
-    int id = table[b];
+    int id = k.a.b.tables[static_cast<int64_t>(of->seq) * k.a.b.T + b];
     if (id < 0 || id >= c.blocks) {
       *bits |= SMC_DEV_BAD_BLOCK;
       id = 0;
     }
     return make_int2(id, t - b * bs);
   };
-  int2 ahead = make_int2(0, 0);  // the place of box `from` + lane
+  // the places of boxes `from` + lane, of two segments half the lanes each
+  int2 ahead = make_int2(0, 0);
   int from = -64;
+  const int span = two ? 16 : 32;
   int unseen = -1;  // the slot whose element copies may still be under way
   bool ok = true;
-  for (int i = 0; i < seg.n; ++i) {
-    const int t0 = seg.t0 + i * kTile, t1 = min(t0 + kTile, end);
-    const bool odd = i & 1;
+  const int turns = two ? 2 * max(seg[0].n, seg[1].n) : seg->n;
+  for (int turn = 0; turn < turns; ++turn) {
+    const bool odd = turn & 1;
+    const int i = two ? turn >> 1 : turn;
+    const Seg *const mine = seg + odd;
+    const int n = mine->n, head = mine->head, begin = mine->t0, end = min(begin + n * kTile, mine->kv1);
+    const int t0 = begin + i * kTile, t1 = min(t0 + kTile, end);
     const uint32_t slot = ring.at(odd);
     char *dst = slots + slot * G::kTileBytes;
     if constexpr (kTma) {
-      if ((i + 1) * per_tile > from + 32) {
+      if ((i + 1) * per_tile > from + span) {
         from = i * per_tile;
-        const int t = t0 + lane * k.box;
-        if (t < end) ahead = place(t);
+        const Seg *const of = seg + (two ? lane >> 4 : 0);
+        const int t = of->t0 + i * kTile + (lane & (span - 1)) * k.box;
+        if (t < min(of->t0 + of->n * kTile, of->kv1)) ahead = place(of, t);
       }
     }
+    if (i >= n) continue;
     // (the first turn of a fresh barrier passes for the one before it)
     if (!(ok = warp_wait(s, &empty[slot], ring.par(odd) ^ 1u, k.a.status))) break;
     if (!pair) warp_arrive(&empty[slot], lane);  // one group uses it
@@ -899,7 +919,7 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
     ring.step(odd);
     if constexpr (kTma) {
       const int boxes = (t1 - t0 + k.box - 1) / k.box;
-      const int at = i * per_tile - from;
+      const int at = i * per_tile - from + (two && odd ? 16 : 0);
       if (elect_one()) mbar_arrive_expect_tx(&full[slot], boxes * kHalves * k.box * 128);
       __syncwarp();
       for (int b = 0; b < boxes; ++b) {
@@ -908,7 +928,7 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
         if (elect_one()) {
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {
-            tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token, seg.head,
+            tma_load_4d(dst + half * (kTile * 128) + b * k.box * 128, map, half * 64, token, head,
                         block, &full[slot]);
           }
         }
@@ -923,8 +943,8 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (t0 + lane + 32 * e < t1) {
-          const int2 at_block = place(t0 + lane + 32 * e);
-          off[e] = (at_block.x * c.block_stride + at_block.y * c.token_stride + seg.head * c.head_stride) * 2;
+          const int2 at_block = place(mine, t0 + lane + 32 * e);
+          off[e] = (at_block.x * c.block_stride + at_block.y * c.token_stride + head * c.head_stride) * 2;
         }
       }
       const char *column = src + (take ? ch * 16 : 0);
@@ -1036,10 +1056,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     Ring<G::kSlotsV> ring_v;
     bool ok = true;
     Seg w;
-    while (ok && take_segment(s, seg, &w, status)) {
+    while (ok && take_segment(s, seg, g, &w, status)) {
       warp_arrive(&s->seg_empty[seg % kSegs], lane);
       ++seg;
-      const bool pair = w.rows > tile_rows;
+      const bool pair = w.rows > tile_rows, two_segs = w.flags & kTwo;
+      const bool apart = pair || two_segs;  // either group has a result of its own
       const int rows = pair ? (g == 0 ? tile_rows : w.rows - tile_rows) : w.rows;  // of this group
       const bool live = r < rows, warp_live = wq * 32 < rows;
       const int tok = (pair && g ? k.tile_tokens : 0) + (live ? r_tok : 0);
@@ -1050,8 +1071,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       // the releases of the V slots of the group's last tile and the one before
       uint64_t *last = nullptr, *before = nullptr;
       uint32_t last_par = 0, before_par = 0;
-      for (int i = pair ? 0 : g; i < w.n; i += pair ? 1 : 2) {
-        const int t0 = w.t0 + i * kTile;
+      const int tiles = two_segs ? 2 * w.n : w.n;
+      for (int i = pair ? 0 : g; i < tiles; i += pair ? 1 : 2) {
+        const int t0 = w.t0 + (two_segs ? i >> 1 : i) * kTile;
         const uint32_t buf = turn & 1u;
         if (!(ok = warp_wait(s, &s->scores[g], buf, status))) break;
         ++turn;
@@ -1193,19 +1215,19 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         ring_v.step(odd);
       }
       if (!ok) break;
-      if (!pair) ring_v.skip(g == 0, (w.n + g) >> 1);  // the other group's tiles
+      if (!pair) ring_v.skip(g == 0, two_segs ? w.join : (w.n + g) >> 1);  // the other group's tiles
       // ---- the unit's result -----------------------------------------------
       const uint32_t par = (seg - 1) & 1u;
-      ok = warp_wait(s, &s->o_full[g], par, status) && (pair || warp_wait(s, &s->o_full[1 - g], par, status));
+      ok = warp_wait(s, &s->o_full[g], par, status) && (apart || warp_wait(s, &s->o_full[1 - g], par, status));
       if (!ok) break;
       tc_fence_after();
       s->stat[g][r] = make_float2(m, l);
       warp_arrive(&s->stats, lane);
-      if (!pair && !(ok = warp_wait(s, &s->stats, par, status))) break;
+      if (!apart && !(ok = warp_wait(s, &s->stats, par, status))) break;
       const bool bad = s->nonfinite[seg & 1u] == seg;
-      const bool two = !pair && w.n > 1;
+      const bool two = !apart && w.n > 1;
       float f0 = 1.f, f1 = 0.f;
-      if (!pair) {
+      if (!apart) {
         const float2 s0 = s->stat[0][r], s1 = s->stat[1][r];
         m = fmaxf(s0.x, s1.x);
         f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
@@ -1219,7 +1241,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       const int kind = own ? 0 : 1;
       const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
       const int64_t cont = static_cast<int64_t>(blockIdx.x) * kUnitRows + (pair && g ? tile_rows : 0) + r;
-      if (live && (pair || g == 0)) {
+      if (live && (apart || g == 0)) {
         const float lse2 = l == 0.f ? -INFINITY : m - Wt::kOffset + log2f(l);
         if (whole) {
           if (k.a.lse) k.a.lse[rh] = lse2 * 0.69314718055994531f;
@@ -1231,12 +1253,12 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       }
       __syncwarp();
       const int half_cols = 32 * kHalves;
-      const int c_begin = pair ? 0 : g * half_cols;
-      const int c_end = min(pair ? 2 * half_cols : c_begin + half_cols, D);
+      const int c_begin = apart ? 0 : g * half_cols;
+      const int c_end = min(apart ? 2 * half_cols : c_begin + half_cols, D);
       T *const out = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head;
       float *const part = base ? k.w.o[kind] + rh * D : k.w.o_c + cont * D;
       if (warp_live) {
-        const uint32_t t_a = tmem + lanes + 256 + (pair ? g * 128 : 0);
+        const uint32_t t_a = tmem + lanes + 256 + (apart ? g * 128 : 0);
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t x[32], y[32];
@@ -1334,14 +1356,15 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     Ring<G::kSlotsV> ring_v;
     bool ok = true;
     Seg w;
-    while (ok && take_segment(s, seg, &w, status)) {
+    while (ok && take_segment(s, seg, g, &w, status)) {
       warp_arrive(&s->seg_empty[seg % kSegs], lane);
-      const bool pair = w.rows > tile_rows;
-      const int n = w.n, step = pair ? 1 : 2, first = pair ? 0 : g;
+      const bool pair = w.rows > tile_rows, two_segs = w.flags & kTwo;
+      const bool apart = pair || two_segs;  // either group has a Q of its own
+      const int n = two_segs ? 2 * w.n : w.n, step = pair ? 1 : 2, first = pair ? 0 : g;
       const Ring<G::kSlotsK> k_before = ring_k;
       const Ring<G::kSlotsV> v_before = ring_v;
-      const uint32_t q_at = q_turn + (pair ? g : 0), q_other = q_turn + 1 - g;
-      q_turn += pair ? 2 : 1;
+      const uint32_t q_at = q_turn + (apart ? g : 0), q_other = q_turn + 1 - g;
+      q_turn += apart ? 2 : 1;
       if (elect_one()) {
         const uint32_t qa = q0 + (q_at & 1u) * (G::kQTile >> 4);
         // scores of tile i, once the last ones are taken and its K is there
@@ -1370,11 +1393,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
         };
         auto free_q = [&] {  // after the segment's last scores
           tc_commit(&s->q_free[q_at & 1u]);
-          if (pair) tc_commit(&s->q_free[q_other & 1u]);
+          if (apart) tc_commit(&s->q_free[q_other & 1u]);
         };
-        // both tiles of a pair, as both issuing threads free both
+        // both of two tiles, as both issuing threads free both
         ok = guarded_wait(s, &s->q_full[q_at & 1u], q_at >> 1 & 1u, status) &&
-             (!pair || guarded_wait(s, &s->q_full[q_other & 1u], q_other >> 1 & 1u, status));
+             (!apart || guarded_wait(s, &s->q_full[q_other & 1u], q_other >> 1 & 1u, status));
         if (ok && first < n) ok = scores(first);
         if (ok && first + step >= n) free_q();
         for (int i = first; ok && i < n; i += step) {
@@ -1405,14 +1428,14 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       }
       // what the elected lane counted, for all: its tiles, and the other group's
       ok = __all_sync(0xffffffffu, ok);
-      const uint32_t mine = pair ? n : (n + 1 - g) >> 1;
-      asked = given = tiles += mine;
+      asked = given = tiles += pair ? n : (n + 1 - g) >> 1;
       ring_k = k_before;
       ring_v = v_before;
-      ring_k.skip(false, (n + 1) >> 1);
-      ring_k.skip(true, n >> 1);
-      ring_v.skip(false, (n + 1) >> 1);
-      ring_v.skip(true, n >> 1);
+      for (int odd = 0; odd < 2; ++odd) {
+        const int half = !two_segs ? (n + 1 - odd) >> 1 : odd == g ? w.n : w.join;
+        ring_k.skip(odd, half);
+        ring_v.skip(odd, half);
+      }
       ++seg;
     }
     if (elect_one()) {
@@ -1428,36 +1451,62 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     unsigned bits = 0;
     uint32_t filled = 0, parities = 0;
     bool ok = true;
+    Seg next{};
+    bool begun = false, held = false;  // next is found and not yet taken
     for (uint32_t seg = 0; ok; ++seg) {
-      const bool more = w.next(k);
-      if (seg == 0 && lane == 0 && !k.join_inside) {
-        const bool cut = more && w.first_cut;
-        int4 *to = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
-        to[0] = cut ? make_int4(w.t.row0 + w.tokens0, w.rows, w.head, w.more) : make_int4(0, 0, 0, 0);
-        to[1] = make_int4(more ? w.t.flags : 0, 0, 0, 0);
-      }
-      Seg t{};
-      t.flags = kEnd;
-      if (more) {
-        t = {w.t.row0 + w.tokens0, w.rows, w.tokens0, w.t.seq, w.head, w.t.kv0 + w.i0 * kTile, w.n,
-             w.t.ctx, w.t.kv1, w.t.tokens, 0, w.owner | w.more << 16};
-        t.flags = (w.t.flags & kShared) | ((w.t.flags & kSolo) && w.n == w.t.tiles ? kWhole : 0) |
-                  (w.i0 == 0 ? kBase : 0);
-      }
       if (seg >= kSegs &&
           !(ok = warp_wait(s, &s->seg_empty[seg % kSegs], (seg / kSegs - 1) & 1u, status))) {
         break;
       }
-      if (lane == 0) {
-        int4 *to = reinterpret_cast<int4 *>(&s->seg[seg % kSegs]);
-        to[0] = make_int4(t.row0, t.rows, t.i0, t.seq);
-        to[1] = make_int4(t.head, t.t0, t.n, t.ctx);
-        to[2] = make_int4(t.kv1, t.n_new, t.flags, t.join);
+      // the next segment, and the one after it beside it where both have one
+      // row tile and are about as long
+      Seg *const to = s->seg[seg % kSegs];
+      int n = 0;
+      bool pair = false;
+      for (int g = 0; g < 2; ++g) {
+        if (!held) {
+          const bool more = w.next(k);
+          if (!begun && lane == 0 && !k.join_inside) {
+            const bool cut = more && w.first_cut;
+            int4 *rec = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
+            rec[0] = cut ? make_int4(w.t.row0 + w.tokens0, w.rows, w.head, w.more) : make_int4(0, 0, 0, 0);
+            rec[1] = make_int4(more ? w.t.flags : 0, 0, 0, 0);
+          }
+          begun = held = true;
+          next.flags = kEnd;
+          if (more) {
+            next = {w.t.row0 + w.tokens0, w.rows, w.tokens0, w.t.seq, w.head, w.t.kv0 + w.i0 * kTile, w.n,
+                    w.t.ctx, w.t.kv1, w.t.tokens, 0, w.owner | w.more << 16};
+            next.flags = (w.t.flags & kShared) | ((w.t.flags & kSolo) && w.n == w.t.tiles ? kWhole : 0) |
+                         (w.i0 == 0 ? kBase : 0);
+          }
+        }
+        // (a join inside is for one unit at a time)
+        const bool may = !(next.flags & kEnd) && next.rows <= tile_rows && (!k.join_inside || (next.flags & kWhole));
+        if (g) {
+          if (!may || abs(n - next.n) > kTwoGap) break;
+          if (lane == 0) {
+            to->flags |= kTwo;
+            to->join = next.n;
+          }
+          next.flags |= kTwo;
+          next.join = n;
+        }
+        if (lane < 2 && lane >= g) {
+          int4 *at = reinterpret_cast<int4 *>(to + lane);
+          at[0] = make_int4(next.row0, next.rows, next.i0, next.seq);
+          at[1] = make_int4(next.head, next.t0, next.n, next.ctx);
+          at[2] = make_int4(next.kv1, next.n_new, next.flags, next.join);
+        }
+        n = next.n;
+        pair = next.rows > tile_rows;
+        held = false;
+        if (!may) break;
       }
       warp_arrive(&s->seg_full[seg % kSegs], lane);
-      if (!more) break;
+      if (to->flags & kEnd) break;
       ok = copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s, ring,
-                                                 t, t.rows > tile_rows, &bits, &filled, &parities);
+                                                 to, pair, &bits, &filled, &parities);
     }
     if (kTma && s->abort) wait_landed(s->full[0], filled, parities);
     if (bits) raise_status(status, bits);
@@ -1469,26 +1518,29 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     uint32_t filled = 0, parities = 0;
     bool ok = true;
     Seg w;
-    while (ok && take_segment(s, seg, &w, status)) {
-      warp_arrive(&s->seg_empty[seg % kSegs], lane);
-      ++seg;
-      const bool pair = w.rows > tile_rows;
-      for (int j = 0; ok && j < (pair ? 2 : 1); ++j, ++q_turn) {
+    while (ok && take_segment(s, seg, 0, &w, status)) {
+      const Seg *const at_seg = s->seg[seg % kSegs];
+      const bool pair = w.rows > tile_rows, two_segs = w.flags & kTwo;
+      for (int j = 0; ok && j < (pair || two_segs ? 2 : 1); ++j, ++q_turn) {
         const uint32_t at = q_turn & 1u;
         if (q_turn >= 2 && !(ok = warp_wait(s, &s->q_free[at], ((q_turn >> 1) - 1) & 1u, status))) break;
+        const int row0 = pair ? w.row0 + j * k.tile_tokens : at_seg[j].row0;
+        const int head0 = at_seg[j].head * k.rep;
         if (elect_one()) {
           mbar_arrive_expect_tx(&s->q_full[at], kHalves * k.q_box * k.rep * 128);
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {
-            tma_load_3d(s_q + at * G::kQTile + half * (kRows * 128), &map_q, half * 64, w.head * k.rep,
-                        w.row0 + j * k.tile_tokens, &s->q_full[at]);
+            tma_load_3d(s_q + at * G::kQTile + half * (kRows * 128), &map_q, half * 64, head0, row0,
+                        &s->q_full[at]);
           }
         }
         __syncwarp();
       }
       if (!ok) break;
       ok = copy_tiles<kHalves, kTma, G::kSlotsV>(k, &map_v, k.a.c.v, s_v, s->full[1], s->empty[1], s, ring,
-                                                 w, pair, &bits, &filled, &parities);
+                                                 at_seg, pair, &bits, &filled, &parities);
+      warp_arrive(&s->seg_empty[seg % kSegs], lane);
+      ++seg;
     }
     if (s->abort) {
       if (kTma) wait_landed(s->full[1], filled, parities);

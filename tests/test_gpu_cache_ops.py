@@ -118,6 +118,27 @@ def test_attention_shared_prefix(group, shared, ctx, new, mask, slots):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("sequences,group,new,low,high,kw", [
+    (150, 1, 1, 0, 260, dict()),                     # units that end inside a multiprocessor's run, joined in it
+    (150, 1, 5, 60, 200, dict(mask="tree", block=20)),  # element copies
+    (270, 1, 3, 1, 130, dict(dim=64)),               # more sequences than are counted without a plan
+    (160, 16, 5, 100, 400, dict(slots=700)),         # own parts after a shared one
+    (96, 1, 40, 0, 300, dict(kv_heads=8, heads=24)),  # units of one row tile and of two, by turns
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_many_short(sequences, group, new, low, high, kw, dtype):
+    """More units than multiprocessors: several to each, of like and of unlike lengths."""
+    ctx = [low + 37 * i * i % (high - low + 1) for i in range(sequences)]
+    news = [1 + (i * 7) % (2 * new) if new > 1 else 1 for i in range(sequences)]
+    shared = min(ctx) // 16 * 16 if group > 1 else 0
+    c = CacheCase(ctx, news, group=group, shared=shared, dtype=dtype, poison=True,
+                  **{"heads": 8, "kv_heads": 4, **kw})
+    out, lse, ws = _attend(c)
+    _check_attention(c, out, lse, ws)
+    again, lse2, _ = _attend(c, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def _check_like_double(c, out, lse):
     """Against torch in 64 bits on padded tensors: for shapes that the loops
     of the reference would take long over."""

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_consta
 //   Measured, 12 535 rows of 56 heads of 96 in fp16 (309 MB): scalar arithmetic
 // with run-time selects 138 us, bound by the instructions issued (389 per
 // vector and warp); this form 102 us with 256 threads a row, 75 us with 128, 66
-// with 64 (4.7 TB/s): what a warp does once a row is shared by more heads.
+// with 64, and 63 since (4.9 TB/s): what a warp does once a row is shared by more heads.
 constexpr int kAhead = 4;  // q heads of a group whose loads are under way at once
 
 template <typename T>

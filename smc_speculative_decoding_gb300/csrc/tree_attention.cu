@@ -65,6 +65,7 @@ struct AttnWorkspace {
   PlanHeader *head;
   unsigned *tickets;  // [kMaxCtas] parts stored of the unit that a CTA's end cuts; return to zero
   int *common;     // [groups] shared tokens
+  int *ref;        // [groups] the sequence by whose table they are read
   int *tile0;      // [entries + 1]
   Entry *entries;  // shared parts of the groups (when group > 1), then the sequences
   float *lse[2];   // own, shared: [rows * q_heads], log2
@@ -92,6 +93,7 @@ static size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, char *b
   t.head = reinterpret_cast<PlanHeader *>(take(sizeof(PlanHeader)));
   t.tickets = reinterpret_cast<unsigned *>(take(sizeof(unsigned) * kMaxCtas));
   t.common = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
+  t.ref = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
   t.tile0 = reinterpret_cast<int *>(take(sizeof(int) * (static_cast<size_t>(t.n_entries) + 1)));
   t.entries = reinterpret_cast<Entry *>(take(sizeof(Entry) * t.n_entries));
   for (int k = 0; k < 2; ++k) {
@@ -170,7 +172,8 @@ __device__ int make_entry(const KernelArgs &k, int e, Entry *out) {
     const int shared = __ldcg(&k.w.common[e]);
     if (shared > 0) {  // every sequence is in order, so the rows are consecutive
       const SeqInfo first = seq_info(b, bs, s0), last = seq_info(b, bs, s0 + b.group - 1);
-      t = {first.row0, last.row0 + last.n - first.row0, s0, 0, shared, shared, 0, kShared};
+      // (a sequence without rows has no part in what the others share: the first one's table may be another)
+      t = {first.row0, last.row0 + last.n - first.row0, __ldcg(&k.w.ref[e]), 0, shared, shared, 0, kShared};
     }
     tiles = entry_tiles(k, t.tokens, 0, shared, &t.tiles);
   } else {
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) {
       const int64_t tokens = static_cast<int64_t>(s_slots) * bs;
       k.w.common[blockIdx.x] = static_cast<int>(tokens / kTile * kTile);
+      k.w.ref[blockIdx.x] = s_ref;
       __threadfence();
       s_last = atomicAdd(&k.w.head->ticket, 1) + 1 == gridDim.x;
     }

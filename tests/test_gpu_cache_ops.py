@@ -118,6 +118,35 @@ def test_attention_shared_prefix(group, shared, ctx, new, mask, slots):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("other", ["ended", "other_blocks"])
+@pytest.mark.parametrize("group,shared,ctx,new", [
+    (4, 512, [600, 512, 700, 530], [0, 5, 5, 5]),                        # the first has no rows
+    (4, 256, [300, 300, 270, 290] * 2, [0, 0, 3, 2, 4, 0, 1, 2]),        # the first two of a prompt; one in the middle
+    (3, 640, [650, 700, 690] * 2, [0, 1, 0, 0, 40, 40]),                 # a prompt with one sequence left
+])
+@pytest.mark.parametrize("slots", [0, 3100])
+def test_attention_shared_prefix_beside_sequences_without_rows(group, shared, ctx, new, other, slots):
+    """Sequences without new tokens have no say in what a prompt's others share: their tables may be given back
+    (-1) or lead to other blocks."""
+    c = CacheCase(ctx, new, group=group, shared=shared, mask="tree", slots=slots)
+    want = CacheCase(ctx, new, group=group, shared=shared, mask="tree", slots=slots).reference()
+    n = shared // c.block
+    for s, m in enumerate(new):
+        if m:
+            continue
+        if other == "ended":
+            c.tables[s], c.seq_len[s] = -1, 0
+        else:
+            c.tables[s, :n] = c.tables[s, 0].clone()  # (an order of the same blocks would give the same result)
+    out, lse, ws = _attend(c)
+    assert smcsd.status_names(smcsd.smc_device_status(ws)) == []
+    ref, ref_lse, tol, tol_lse = want
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert ((lse.double() - ref_lse).abs() <= tol_lse).all()
+    again, lse2, _ = _attend(c, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("sequences,group,new,low,high,kw", [
     (150, 1, 1, 0, 260, dict()),                     # units that end inside a multiprocessor's run, joined in it
     (150, 1, 5, 60, 200, dict(mask="tree", block=20)),  # element copies

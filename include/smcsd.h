@@ -539,8 +539,9 @@ int32_t kv_copy_blocks(const smc_cache *cache, const int32_t *pairs, const int32
  * tokens, keys and values of every layer: new token path[s, i] goes to new
  * token i for i < n_path[s].  path [S, max_path] int32 holds indices among the
  * sequence's new tokens in strictly ascending order (a parent precedes its
- * children); n_path [S] int32 in [0, max_path].  An index that is out of range
- * or does not ascend sets SMC_DEV_BAD_ROWS and is skipped.  The token counts
+ * children); n_path [S] int32 in [0, max_path].  An index that is out of range,
+ * does not ascend (past every index in range before it) or is less than its
+ * place i (possible behind a skipped one) sets SMC_DEV_BAD_ROWS and is skipped.  The token counts
  * stay: kv_truncate gives back what the path leaves over. */
 int32_t kv_compact_tokens(const smc_cache *cache, const smc_batch *batch, const int32_t *path,
                           const int32_t *n_path, int32_t max_path, void *workspace,

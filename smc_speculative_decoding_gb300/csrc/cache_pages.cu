@@ -80,9 +80,10 @@ copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_
 }
 
 // Thread t owns column t of a token's (head, d) elements for the whole path.
-// A path ascends, so path[i] >= i: taken in order, with a batch's loads before
-// its stores, no move overwrites a later source, and no thread touches
-// another's column.  The places of 64 moves at a time are found by as many
+// A path ascends, so path[i] >= i; behind a skipped entry that is asked for, as
+// a place past its token may lie past the new tokens and the table.  Taken in
+// order, with a batch's loads before its stores, no move then overwrites a later
+// source, and no thread touches another's column.  The places of 64 moves at a time are found by as many
 // threads; a CTA's time is then three dependent loads (the path, the blocks,
 // the first batch) and the bytes'.  64 paths of up to 9 tokens in 32 layers, 8
 // heads of 128 in bf16, 151 MB: 26.3 us (5.7 TB/s).
@@ -117,8 +118,9 @@ compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32
     if (tid < kMoves) {
       const int i = i0 + tid, lane = tid & 31;
       if (i0 > 0) mine = i < n ? p[i] : -1;
-      // an index counts when it is past every counting one before it: a
-      // running maximum over the warp, the warps and the moves before
+      // an index counts when it is in range, past every one in range before it
+      // (a running maximum over the warp, the warps and the moves before) and
+      // not ahead of its place
       const bool in = i < n && mine >= 0 && mine < si.n;
       int top = in ? mine : -1;
 #pragma unroll
@@ -135,7 +137,7 @@ compact_tokens_kernel(CacheArgs c, BatchArgs b, const int32_t *path, const int32
       asm volatile("bar.sync 1, 64;" ::: "memory");
       if (tid == kMoves - 1) s_last = max(before, in ? mine : -1);
       int64_t from = -1, to = -1;
-      const bool good = in && mine > before;
+      const bool good = in && mine > before && mine >= i;
       unsigned bits = i < n && !good ? SMC_DEV_BAD_ROWS : 0;
       if (good && mine != i) {
         const int ft = first + mine, tt = first + i;

@@ -579,6 +579,42 @@ def test_compact_reports_bad_paths():
     assert smcsd.status_names(smcsd.smc_device_status(ws, clear=True)) == ["bad_rows"]
 
 
+@pytest.mark.parametrize("dim,block,kw", [(64, 16, {}), (3, 7, {}), (64, 4, dict(order="hnd")), (128, 1, {})])
+def test_compact_skips_bad_entries_and_touches_nothing_else(dim, block, kw):
+    """Entries that are out of range, do not ascend, or lie ahead of their place are skipped alone; paths may be
+    longer than the new tokens, whose last sequence fills its table and the pool."""
+    rng = np.random.default_rng(block)
+    new = [2, 30, 0, 9, 2]
+    ctx = [5, 31, 7, 0, 4 * block - 2]
+    most = 100
+    path = rng.integers(-3, 33, (5, most))
+    path[0] = [0] * 99 + [1]
+    path[1, :40] = np.sort(path[1, :40])
+    path[3] = [-1] * 4 + list(range(96))
+    path[4] = [9] * 98 + [0, 1]
+    n_path = [100, 100, 3, 12, 100]
+    c = CacheCase(ctx, new, dim=dim, block=block, layers=2, **kw)
+    T = max(-(-n // block) for n in c.lengths)
+    c.tables = c.tables[:, :T].contiguous()
+    want = c.k.clone(), c.v.clone()
+    for s, m in enumerate(new):
+        last = -1
+        for i, j in enumerate(path[s, :n_path[s]].tolist()):
+            if not 0 <= j < m:
+                continue
+            if j > last and j >= i:
+                a, b = ctx[s] + j, ctx[s] + i
+                for w in want:  # (no place is a later source)
+                    w[:, c.tables[s, b // block], b % block] = w[:, c.tables[s, a // block], a % block].clone()
+            last = max(last, j)
+    cache = c.cache(smcsd)
+    ws = smcsd.alloc_cache_workspace(cache)
+    smcsd.kv_compact_tokens(cache, c.batch(smcsd), torch.tensor(path, dtype=torch.int32, device="cuda"),
+                            torch.tensor(n_path, dtype=torch.int32, device="cuda"), ws)
+    assert smcsd.status_names(smcsd.smc_device_status(ws)) == ["bad_rows"]
+    assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1])
+
+
 def _truncated(kv, new_len, block, pool):
     """The KV state after kv_truncate, by loops."""
     kv = {k: v.copy() for k, v in kv.items()}

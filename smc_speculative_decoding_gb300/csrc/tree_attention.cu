@@ -1231,7 +1231,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       tc_fence_after();
       s->stat[g][r] = make_float2(m, l);
       warp_arrive(&s->stats, lane);
-      if (!apart && !(ok = warp_wait(s, &s->stats, par, status))) break;
+      // (for two row tiles too: the group that zeroes a value of V which is not finite tells the other)
+      if (!two_segs && !(ok = warp_wait(s, &s->stats, par, status))) break;
       const bool bad = s->nonfinite[seg & 1u] == seg;
       const bool two = !apart && w.n > 1;
       float f0 = 1.f, f1 = 0.f;

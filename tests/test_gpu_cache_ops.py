@@ -260,6 +260,33 @@ def test_attention_ignores_what_a_row_does_not_see(value):
             assert ((out[r].double() - ref[r]).abs() <= tol[r]).all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx,new,bad,kw", [
+    ([150, 10], [9, 40], 3, dict(heads=8)),            # 160 rows of a key head: two row tiles, one of them in part
+    ([0, 30], [50, 64], 5, dict(heads=8)),            # 256 rows; the tile before the last one holds the token
+    ([9000], [48], 1, dict(heads=8)),                 # cut between multiprocessors
+    ([700, 90], [33, 60], 0, dict(heads=12, dim=64)),  # six heads of a key head: units of 252 rows and of the rest
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_of_two_row_tiles_ignores_what_a_row_does_not_see(ctx, new, bad, kw, value, dtype):
+    """Both softmax groups read the tile of V that holds the token, and either may be the one that zeroes it."""
+    s = len(ctx) - 1
+    at = ctx[s] + bad
+    c = CacheCase(ctx, new, mask="tree", kv_heads=2, dtype=dtype, **kw)
+    ref, _, tol, _ = c.reference()
+    c.v[0, c.tables[s, at // c.block], at % c.block] = value
+    out, lse, ws = _attend(c)
+    sees = torch.tensor([r >= c.starts[s] and bad in c.seen[r] for r in range(c.rows)], device="cuda")
+    assert sees.any() and not sees.all()
+    if math.isnan(value):
+        assert torch.isnan(out[sees]).all()
+    else:
+        assert torch.all(out[sees] == value)
+    assert ((out.double() - ref).abs() <= tol)[~sees].all()
+    again, _, _ = _attend(c, workspace=ws)
+    assert torch.equal(torch.nan_to_num(out, nan=7.0), torch.nan_to_num(again, nan=7.0))
+
+
 def test_attention_of_large_scores():
     """Scores of several hundred: only differences from the maximum matter."""
     c = CacheCase([300, 40], [5, 5], sigma=20.0, mask="tree")

@@ -466,7 +466,8 @@ constexpr float kLazy = 8.f;
 // took 2700 cycles, of which 1100 were that wait.
 //   Every wait is on a barrier all of whose turns the waiting thread follows:
 // a slot is one group's for good (see Geometry), and before both groups use a
-// tile, all earlier tiles are done with.
+// tile, all earlier tiles are done with.  tests/test_attention_protocol.py runs
+// the roles and their barriers on the CPU.
 // ---------------------------------------------------------------------------
 constexpr int kAttnThreads = 384;
 constexpr int kRingBytes = 160 * 1024;
@@ -498,8 +499,8 @@ struct Seg {
   int flags;
   int join;        // of a cut unit: the owner CTA, and continuations << 16; with kTwo the other's tiles
 };
-// with kShared: final result, first tiles, none left, two segments side by side
-constexpr int kWhole = 4, kBase = 8, kEnd = 16, kTwo = 32;
+// with kShared: final result, first tiles, none left, two segments side by side, the last one was
+constexpr int kWhole = 4, kBase = 8, kEnd = 16, kTwo = 32, kBehindTwo = 64;
 
 struct AttnTail {
   uint64_t full[2][12], empty[2][12];  // K, V
@@ -1068,6 +1069,11 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       warp_arrive(&s->seg_empty[seg % kSegs], lane);
       ++seg;
       const bool pair = w.rows > tile_rows, two_segs = w.flags & kTwo;
+      // Groups side by side do not end together, and a unit of two row tiles takes either half
+      // of V's slots: first the other group is done with its own, so that no wait on their
+      // barriers is more than a turn ahead of them.  (What the issuing threads wait for says
+      // as much.)
+      if (pair && (w.flags & kBehindTwo) && !(ok = warp_wait(s, &s->o_free, seg & 1u, status))) break;
       const bool apart = pair || two_segs;  // either group has a result of its own
       const int rows = pair ? (g == 0 ? tile_rows : w.rows - tile_rows) : w.rows;  // of this group
       const bool live = r < rows, warp_live = wq * 32 < rows;
@@ -1462,6 +1468,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     bool ok = true;
     Seg next{};
     bool begun = false, held = false;  // next is found and not yet taken
+    int behind = 0;                    // kBehindTwo, behind two segments side by side
     for (uint32_t seg = 0; ok; ++seg) {
       if (seg >= kSegs &&
           !(ok = warp_wait(s, &s->seg_empty[seg % kSegs], (seg / kSegs - 1) & 1u, status))) {
@@ -1505,7 +1512,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           int4 *at = reinterpret_cast<int4 *>(to + lane);
           at[0] = make_int4(next.row0, next.rows, next.i0, next.seq);
           at[1] = make_int4(next.head, next.t0, next.n, next.ctx);
-          at[2] = make_int4(next.kv1, next.n_new, next.flags, next.join);
+          at[2] = make_int4(next.kv1, next.n_new, next.flags | behind, next.join);
         }
         n = next.n;
         pair = next.rows > tile_rows;
@@ -1514,6 +1521,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
       }
       warp_arrive(&s->seg_full[seg % kSegs], lane);
       if (to->flags & kEnd) break;
+      behind = to->flags & kTwo ? kBehindTwo : 0;
       ok = copy_tiles<kHalves, kTma, G::kSlotsK>(k, &map_k, k.a.c.k, s_k, s->full[0], s->empty[0], s, ring,
                                                  to, pair, &bits, &filled, &parities);
     }

@@ -168,6 +168,25 @@ def test_attention_many_short(sequences, group, new, low, high, kw, dtype):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("news,low,high,kw", [
+    ([2, 2, 3, 40], 0, 60, {}),             # tiles that reach past the committed tokens from the first on
+    ([1, 5, 5, 64, 33], 0, 400, {}),
+    ([1, 2, 60], 0, 150, dict(dim=64)),
+    ([2, 40, 1, 1], 30, 200, dict(block=20)),  # element copies
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_attention_of_two_row_tiles_behind_units_side_by_side(news, low, high, kw, dtype):
+    """Several units to a multiprocessor: short ones side by side, then one whose tiles both softmax groups use."""
+    ctx = [low + 53 * i * i % (high - low + 1) for i in range(160)]
+    c = CacheCase(ctx, [news[i % len(news)] for i in range(160)], mask="tree", dtype=dtype, poison=True, sigma=3.0,
+                  heads=8, kv_heads=2, **kw)
+    out, lse, ws = _attend(c)
+    _check_attention(c, out, lse, ws)
+    for _ in range(3):
+        again, lse2, _ = _attend(c, workspace=ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def _check_like_double(c, out, lse):
     """Against torch in 64 bits on padded tensors: for shapes that the loops
     of the reference would take long over."""

@@ -537,8 +537,9 @@ def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=No
     op, o_row, o_head = _rows(out, "out", dtype, shape)
     words = 0
     if mask is not None:
-        if mask.dim() != 2 or mask.shape[0] != rows:
-            raise ValueError(f"mask must be [{rows}, words], got {tuple(mask.shape)}")
+        # (a tensor of no words has no address: it would count as no mask, which is a chain)
+        if mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] < 1:
+            raise ValueError(f"mask must be [{rows}, words] with at least one word, got {tuple(mask.shape)}")
         words = mask.shape[1]
     params = smc_attn_params(heads, words, dim ** -0.5 if scale is None else scale, 0,
                              q_row, q_head, o_row, o_head)

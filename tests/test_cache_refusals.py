@@ -169,3 +169,13 @@ def test_the_binding_refuses_tensors_it_cannot_pass():
         bd.make_cache(t, t)
     with pytest.raises(TypeError):
         bd.make_cache(None, t)
+
+
+def test_the_binding_refuses_a_mask_without_words(monkeypatch):
+    """It has no address, and no mask means a chain."""
+    import torch
+    monkeypatch.setattr(bd, "_rows", lambda *a: (PTR, 1024, 128))
+    q = torch.zeros((12, 8, 128), dtype=torch.bfloat16)
+    for shape in ((12, 0), (11, 1), (12,)):
+        with pytest.raises(ValueError, match="at least one word"):
+            bd.smc_tree_attention(_cache(), 0, _batch(), q, q, None, mask=torch.zeros(shape, dtype=torch.int32))

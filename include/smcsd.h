@@ -445,6 +445,8 @@ typedef struct {
 } smc_batch;
 
 #define SMC_MAX_NEW (1 << 16)
+/* most tokens that a table has room for (T * block_size) in smc_tree_attention  */
+#define SMC_MAX_TABLE_TOKENS 2147479552 /* 2^31 - 4096 */
 
 /* Bytes of workspace for the entry points below: for any of them with `batch`
  * and q_heads query heads; with batch NULL, for those that take no batch.

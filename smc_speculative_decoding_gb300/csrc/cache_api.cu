@@ -53,6 +53,8 @@ static BatchArgs to_batch(const smc_batch *b) {
 
 static bool attention_shape_ok(const smc_cache *c, const smc_batch *b, int q_heads) {
   if (q_heads < 1 || q_heads > (1 << 16) || q_heads % c->kv_heads != 0) return false;
+  // a token's number, and that of one up to 32 tiles on, is counted in 32 bits
+  if (static_cast<double>(b->T) * c->block_size > SMC_MAX_TABLE_TOKENS) return false;
   // tiles of 64 tokens and at least one row of a key head, counted in 32 bits
   const double tiles = (static_cast<double>(b->T) * c->block_size / 64 + 1) * c->kv_heads * b->S *
                        (static_cast<double>(b->max_new) * (q_heads / c->kv_heads) / 128 + 1);

@@ -131,6 +131,16 @@ def test_bad_block_calls(lib):
     assert lib.kv_truncate(ctypes.byref(bad), ctypes.byref(kv), PTR, PTR, need, None) == DTYPE
 
 
+def test_tables_with_room_for_more_tokens_than_32_bits_count(lib):
+    c = _cache(kv_heads=1, head_dim=8, token_stride=8, head_stride=8, block_stride=128, layer_stride=1024)
+    kw = dict(S=1, rows=1, max_new=1, group=1)
+    for T, fits in (((1 << 31) // 16, False), ((1 << 31) // 16 - 255, False), ((1 << 31) // 16 - 256, True)):
+        b = _batch(T=T, **kw)
+        assert (lib.smc_cache_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 1) > 0) == fits
+        if not fits:
+            assert _attn(lib, cache=c, batch=b, q_heads=1) == ARG
+
+
 def test_a_call_without_rows_is_accepted(lib):
     b = _batch(rows=0)
     need = lib.smc_cache_workspace_bytes(ctypes.byref(_cache()), ctypes.byref(b), 8)

@@ -221,6 +221,8 @@ class Cta:
             yield from self.wait(self.q_full[q_at & 1], q_at >> 1 & 1)
             if apart:
                 yield from self.wait(self.q_full[q_other & 1], q_other >> 1 & 1)
+            if [s[0] for s in self.segments[max(x - 1, 0):x + 1]] == [TWO, PAIR] and self.without != "o_free":
+                yield from self.wait(self.o_free, x - 1 & 1)
             if tiles:
                 yield from ask(tiles[0])
             if len(tiles) <= 1:
@@ -282,9 +284,6 @@ class Cta:
             kind, n, m, cut, edges, bad = self.segments[x]
             self.seg_empty[x % 4].arrive()
             seg = x + 1
-            if kind == PAIR and x > 0 and self.segments[x - 1][0] == TWO:
-                if self.without != "o_free":
-                    yield from self.wait(self.o_free, x - 1 & 1)
             v0 = list(ring.used)
             last = before = None
             for i in self.own(x, g):

@@ -31,7 +31,8 @@
  *     leaves the workspace's counters zero again, so it can be reused by the
  *     next call on the same stream without clearing, by calls of the same
  *     entry point and shape (the layout depends on both; another shape or
- *     entry point takes its own workspace, or smc_workspace_init first).  Two
+ *     entry point takes its own workspace, or smc_workspace_init first; only
+ *     the entry points that say so share one).  Two
  *     calls that run concurrently must not share a workspace.  Consecutive
  *     steps on one workspace may overlap on the GPU (a step's first kernel
  *     starts while the previous step's last kernel finishes); the library
@@ -405,8 +406,10 @@ int32_t smc_step_noalloc(const smc_params *p, const void *target_logits,
  *   - The calls take strides in elements, so the cache may be token-major,
  *     head-major or one layer of a larger array; only the head_dim axis must
  *     be contiguous.  Offsets are 64-bit.
- *   - One workspace of smc_cache_workspace_bytes() serves all of them on one
- *     stream.  Its status word is read with smc_device_status.
+ *   - One workspace of smc_cache_workspace_bytes() for the largest batch,
+ *     zero-filled once, serves all of them, and batches of other shapes, on one
+ *     stream (kv_truncate takes one of smc_workspace_bytes()).  Its status word
+ *     is read with smc_device_status.
  *   - The entry points that touch keys and values wait for the kernel ahead of
  *     them in the stream in full, whenever it lets its dependents start.
  *   - A table entry outside [0, blocks) or a token count that is negative, too
@@ -439,9 +442,10 @@ typedef struct {
                                1..SMC_MAX_NEW                                    */
   int32_t group;            /* sequences per prompt, consecutive (a divisor of S;
                                1: unrelated).  Leading blocks that all of a
-                               prompt's sequences share are read once (where the
-                               tables hold more than the L2 cache does); the
-                               result is that of group 1 up to rounding          */
+                               prompt's sequences with new tokens share are read
+                               once (where the S tables have room for 96 MB of
+                               keys and values or more, held or not); the result
+                               is that of group 1 up to rounding                 */
 } smc_batch;
 
 #define SMC_MAX_NEW (1 << 16)
@@ -480,7 +484,8 @@ typedef struct {
  *
  * The new tokens' keys and values must be in the cache already
  * (smc_qk_norm_rope); out must not overlap q.  dtype SMC_BF16 or SMC_F16; head_dim a multiple of 8, at
- * most 128; pointers and strides in multiples of 16 bytes.  Scores, statistics
+ * most 128; T * block_size at most SMC_MAX_TABLE_TOKENS; pointers and strides in
+ * multiples of 16 bytes.  Scores, statistics
  * and sums are fp32; the weights are rounded to the cache's dtype for the
  * product with v.  Equal inputs give equal bits. */
 int32_t smc_tree_attention(const smc_attn_params *p, const smc_cache *cache, int32_t layer,
@@ -556,7 +561,9 @@ int32_t kv_compact_tokens(const smc_cache *cache, const smc_batch *batch, const 
  * frees a particle).  A new_len outside [0, seq_len], a block outside its
  * prompt's pool or one with no reference left sets SMC_DEV_BAD_BLOCK; that
  * particle, or that block, is left as it is.  p supplies B and N; the
- * workspace is one of smc_workspace_bytes(p, kv). */
+ * workspace is one of smc_workspace_bytes(p, kv).  With p and kv of the same
+ * shapes, smc_step, kv_blocktable_remap and kv_truncate may share one on one
+ * stream: the layout is the same, and each leaves it as it needs it. */
 int32_t kv_truncate(const smc_params *p, const smc_kv *kv, const int32_t *new_len,
                     void *workspace, size_t ws_bytes, void *stream);
 

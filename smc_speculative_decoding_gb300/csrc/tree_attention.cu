@@ -5,13 +5,13 @@
 //   plan_kernel       lists the call's work in tiles of 64 tokens;
 //   attention_kernel  persistent, one CTA per SM, on the 5th-generation tensor
 //                     cores; every CTA takes an equal run of the tiles;
-//   join_cut_units_kernel, or with shared parts join_shared_kernel,
-//                     joins the rows that several CTAs, or a shared and an own
-//                     part, contributed to.
+//   join_cut_units_kernel  joins the rows that several CTAs contributed to
+//                     (with few rows the last of these CTAs does);
+//   join_shared_kernel  behind it, joins a shared and an own part.
 // Measured (bf16, 8 key heads of 128): 64 trees of 16 tokens over up to 8192,
-// 32 heads, 263 us (6.3 TB/s); 8 tokens of 64 heads over 131072, 92 us (5.8
-// TB/s); 16 trees of 64 tokens over up to 4096, 90 us, bound by the softmax; one
-// token over 513, 12 us, bound by latency.
+// 32 heads, 264 to 270 us (6.1 to 6.3 TB/s); 8 tokens of 64 heads over 131072,
+// 93 us (5.8 TB/s); 16 trees of 64 tokens over up to 4096, 90 us, bound by the
+// softmax; one token over 513, 12 us, bound by latency.
 #include <cuda.h>
 
 #include <atomic>
@@ -1176,6 +1176,8 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           }
           __syncwarp();
           tmem_st16(t_s + 64 + 32 * buf + 16, p + 16);
+          // (the product takes weights in the cache's type, each off by at most half a step
+          // of it; their sum is of the unrounded ones)
           float sa, sb;
           f2unpack(add2(sum2[0], sum2[1]), sa, sb);
           l += sa + sb;
@@ -1750,10 +1752,13 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   KernelArgs k{};
   k.a = a;
   // Reading shared blocks once takes two more kernels and a second part of
-  // every row.  While all the sequences' tables hold less than what the L2
-  // cache does, reading them again costs less than that.  Measured, once and
-  // again: 8 sequences that share 512 of 700 tokens 26.9 and 19.4 us; 16 x 16
-  // that share 2048 of 2690 272 and 437 us.
+  // every row.  While all that the sequences' tables have room for is less than
+  // what the L2 cache holds, reading it again costs less than that.  The host
+  // knows the tables' room, not the tokens held (they are on the device): tables
+  // with much room to spare are read once though they hold little.  Measured,
+  // once and again: 8 sequences that share 512 of 700 tokens 27.4 and 20.2 us
+  // (room for 96 MB and more, and for 24 to 92 MB); 16 x 16 that share 2048 of
+  // 2690 272 and 437 us.
   const double table_bytes = static_cast<double>(a.b.S) * a.b.T * a.c.block_size * a.c.kv_heads * a.c.head_dim * 4;
   if (table_bytes < 96e6) k.a.b.group = 1;
   carve(a.c, k.a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
@@ -1770,8 +1775,9 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   k.shift = log2 ? log2 - 1 : 0;
   // a box is a run of tokens inside one block and one tile; the swizzle
   // repeats every eight rows, so a box starts on a multiple of eight.  Blocks
-  // of other sizes are copied by the lanes, 16 bytes each: 34 x 64 rows over up
-  // to 7379 tokens in blocks of 20 take 294 us, 1.9 times their bytes' time
+  // of other sizes are copied by the lanes, 16 bytes each: 34 trees of 64 rows,
+  // 16 heads over 8, 7379 tokens in blocks of 20 take 328 us, 2.1 times their
+  // bytes' time
   int box = kTile;
   while (a.c.block_size % box) box >>= 1;
   CUtensorMap map_q{}, map_k{}, map_v{};

@@ -110,7 +110,9 @@ extern "C" {
 #define SMC_PURPOSE_RESAMPLE  4  /* stream b, position 0                         */
 
 /* SMC_F16 is a type of the paged cache only: logits are SMC_F32 or SMC_BF16. */
-typedef enum { SMC_F32 = 0, SMC_BF16 = 1, SMC_F16 = 2 } smc_dtype;
+/* SMC_E4M3 (8 bits: sign, 4 exponent and 3 mantissa bits, largest 448, no
+ * infinities, NaN 0x7f) is the type of an smc_cache8's elements only. */
+typedef enum { SMC_F32 = 0, SMC_BF16 = 1, SMC_F16 = 2, SMC_E4M3 = 3 } smc_dtype;
 
 /* Shape and scalars of one step. */
 typedef struct {
@@ -566,6 +568,82 @@ int32_t kv_compact_tokens(const smc_cache *cache, const smc_batch *batch, const 
  * stream: the layout is the same, and each leaves it as it needs it. */
 int32_t kv_truncate(const smc_params *p, const smc_kv *kv, const int32_t *new_len,
                     void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- the paged cache in 8 bits -----------------------------------------
+ * Half the bytes of a 16-bit cache, so twice the particles, or twice the
+ * context, in the same pool ([SMC] section 2, "系统优化设计": the KV cache is what
+ * the particles cost).  The block tables stay as they are; smc_step,
+ * kv_blocktable_remap and kv_truncate, which move tables only, serve it too.
+ *
+ * Keys and values are e4m3 numbers x with one fp32 scale s for each layer,
+ * block and key head, of keys and of values: an element is x * s.  A scale is
+ * read as one within [2^-100, 2^100]; the entry points write powers of two, so
+ * that putting a block under a larger scale rounds only what falls below its
+ * smallest normal number.  NaN and infinities are stored as NaN.
+ *
+ * Conventions, batches, status bits and the order behind the kernels ahead are
+ * those of the entry points above.  One workspace of
+ * smc_cache8_workspace_bytes() for the largest batch, zero-filled once, serves
+ * all of them on one stream. */
+
+/* An 8-bit cache: data.dtype SMC_E4M3 (strides in elements, that is in bytes);
+ * element (layer, block, head) of k_scale, and of v_scale, is at
+ * layer*scale_layer_stride + block*scale_block_stride + head*scale_head_stride
+ * (elements).  Scales of different blocks and heads do not overlap. */
+typedef struct {
+  smc_cache data;
+  float *k_scale, *v_scale; /* DEVICE                                            */
+  int64_t scale_layer_stride, scale_block_stride, scale_head_stride;
+} smc_cache8;
+
+/* smc_cache_workspace_bytes for the entry points below. */
+size_t smc_cache8_workspace_bytes(const smc_cache8 *cache, const smc_batch *batch,
+                                  int32_t q_heads);
+
+/* smc_tree_attention over an 8-bit cache: with z_j = scale * <q, k_j> over the
+ * visible tokens, k_j and v_j the elements times their scales,
+ *   out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j).
+ * q and out have `dtype`, SMC_BF16 or SMC_F16; arguments and rows that see
+ * nothing are otherwise as there.  head_dim a multiple of 16, at most 128;
+ * pointers and the cache's strides in multiples of 16 bytes, those of q and out
+ * in multiples of 8 elements.  Scores, statistics and sums are fp32; a row of q
+ * keeps what is above 2^-18 of its largest element, and a weight what is above
+ * 2^-28 of the row's largest weight times scale.  Equal inputs give equal bits. */
+int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, int32_t layer,
+                            const smc_batch *batch, int32_t dtype, const void *q,
+                            const uint32_t *mask, void *out, float *lse, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/* smc_qk_norm_rope into an 8-bit cache.  q, k, v, q_out and the norm weights
+ * have `dtype` (SMC_F32, SMC_BF16 or SMC_F16); with y a key after norm and
+ * rotation, or a value, in fp32, and for each layer, head and block that a
+ * sequence's new tokens lie in:
+ *   need  = the least 2^t, -100 <= t <= 100, with |y| <= 448 * 2^t for all
+ *           finite y of the block's new tokens;
+ *   scale = max(need, the block's scale) where the block holds tokens ahead of
+ *           the first new one, else need;
+ *   x     = y / scale, rounded to e4m3 (to nearest, ties to even; past 448: 448).
+ * Tokens ahead of the new ones are rounded again under a scale that has grown.
+ * A row that is skipped (its position out of range) leaves its slot's bytes. */
+int32_t smc_qk_norm_rope8(const smc_qk_params *p, const smc_cache8 *cache, int32_t layer,
+                          const smc_batch *batch, int32_t dtype, const void *q, const void *k,
+                          const void *v, const void *q_weight, const void *k_weight,
+                          const int32_t *positions, const float *rope, void *q_out,
+                          void *workspace, size_t ws_bytes, void *stream);
+
+/* kv_copy_blocks of an 8-bit cache: the blocks' elements and their scales. */
+int32_t kv_copy_blocks8(const smc_cache8 *cache, const int32_t *pairs, const int32_t *counts,
+                        int32_t lists, int32_t max_pairs, void *workspace, size_t ws_bytes,
+                        void *stream);
+
+/* kv_compact_tokens of an 8-bit cache.  A block that tokens move into gets the
+ * largest of its scale and the scales of the blocks that they come from; what
+ * moves, and where that scale has grown every other token that the sequence
+ * holds in the block, is rounded again under it (to nearest, ties to even).
+ * block_size at most 1024. */
+int32_t kv_compact_tokens8(const smc_cache8 *cache, const smc_batch *batch, const int32_t *path,
+                           const int32_t *n_path, int32_t max_path, void *workspace,
+                           size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ from .binding import (  # noqa: F401
     SMC_F16, smc_cache, smc_batch, make_cache, make_batch, smc_cache_workspace_bytes,
     alloc_cache_workspace, smc_tree_attention, smc_qk_norm_rope, kv_copy_blocks,
     kv_compact_tokens, kv_truncate,
+    SMC_E4M3, smc_cache8, make_cache8, smc_cache8_workspace_bytes, alloc_cache8_workspace,
+    smc_tree_attention8, smc_qk_norm_rope8, kv_copy_blocks8, kv_compact_tokens8,
 )
 
 __all__ = [
@@ -30,4 +32,6 @@ __all__ = [
     "SMC_F16", "smc_cache", "smc_batch", "make_cache", "make_batch", "smc_cache_workspace_bytes",
     "alloc_cache_workspace", "smc_tree_attention", "smc_qk_norm_rope", "kv_copy_blocks",
     "kv_compact_tokens", "kv_truncate",
+    "SMC_E4M3", "smc_cache8", "make_cache8", "smc_cache8_workspace_bytes", "alloc_cache8_workspace",
+    "smc_tree_attention8", "smc_qk_norm_rope8", "kv_copy_blocks8", "kv_compact_tokens8",
 ]

@@ -15,7 +15,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmcsd.so")
 
-SMC_F32, SMC_BF16, SMC_F16 = 0, 1, 2
+SMC_F32, SMC_BF16, SMC_F16, SMC_E4M3 = 0, 1, 2, 3
 
 # device status bits (smcsd.h)
 DEV_BITS = {
@@ -84,6 +84,12 @@ class smc_qk_params(ctypes.Structure):
                 ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
+class smc_cache8(ctypes.Structure):
+    _fields_ = [("data", smc_cache), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("scale_layer_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 _SIGS = {
@@ -136,6 +142,24 @@ _SIGS = {
     "kv_truncate": (ctypes.c_int32, [ctypes.POINTER(smc_params), ctypes.POINTER(smc_kv),
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                      ctypes.c_void_p]),
+    "smc_cache8_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(smc_cache8),
+                                                     ctypes.POINTER(smc_batch), ctypes.c_int32]),
+    "smc_tree_attention8": (ctypes.c_int32, [ctypes.POINTER(smc_attn_params),
+                                             ctypes.POINTER(smc_cache8), ctypes.c_int32,
+                                             ctypes.POINTER(smc_batch), ctypes.c_int32] +
+                            [ctypes.c_void_p] * 4 +
+                            [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "smc_qk_norm_rope8": (ctypes.c_int32, [ctypes.POINTER(smc_qk_params),
+                                           ctypes.POINTER(smc_cache8), ctypes.c_int32,
+                                           ctypes.POINTER(smc_batch), ctypes.c_int32] +
+                          [ctypes.c_void_p] * 8 +
+                          [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kv_copy_blocks8": (ctypes.c_int32, [ctypes.POINTER(smc_cache8), ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kv_compact_tokens8": (ctypes.c_int32, [ctypes.POINTER(smc_cache8), ctypes.POINTER(smc_batch),
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -522,13 +546,9 @@ def _rows(t, name, dtype, shape):
     raise ValueError(f"{name}'s last axis must be contiguous")
 
 
-def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=None, scale=None,
-                       stream=None):
-    """Attention of the new tokens q [rows, q_heads, head_dim] over their
-    sequences' caches into out; mask [rows, words] int32 of packed bits (None:
-    a chain), lse [rows, q_heads] fp32 (None: not wanted), scale (None:
-    head_dim ** -0.5).  See smc_tree_attention in smcsd.h."""
-    rows, dim, dtype = batch.rows, cache.head_dim, _CACHE_TORCH[cache.dtype]
+def _attention_args(cache, dtype, batch, q, out, workspace, mask, lse, scale):
+    """smc_attn_params and the arrays of an attention call."""
+    rows, dim = batch.rows, cache.head_dim
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
     heads = q.shape[1]
@@ -543,22 +563,27 @@ def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=No
         words = mask.shape[1]
     params = smc_attn_params(heads, words, dim ** -0.5 if scale is None else scale, 0,
                              q_row, q_head, o_row, o_head)
+    return (params, qp, None if mask is None else _addr(mask, "mask", torch.int32), op,
+            None if lse is None else _addr(lse, "lse", torch.float32, rows * heads),
+            _addr(workspace, "workspace", torch.uint8))
+
+
+def smc_tree_attention(cache, layer, batch, q, out, workspace, mask=None, lse=None, scale=None,
+                       stream=None):
+    """Attention of the new tokens q [rows, q_heads, head_dim] over their
+    sequences' caches into out; mask [rows, words] int32 of packed bits (None:
+    a chain), lse [rows, q_heads] fp32 (None: not wanted), scale (None:
+    head_dim ** -0.5).  See smc_tree_attention in smcsd.h."""
+    params, *arrays = _attention_args(cache, _CACHE_TORCH[cache.dtype], batch, q, out, workspace, mask, lse, scale)
     _check("smc_tree_attention", (_lib or lib()).smc_tree_attention(
-        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp,
-        None if mask is None else _addr(mask, "mask", torch.int32), op,
-        None if lse is None else _addr(lse, "lse", torch.float32, rows * heads),
-        _addr(workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(stream, workspace)))
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), *arrays,
+        workspace.numel(), _raw_stream(stream, workspace)))
 
 
-def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, positions=None,
-                     q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
-                     stream=None):
-    """Norms and rotation of the new tokens' q [rows, q_heads, head_dim] (into
-    q_out) and k [rows, kv_heads, head_dim] (into the cache, with v).  rope
-    [max_pos, rot_dim] fp32: cosines, then sines; positions [rows] int32
-    (None: the tokens' own); weights [head_dim] (None: no norm).  See
-    smc_qk_norm_rope in smcsd.h."""
-    rows, dim, dtype = batch.rows, cache.head_dim, _CACHE_TORCH[cache.dtype]
+def _qk_args(cache, dtype, batch, q, k, v, rope, q_out, workspace, positions, q_weight, k_weight, eps,
+             weight_offset, interleaved):
+    """smc_qk_params and the arrays of a call that norms, rotates and stores."""
+    rows, dim = batch.rows, cache.head_dim
     if q.dim() != 3 or rope.dim() != 2:
         raise ValueError("q must be [rows, q_heads, head_dim] and rope [max_pos, rot_dim]")
     heads = q.shape[1]
@@ -570,13 +595,26 @@ def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, posit
     max_pos, rot = rope.shape
     params = smc_qk_params(heads, rot, max_pos, 1 if interleaved else 0, eps, weight_offset, q_row,
                            q_head, k_row, k_head, v_row, v_head, o_row, o_head)
+    return (params, qp, kp, vp,
+            None if q_weight is None else _addr(q_weight, "q_weight", dtype, dim),
+            None if k_weight is None else _addr(k_weight, "k_weight", dtype, dim),
+            None if positions is None else _addr(positions, "positions", torch.int32, rows),
+            _addr(rope, "rope", torch.float32), op, _addr(workspace, "workspace", torch.uint8))
+
+
+def smc_qk_norm_rope(cache, layer, batch, q, k, v, rope, q_out, workspace, positions=None,
+                     q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
+                     stream=None):
+    """Norms and rotation of the new tokens' q [rows, q_heads, head_dim] (into
+    q_out) and k [rows, kv_heads, head_dim] (into the cache, with v).  rope
+    [max_pos, rot_dim] fp32: cosines, then sines; positions [rows] int32
+    (None: the tokens' own); weights [head_dim] (None: no norm).  See
+    smc_qk_norm_rope in smcsd.h."""
+    params, *arrays = _qk_args(cache, _CACHE_TORCH[cache.dtype], batch, q, k, v, rope, q_out, workspace, positions,
+                               q_weight, k_weight, eps, weight_offset, interleaved)
     _check("smc_qk_norm_rope", (_lib or lib()).smc_qk_norm_rope(
-        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), qp, kp, vp,
-        None if q_weight is None else _addr(q_weight, "q_weight", dtype, dim),
-        None if k_weight is None else _addr(k_weight, "k_weight", dtype, dim),
-        None if positions is None else _addr(positions, "positions", torch.int32, rows),
-        _addr(rope, "rope", torch.float32), op, _addr(workspace, "workspace", torch.uint8), workspace.numel(),
-        _raw_stream(stream, workspace)))
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), *arrays,
+        workspace.numel(), _raw_stream(stream, workspace)))
 
 
 def kv_copy_blocks(cache, pairs, counts, workspace, stream=None):
@@ -610,3 +648,110 @@ def kv_truncate(params, kv, new_len, workspace, stream=None):
         ctypes.byref(params), ctypes.byref(kv),
         _addr(new_len, "new_len", torch.int32, params.B * params.N), _addr(workspace, "workspace", torch.uint8),
         workspace.numel(), _raw_stream(stream, workspace)))
+
+
+# ---- the paged cache in 8 bits ----------------------------------------------
+
+
+def make_cache8(k, v, k_scale, v_scale):
+    """smc_cache8 over keys and values [layers, blocks, block_size, kv_heads,
+    head_dim] in float8_e4m3fn, as make_cache takes them, and their scales
+    [layers, blocks, kv_heads] fp32 (one set of strides).  The struct keeps the
+    tensors alive."""
+    arrays = (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale))
+    for name, t in arrays:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    for name, t in arrays:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 5 or t.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"{name} must be [layers, blocks, block_size, kv_heads, head_dim] "
+                             f"in float8_e4m3fn, got {tuple(t.shape)} {t.dtype}")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have one shape and set of strides")
+    if k.numel() == 0 or (k.stride(4) != 1 and k.shape[4] > 1):
+        raise ValueError("k and v must not be empty and their last axis must be contiguous")
+    shape = (k.shape[0], k.shape[1], k.shape[3])
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.shape != shape or t.dtype != torch.float32:
+            raise ValueError(f"{name} must be {shape} in float32, got {tuple(t.shape)} {t.dtype}")
+    if k_scale.stride() != v_scale.stride():
+        raise ValueError("k_scale and v_scale must have one set of strides")
+    if any(n > 1 and s == 0 for n, s in zip(shape, k_scale.stride())):
+        raise ValueError("k_scale and v_scale must not be broadcast")
+    data = smc_cache(k.data_ptr(), v.data_ptr(), *k.stride()[:4], *k.shape, SMC_E4M3)
+    cache = smc_cache8(data, k_scale.data_ptr(), v_scale.data_ptr(), *k_scale.stride())
+    cache.tensors = (k, v, k_scale, v_scale)
+    return cache
+
+
+def smc_cache8_workspace_bytes(cache, batch=None, q_heads=0):
+    n = lib().smc_cache8_workspace_bytes(
+        ctypes.byref(cache), None if batch is None else ctypes.byref(batch), int(q_heads))
+    if n == 0:
+        raise SmcError("smc_cache8_workspace_bytes", -1, "invalid shape")
+    return n
+
+
+def alloc_cache8_workspace(cache, batch=None, q_heads=0, device="cuda"):
+    """A zero-filled workspace for the 8-bit cache's entry points: with a batch
+    and q_heads for all of them, without for those that take no batch."""
+    return torch.zeros(smc_cache8_workspace_bytes(cache, batch, q_heads), dtype=torch.uint8,
+                       device=device)
+
+
+def _row_dtype(q, allowed):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dtype not in allowed:
+        raise ValueError(f"q must be one of {', '.join(map(str, allowed))}, got {q.dtype}")
+    return q.dtype
+
+
+def smc_tree_attention8(cache, layer, batch, q, out, workspace, mask=None, lse=None, scale=None,
+                        stream=None):
+    """smc_tree_attention over an 8-bit cache; q and out in bf16 or fp16.  See
+    smc_tree_attention8 in smcsd.h."""
+    dtype = _row_dtype(q, (torch.bfloat16, torch.float16))
+    params, *arrays = _attention_args(cache.data, dtype, batch, q, out, workspace, mask, lse, scale)
+    _check("smc_tree_attention8", (_lib or lib()).smc_tree_attention8(
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), _CACHE_DTYPES[dtype], *arrays,
+        workspace.numel(), _raw_stream(stream, workspace)))
+
+
+def smc_qk_norm_rope8(cache, layer, batch, q, k, v, rope, q_out, workspace, positions=None,
+                      q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
+                      stream=None):
+    """smc_qk_norm_rope into an 8-bit cache; q, k, v, q_out and the weights in
+    one dtype (fp32, bf16 or fp16).  See smc_qk_norm_rope8 in smcsd.h."""
+    dtype = _row_dtype(q, tuple(_CACHE_DTYPES))
+    params, *arrays = _qk_args(cache.data, dtype, batch, q, k, v, rope, q_out, workspace, positions, q_weight,
+                               k_weight, eps, weight_offset, interleaved)
+    _check("smc_qk_norm_rope8", (_lib or lib()).smc_qk_norm_rope8(
+        ctypes.byref(params), ctypes.byref(cache), layer, ctypes.byref(batch), _CACHE_DTYPES[dtype], *arrays,
+        workspace.numel(), _raw_stream(stream, workspace)))
+
+
+def kv_copy_blocks8(cache, pairs, counts, workspace, stream=None):
+    """kv_copy_blocks of an 8-bit cache: the blocks' elements and scales."""
+    if pairs.dim() != 3 or pairs.shape[2] != 2:
+        raise ValueError(f"pairs must be [lists, max_pairs, 2], got {tuple(pairs.shape)}")
+    lists, most = pairs.shape[:2]
+    _check("kv_copy_blocks8", (_lib or lib()).kv_copy_blocks8(
+        ctypes.byref(cache), _addr(pairs, "pairs", torch.int32),
+        _addr(counts, "counts", torch.int32, lists), lists, most, _addr(workspace, "workspace", torch.uint8),
+        workspace.numel(), _raw_stream(stream, workspace)))
+
+
+def kv_compact_tokens8(cache, batch, path, n_path, workspace, stream=None):
+    """kv_compact_tokens of an 8-bit cache: what meets a larger scale is
+    rounded again under it."""
+    if path.dim() != 2:
+        raise ValueError(f"path must be [S, max_path], got {tuple(path.shape)}")
+    _check("kv_compact_tokens8", (_lib or lib()).kv_compact_tokens8(
+        ctypes.byref(cache), ctypes.byref(batch),
+        _addr(path, "path", torch.int32, batch.S * path.shape[1]),
+        _addr(n_path, "n_path", torch.int32, batch.S), path.shape[1],
+        _addr(workspace, "workspace", torch.uint8), workspace.numel(), _raw_stream(stream, workspace)))

@@ -37,6 +37,47 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// ---- 8 bits ----------------------------------------------------------------
+constexpr float kLeastScale = 0x1p-100f, kMostScale = 0x1p100f;
+
+// A stored scale as it counts: within [2^-100, 2^100], NaN as the least.
+__device__ __forceinline__ float scale_of(float s) { return fminf(fmaxf(s, kLeastScale), kMostScale); }
+
+// The least 2^t in that range with top <= 448 * 2^t = 1.75 * 2^(t + 8); top >= 0.
+__device__ __forceinline__ float least_scale(float top) {
+  const uint32_t bits = __float_as_uint(top);
+  const int t = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return __uint_as_float(static_cast<uint32_t>(min(max(t, -100), 100) + 127) << 23);
+}
+// Two numbers to e4m3, a in the low byte: to nearest, ties to even; past 448
+// to 448, NaN to NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Infinities are stored as NaN.
+__device__ __forceinline__ float finite_or_nan(float x) {
+  return fabsf(x) < INFINITY ? x : __uint_as_float(0x7fffffffu);
+}
+// Two e4m3 numbers (the low 16 bits) as fp16, exactly.
+__device__ __forceinline__ uint32_t from_e4m3x2(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
+  return r;
+}
+// Four e4m3 numbers under another scale: each times f, rounded again.
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t x, float f) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = from_e4m3x2(x >> (16 * i));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    r |= to_e4m3x2(v.x * f, v.y * f) << (16 * i);
+  }
+  return r;
+}
+
 // A sequence's rows [row0, row0 + n) and the tokens it holds.  n = 0 and bits
 // set when its offsets or its token count are out of range, so that a caller
 // which honours n touches nothing outside the arrays.

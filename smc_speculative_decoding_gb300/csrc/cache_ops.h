@@ -24,7 +24,13 @@ struct BatchArgs {
   int32_t S, T, rows, max_new, group;
 };
 
-inline int dtype_bytes(int dtype) { return dtype == SMC_F32 ? 4 : 2; }
+inline int dtype_bytes(int dtype) { return dtype == SMC_F32 ? 4 : dtype == SMC_E4M3 ? 1 : 2; }
+
+// Scales of an 8-bit cache: k, v at the layer's first one.  Strides in elements.
+struct ScaleArgs {
+  float *k, *v;
+  int64_t layer, block, head;
+};
 
 struct QkArgs {
   CacheArgs c;
@@ -71,6 +77,21 @@ cudaError_t launch_copy_blocks(const CacheArgs &c, const int32_t *pairs, const i
 cudaError_t launch_compact_tokens(const CacheArgs &c, const BatchArgs &b, const int32_t *path,
                                   const int32_t *n_path, int max_path, unsigned *status,
                                   cudaStream_t st);
+
+// The same over 8-bit caches.  `a.c` is the cache (dtype SMC_E4M3); `dtype` that
+// of the rows of q, k, v and out.
+size_t attention8_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads);
+cudaError_t launch_tree_attention8(const AttnArgs &a, const ScaleArgs &s, int dtype, void *workspace,
+                                   cudaStream_t st);
+cudaError_t launch_qk_norm_rope8(const QkArgs &a, const ScaleArgs &s, int dtype, cudaStream_t st);
+cudaError_t launch_copy_blocks8(const CacheArgs &c, const ScaleArgs &s, const int32_t *pairs,
+                                const int32_t *counts, int lists, int max_pairs, unsigned *status,
+                                cudaStream_t st);
+// Most tokens of a block that launch_compact_tokens8 takes.
+constexpr int kMostCompactBlock = 1024;
+cudaError_t launch_compact_tokens8(const CacheArgs &c, const ScaleArgs &s, const BatchArgs &b,
+                                   const int32_t *path, const int32_t *n_path, int max_path,
+                                   unsigned *status, cudaStream_t st);
 cudaError_t launch_kv_truncate(int B, int N, const KvArgs &kv, const int32_t *new_len,
                                const Workspace &ws, cudaStream_t st);
 

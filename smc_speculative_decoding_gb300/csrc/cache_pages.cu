@@ -34,10 +34,11 @@ static BlockRows block_rows(const CacheArgs &c) {
 // way before their stores.  Bound by DRAM: the pairs of 256 particles in 32
 // layers, blocks of 16 tokens of 8 heads of 128 in bf16, 641 MB, take 95.5 us
 // (6.7 TB/s).
-template <typename U>
+// kScaled: an 8-bit cache, whose blocks' scales go with them.
+template <typename U, bool kScaled>
 __global__ void __launch_bounds__(kPageThreads)
 copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_t *counts,
-                   int max_pairs, int esz, unsigned *status) {
+                   int max_pairs, int esz, unsigned *status, ScaleArgs sc) {
   const int list = blockIdx.x / max_pairs, i = blockIdx.x % max_pairs;
   wait_for_stream();
   const int n = counts[list];
@@ -53,6 +54,12 @@ copy_blocks_kernel(CacheArgs c, BlockRows br, const int32_t *pairs, const int32_
     return;
   }
   const int layer = blockIdx.y >> 1;
+  if constexpr (kScaled) {
+    float *s = ((blockIdx.y & 1) ? sc.v : sc.k) + layer * sc.layer;
+    for (int h = threadIdx.x; h < c.kv_heads; h += kPageThreads) {
+      s[dst * sc.block + h * sc.head] = s[src * sc.block + h * sc.head];
+    }
+  }
   char *base = ((blockIdx.y & 1) ? c.v : c.k) + layer * c.layer_stride * esz;
   const char *from = base + src * c.block_stride * esz;
   char *to = base + dst * c.block_stride * esz;
@@ -261,20 +268,41 @@ static int access_bytes(const CacheArgs &c) {
                         static_cast<uint64_t>(c.head_stride * esz) |
                         static_cast<uint64_t>(c.head_dim) * esz;
   if (bits % 16 == 0) return 16;
-  return bits % 4 == 0 ? 4 : 2;
+  return bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+template <bool kScaled>
+static const void *copy_blocks_fn(int width) {
+  switch (width) {
+    case 16: return reinterpret_cast<const void *>(copy_blocks_kernel<uint4, kScaled>);
+    case 4: return reinterpret_cast<const void *>(copy_blocks_kernel<uint32_t, kScaled>);
+    default: return reinterpret_cast<const void *>(copy_blocks_kernel<uint16_t, kScaled>);
+  }
+}
+
+static cudaError_t launch_copies(const void *fn, const CacheArgs &c, const ScaleArgs &s, const int32_t *pairs,
+                                 const int32_t *counts, int lists, int max_pairs, unsigned *status, cudaStream_t st) {
+  CacheArgs cache = c;
+  ScaleArgs scales = s;
+  BlockRows rows = block_rows(c);
+  int esz = dtype_bytes(c.dtype);
+  void *args[] = {&cache, &rows, &pairs, &counts, &max_pairs, &esz, &status, &scales};
+  return launch_early(fn, dim3(lists * max_pairs, 2 * c.layers), kPageThreads, 0, args, st);
 }
 
 cudaError_t launch_copy_blocks(const CacheArgs &c, const int32_t *pairs, const int32_t *counts,
                                int lists, int max_pairs, unsigned *status, cudaStream_t st) {
-  CacheArgs cache = c;
-  BlockRows rows = block_rows(c);
-  int esz = dtype_bytes(c.dtype);
+  return launch_copies(copy_blocks_fn<false>(access_bytes(c)), c, ScaleArgs{}, pairs, counts, lists, max_pairs,
+                       status, st);
+}
+
+cudaError_t launch_copy_blocks8(const CacheArgs &c, const ScaleArgs &s, const int32_t *pairs,
+                                const int32_t *counts, int lists, int max_pairs, unsigned *status,
+                                cudaStream_t st) {
   const int width = access_bytes(c);
-  const void *fn = width == 16  ? reinterpret_cast<const void *>(copy_blocks_kernel<uint4>)
-                   : width == 4 ? reinterpret_cast<const void *>(copy_blocks_kernel<uint32_t>)
-                                : reinterpret_cast<const void *>(copy_blocks_kernel<uint16_t>);
-  void *args[] = {&cache, &rows, &pairs, &counts, &max_pairs, &esz, &status};
-  return launch_early(fn, dim3(lists * max_pairs, 2 * c.layers), kPageThreads, 0, args, st);
+  const void *fn = width == 1 ? reinterpret_cast<const void *>(copy_blocks_kernel<uint8_t, true>)
+                              : copy_blocks_fn<true>(width);
+  return launch_copies(fn, c, s, pairs, counts, lists, max_pairs, status, st);
 }
 
 cudaError_t launch_compact_tokens(const CacheArgs &c, const BatchArgs &b, const int32_t *path,

@@ -12,403 +12,29 @@
 // 32 heads, 264 to 270 us (6.1 to 6.3 TB/s); 8 tokens of 64 heads over 131072,
 // 93 us (5.8 TB/s); 16 trees of 64 tokens over up to 4096, 90 us, bound by the
 // softmax; one token over 513, 12 us, bound by latency.
-#include <cuda.h>
-
 #include <atomic>
 
-#include "cache_common.cuh"
+#include "attention_work.cuh"
+#include "tensor_core.cuh"
 
 namespace smcsd {
 
-// ---------------------------------------------------------------------------
-// Work.  An *entry* is a run of consecutive rows and a range of tokens that
-// they all attend: the own part of one sequence, or the part that the
-// sequences of a prompt share (their leading equal table slots).  Per key
-// head and per two row tiles an entry makes one *unit* of ceil(tokens / 64)
-// tiles.  A row tile is floor(128 / rep) new tokens times the rep query heads
-// of the key head, so a tile starts on a token.  The units' tiles form one
-// line; CTA c takes tiles [c * per, (c + 1) * per) of it, so ragged lengths
-// load every SM alike.  A unit's first tiles' CTA owns the unit's result;
-// every later CTA of the unit has exactly one such continuation (its first
-// segment) and stores it in its own slot.
-// ---------------------------------------------------------------------------
+// A unit has two row tiles of 128 rows, each floor(128 / rep) new tokens times
+// the rep query heads of a key head, so that a row tile starts on a token.
 constexpr int kTile = 64;         // tokens per tile
 constexpr int kRows = 128;        // rows of a tensor-core tile
 constexpr int kUnitRows = 256;    // most rows of a unit: two tensor-core tiles of 128
 constexpr int kMaxCtas = 192;     // slots for continuations
-constexpr int kPlanThreads = 1024;
-constexpr uint32_t kWaitPolls = 1u << 17;  // each may suspend up to 20 us
-
-struct Entry {
-  int row0;    // first row
-  int tokens;  // rows of one query head
-  int seq;     // whose table
-  int kv0, kv1;
-  int ctx;     // tokens before ctx are seen by every row
-  int tiles;   // per unit
-  int flags;
-};
-constexpr int kShared = 1, kSolo = 2;  // a shared part; the rows have no other part
-
-// The unit that the boundary before a CTA is the first to cut.
-struct Cut {
-  int row0, rows, head, more;  // first row, rows of the unit (0: no such unit), key head,
-  int flags, pad[3];           // continuations; the entry's flags
-};
-
-struct PlanHeader {
-  unsigned ticket;  // plan CTAs done; returns to zero
-  int total, per;   // tiles, tiles per CTA
-};
-
-struct AttnWorkspace {
-  PlanHeader *head;
-  unsigned *tickets;  // [kMaxCtas] parts stored of the unit that a CTA's end cuts; return to zero
-  int *common;     // [groups] shared tokens
-  int *ref;        // [groups] the sequence by whose table they are read
-  int *tile0;      // [entries + 1]
-  Entry *entries;  // shared parts of the groups (when group > 1), then the sequences
-  float *lse[2];   // own, shared: [rows * q_heads], log2
-  float *o[2];     // [rows * q_heads][head_dim], normalised
-  Cut *cuts;       // [kMaxCtas]
-  float *lse_c;    // [kMaxCtas][kUnitRows] continuations
-  float *o_c;      // [kMaxCtas][kUnitRows][head_dim]
-  int groups;      // 0 when group == 1
-  int n_entries;
-};
-
-static size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, char *base,
-                    AttnWorkspace *w) {
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = off;
-    off = (off + bytes + 255) / 256 * 256;
-    return base + at;
-  };
-  AttnWorkspace t{};
-  const size_t rh = static_cast<size_t>(b.rows) * q_heads, D = c.head_dim;
-  t.groups = b.group > 1 ? b.S / b.group : 0;
-  t.n_entries = b.S + t.groups;
-  take(kCacheStatusBytes);
-  t.head = reinterpret_cast<PlanHeader *>(take(sizeof(PlanHeader)));
-  t.tickets = reinterpret_cast<unsigned *>(take(sizeof(unsigned) * kMaxCtas));
-  t.common = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
-  t.ref = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
-  t.tile0 = reinterpret_cast<int *>(take(sizeof(int) * (static_cast<size_t>(t.n_entries) + 1)));
-  t.entries = reinterpret_cast<Entry *>(take(sizeof(Entry) * t.n_entries));
-  for (int k = 0; k < 2; ++k) {
-    const size_t n = k == 0 || t.groups ? rh : 0;
-    t.lse[k] = reinterpret_cast<float *>(take(sizeof(float) * n));
-    t.o[k] = reinterpret_cast<float *>(take(sizeof(float) * n * D));
-  }
-  t.cuts = reinterpret_cast<Cut *>(take(sizeof(Cut) * kMaxCtas));
-  t.lse_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows));
-  t.o_c = reinterpret_cast<float *>(take(sizeof(float) * kMaxCtas * kUnitRows * D));
-  if (w) *w = t;
-  return off;
-}
 
 size_t attention_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads) {
-  return carve(c, b, q_heads, nullptr, nullptr);
+  return carve(c, b, q_heads, kMaxCtas, kUnitRows, nullptr, nullptr);
 }
 
-struct KernelArgs {
-  AttnArgs a;
-  AttnWorkspace w;
-  int rep;      // query heads per key head, at most 128
-  int tile_tokens;  // new tokens of a row tile: floor(128 / rep)
-  int q_box;    // new tokens of a copied box of Q
-  int planned;      // plan_kernel has run (else each CTA finds its own work)
-  int more_kernels; // joins follow (a call's last kernel lets nothing start before its end)
-  int join_inside;  // the last CTA of a cut unit joins its parts
-  int box;      // tokens per copied box
-  uint32_t magic, shift;  // t / block_size == umulhi(t, magic) >> shift
-  float sc;     // scale * log2 e
+using KernelArgs = WorkArgs;
+struct Units {
+  static constexpr int kTile = smcsd::kTile, kRowTiles = 2, kUnitRows = smcsd::kUnitRows;
+  static constexpr bool kParts = false;
 };
-
-// ---------------------------------------------------------------------------
-// plan_kernel: the tokens that each prompt's sequences share, then (the last
-// CTA to finish) the entries and the prefix of their tiles.
-// ---------------------------------------------------------------------------
-__device__ int block_scan_excl(int v, int *warps, int *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) warps[warp] = incl;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int k = 0; k < kPlanThreads / 32; ++k) {
-    if (k < warp) before += warps[k];
-    all += warps[k];
-  }
-  __syncthreads();
-  *total = all;
-  return before + incl - v;
-}
-
-// Units of one key head: row tiles of an entry, two by two.
-__device__ __forceinline__ int unit_tiles(const KernelArgs &k, int tokens) {
-  return (tokens + 2 * k.tile_tokens - 1) / (2 * k.tile_tokens);
-}
-
-__device__ __forceinline__ int entry_tiles(const KernelArgs &k, int tokens, int kv0, int kv1,
-                                           int *per_unit) {
-  *per_unit = (kv1 - kv0 + kTile - 1) / kTile;
-  if (tokens <= 0 || kv1 <= kv0) return 0;
-  return *per_unit * k.a.c.kv_heads * unit_tiles(k, tokens);
-}
-
-__device__ int make_entry(const KernelArgs &k, int e, Entry *out) {
-  const BatchArgs &b = k.a.b;
-  const int bs = k.a.c.block_size;
-  Entry t{};
-  int tiles;
-  if (e < k.w.groups) {
-    const int s0 = e * b.group;
-    const int shared = __ldcg(&k.w.common[e]);
-    if (shared > 0) {  // every sequence is in order, so the rows are consecutive
-      const SeqInfo first = seq_info(b, bs, s0), last = seq_info(b, bs, s0 + b.group - 1);
-      // (a sequence without rows has no part in what the others share: the first one's table may be another)
-      t = {first.row0, last.row0 + last.n - first.row0, __ldcg(&k.w.ref[e]), 0, shared, shared, 0, kShared};
-    }
-    tiles = entry_tiles(k, t.tokens, 0, shared, &t.tiles);
-  } else {
-    const int s = e - k.w.groups;
-    const SeqInfo si = seq_info(b, bs, s);
-    if (si.bits) raise_status(k.a.status, si.bits);
-    const int shared = k.w.groups ? __ldcg(&k.w.common[s / b.group]) : 0;
-    t = {si.row0, si.n, s, shared, si.len, si.len - si.n, 0, shared ? 0 : kSolo};
-    tiles = entry_tiles(k, t.tokens, t.kv0, t.kv1, &t.tiles);
-  }
-  if (out) *out = t;
-  return tiles;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ KernelArgs k, int ctas) {
-  __shared__ int warps[kPlanThreads / 32];
-  __shared__ int s_slots, s_limit, s_seqs, s_bad, s_ref;
-  __shared__ bool s_last;
-  const int tid = threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  wait_for_stream();
-  const BatchArgs &b = k.a.b;
-  const int bs = k.a.c.block_size;
-  if (k.w.groups) {
-    const int s0 = blockIdx.x * b.group;
-    if (tid == 0) {
-      s_limit = 0x7fffffff;
-      s_seqs = s_bad = 0;
-      s_ref = 0x7fffffff;
-    }
-    __syncthreads();
-    for (int i = tid; i < b.group; i += kPlanThreads) {
-      const SeqInfo si = seq_info(b, bs, s0 + i);
-      if (si.bits) s_bad = 1;
-      if (si.n > 0) {
-        atomicMin(&s_limit, si.len - si.n);
-        atomicAdd(&s_seqs, 1);
-        atomicMin(&s_ref, s0 + i);
-      }
-    }
-    __syncthreads();
-    if (tid == 0) s_slots = s_seqs > 1 && !s_bad ? s_limit / bs : 0;
-    __syncthreads();
-    const int slots = s_slots;
-    if (slots > 0) {  // a warp per sequence, against the first one that has rows
-      const int32_t *ref = b.tables + static_cast<int64_t>(s_ref) * b.T;
-      int mine = slots;
-      for (int i = s_ref - s0 + 1 + (tid >> 5); i < b.group; i += kPlanThreads / 32) {
-        if (b.row_start && b.row_start[s0 + i] == b.row_start[s0 + i + 1]) continue;  // no rows
-        const int32_t *row = b.tables + static_cast<int64_t>(s0 + i) * b.T;
-#pragma unroll 4
-        for (int t = tid & 31; t < slots; t += 32) {
-          if (row[t] != ref[t]) mine = min(mine, t);
-        }
-      }
-      if (mine < slots) atomicMin(&s_slots, mine);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      const int64_t tokens = static_cast<int64_t>(s_slots) * bs;
-      k.w.common[blockIdx.x] = static_cast<int>(tokens / kTile * kTile);
-      k.w.ref[blockIdx.x] = s_ref;
-      __threadfence();
-      s_last = atomicAdd(&k.w.head->ticket, 1) + 1 == gridDim.x;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    if (tid == 0) k.w.head->ticket = 0;
-    __threadfence();
-  }
-  // the prefix of the tiles: thread t takes a run of entries
-  const int run = (k.w.n_entries + kPlanThreads - 1) / kPlanThreads;
-  const int e0 = min(tid * run, k.w.n_entries), e1 = min(e0 + run, k.w.n_entries);
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    Entry t;
-    mine += make_entry(k, e, &t);
-    k.w.entries[e] = t;
-  }
-  int total;
-  int at = block_scan_excl(mine, warps, &total);
-  for (int e = e0; e < e1; ++e) {
-    k.w.tile0[e] = at;
-    const Entry &t = k.w.entries[e];
-    int unused;
-    at += entry_tiles(k, t.tokens, t.kv0, t.kv1, &unused);
-  }
-  if (tid == 0) {
-    k.w.tile0[k.w.n_entries] = total;
-    k.w.head->total = total;
-    k.w.head->per = max(1, (total + ctas - 1) / ctas);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Tensor-core and tensor-memory primitives (PTX for sm_103a).
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc_512(uint32_t *dst) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                   smem_addr(dst))
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free_512(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-// Shared-memory operand in 128-byte-swizzled rows of 64 elements: `lbo` bytes
-// between 64-element panels (of the contiguous axis, MN-major operands only),
-// 1024 bytes between groups of eight rows.  Only the low word of a descriptor
-// varies.  The products take it as 32 bits and are issued by an elected
-// thread: with 64-bit descriptors in an unrolled `lane == 0` branch the
-// compiled code used wrong addresses for all but the first step.
-constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;  // version, swizzle
-__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lbo) {  // low word
-  return (addr & 0x3ffffu) >> 4 | (lbo >> 4) << 16;
-}
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
-      : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(yes));
-  return yes != 0;
-}
-#define SMC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
-                     "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-#define SMC_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), \
-                     "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-// 32 columns of the calling warp's 32 lanes: thread = lane, register = column.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : SMC_R8(r, 0), SMC_R8(r, 8), SMC_R8(r, 16), SMC_R8(r, 24)
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
-          SMC_I8(r, 0),
-      SMC_I8(r, 8), SMC_I8(r, 16), SMC_I8(r, 24), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::SMC_I8(r, 0),
-      SMC_I8(r, 8), "r"(addr)
-      : "memory");
-}
-// Waits for the warp's loads.  The registers of a load count as written only
-// here, so that no use of them moves ahead of the wait.
-#define SMC_T8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
-                     "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24)::"memory");
-}
-__device__ __forceinline__ void tmem_tie(uint32_t *r) {
-  asm volatile("" : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24));
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// kind::f16 with 128 rows, n columns, fp32 accumulators; b_mn: B is stored
-// with its n axis contiguous.
-__host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) |
-         static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
-}
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int d, int token,
-                                            int head, int block, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(token), "r"(head), "r"(block)
-      : "memory");
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int d, int head,
-                                            int row, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(head), "r"(row)
-      : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
-}
-
-// Eight words to a 32-byte boundary, one whole sector a thread.
-__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]),
-               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
 
 template <typename T>
 struct Weights;
@@ -418,11 +44,6 @@ struct Weights<__nv_bfloat16> {
   // weights are 2^(z - m), m at most kLazy below the running maximum
   static constexpr float kOffset = 0.f;
   static constexpr uint32_t kExpMask = 0x7f807f80u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-  }
 };
 template <>
 struct Weights<__half> {
@@ -431,11 +52,6 @@ struct Weights<__half> {
   // they stay below 2^15 and small ones keep 7 more bits
   static constexpr float kOffset = 7.f;
   static constexpr uint32_t kExpMask = 0x7c007c00u;
-  static __device__ __forceinline__ uint32_t pack(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-  }
 };
 // The accumulators are rescaled only when the running maximum (log2) rises
 // by more than this; until then weights may reach 2^kLazy.
@@ -515,153 +131,6 @@ struct AttnTail {
   int joins;              // this CTA stored the last part of the unit
 };
 
-// A CTA's walk over its tiles: one segment (part of a unit) at a time.  All
-// lanes of a warp walk together.
-//   Without a plan, and with no more units than CTAs, the line may be laid out
-// so that a CTA's run never crosses a unit: every unit's tiles are rounded up
-// to a multiple of the run `per`, the least for which the runs suffice.  Each
-// CTA then has one segment, and no unit is cut more often than it must.  It is
-// taken where it lengthens the longest run by at most a tenth and two tiles.
-// Measured, with equal runs and so: 8 sequences of 8 key heads and 11 tiles
-// 26.9 and 18.8 us; 5 of 12 heads, 0 to 13 tiles, 21.9 and 16.3 us; one of 8
-// heads and 2049 tiles 98.6 and 93.5 us.
-struct Walk {
-  int x, x1, per, e;
-  Entry t;
-  int base;       // tiles of the line before entry e
-  int span;       // tiles of the line of each of its units
-  bool aligned;
-  int head, rt;   // unit
-  int i0, n;      // tiles [i0, i0 + n) of the unit
-  int tokens0;    // new token of the unit's first row
-  int rows;       // rows of the unit
-
-  __device__ __forceinline__ int span_of(int tiles) const {
-    return aligned ? (tiles + per - 1) / per * per : tiles;
-  }
-  // units and tiles per unit of sequence e
-  __device__ __forceinline__ int2 sequence_units(const KernelArgs &k, int e, unsigned *bits) {
-    if (e >= k.w.n_entries) return make_int2(0, 0);
-    const SeqInfo si = seq_info(k.a.b, k.a.c.block_size, e);
-    *bits |= si.bits;
-    if (si.n <= 0) return make_int2(0, 0);
-    return make_int2(k.a.c.kv_heads * unit_tiles(k, si.n), (si.len + kTile - 1) / kTile);
-  }
-  __device__ __forceinline__ void start(const KernelArgs &k) {
-    const int lane = threadIdx.x & 31;
-    aligned = false;
-    int total;
-    if (k.planned) {
-      per = __ldcg(&k.w.head->per);
-      total = __ldcg(&k.w.head->total);
-      x = min(static_cast<int>(blockIdx.x) * per, total);
-      x1 = min(x + per, total);
-      if (x >= x1) return;
-      int lo = 0, hi = k.w.n_entries - 1;  // the last entry with tile0 <= x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldcg(&k.w.tile0[mid]) <= x) lo = mid; else hi = mid - 1;
-      }
-      e = lo;
-    } else {
-      // the entries are the sequences: a lane each, 32 at a time
-      unsigned bits = 0;
-      const int entries = k.w.n_entries, ctas = gridDim.x;
-      int2 mine = make_int2(0, 0);
-      int units = 0;
-      total = 0;
-      for (int s0 = 0; s0 < entries; s0 += 32) {
-        mine = sequence_units(k, s0 + lane, &bits);
-        units += mine.x;
-        total += mine.x * mine.y;
-      }
-      units = __reduce_add_sync(0xffffffffu, units);
-      total = __reduce_add_sync(0xffffffffu, total);
-      if (bits && blockIdx.x == 0) raise_status(k.a.status, bits);
-      per = max(1, (total + ctas - 1) / ctas);
-      if (units <= ctas) {
-        for (int run = max(per, 2); 10 * run <= 11 * per + 20; run += 1 + run / 32) {
-          int runs = 0;
-          for (int s0 = 0; s0 < entries; s0 += 32) {
-            if (entries > 32) mine = sequence_units(k, s0 + lane, &bits);
-            runs += mine.x * ((mine.y + run - 1) / run);
-          }
-          runs = __reduce_add_sync(0xffffffffu, runs);
-          if (runs <= ctas) {
-            per = run;
-            total = runs * run;
-            aligned = true;
-            break;
-          }
-        }
-      }
-      x = min(static_cast<int>(blockIdx.x) * per, total);
-      x1 = min(x + per, total);
-      if (x >= x1) return;
-      base = 0;
-      for (int s0 = 0;; s0 += 32) {
-        if (entries > 32) mine = sequence_units(k, s0 + lane, &bits);
-        const int tiles = mine.x * span_of(mine.y);
-        int incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, base + incl > x);
-        if (past) {
-          const int first = __ffs(past) - 1;
-          e = s0 + first;
-          base += __shfl_sync(0xffffffffu, incl - tiles, first);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    load(k);
-  }
-  __device__ __forceinline__ void load(const KernelArgs &k) {
-    if (k.planned) {
-      const int4 *p = reinterpret_cast<const int4 *>(&k.w.entries[e]);
-      const int4 a = __ldcg(p), b = __ldcg(p + 1);
-      t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      base = __ldcg(&k.w.tile0[e]);
-    } else {
-      const SeqInfo si = seq_info(k.a.b, k.a.c.block_size, e);
-      t = {si.row0, si.n, e, 0, si.len, si.len - si.n, (si.len + kTile - 1) / kTile, kSolo};
-    }
-    span = span_of(t.tiles);
-  }
-  __device__ __forceinline__ bool next(const KernelArgs &k) {
-    if (x >= x1) return false;
-    int rts;
-    for (;;) {
-      rts = unit_tiles(k, t.tokens);
-      const int tiles = t.tokens > 0 && t.kv1 > t.kv0 ? rts * k.a.c.kv_heads * span : 0;
-      if (x - base < tiles) break;
-      base += tiles;
-      ++e;
-      load(k);
-    }
-    const int local = x - base, u = local / span;
-    i0 = local - u * span;
-    n = min(t.tiles - i0, x1 - x);
-    head = u / rts;
-    rt = u - head * rts;
-    tokens0 = rt * 2 * k.tile_tokens;
-    rows = min(t.tokens - tokens0, 2 * k.tile_tokens) * k.rep;
-    // the unit's place on the line, in CTAs
-    const int unit0 = x - i0;
-    owner = unit0 / per;
-    more = (unit0 + span - 1) / per - owner;
-    first_cut = i0 > 0 && i0 <= per;
-    x = aligned ? x1 : x + n;
-    return true;
-  }
-  int owner, more;  // the CTA of the unit's first tiles; the CTAs after it
-  bool first_cut;   // this segment begins at the first cut of its unit
-};
-
 // A ring's slots, tile by tile.  Either half of the slots (the even and the odd
 // ones) is used in turn; `pos` and `parity` are the half's next slot and the
 // parity of that slot's barriers.
@@ -690,70 +159,6 @@ struct Ring {
   }
 };
 
-// Waits.  Every one is bounded, and gives up for the whole CTA: the one that
-// ran out raises the status bit and the abort flag, at which the others end.
-// What is done when a barrier has already completed is kept to a few
-// instructions: each role's code runs once a tile, after other roles' code has
-// displaced it from the instruction cache, and is paid for by its length.
-__device__ __noinline__ bool wait_slowly(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (s->abort) return false;
-  }
-  s->abort = 1;
-  raise_status(status, SMC_DEV_TIMEOUT);
-  return false;
-}
-__device__ __forceinline__ bool guarded_wait(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-  return mbar_try_wait(bar, parity) || wait_slowly(s, bar, parity, status);
-}
-// The same for a whole warp, in step: every lane polls and takes the same
-// branch, so that the warp is converged for the .aligned instructions that
-// follow.
-__device__ __noinline__ bool warp_wait_slowly(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, s->abort)) return false;
-  }
-  s->abort = 1;
-  raise_status(status, SMC_DEV_TIMEOUT);
-  return false;
-}
-__device__ __forceinline__ bool warp_wait(AttnTail *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_slowly(s, bar, parity, status);
-}
-// One arrival for a warp (lane 0's), by predicate and not by a branch, for
-// the same reason.  What the other lanes did before is ordered by __syncwarp.
-__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
-  __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
-      "r"(lane)
-      : "memory");
-}
-
-// Bits of a row's view of new tokens j0 .. j0 + 31: 1 for committed tokens
-// (j < 0), the mask's bit or the chain's for new ones, 0 past them.
-__device__ __forceinline__ uint32_t view_bits(const uint32_t *mask, int words, int i, int n_new,
-                                              int j0) {
-  if (j0 + 32 <= 0) return 0xffffffffu;
-  if (j0 >= n_new) return 0u;
-  uint32_t bits;
-  if (mask) {
-    const int w = j0 >> 5;
-    const uint32_t lo = w < 0 ? 0xffffffffu : (w < words ? __ldg(mask + w) : 0u);
-    const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < words ? __ldg(mask + w + 1) : 0u);
-    bits = __funnelshift_r(lo, hi, j0 & 31);
-  } else {
-    const int c = i - j0 + 1;  // new tokens 0..i
-    bits = c <= 0 ? 0u : (c >= 32 ? 0xffffffffu : (1u << c) - 1u);
-  }
-  const int left = n_new - j0;
-  if (left < 32) bits &= (1u << left) - 1u;
-  return bits;
-}
-
 // A new token that holds an infinity or NaN had it zeroed in the products, as
 // rows that do not see the token must not meet it.  Rows that see it get it
 // here: columns [c0, c1) of the row's result whose visible new tokens in
@@ -777,90 +182,6 @@ __device__ __noinline__ void patch_nonfinite(const KernelArgs &k, int seq, int c
     }
     if (sum != 0.f) o[d] = from_f32<Out>(sum);
   }
-}
-
-// ---------------------------------------------------------------------------
-// Joining a row's parts: each part p has a log-sum-exp L_p (log2) and a
-// normalised result o_p;
-//   out = sum 2^(L_p - M) o_p / sum 2^(L_p - M),  M = max L_p.
-// A warp joins a row, with as many parts' loads under way as it can.
-// ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
-
-struct Joined {
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void raise(float to) {
-    const float f = top == -INFINITY ? 0.f : fast_exp2(top - to);
-    sum *= f;
-    acc.x *= f;
-    acc.y *= f;
-    acc.z *= f;
-    acc.w *= f;
-    top = to;
-  }
-  __device__ __forceinline__ void add(float lse, float4 x) {  // lse <= top
-    const float f = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
-    sum += f;
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
-  }
-  __device__ __forceinline__ float lse2() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
-  __device__ __forceinline__ float4 result() const {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  }
-};
-
-__device__ __forceinline__ float4 load_part(const float *o, bool live) {
-  return live ? __ldcg(reinterpret_cast<const float4 *>(o) + (threadIdx.x & 31))
-              : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
-template <typename T>
-__device__ __forceinline__ void write_row(const KernelArgs &k, int64_t rh, int row, int qh, const Joined &j) {
-  const int lane = threadIdx.x & 31;
-  const float4 x = j.result();
-  if (4 * lane < k.a.c.head_dim) {
-    T *dst = reinterpret_cast<T *>(k.a.out) + row * k.a.o_row + qh * k.a.o_head + 4 * lane;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(Weights<T>::pack(x.x, x.y), Weights<T>::pack(x.z, x.w));
-  }
-  if (k.a.lse && lane == 0) k.a.lse[rh] = j.lse2() * 0.69314718055994531f;
-}
-
-// A row of a cut unit: its owner's part, and a continuation each of CTAs
-// cta + 1 .. cta + more at row `slot` of their slots.
-__device__ __forceinline__ Joined join_parts(const KernelArgs &k, int kind, int64_t rh, int cta, int more,
-                                             int slot) {
-  const int D = k.a.c.head_dim;
-  const bool live = 4 * static_cast<int>(threadIdx.x & 31) < D;
-  Joined j;
-  float l = __ldcg(&k.w.lse[kind][rh]);
-  float4 x = load_part(k.w.o[kind] + rh * D, live);
-  const int64_t slot0 = static_cast<int64_t>(cta + 1) * kUnitRows + slot;
-  constexpr int kBatch = 8;
-  for (int p = 0; p < more; p += kBatch) {
-    float ls[kBatch];
-    float4 xs[kBatch];
-    float top = fmaxf(j.top, l);
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int64_t at = slot0 + static_cast<int64_t>(p + e) * kUnitRows;
-      const bool in = p + e < more;
-      ls[e] = in ? __ldcg(&k.w.lse_c[at]) : -INFINITY;
-      xs[e] = load_part(k.w.o_c + at * D, live && in);
-    }
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) top = fmaxf(top, ls[e]);
-    j.raise(top);
-    j.add(l, x);
-    l = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) j.add(ls[e], xs[e]);
-  }
-  return j;
 }
 
 // Segment number `seg` (from 0) of a group as warp 10 left it.  False when the wait gave
@@ -888,7 +209,7 @@ __device__ __forceinline__ bool copy_tiles(const KernelArgs &k, const CUtensorMa
   const bool two = seg->flags & kTwo;
   // (block, token in it) of token t of a segment's sequence
   auto place = [&](const Seg *of, uint32_t t) {
-    const uint32_t b = bs == 1 ? t : __umulhi(t, k.magic) >> k.shift;
+    const uint32_t b = block_of(k, t);
     int id = k.a.b.tables[static_cast<int64_t>(of->seq) * k.a.b.T + b];
     if (id < 0 || id >= c.blocks) {
       *bits |= SMC_DEV_BAD_BLOCK;
@@ -1172,7 +493,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
             a = fast_exp2(a);
             b = fast_exp2(b);
             sum2[c & 1] = add2(sum2[c & 1], f2pack(a, b));
-            p[c] = Wt::pack(a, b);
+            p[c] = pack2<T>(a, b);
           }
           __syncwarp();
           tmem_st16(t_s + 64 + 32 * buf + 16, p + 16);
@@ -1300,7 +621,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
                   uint32_t *words = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
-                    words[j] = Wt::pack(__uint_as_float(x[e + 2 * j]), __uint_as_float(x[e + 2 * j + 1]));
+                    words[j] = pack2<T>(__uint_as_float(x[e + 2 * j]), __uint_as_float(x[e + 2 * j + 1]));
                   }
                   *reinterpret_cast<uint4 *>(out + c + e) = v;
                 }
@@ -1346,7 +667,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
           for (int slot = warp; slot < w.rows; slot += 8) {
             const int tok_in = slot / k.rep, head = w.head * k.rep + slot - tok_in * k.rep;
             const int64_t to = static_cast<int64_t>(w.row0 + tok_in) * k.a.q_heads + head;
-            write_row<T>(k, to, w.row0 + tok_in, head, join_parts(k, 0, to, owner, more, slot));
+            write_row<T>(k, to, w.row0 + tok_in, head, join_parts<Units>(k, 0, to, owner, more, slot));
           }
         }
         __syncwarp();
@@ -1463,7 +784,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     __syncwarp();
   } else if (warp == 10) {
     // ---- segments, K ------------------------------------------------------------
-    Walk w;
+    Walk<Units> w;
     w.start(k);
     Ring<G::kSlotsK> ring;
     unsigned bits = 0;
@@ -1577,96 +898,9 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   }
 }
 
-// The units that a CTA's range cuts: CTA (c, chunk) takes eight rows of the
-// unit that the boundary between CTAs c and c + 1 is the first to cut (CTA
-// c + 1 left its record): its owner's part and a continuation each of CTAs
-// c + 1 .. c + more.  Rows that have another unit too get their joined part
-// back for join_shared_kernel.
-template <typename T>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-join_cut_units_kernel(const __grid_constant__ KernelArgs k) {
-  // the last kernel of a call lets nothing start before it has ended
-  if (k.w.groups) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  wait_for_stream();
-  const int cta = blockIdx.x, lane = threadIdx.x & 31;
-  const int4 *cut = reinterpret_cast<const int4 *>(&k.w.cuts[cta + 1]);
-  const int4 c = __ldcg(cut);  // row0, rows, head, more
-  const int flags = __ldcg(cut + 1).x;
-  const int slot = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (slot >= c.y) return;
-  const int D = k.a.c.head_dim, i = slot / k.rep, row = c.x + i, qh = c.z * k.rep + slot - i * k.rep;
-  const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
-  const bool live = 4 * lane < D;
-  const int kind = flags & kShared;
-  const Joined j = join_parts(k, kind, rh, cta, c.w, slot);
-  if (flags & kSolo) {
-    write_row<T>(k, rh, row, qh, j);
-  } else {
-    const float4 y = j.result();
-    if (live) reinterpret_cast<float4 *>(k.w.o[kind] + rh * D)[lane] = y;
-    if (lane == 0) k.w.lse[kind][rh] = j.lse2();
-  }
-}
-
-// The rows of prompts with a shared part: its result and the own part's.  A
-// CTA per row, four heads a warp at a time.
-constexpr int kJoinHeads = 4;
-template <typename T>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-join_shared_kernel(const __grid_constant__ KernelArgs k) {
-  const BatchArgs &b = k.a.b;
-  const int row = blockIdx.x;
-  wait_for_stream();
-  int seq = min(row / b.max_new, b.S - 1);  // right when every sequence has max_new rows
-  if (b.row_start && !(b.row_start[seq] <= row && row < b.row_start[seq + 1])) seq = seq_of_row(b, row);
-  // without a shared part the row is written already; its rows are in order with one
-  if (seq < 0 || __ldcg(&k.w.common[seq / b.group]) == 0) return;
-  const int D = k.a.c.head_dim, lane = threadIdx.x & 31;
-  const bool live = 4 * lane < D;
-  for (int q0 = (threadIdx.x >> 5) * kJoinHeads; q0 < k.a.q_heads; q0 += kJoinWarps * kJoinHeads) {
-    float l[kJoinHeads][2];
-    float4 x[kJoinHeads][2];
-#pragma unroll
-    for (int e = 0; e < kJoinHeads; ++e) {
-      const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + q0 + e;
-      const bool in = q0 + e < k.a.q_heads;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        l[e][p] = in ? __ldcg(&k.w.lse[p][rh]) : -INFINITY;
-        x[e][p] = load_part(k.w.o[p] + rh * D, live && in);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kJoinHeads; ++e) {
-      if (q0 + e >= k.a.q_heads) break;
-      Joined j;
-      j.top = fmaxf(l[e][0], l[e][1]);
-      j.add(l[e][0], x[e][0]);
-      j.add(l[e][1], x[e][1]);
-      write_row<T>(k, static_cast<int64_t>(row) * k.a.q_heads + q0 + e, row, q0 + e, j);
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Launch.
 // ---------------------------------------------------------------------------
-using EncodeFn = decltype(&cuTensorMapEncodeTiled);
-
-static EncodeFn encode_fn() {
-  static EncodeFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess) {
-      p = nullptr;
-    }
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
 // [rows][q_heads][head_dim] in boxes of 64 elements x the heads of a key head x
 // a row tile's tokens; rows past the last read as 0.
 static bool make_q_map(CUtensorMap *map, const KernelArgs &k) {
@@ -1761,18 +995,12 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   // 2690 272 and 437 us.
   const double table_bytes = static_cast<double>(a.b.S) * a.b.T * a.c.block_size * a.c.kv_heads * a.c.head_dim * 4;
   if (table_bytes < 96e6) k.a.b.group = 1;
-  carve(a.c, k.a.b, a.q_heads, static_cast<char *>(workspace), &k.w);
+  carve(a.c, k.a.b, a.q_heads, kMaxCtas, kUnitRows, static_cast<char *>(workspace), &k.w);
   k.rep = a.q_heads / a.c.kv_heads;
   k.tile_tokens = kRows / k.rep;
   k.q_box = a.b.rows < k.tile_tokens ? a.b.rows : k.tile_tokens;
   k.sc = a.scale * 1.4426950408889634f;
-  // with 2^s the power of two at or above the block size, 2^(31 + s) / size
-  // rounded up divides every t < 2^31 exactly
-  const uint64_t bs = a.c.block_size;
-  uint32_t log2 = 0;
-  while ((1ull << log2) < bs) ++log2;
-  k.magic = static_cast<uint32_t>(((1ull << (31 + log2)) + bs - 1) / bs);
-  k.shift = log2 ? log2 - 1 : 0;
+  divide_by(a.c.block_size, &k);
   // a box is a run of tokens inside one block and one tile; the swizzle
   // repeats every eight rows, so a box starts on a multiple of eight.  Blocks
   // of other sizes are copied by the lanes, 16 bytes each: 34 trees of 64 rows,
@@ -1806,7 +1034,7 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   if (k.planned) {
     int n = ctas;
     void *pargs[] = {&k, &n};
-    e = launch_early(reinterpret_cast<const void *>(plan_kernel), dim3(k.w.groups ? k.w.groups : 1), kPlanThreads,
+    e = launch_early(reinterpret_cast<const void *>(plan_kernel<Units>), dim3(k.w.groups ? k.w.groups : 1), kPlanThreads,
                      0, pargs, st);
     if (e != cudaSuccess) return e;
   }
@@ -1817,8 +1045,8 @@ cudaError_t launch_tree_attention(const AttnArgs &a, void *workspace, cudaStream
   if (e != cudaSuccess) return e;
   void *jargs[] = {&k};
   if (ctas > 1 && !k.join_inside) {  // with one CTA nothing is cut
-    e = launch_early(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16>)
-                        : reinterpret_cast<const void *>(join_cut_units_kernel<__half>),
+    e = launch_early(bf16 ? reinterpret_cast<const void *>(join_cut_units_kernel<__nv_bfloat16, Units>)
+                        : reinterpret_cast<const void *>(join_cut_units_kernel<__half, Units>),
                    dim3(ctas - 1, (unit_rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, jargs, st);
     if (e != cudaSuccess) return e;
   }

@@ -12,14 +12,18 @@ constexpr uint32_t kWaitPolls = 1u << 17;  // each may suspend up to 20 us
 // ---------------------------------------------------------------------------
 // Tensor-core and tensor-memory primitives (PTX for sm_103a).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc_512(uint32_t *dst) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                   smem_addr(dst))
+template <int kColumns>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst)),
+               "n"(kColumns)
                : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_free_512(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+template <int kColumns>
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kColumns)
+               : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -53,6 +57,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
+// D[tmem] (+)= A[smem] * B[smem] of 8-bit numbers; `b_high`, the high word of B's descriptor.
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_high), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -83,6 +97,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
       : SMC_R8(r, 0), SMC_R8(r, 8), SMC_R8(r, 16), SMC_R8(r, 24)
       : "r"(addr));
 }
+// 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SMC_R8(r, 0), SMC_R8(r, 8)
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -107,6 +129,12 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t *r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24)::"memory");
 }
+__device__ __forceinline__ void tmem_wait_all() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_tie16(uint32_t *r) {
+  asm volatile("" : SMC_T8(r, 0), SMC_T8(r, 8));
+}
 __device__ __forceinline__ void tmem_tie(uint32_t *r) {
   asm volatile("" : SMC_T8(r, 0), SMC_T8(r, 8), SMC_T8(r, 16), SMC_T8(r, 24));
 }
@@ -117,6 +145,12 @@ __device__ __forceinline__ void tmem_wait_st() {
 // with its n axis contiguous.
 __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
+}
+// kind::f8f6f4 with 128 rows, n columns, fp32 accumulators; A in e4m3, B in e4m3
+// or e5m2; *_mn: the operand is stored with its m or n axis contiguous.
+__host__ __device__ constexpr uint32_t instr_desc8(int n, bool a_mn, bool b_mn, bool b_e5m2) {
+  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int d, int token,

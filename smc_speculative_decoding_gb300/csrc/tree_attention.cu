@@ -358,7 +358,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
     s->abort = (smem_addr(smem) & 1023u) != 0;  // the swizzle counts from 1 KB boundaries
     mbar_init_fence();
   }
-  if (warp == 8) tmem_alloc_512(&s->tmem);
+  if (warp == 8) tmem_alloc<512>(&s->tmem);
   if (warp == 9 && elect_one()) {
     prefetch_map(&map_q);
     if (kTma) {
@@ -894,7 +894,7 @@ attention_kernel(const __grid_constant__ KernelArgs k, const __grid_constant__ C
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
-    tmem_free_512(tmem);
+    tmem_free<512>(tmem);
   }
 }
 

@@ -1,100 +1,973 @@
 // Attention of each sequence's new tokens over its paged 8-bit cache, under a
-// tree mask (smc_tree_attention8 in smcsd.h).
-#include "cache_common.cuh"
+// tree mask (smc_tree_attention8 in smcsd.h).  The calls' work and the joins of
+// parts are those of attention_work.cuh; the kernel here is its own.
+//
+// Mathematics.  The cache's bytes go to the tensor cores as they are, by TMA and
+// with no conversion on the way, so that a tile costs the CUDA cores nothing but
+// its softmax.  The other operands are cut into 8-bit pieces whose products add
+// up in the fp32 accumulators:
+//  - a row of q, under one power of two, into e4m3 pieces q1 = e4m3(q), q2 =
+//    e4m3(q - q1), for fp16 a third: each takes four significant bits and a sign,
+//    so two hold bf16's eight and three fp16's eleven (down to 2^-10 beside a
+//    largest element of 224 to 448);
+//  - a weight w <= 2^15, as fp16, into three e5m2 pieces: three significant bits
+//    and a sign each, 2^-11 of w left over, and half of 2^-16 where w is small.
+//    (e4m3 has two bits more in two pieces, but ends at 2^-9: beside a weight of
+//    2^8, tokens of 2^-18 and less of the largest weight would be lost, and a
+//    long context has many.)
+// The scales of k go to the scores.  Those of v go into the weights' exponents,
+//   w_j = 2^(z_j + log2 s_v(j) - M + 11),  out = sum w_j v8_j / sum w_j / s_v(j),
+// with M a running maximum of z + log2 s_v, so that weights stay in range
+// whatever the scales.
+//   The products are the transposed ones, S^T = K Q^T and O^T = V^T P^T: a tile's
+// 128 tokens, and the head's dims, are the 128 rows that a tensor-core tile has,
+// and the rows of q its columns, of which there are as few as there are.  A
+// softmax thread holds one token's scores: a token's two scales are two registers,
+// and every thread has work whatever the number of rows.  What must agree
+// between tokens, the maximum, is only looked at for a rise (a vote a tile).
+#include <atomic>
+
+#include "attention_work.cuh"
+#include "tensor_core.cuh"
 
 namespace smcsd {
 
-size_t attention8_workspace_bytes(const CacheArgs &, const BatchArgs &, int) { return kCacheStatusBytes; }
+constexpr int kTile8 = 128;    // tokens per tile
+constexpr int kMaxCtas8 = 384; // slots for continuations
+constexpr int kCtasPerSm = 2;
+constexpr int kThreads8 = 256;
+constexpr int kSegs8 = 4;      // segments found ahead
+constexpr int kTileBytes8 = kTile8 * 128;
 
-constexpr int kThreads8 = 128;
-constexpr int kWarps8 = kThreads8 / 32;
-
-// A CTA takes one row of one query head; its warps every fourth token, each
-// with a running maximum, sum and accumulator, joined at the end.
 template <typename T>
-__global__ void __launch_bounds__(kThreads8)
-attention8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ ScaleArgs sc) {
-  __shared__ float s_m[kWarps8], s_l[kWarps8], s_o[kWarps8][128];
-  const int row = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int D = a.c.head_dim, bs = a.c.block_size, h = qh / (a.q_heads / a.c.kv_heads);
-  wait_for_stream();
-  const int s = seq_of_row(a.b, row);
-  if (s < 0 || s >= a.b.S) return;
-  const SeqInfo si = seq_info(a.b, bs, s);
-  const int i = row - si.row0;
-  if (i < 0 || i >= si.n) {
-    if (si.bits && threadIdx.x == 0) raise_status(a.status, si.bits);
-    return;
+struct Rows8;  // most rows of a unit, pieces of q
+template <>
+struct Rows8<__nv_bfloat16> { static constexpr int kRows = 64, kPieces = 2; };
+template <>
+struct Rows8<__half> { static constexpr int kRows = 48, kPieces = 3; };
+
+template <typename T>
+struct Units8 {
+  static constexpr int kTile = kTile8, kRowTiles = 1, kUnitRows = Rows8<T>::kRows;
+  static constexpr bool kParts = true;
+};
+
+size_t attention8_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads) {
+  return carve(c, b, q_heads, kMaxCtas8, 64, nullptr, nullptr);
+}
+
+struct Kernel8Args : WorkArgs {
+  ScaleArgs sc8;
+};
+
+constexpr float kTop = 15.f;      // weights are at most 2^kTop ...
+constexpr float kTopFresh = 11.f; // ... and the largest one 2^kTopFresh when the maximum is taken
+constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
+constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
+
+// ---------------------------------------------------------------------------
+// attention8_kernel.  Two CTAs to a multiprocessor, each: warps 0-3 the softmax
+// (thread = token of a tile), warp 4 issues the matrix products, warp 5 finds
+// the CTA's segments (parts of units) and copies K and V, warps 6 and 7 cut the
+// next segment's rows of q into pieces.  Shared memory: two slots each of K and
+// V tiles, q's pieces, the weights' pieces.  Tensor memory: two tiles' scores
+// and the accumulator, 64 columns each.
+//   The scores of a tile are computed beside the softmax of the one before; one
+// CTA's waits are covered by the other's work.
+//   Every wait is bounded, and on a barrier all of whose turns the waiting
+// thread follows.
+// ---------------------------------------------------------------------------
+struct alignas(16) Seg8 {  // read and written in 16-byte words
+  int row0, rows;  // first row of the unit, rows of it
+  int i0;          // new token of the first row (own parts)
+  int seq, head;   // head unit
+  int t0, n;       // first token, tiles
+  int ctx, kv1;    // tokens before ctx are seen by all; end of the entry's tokens
+  int n_new;       // new tokens of the sequence (own parts)
+  int flags;
+  int join;        // of a cut unit: the owner CTA, and continuations << 16
+};
+constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final result, first tiles, none left
+
+struct Tail8 {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2];
+  uint64_t p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
+  uint64_t seg_full[kSegs8], seg_empty[kSegs8], group;
+  Seg8 seg[kSegs8];
+  float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
+  float q_scale[64];  // of the next segment's rows
+  int top[32];        // maxima of a tile, then factors
+  int rise[2];        // the last vote (from 1) in which a maximum rose
+  unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
+  uint32_t tmem;
+  volatile int abort;
+  int joins;          // this CTA stored the last part of the unit
+};
+
+static_assert(sizeof(Seg8) == 48 && offsetof(Tail8, seg) % 16 == 0 && offsetof(Tail8, col) % 16 == 0, "16-byte words");
+
+template <typename T>
+struct Smem8 {
+  static constexpr int kRows = Rows8<T>::kRows;
+  static constexpr int kPiece = kRows * 128;  // bytes of one piece of q, or of a tile's weights
+  static constexpr int kK = 0, kV = 2 * kTileBytes8, kQ = 4 * kTileBytes8;
+  static constexpr int kP = kQ + Rows8<T>::kPieces * kPiece;
+  static constexpr int kTail = kP + 3 * kPiece;
+  static constexpr int kBytes = kTail + static_cast<int>(sizeof(Tail8));
+};
+// an SM's 228 KB less 1 KB of the system's for each CTA
+static_assert(Smem8<__nv_bfloat16>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "shared memory");
+static_assert(Smem8<__half>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "shared memory");
+static_assert(Smem8<__half>::kPiece % 1024 == 0, "the swizzle counts from 1 KB boundaries");
+
+// Waits, bounded as those of tensor_core.cuh, but without a call: the registers
+// of the warps that take more than the launch gave them (setmaxnreg) cannot be
+// saved around one.
+__device__ __forceinline__ void give_up(Tail8 *s, unsigned *status) {
+  s->abort = 1;
+  raise_status(status, SMC_DEV_TIMEOUT);
+}
+__device__ __forceinline__ bool wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (s->abort) return false;
   }
-  const T *q = reinterpret_cast<const T *>(a.q) + row * a.q_row + qh * a.q_head;
-  float x[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = 4 * lane + e < D ? to_f32(q[4 * lane + e]) : 0.f;
-  const int32_t *table = a.b.tables + static_cast<int64_t>(s) * a.b.T;
-  const uint32_t *mask = a.mask ? a.mask + static_cast<int64_t>(row) * a.mask_words : nullptr;
-  for (int t = warp; t < si.len; t += kWarps8) {
-    const int j = t - (si.len - si.n);
-    if (j >= 0 && (mask ? j / 32 >= a.mask_words || !(mask[j / 32] >> (j % 32) & 1u) : j > i)) continue;
-    const int block = table[t / bs];
-    if (block < 0 || block >= a.c.blocks) {
-      if (lane == 0) raise_status(a.status, SMC_DEV_BAD_BLOCK);
-      continue;
+  give_up(s, status);
+  return false;
+}
+// A whole warp, in step.
+__device__ __forceinline__ bool warp_wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, s->abort)) return false;
+  }
+  give_up(s, status);
+  return false;
+}
+
+__device__ __forceinline__ bool take_segment8(Tail8 *s, uint32_t seg, Seg8 *to, unsigned *status) {
+  if (!warp_wait8(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) return false;
+  const int4 *from = reinterpret_cast<const int4 *>(&s->seg[seg % kSegs8]);
+  const int4 a = from[0], b = from[1], c = from[2];
+  *to = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  return !(to->flags & kEnd8);
+}
+
+// The order of floats in that of ints (and back: its own inverse).
+__device__ __forceinline__ int ordered(int bits) { return bits ^ (bits >> 31 & 0x7fffffff); }
+
+// Which rows of a unit see token `at` (at or past w.ctx): bits [i * heads, (i + 1)
+// * heads) for new token w.i0 + i.
+__device__ __forceinline__ uint64_t rows_that_see(const WorkArgs &k, const Seg8 &w, int heads, int at) {
+  if (at < w.ctx) return ~0ull;
+  if (at >= w.kv1) return 0;
+  const int j = at - w.ctx, tokens = w.rows / heads, word = j >> 5;
+  const uint64_t one = heads >= 64 ? ~0ull : (1ull << heads) - 1;
+  uint64_t see = 0;
+  if (!k.a.mask) {  // a chain: new tokens j and later
+    for (int i = max(j - w.i0, 0); i < tokens; ++i) see |= one << (i * heads);
+    return see;
+  }
+  if (word >= k.a.mask_words) return 0;
+  const uint32_t *mask = k.a.mask + static_cast<int64_t>(w.row0) * k.a.mask_words + word;
+#pragma unroll 4
+  for (int i = 0; i < tokens; ++i) {
+    if (__ldg(mask + static_cast<int64_t>(i) * k.a.mask_words) >> (j & 31) & 1u) see |= one << (i * heads);
+  }
+  return see;
+}
+
+// Rows that see a new token whose element d of v is NaN get NaN there: the
+// products met it as 0.
+template <typename Out>
+__device__ __forceinline__ void patch_nan8(const WorkArgs &k, const Seg8 &w, const UnitHeads &heads, int d, char *const *to) {
+  const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
+  const int t1 = min(w.t0 + w.n * kTile8, w.kv1);
+  for (int at = max(w.t0, w.ctx); at < t1; ++at) {
+    const int block = table[block_of(k, at)];
+    if (block < 0 || block >= k.a.c.blocks) continue;
+    const char *v = k.a.c.v + block * k.a.c.block_stride + (at % k.a.c.block_size) * k.a.c.token_stride +
+                    heads.key * k.a.c.head_stride;
+    if ((v[d] & 0x7f) != 0x7f) continue;
+    const uint64_t see = rows_that_see(k, w, heads.n, at);
+    for (int r = 0; r < w.rows; ++r) {
+      if (see >> r & 1) reinterpret_cast<Out *>(to[r])[d] = from_f32<Out>(__uint_as_float(0x7fffffffu));
     }
-    const int64_t at = block * a.c.block_stride + (t % bs) * a.c.token_stride + h * a.c.head_stride + 4 * lane;
-    float k[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (4 * lane < D) {
-      const uint32_t kb = *reinterpret_cast<const uint32_t *>(a.c.k + at), vb = *reinterpret_cast<const uint32_t *>(a.c.v + at);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const uint32_t kh = from_e4m3x2(kb >> (8 * e)), vh = from_e4m3x2(vb >> (8 * e));
-        const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&kh));
-        const float2 vf = __half22float2(*reinterpret_cast<const __half2 *>(&vh));
-        k[e] = kf.x; k[e + 1] = kf.y;
-        v[e] = vf.x; v[e + 1] = vf.y;
-      }
-    }
-    const float ks = scale_of(sc.k[block * sc.block + h * sc.head]), vs = scale_of(sc.v[block * sc.block + h * sc.head]);
-    float z = x[0] * k[0] + x[1] * k[1] + x[2] * k[2] + x[3] * k[3];
-#pragma unroll
-    for (int step = 16; step > 0; step >>= 1) z += __shfl_xor_sync(0xffffffffu, z, step);
-    z *= a.scale * ks;
-    const float top = fmaxf(m, z), f = m == -INFINITY ? 0.f : expf(m - top), w = expf(z - top);
-    m = top;
-    l = l * f + w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = o[e] * f + w * vs * v[e];
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) s_o[warp][4 * lane + e] = o[e];
-  __syncthreads();
-  float top = s_m[0], sum = 0.f, r = 0.f;
-  for (int w = 1; w < kWarps8; ++w) top = fmaxf(top, s_m[w]);
-  const int d = threadIdx.x;
-  for (int w = 0; w < kWarps8; ++w) {
-    if (s_m[w] == -INFINITY && s_l[w] == 0.f) continue;
-    const float f = expf(s_m[w] - top);
-    sum += f * s_l[w];
-    r += f * s_o[w][d];
-  }
-  if (d < D) {
-    reinterpret_cast<T *>(a.out)[row * a.o_row + qh * a.o_head + d] = from_f32<T>(sum == 0.f ? 0.f : r / sum);
-  }
-  if (a.lse && d == 0) {
-    a.lse[static_cast<int64_t>(row) * a.q_heads + qh] = sum == 0.f ? -INFINITY : top + logf(sum);
   }
 }
 
-cudaError_t launch_tree_attention8(const AttnArgs &a, const ScaleArgs &s, int dtype, void *, cudaStream_t st) {
+// Sums v[0..31] over the warp's lanes; lane l gets that of v[l].
+__device__ __forceinline__ float transposed_sum(float *v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int j = 0; j < s; ++j) {
+      const float send = up ? v[j] : v[j + s], keep = up ? v[j + s] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+    }
+  }
+  return v[0];
+}
+
+template <typename T, bool kTma>
+__global__ void __launch_bounds__(kThreads8, kCtasPerSm)
+attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  using M = Smem8<T>;
+  constexpr int kRows = Rows8<T>::kRows, kPieces = Rows8<T>::kPieces, kHalves = (kRows + 31) / 32;
+  extern __shared__ __align__(1024) char smem[];
+  Tail8 *const s = reinterpret_cast<Tail8 *>(smem + M::kTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const CacheArgs &c8 = k.a.c;
+  const int D = c8.head_dim;
+  unsigned *const status = k.a.status;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s->k_full[i], 1);
+      mbar_init(&s->k_empty[i], 1);
+      mbar_init(&s->v_full[i], 1);
+      mbar_init(&s->v_empty[i], 1);
+      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->s_free[i], 4);
+      s->rise[i] = 0;
+    }
+    mbar_init(&s->p_full, 4);
+    mbar_init(&s->pv_done, 1);
+    mbar_init(&s->q_full, 2);
+    mbar_init(&s->q_free, 1);
+    mbar_init(&s->q_taken, 4);
+    mbar_init(&s->o_full, 1);
+    mbar_init(&s->o_free, 4);
+    mbar_init(&s->drained, 1);
+    mbar_init(&s->group, 4);
+    for (int i = 0; i < kSegs8; ++i) {
+      mbar_init(&s->seg_full[i], 1);
+      mbar_init(&s->seg_empty[i], 7);  // every warp but the one that fills it
+    }
+    s->nonfinite = 0;
+    s->abort = (smem_addr(smem) & 1023u) != 0;
+    mbar_init_fence();
+  }
+  if (warp == 4) tmem_alloc<256>(&s->tmem);
+  if (kTma && warp == 5 && elect_one()) {
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+  wait_for_stream();
+  if (k.more_kernels) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (s->abort) {
+    if (tid == 0) raise_status(status, SMC_DEV_TIMEOUT);
+  } else if (warp < 4) {
+    // ---- softmax --------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t t_s = tmem + lanes, t_o = tmem + lanes + 128;
+    char *const p_at = smem + M::kP + (tid >> 3) * 128 + (tid & 7) * 16;
+    char *const v_tile = smem + M::kV;
+    uint32_t seg = 0, tile = 0, syncs = 0, votes = 0;
+    bool ok = true;
+    auto group_sync = [&] {
+      warp_arrive(&s->group, lane);
+      return warp_wait8(s, &s->group, syncs++ & 1u, status);
+    };
+    Seg8 w;
+    while (ok && take_segment8(s, seg, &w, status)) {
+      warp_arrive(&s->seg_empty[seg % kSegs8], lane);
+      const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
+      const int chunks = (w.rows + 15) >> 4;
+      const bool own = !(w.flags & kShared);
+      const int t_end = min(w.t0 + w.n * kTile8, w.kv1);
+      const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
+      // scales: of the tile at hand, of the next one the block
+      auto block_at = [&](int t) {
+        int id = t < t_end ? table[block_of(k, t)] : -1;
+        return id < 0 || id >= c8.blocks ? 0 : id;
+      };
+      const float *ks_of = k.sc8.k + heads.key * k.sc8.head, *vs_of = k.sc8.v + heads.key * k.sc8.head;
+      int at = w.t0 + tid;
+      int64_t next = block_at(at) * k.sc8.block;
+      float ks = ks_of[next], vs = vs_of[next];
+      next = block_at(at + kTile8) * k.sc8.block;
+      // the rows' scales and maxima
+      if (!(ok = warp_wait8(s, &s->q_full, seg & 1u, status))) break;
+      if (tid < 32) {
+        const float unset[2] = {2 * tid < w.rows ? kUnset : -INFINITY, 2 * tid + 1 < w.rows ? kUnset : -INFINITY};
+        s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
+      }
+      ++seg;
+      if (!(ok = group_sync())) break;
+      warp_arrive(&s->q_taken, lane);
+      unsigned long long l2[16 * kHalves];  // sums of w / s_v, this thread's tokens
+#pragma unroll
+      for (int i = 0; i < 16 * kHalves; ++i) l2[i] = 0;
+
+      for (int i = 0; i < w.n; ++i, ++tile, at += kTile8) {
+        const uint32_t buf = tile & 1u, t_sb = t_s + buf * 64;
+        const float sk = scale_of(ks), sv = scale_of(vs);
+        const unsigned long long a2 = f2dup(k.sc * sk);
+        const float b = log2f(sv), c = kSumScale / sv;
+        if (i + 1 < w.n) {
+          ks = ks_of[next];
+          vs = vs_of[next];
+          next = block_at(at + 2 * kTile8) * k.sc8.block;
+        }
+        const int t0 = w.t0 + i * kTile8;
+        const bool edge = own && t0 + kTile8 > w.ctx;
+        const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : 0;
+        if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
+        tc_fence_after();
+        const unsigned long long b2 = f2dup(b), c2 = f2dup(c);
+        // 32 rows at a time
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          if (half && w.rows <= 32) break;
+          constexpr int kMost = kRows < 32 ? kRows : 32;
+          const int some = min(chunks - 2 * half, 2);  // chunks of 16
+          uint32_t z[kMost];
+          float hi;
+          // the rows' z + log2 s_v, less (with `past`) M and plus kTopFresh
+          auto scores = [&](bool past) {
+            __syncwarp();
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb) {
+              if (cb < some) tmem_ld16(t_sb + half * 32 + cb * 16, z + cb * 16);
+            }
+            tmem_wait_all();
+            hi = -INFINITY;
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb) {
+              if (cb >= some) break;
+              tmem_tie16(z + cb * 16);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const int at_z = cb * 16 + e, r = half * 32 + at_z;
+                const float4 col = s->col[r / 2];
+                unsigned long long y = fma2(f2pack(__uint_as_float(z[at_z]), __uint_as_float(z[at_z + 1])),
+                                            mul2(a2, f2pack(col.x, col.y)), b2);
+                if (past) y = add2(y, f2pack(col.z, col.w));  // (behind the same rounding as the maximum's)
+                float y0, y1;
+                f2unpack(y, y0, y1);
+                if (edge) {
+                  if (!(see >> r & 1)) y0 = -INFINITY;
+                  if (!(see >> (r + 1) & 1)) y1 = -INFINITY;
+                }
+                hi = fmaxf(hi, fmaxf(y0, y1));
+                z[at_z] = __float_as_uint(y0);
+                z[at_z + 1] = __float_as_uint(y1);
+              }
+            }
+          };
+          scores(true);
+          int *const rise = &s->rise[votes & 1u];
+          ++votes;
+          if (__any_sync(0xffffffffu, hi > kTop) && lane == 0) *rise = votes;
+          if (!(ok = group_sync())) break;
+          if (*reinterpret_cast<volatile int *>(rise) == static_cast<int>(votes)) {
+            // new maxima of the rows whose weights would pass 2^kTop
+            if (tid < 32) s->top[tid] = INT32_MIN;
+            scores(false);
+            if (!(ok = group_sync())) break;
+#pragma unroll
+            for (int e = 0; e < kMost; ++e) {
+              if (e >= 16 && some < 2) break;
+              const float y = __uint_as_float(z[e]);
+              const int top = __reduce_max_sync(0xffffffffu, ordered(__float_as_int(y == y ? y : -INFINITY)));
+              if (lane == 0) atomicMax(&s->top[e], top);
+            }
+            if (!(ok = group_sync())) break;
+            if (tid < 32) {
+              const int r = half * 32 + tid;
+              float f = 1.f;
+              if (r < w.rows) {
+                const float top = __int_as_float(ordered(s->top[tid]));
+                float *less = reinterpret_cast<float *>(&s->col[r >> 1]) + 2 + (r & 1);
+                if (top > -INFINITY && top + *less > kTop) {
+                  f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
+                  const float fresh = kTopFresh - top;
+                  *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
+                }
+              }
+              s->top[tid] = __float_as_int(f);
+            }
+            if (!(ok = group_sync())) break;
+#pragma unroll
+            for (int e = 0; e < kMost; e += 2) {
+              l2[half * 16 + e / 2] = mul2(l2[half * 16 + e / 2], f2pack(__int_as_float(s->top[e]), __int_as_float(s->top[e + 1])));
+            }
+            if (i > 0) {  // the last product is in the accumulator
+              if (!(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < some; ++cb) {
+                uint32_t o[16];
+                __syncwarp();
+                tmem_ld16(t_o + half * 32 + cb * 16, o);
+                tmem_wait_all();
+                tmem_tie16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * __int_as_float(s->top[cb * 16 + e]));
+                }
+                tmem_st16(t_o + half * 32 + cb * 16, o);
+              }
+              tmem_wait_st();
+            }
+            scores(true);
+          }
+          if (half + 1 == kHalves || w.rows <= 32) {
+            tc_fence_before();
+            warp_arrive(&s->s_free[buf], lane);
+          }
+          // the weights' slots are free when the last product is done
+          if (half == 0 && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+#pragma unroll
+          for (int cb = 0; cb < 2; ++cb) {
+            if (cb >= some) break;
+            uint32_t h[8], p[4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at_z = cb * 16 + 2 * e, r = half * 32 + at_z;
+              const float w0 = fast_exp2(__uint_as_float(z[at_z])), w1 = fast_exp2(__uint_as_float(z[at_z + 1]));
+              l2[r / 2] = fma2(f2pack(w0, w1), c2, l2[r / 2]);
+              h[e] = pack2<__half>(w0, w1);
+            }
+            // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
+#pragma unroll
+            for (int piece = 0; piece < 3; ++piece) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
+                p[e / 2] = __byte_perm(u, v, 0x7531);
+                if (piece < 2) {
+                  const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
+                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(hu));
+                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e + 1]) : "r"(hv));
+                }
+              }
+              *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + (half * 2 + cb) * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          }
+        }
+        if (!ok) break;
+        if (edge) {
+          // the tile reaches past the committed tokens: rows of V past the last
+          // token become 0 (they may hold anything), and so do NaN of new tokens,
+          // which patch_nan8 puts back
+          if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
+          if (at >= w.ctx) {
+            uint4 *row = reinterpret_cast<uint4 *>(v_tile + buf * kTileBytes8 + tid * 128);
+            bool found = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint4 *x16 = row + ((e + lane) & 7);
+              uint4 x = make_uint4(0, 0, 0, 0);
+              bool change = at >= w.kv1;
+              if (!change) {
+                x = *x16;
+                uint32_t *words = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t bad = __vcmpeq4(words[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  if (bad) {
+                    words[j] &= ~bad;
+                    change = found = true;
+                  }
+                }
+              }
+              if (change) *x16 = x;
+            }
+            if (found) s->nonfinite = seg;
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&s->p_full, lane);
+      }
+      if (!ok) break;
+      // ---- the unit's result --------------------------------------------------
+      if (!(ok = warp_wait8(s, &s->o_full, (seg - 1) & 1u, status))) break;
+      tc_fence_after();
+      // (the weights' slots are free: the sums of four warps, factors and rows' addresses)
+      float *const sums = reinterpret_cast<float *>(smem + M::kP), *const inverse = sums + 4 * 64;
+      char **const to = reinterpret_cast<char **>(inverse + 64);
+#pragma unroll
+      for (int r0 = 0; r0 < kRows; r0 += 32) {
+        if (r0 >= w.rows) break;
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f2unpack(l2[r0 / 2 + e], v[2 * e], v[2 * e + 1]);
+        sums[warp * 64 + r0 + lane] = transposed_sum(v);
+      }
+      if (!(ok = group_sync())) break;
+      const bool whole = w.flags & kWhole8, base = w.flags & kBase8;
+      const int kind = own ? 0 : 1;
+      if (tid < w.rows) {
+        const float l = (sums[tid] + sums[64 + tid]) + (sums[128 + tid] + sums[192 + tid]);
+        const int token = tid / heads.n, row = w.row0 + token, qh = heads.first + tid - token * heads.n;
+        const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
+        const int64_t cont = static_cast<int64_t>(blockIdx.x) * kRows + tid;
+        const float less = *(reinterpret_cast<const float *>(&s->col[tid >> 1]) + 2 + (tid & 1));
+        const float lse2 = l == 0.f ? -INFINITY : log2f(l) + (32.f - less);
+        inverse[tid] = l == 0.f ? 0.f : 1.f / l * kSumScale;
+        if (whole) {
+          if (k.a.lse) k.a.lse[rh] = lse2 * 0.69314718055994531f;
+          to[tid] = k.a.out + (row * k.a.o_row + qh * k.a.o_head) * static_cast<int64_t>(sizeof(T));
+        } else if (base) {
+          k.w.lse[kind][rh] = lse2;
+          to[tid] = reinterpret_cast<char *>(k.w.o[kind] + rh * D);
+        } else {
+          k.w.lse_c[cont] = lse2;
+          to[tid] = reinterpret_cast<char *>(k.w.o_c + cont * D);
+        }
+      }
+      if (!(ok = group_sync())) break;
+      const bool bad = *reinterpret_cast<volatile unsigned *>(&s->nonfinite) == seg;
+#pragma unroll 1
+      for (int cb = 0; cb < chunks; ++cb) {
+        uint32_t o[16];
+        __syncwarp();
+        tmem_ld16(t_o + cb * 16, o);
+        tmem_wait_all();
+        tmem_tie16(o);
+        if (cb + 1 == chunks) {  // the accumulator may be written again
+          tc_fence_before();
+          warp_arrive(&s->o_free, lane);
+        }
+        if (tid < D) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = cb * 16 + e;
+            if (r < w.rows) {
+              const float x = inverse[r] == 0.f ? 0.f : __uint_as_float(o[e]) * inverse[r];
+              if (whole) {
+                reinterpret_cast<T *>(to[r])[tid] = from_f32<T>(x);
+              } else {
+                reinterpret_cast<float *>(to[r])[tid] = x;
+              }
+            }
+          }
+        }
+      }
+      if (bad && tid < D) {
+        if (whole) patch_nan8<T>(k, w, heads, tid, to);
+        else patch_nan8<float>(k, w, heads, tid, to);
+      }
+      __syncwarp();
+      if (k.join_inside && !whole) {
+        // the CTA that stores a cut unit's last part joins them, in their order
+        const int owner = w.join & 0xffff, more = w.join >> 16;
+        if (!(ok = group_sync())) break;
+        if (tid == 0) {
+          __threadfence();  // what the CTA stored, ahead of the count
+          const bool all = atomicAdd(&k.w.tickets[owner], 1u) == static_cast<unsigned>(more);
+          if (all) k.w.tickets[owner] = 0;
+          s->joins = all;
+          __threadfence();
+        }
+        if (!(ok = group_sync())) break;
+        if (s->joins) {
+          for (int slot = warp; slot < w.rows; slot += 4) {
+            const int token = slot / heads.n, qh = heads.first + slot - token * heads.n;
+            const int64_t rh = static_cast<int64_t>(w.row0 + token) * k.a.q_heads + qh;
+            write_row<T>(k, rh, w.row0 + token, qh, join_parts<Units8<T>>(k, 0, rh, owner, more, slot));
+          }
+        }
+        __syncwarp();
+      }
+      // (the next segment's first weights are written behind a turn of `group`, and so behind all of this)
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 4) {
+      // ---- matrix products ----------------------------------------------------
+      const int k_steps = (D + 31) / 32;
+      const uint32_t k0 = smem_desc(smem_addr(smem + M::kK), 16), v0 = smem_desc(smem_addr(smem + M::kV), 16);
+      const uint32_t q0 = smem_desc(smem_addr(smem + M::kQ), 16);
+      // weights: 8 tokens x 16 rows of 16 bytes each, 128 bytes to the next tokens, 2048 to the next rows
+      const uint32_t p0 = smem_desc(smem_addr(smem + M::kP), 128);
+      constexpr uint32_t kHighP = 2048u >> 4 | 1u << 14;
+      uint32_t seg = 0, tile = 0;
+      bool ok = true;
+      Seg8 w;
+      while (ok && take_segment8(s, seg, &w, status)) {
+        warp_arrive(&s->seg_empty[seg % kSegs8], lane);
+        const int n = w.n, columns = (w.rows + 15) & ~15;
+        const uint32_t id_s = instr_desc8(columns, false, false, false), id_o = instr_desc8(columns, true, true, true);
+        if (elect_one()) {
+          auto scores = [&](int i) {
+            const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
+            // (the first turn of a fresh barrier passes for the one before it)
+            if (!wait8(s, &s->s_free[at], turn ^ 1u, status) || !wait8(s, &s->k_full[at], turn, status)) {
+              return false;
+            }
+            tc_fence_after();
+            const uint32_t ka = k0 + at * (kTileBytes8 >> 4);
+#pragma unroll
+            for (int piece = 0; piece < kPieces; ++piece) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (c < k_steps) {
+                  mma8_ss(tmem + at * 64, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
+                          piece > 0 || c > 0);
+                }
+              }
+            }
+            tc_commit(&s->s_full[at]);
+            tc_commit(&s->k_empty[at]);
+            if (i + 1 == n) tc_commit(&s->q_free);
+            return true;
+          };
+          ok = wait8(s, &s->q_full, seg & 1u, status) && scores(0);
+          for (int i = 0; ok && i < n; ++i) {
+            if (i + 1 < n && !(ok = scores(i + 1))) break;
+            // the last segment's result has been read
+            if (i == 0 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
+            const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
+            if (!(ok = wait8(s, &s->v_full[at], turn, status) &&
+                       wait8(s, &s->p_full, (tile + i) & 1u, status))) {
+              break;
+            }
+            tc_fence_after();
+            const uint32_t va = v0 + at * (kTileBytes8 >> 4);
+#pragma unroll
+            for (int piece = 0; piece < 3; ++piece) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                mma8_ss(tmem + 128, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
+                        i > 0 || piece > 0 || c > 0);
+              }
+            }
+            tc_commit(&s->v_empty[at]);
+            tc_commit(&s->pv_done);
+          }
+          if (ok) tc_commit(&s->o_full);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        tile += n;
+        ++seg;
+      }
+      if (elect_one()) {
+        tc_commit(&s->drained);  // nothing of this CTA runs on when it ends
+        if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(status, SMC_DEV_TIMEOUT);
+      }
+      __syncwarp();
+    } else if (warp == 5) {
+      // ---- segments, K and V ----------------------------------------------------
+      Walk<Units8<T>> walk;
+      walk.start(k);
+      unsigned bits = 0;
+      uint32_t tile = 0;
+      bool ok = true, begun = false;
+      for (uint32_t seg = 0; ok; ++seg) {
+        if (seg >= kSegs8 && !(ok = warp_wait8(s, &s->seg_empty[seg % kSegs8], (seg / kSegs8 - 1) & 1u, status))) break;
+        const bool more = walk.next(k);
+        if (!begun && lane == 0 && !k.join_inside) {
+          const bool cut = more && walk.first_cut;
+          int4 *rec = reinterpret_cast<int4 *>(&k.w.cuts[blockIdx.x]);
+          rec[0] = cut ? make_int4(walk.t.row0 + walk.tokens0, walk.rows, walk.head, walk.more) : make_int4(0, 0, 0, 0);
+          rec[1] = make_int4(more ? walk.t.flags : 0, 0, 0, 0);
+        }
+        begun = true;
+        Seg8 w{};
+        w.flags = kEnd8;
+        if (more) {
+          w = {walk.t.row0 + walk.tokens0, walk.rows, walk.tokens0, walk.t.seq, walk.head, walk.t.kv0 + walk.i0 * kTile8,
+               walk.n, walk.t.ctx, walk.t.kv1, walk.t.tokens, 0, walk.owner | walk.more << 16};
+          w.flags = (walk.t.flags & kShared) | ((walk.t.flags & kSolo) && walk.n == walk.t.tiles ? kWhole8 : 0) |
+                    (walk.i0 == 0 ? kBase8 : 0);
+        }
+        if (lane == 0) {
+          int4 *to = reinterpret_cast<int4 *>(&s->seg[seg % kSegs8]);
+          to[0] = make_int4(w.row0, w.rows, w.i0, w.seq);
+          to[1] = make_int4(w.head, w.t0, w.n, w.ctx);
+          to[2] = make_int4(w.kv1, w.n_new, w.flags, w.join);
+        }
+        warp_arrive(&s->seg_full[seg % kSegs8], lane);
+        if (!more) break;
+        // the tiles
+        const int head = unit_heads<Units8<T>>(k, w.head).key, t_end = min(w.t0 + w.n * kTile8, w.kv1);
+        const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
+        auto place = [&](int t) {  // (block, token in it)
+          const int slot = block_of(k, t);
+          int id = table[slot];
+          if (id < 0 || id >= c8.blocks) {
+            bits |= SMC_DEV_BAD_BLOCK;
+            id = 0;
+          }
+          return make_int2(id, t - slot * c8.block_size);
+        };
+        // places of 32 boxes, a lane each, and of the 32 after them
+        const int per_tile = kTile8 / k.box;
+        int2 here = make_int2(0, 0), ahead = make_int2(0, 0);
+        int from = -32;
+        if constexpr (kTma) {
+          if (w.t0 + lane * k.box < t_end) ahead = place(w.t0 + lane * k.box);
+        }
+        for (int i = 0; i < w.n; ++i, ++tile) {
+          const uint32_t slot = tile & 1u, turn = tile >> 1 & 1u;
+          const int t0 = w.t0 + i * kTile8, t1 = min(t0 + kTile8, t_end);
+          char *const to_k = smem + M::kK + slot * kTileBytes8, *const to_v = smem + M::kV + slot * kTileBytes8;
+          if constexpr (kTma) {
+            if ((i + 1) * per_tile > from + 32) {
+              from = i * per_tile;
+              here = ahead;
+              const int t = t0 + (32 + lane) * k.box;
+              if (t < t_end) ahead = place(t);
+            }
+            const int boxes = (t1 - t0 + k.box - 1) / k.box, mine = i * per_tile - from + lane;
+            const int block = __shfl_sync(0xffffffffu, here.x, mine & 31), token = __shfl_sync(0xffffffffu, here.y, mine & 31);
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              uint64_t *full = which ? &s->v_full[slot] : &s->k_full[slot];
+              if (!(ok = warp_wait8(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
+              if (lane == 0) mbar_arrive_expect_tx(full, boxes * k.box * 128);
+              __syncwarp();
+              if (lane < boxes) {
+                tma_load_4d((which ? to_v : to_k) + lane * k.box * 128, which ? &map_v : &map_k, 0, token, head, block, full);
+              }
+              __syncwarp();
+            }
+          } else {
+            // lane l finds rows l, l + 32, ...; a copy's lanes take their rows' places
+            int64_t off[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (t0 + lane + 32 * e < t1) {
+                const int2 p = place(t0 + lane + 32 * e);
+                off[e] = p.x * c8.block_stride + p.y * c8.token_stride + head * c8.head_stride;
+              }
+            }
+            const int chunk = lane & 7;
+            const bool take = chunk * 16 < D;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              if (!(ok = warp_wait8(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
+              const char *column = (which ? c8.v : c8.k) + (take ? chunk * 16 : 0);
+              const uint32_t to = smem_addr(which ? to_v : to_k);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int r = lane >> 3; r < 32; r += 4) {
+                  const int64_t from_row = __shfl_sync(0xffffffffu, off[e], r);
+                  const int row = r + 32 * e;
+                  if (t0 + row < t1) cp_async16(to + row * 128 + ((chunk ^ (row & 7)) << 4), column + from_row, take);
+                }
+              }
+              asm volatile("cp.async.commit_group;" ::: "memory");
+              if (which) {  // K has arrived
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                fence_proxy_async_smem();
+                warp_arrive(&s->k_full[slot], lane);
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                fence_proxy_async_smem();
+                warp_arrive(&s->v_full[slot], lane);
+              }
+            }
+            if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
+          }
+          if (!ok) break;
+        }
+      }
+      if (kTma && s->abort) {  // copies that may be under way
+        for (uint32_t t = tile < 2 ? 0 : tile - 2; t <= tile; ++t) {
+          mbar_wait(&s->k_full[t & 1u], t >> 1 & 1u, 1u << 12);
+          mbar_wait(&s->v_full[t & 1u], t >> 1 & 1u, 1u << 12);
+        }
+      }
+      if (bits) raise_status(status, bits);
+    } else {
+      // ---- q's pieces -----------------------------------------------------------
+      const int r = tid - 192;  // row of the unit
+      uint32_t seg = 0;
+      bool ok = true;
+      Seg8 w;
+      while (ok && take_segment8(s, seg, &w, status)) {
+        warp_arrive(&s->seg_empty[seg % kSegs8], lane);
+        const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
+        const bool live = r < w.rows;
+        const int token = live ? r / heads.n : 0, qh = heads.first + (live ? r - token * heads.n : 0);
+        const uint4 *q = reinterpret_cast<const uint4 *>(
+            k.a.q + ((w.row0 + token) * k.a.q_row + qh * k.a.q_head) * static_cast<int64_t>(sizeof(T)));
+        float top = 0.f;
+        if (live) {
+#pragma unroll 4
+          for (int e = 0; e < D / 8; ++e) {
+            const uint4 v = q[e];
+            const T *x = reinterpret_cast<const T *>(&v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float a = fabsf(to_f32(x[j]));
+              if (a < INFINITY) top = fmaxf(top, a);
+            }
+          }
+        }
+        const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
+        // the rows before have been read: their scales, and their pieces by the last scores
+        if (seg > 0 && !(ok = warp_wait8(s, &s->q_taken, (seg - 1) & 1u, status) &&
+                              warp_wait8(s, &s->q_free, (seg - 1) & 1u, status))) {
+          break;
+        }
+        if (r < ((w.rows + 15) & ~15)) {
+          char *to = smem + M::kQ + r * 128;
+#pragma unroll 2
+          for (int c = 0; c < 8; ++c) {
+            uint32_t words[kPieces][4] = {};
+            if (live && c * 16 < D) {
+              const uint4 v[2] = {q[2 * c], q[2 * c + 1]};
+              const T *x = reinterpret_cast<const T *>(v);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float a = finite_or_nan(to_f32(x[j])) * inv, b = finite_or_nan(to_f32(x[j + 1])) * inv;
+#pragma unroll
+                for (int piece = 0; piece < kPieces; ++piece) {
+                  const uint32_t e = to_e4m3x2(a, b), h = from_e4m3x2(e);
+                  words[piece][j / 4] |= e << (j & 2) * 8;
+                  const float2 taken = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                  a -= taken.x;
+                  b -= taken.y;
+                }
+              }
+            }
+#pragma unroll
+            for (int piece = 0; piece < kPieces; ++piece) {
+              *reinterpret_cast<uint4 *>(to + piece * M::kPiece + ((c ^ (r & 7)) << 4)) =
+                  make_uint4(words[piece][0], words[piece][1], words[piece][2], words[piece][3]);
+            }
+          }
+        }
+        s->q_scale[r] = live ? scale : 0.f;
+        fence_proxy_async_smem();
+        warp_arrive(&s->q_full, lane);
+        ++seg;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_free<256>(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launch.
+// ---------------------------------------------------------------------------
+// [blocks][kv_heads][block_size][head_dim] in boxes of 128 bytes x `box` tokens;
+// columns past head_dim read as 0.
+static bool make_map8(CUtensorMap *map, const CacheArgs &c, void *base, int box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.block_size),
+                              static_cast<cuuint64_t>(c.kv_heads), static_cast<cuuint64_t>(c.blocks)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride), static_cast<cuuint64_t>(c.head_stride),
+                                 static_cast<cuuint64_t>(c.block_stride)};
+  const cuuint32_t boxes[4] = {128, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+static const void *attention8_fn(bool tma) {
+  return tma ? reinterpret_cast<const void *>(attention8_kernel<T, true>)
+             : reinterpret_cast<const void *>(attention8_kernel<T, false>);
+}
+
+static cudaError_t configure8(int *ctas) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int slot = dev < kMaxDev ? dev : kMaxDev - 1;
+  *ctas = dev < kMaxDev ? known[slot].load(std::memory_order_acquire) : 0;
+  if (*ctas) return cudaSuccess;
+  for (const bool tma : {false, true}) {
+    e = cudaFuncSetAttribute(attention8_fn<__nv_bfloat16>(tma), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem8<__nv_bfloat16>::kBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attention8_fn<__half>(tma), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem8<__half>::kBytes);
+    if (e != cudaSuccess) return e;
+  }
+  int n = 0;
+  e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  n *= kCtasPerSm;
+  *ctas = n < kMaxCtas8 ? n : kMaxCtas8;
+  if (dev < kMaxDev) known[slot].store(*ctas, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <typename T>
+static cudaError_t launch8(const AttnArgs &a, const ScaleArgs &s, void *workspace, int most_ctas, cudaStream_t st) {
+  constexpr int kRows = Rows8<T>::kRows;
+  Kernel8Args k{};
+  k.a = a;
+  k.sc8 = s;
+  // as for 16 bits: shared blocks are read once where reading them again is not the L2 cache's work
+  const double table_bytes = static_cast<double>(a.b.S) * a.b.T * a.c.block_size * a.c.kv_heads * a.c.head_dim * 2;
+  if (table_bytes < 96e6) k.a.b.group = 1;
+  carve(a.c, k.a.b, a.q_heads, kMaxCtas8, 64, static_cast<char *>(workspace), &k.w);
+  k.rep = a.q_heads / a.c.kv_heads;
+  const int parts = (k.rep + kRows - 1) / kRows;
+  k.head_units = a.c.kv_heads * parts;
+  k.unit_rep = (k.rep + parts - 1) / parts;
+  k.tile_tokens = kRows / k.unit_rep;
+  k.sc = a.scale * 1.4426950408889634f;
+  divide_by(a.c.block_size, &k);
+  // a box is a run of tokens inside one block and one tile; the swizzle repeats every eight rows, so a box
+  // starts on a multiple of eight.  Blocks of other sizes are copied by a warp's lanes, 16 bytes each
+  int box = kTile8;
+  while (a.c.block_size % box) box >>= 1;
+  CUtensorMap map_k{}, map_v{};
+  const bool tma = box >= 8 && make_map8(&map_k, a.c, a.c.k, box) && make_map8(&map_v, a.c, a.c.v, box);
+  k.box = box;
+  // no more CTAs than tiles there can be
+  const int64_t units = a.b.S * ((static_cast<int64_t>(a.b.max_new) + k.tile_tokens - 1) / k.tile_tokens);
+  const int64_t most = (static_cast<int64_t>(a.b.T) * a.c.block_size + kTile8 - 1) / kTile8 * k.head_units * units;
+  const int ctas = most < most_ctas ? static_cast<int>(most) : most_ctas;
+  k.planned = k.w.groups > 0 || a.b.S > 256;
+  const int64_t most_rows = static_cast<int64_t>(a.b.max_new) * k.a.b.group * k.unit_rep;
+  const int unit_rows = static_cast<int>(most_rows < kRows ? most_rows : kRows);
+  k.join_inside = !k.w.groups && unit_rows * (ctas / k.head_units + 2) <= 1024;
+  k.more_kernels = k.w.groups > 0 || (ctas > 1 && !k.join_inside);
+  cudaError_t e;
+  void *work[] = {static_cast<WorkArgs *>(&k)};
+  if (k.planned) {
+    int n = ctas;
+    void *args[] = {static_cast<WorkArgs *>(&k), &n};
+    e = launch_early(reinterpret_cast<const void *>(plan_kernel<Units8<T>>), dim3(k.w.groups ? k.w.groups : 1),
+                     kPlanThreads, 0, args, st);
+    if (e != cudaSuccess) return e;
+  }
+  void *args[] = {&k, &map_k, &map_v};
+  e = launch_early(attention8_fn<T>(tma), dim3(ctas), kThreads8, Smem8<T>::kBytes, args, st);
+  if (e != cudaSuccess) return e;
+  if (ctas > 1 && !k.join_inside) {
+    e = launch_early(reinterpret_cast<const void *>(join_cut_units_kernel<T, Units8<T>>),
+                     dim3(ctas - 1, (unit_rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, work, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (!k.w.groups) return cudaSuccess;
+  return launch_early(reinterpret_cast<const void *>(join_shared_kernel<T>), dim3(a.b.rows), 32 * kJoinWarps, 0, work, st);
+}
+
+cudaError_t launch_tree_attention8(const AttnArgs &a, const ScaleArgs &s, int dtype, void *workspace, cudaStream_t st) {
   if (a.b.rows == 0) return cudaSuccess;
-  ScaleArgs scales = s;
-  void *args[] = {const_cast<AttnArgs *>(&a), &scales};
-  return launch_early(dtype == SMC_BF16 ? reinterpret_cast<const void *>(attention8_kernel<__nv_bfloat16>)
-                                        : reinterpret_cast<const void *>(attention8_kernel<__half>),
-                      dim3(a.b.rows, a.q_heads), kThreads8, 0, args, st);
+  int ctas = 0;
+  const cudaError_t e = configure8(&ctas);
+  if (e != cudaSuccess) return e;
+  return dtype == SMC_BF16 ? launch8<__nv_bfloat16>(a, s, workspace, ctas, st) : launch8<__half>(a, s, workspace, ctas, st);
 }
 
 }  // namespace smcsd

@@ -92,12 +92,11 @@ constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final resul
 struct Tail8 {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2];
   uint64_t p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
-  uint64_t seg_full[kSegs8], seg_empty[kSegs8], group;
+  uint64_t seg_full[kSegs8], seg_empty[kSegs8];
   Seg8 seg[kSegs8];
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
-  int top[32];        // maxima of a tile, then factors
-  int rise[2];        // the last vote (from 1) in which a maximum rose
+  int top[64];        // maxima of a tile, then factors
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
   uint32_t tmem;
   volatile int abort;
@@ -152,6 +151,29 @@ __device__ __forceinline__ bool take_segment8(Tail8 *s, uint32_t seg, Seg8 *to, 
   *to = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
   return !(to->flags & kEnd8);
 }
+
+// The four softmax warps' barrier, and the vote on it.  A hardware barrier (30
+// cycles against an mbarrier's 300) has no bound of its own; it is kept by this
+// rule: every warp looks at `abort` behind each turn and each wait, and one that
+// finds it set, or sets it, arrives once more (leave_group) and comes no more.
+// A warp that saw nothing behind turn n so finds the others' arrivals at turn
+// n + 1; they are behind the flag, so it leaves there, and no one waits at n + 2.
+__device__ __forceinline__ bool group_any(Tail8 *s, bool mine, bool *ok) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  *ok = !s->abort;
+  return any;
+}
+__device__ __forceinline__ bool group_sync(Tail8 *s) {
+  asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  return !s->abort;
+}
+__device__ __forceinline__ void leave_group() { asm volatile("barrier.cta.arrive 1, 128;" ::: "memory"); }
 
 // The order of floats in that of ints (and back: its own inverse).
 __device__ __forceinline__ int ordered(int bits) { return bits ^ (bits >> 31 & 0x7fffffff); }
@@ -211,12 +233,34 @@ __device__ __forceinline__ float transposed_sum(float *v) {
   return v[0];
 }
 
+// Their maximum likewise, NaN as -inf.
+__device__ __forceinline__ float transposed_max(const uint32_t *z) {
+  const int lane = threadIdx.x & 31;
+  float v[16];
+  const bool up = lane & 16;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t send = up ? z[j] : z[j + 16], keep = up ? z[j + 16] : z[j];
+    v[j] = fmaxf(fmaxf(__uint_as_float(keep), __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16))), -INFINITY);
+  }
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int j = 0; j < s; ++j) {
+      const float send = up ? v[j] : v[j + s], keep = up ? v[j + s] : v[j];
+      v[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, s));
+    }
+  }
+  return v[0];
+}
+
 template <typename T, bool kTma>
 __global__ void __launch_bounds__(kThreads8, kCtasPerSm)
 attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
   using M = Smem8<T>;
-  constexpr int kRows = Rows8<T>::kRows, kPieces = Rows8<T>::kPieces, kHalves = (kRows + 31) / 32;
+  constexpr int kRows = Rows8<T>::kRows, kPieces = Rows8<T>::kPieces, kChunks = kRows / 16, kPad = (kRows + 31) / 32 * 32;
   extern __shared__ __align__(1024) char smem[];
   Tail8 *const s = reinterpret_cast<Tail8 *>(smem + M::kTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -232,7 +276,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->v_empty[i], 1);
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_free[i], 4);
-      s->rise[i] = 0;
     }
     mbar_init(&s->p_full, 4);
     mbar_init(&s->pv_done, 1);
@@ -242,7 +285,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     mbar_init(&s->o_full, 1);
     mbar_init(&s->o_free, 4);
     mbar_init(&s->drained, 1);
-    mbar_init(&s->group, 4);
     for (int i = 0; i < kSegs8; ++i) {
       mbar_init(&s->seg_full[i], 1);
       mbar_init(&s->seg_empty[i], 7);  // every warp but the one that fills it
@@ -272,12 +314,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     const uint32_t t_s = tmem + lanes, t_o = tmem + lanes + 128;
     char *const p_at = smem + M::kP + (tid >> 3) * 128 + (tid & 7) * 16;
     char *const v_tile = smem + M::kV;
-    uint32_t seg = 0, tile = 0, syncs = 0, votes = 0;
+    uint32_t seg = 0, tile = 0;
     bool ok = true;
-    auto group_sync = [&] {
-      warp_arrive(&s->group, lane);
-      return warp_wait8(s, &s->group, syncs++ & 1u, status);
-    };
     Seg8 w;
     while (ok && take_segment8(s, seg, &w, status)) {
       warp_arrive(&s->seg_empty[seg % kSegs8], lane);
@@ -286,16 +324,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       const bool own = !(w.flags & kShared);
       const int t_end = min(w.t0 + w.n * kTile8, w.kv1);
       const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
-      // scales: of the tile at hand, of the next one the block
-      auto block_at = [&](int t) {
-        int id = t < t_end ? table[block_of(k, t)] : -1;
-        return id < 0 || id >= c8.blocks ? 0 : id;
-      };
+      // scales: of the tile at hand, of the next one the block (its table entry as it is read: looked at a tile later)
+      auto entry_at = [&](int t) { return t < t_end ? table[block_of(k, t)] : -1; };
+      auto scale_at = [&](int id) { return (id < 0 || id >= c8.blocks ? 0 : id) * k.sc8.block; };
       const float *ks_of = k.sc8.k + heads.key * k.sc8.head, *vs_of = k.sc8.v + heads.key * k.sc8.head;
-      int at = w.t0 + tid;
-      int64_t next = block_at(at) * k.sc8.block;
-      float ks = ks_of[next], vs = vs_of[next];
-      next = block_at(at + kTile8) * k.sc8.block;
+      int at = w.t0 + tid, next = entry_at(at + kTile8);
+      int64_t from = scale_at(entry_at(at));
+      float ks = ks_of[from], vs = vs_of[from];
       // the rows' scales and maxima
       if (!(ok = warp_wait8(s, &s->q_full, seg & 1u, status))) break;
       if (tid < 32) {
@@ -303,11 +338,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
       }
       ++seg;
-      if (!(ok = group_sync())) break;
+      if (!(ok = group_sync(s))) break;
       warp_arrive(&s->q_taken, lane);
-      unsigned long long l2[16 * kHalves];  // sums of w / s_v, this thread's tokens
+      unsigned long long l2[kPad / 2];  // sums of w / s_v, this thread's tokens
 #pragma unroll
-      for (int i = 0; i < 16 * kHalves; ++i) l2[i] = 0;
+      for (int i = 0; i < kPad / 2; ++i) l2[i] = 0;
 
       for (int i = 0; i < w.n; ++i, ++tile, at += kTile8) {
         const uint32_t buf = tile & 1u, t_sb = t_s + buf * 64;
@@ -315,9 +350,10 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const unsigned long long a2 = f2dup(k.sc * sk);
         const float b = log2f(sv), c = kSumScale / sv;
         if (i + 1 < w.n) {
-          ks = ks_of[next];
-          vs = vs_of[next];
-          next = block_at(at + 2 * kTile8) * k.sc8.block;
+          from = scale_at(next);
+          ks = ks_of[from];
+          vs = vs_of[from];
+          next = entry_at(at + 2 * kTile8);
         }
         const int t0 = w.t0 + i * kTile8;
         const bool edge = own && t0 + kTile8 > w.ctx;
@@ -325,138 +361,133 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
         tc_fence_after();
         const unsigned long long b2 = f2dup(b), c2 = f2dup(c);
-        // 32 rows at a time
+        uint32_t z[kPad];
+        float hi;
+        // the rows' z + log2 s_v, less (with `past`) M and plus kTopFresh
+        auto scores = [&](bool past) {
+          __syncwarp();
 #pragma unroll
-        for (int half = 0; half < kHalves; ++half) {
-          if (half && w.rows <= 32) break;
-          constexpr int kMost = kRows < 32 ? kRows : 32;
-          const int some = min(chunks - 2 * half, 2);  // chunks of 16
-          uint32_t z[kMost];
-          float hi;
-          // the rows' z + log2 s_v, less (with `past`) M and plus kTopFresh
-          auto scores = [&](bool past) {
-            __syncwarp();
+          for (int cb = 0; cb < kChunks; ++cb) {
+            if (cb < chunks) tmem_ld16(t_sb + cb * 16, z + cb * 16);
+          }
+          tmem_wait_all();
+          hi = -INFINITY;
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {
-              if (cb < some) tmem_ld16(t_sb + half * 32 + cb * 16, z + cb * 16);
+          for (int cb = 0; cb < kChunks; ++cb) {
+            if (cb >= chunks) break;
+            tmem_tie16(z + cb * 16);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int r = cb * 16 + e;
+              const float4 col = s->col[r / 2];
+              unsigned long long y = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])),
+                                          mul2(a2, f2pack(col.x, col.y)), b2);
+              if (past) y = add2(y, f2pack(col.z, col.w));  // (behind the same rounding as the maximum's)
+              float y0, y1;
+              f2unpack(y, y0, y1);
+              z[r] = __float_as_uint(y0);
+              z[r + 1] = __float_as_uint(y1);
             }
-            tmem_wait_all();
-            hi = -INFINITY;
+            if (edge) {
+              const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {
-              if (cb >= some) break;
-              tmem_tie16(z + cb * 16);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const int at_z = cb * 16 + e, r = half * 32 + at_z;
-                const float4 col = s->col[r / 2];
-                unsigned long long y = fma2(f2pack(__uint_as_float(z[at_z]), __uint_as_float(z[at_z + 1])),
-                                            mul2(a2, f2pack(col.x, col.y)), b2);
-                if (past) y = add2(y, f2pack(col.z, col.w));  // (behind the same rounding as the maximum's)
-                float y0, y1;
-                f2unpack(y, y0, y1);
-                if (edge) {
-                  if (!(see >> r & 1)) y0 = -INFINITY;
-                  if (!(see >> (r + 1) & 1)) y1 = -INFINITY;
-                }
-                hi = fmaxf(hi, fmaxf(y0, y1));
-                z[at_z] = __float_as_uint(y0);
-                z[at_z + 1] = __float_as_uint(y1);
+              for (int e = 0; e < 16; ++e) {
+                if (!(some >> e & 1)) z[cb * 16 + e] = 0xff800000u;
               }
             }
-          };
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              hi = fmaxf(fmaxf(hi, __uint_as_float(z[cb * 16 + e])), __uint_as_float(z[cb * 16 + e + 1]));
+            }
+          }
+        };
+        bool rise = i == 0;
+        if (!rise) {
           scores(true);
-          int *const rise = &s->rise[votes & 1u];
-          ++votes;
-          if (__any_sync(0xffffffffu, hi > kTop) && lane == 0) *rise = votes;
-          if (!(ok = group_sync())) break;
-          if (*reinterpret_cast<volatile int *>(rise) == static_cast<int>(votes)) {
-            // new maxima of the rows whose weights would pass 2^kTop
-            if (tid < 32) s->top[tid] = INT32_MIN;
-            scores(false);
-            if (!(ok = group_sync())) break;
+          rise = group_any(s, hi > kTop, &ok);
+          if (!ok) break;
+        }
+        if (rise) {
+          // new maxima: of every row whose weights would pass 2^kTopFresh, while at it
+          if (tid < 64) s->top[tid] = INT32_MIN;
 #pragma unroll
-            for (int e = 0; e < kMost; ++e) {
-              if (e >= 16 && some < 2) break;
-              const float y = __uint_as_float(z[e]);
-              const int top = __reduce_max_sync(0xffffffffu, ordered(__float_as_int(y == y ? y : -INFINITY)));
-              if (lane == 0) atomicMax(&s->top[e], top);
-            }
-            if (!(ok = group_sync())) break;
-            if (tid < 32) {
-              const int r = half * 32 + tid;
-              float f = 1.f;
-              if (r < w.rows) {
-                const float top = __int_as_float(ordered(s->top[tid]));
-                float *less = reinterpret_cast<float *>(&s->col[r >> 1]) + 2 + (r & 1);
-                if (top > -INFINITY && top + *less > kTop) {
-                  f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
-                  const float fresh = kTopFresh - top;
-                  *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
-                }
+          for (int r = 0; r < kPad; ++r) z[r] = 0xff800000u;
+          scores(false);
+          if (!(ok = group_sync(s))) break;
+#pragma unroll
+          for (int half = 0; half < kPad; half += 32) {
+            if (half < w.rows) atomicMax(&s->top[half + lane], ordered(__float_as_int(transposed_max(z + half))));
+          }
+          if (!(ok = group_sync(s))) break;
+          if (tid < 64) {
+            float f = 1.f;
+            if (tid < w.rows) {
+              const float top = __int_as_float(ordered(s->top[tid]));
+              float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);
+              if (top > -INFINITY && top + *less > kTopFresh) {
+                f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
+                const float fresh = kTopFresh - top;
+                *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
               }
-              s->top[tid] = __float_as_int(f);
             }
-            if (!(ok = group_sync())) break;
+            s->top[tid] = __float_as_int(f);
+          }
+          if (!(ok = group_sync(s))) break;
 #pragma unroll
-            for (int e = 0; e < kMost; e += 2) {
-              l2[half * 16 + e / 2] = mul2(l2[half * 16 + e / 2], f2pack(__int_as_float(s->top[e]), __int_as_float(s->top[e + 1])));
-            }
-            if (i > 0) {  // the last product is in the accumulator
-              if (!(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
-              tc_fence_after();
+          for (int r = 0; r < kRows; r += 2) {
+            l2[r / 2] = mul2(l2[r / 2], f2pack(__int_as_float(s->top[r]), __int_as_float(s->top[r + 1])));
+          }
+          if (i > 0) {  // the last product is in the accumulator
+            if (!(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+            tc_fence_after();
 #pragma unroll 1
-              for (int cb = 0; cb < some; ++cb) {
-                uint32_t o[16];
-                __syncwarp();
-                tmem_ld16(t_o + half * 32 + cb * 16, o);
-                tmem_wait_all();
-                tmem_tie16(o);
+            for (int cb = 0; cb < chunks; ++cb) {
+              uint32_t o[16];
+              __syncwarp();
+              tmem_ld16(t_o + cb * 16, o);
+              tmem_wait_all();
+              tmem_tie16(o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * __int_as_float(s->top[cb * 16 + e]));
-                }
-                tmem_st16(t_o + half * 32 + cb * 16, o);
+              for (int e = 0; e < 16; ++e) {
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * __int_as_float(s->top[cb * 16 + e]));
               }
-              tmem_wait_st();
+              tmem_st16(t_o + cb * 16, o);
             }
-            scores(true);
+            tmem_wait_st();
           }
-          if (half + 1 == kHalves || w.rows <= 32) {
-            tc_fence_before();
-            warp_arrive(&s->s_free[buf], lane);
+          scores(true);
+        }
+        tc_fence_before();
+        warp_arrive(&s->s_free[buf], lane);
+        // the weights' slots are free when the last product is done
+        if (tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+#pragma unroll
+        for (int cb = 0; cb < kChunks; ++cb) {
+          if (cb >= chunks) break;
+          uint32_t h[8], p[4];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = cb * 16 + 2 * e;
+            const float w0 = fast_exp2(__uint_as_float(z[r])), w1 = fast_exp2(__uint_as_float(z[r + 1]));
+            l2[r / 2] = fma2(f2pack(w0, w1), c2, l2[r / 2]);
+            h[e] = pack2<__half>(w0, w1);
           }
-          // the weights' slots are free when the last product is done
-          if (half == 0 && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+          // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
 #pragma unroll
-          for (int cb = 0; cb < 2; ++cb) {
-            if (cb >= some) break;
-            uint32_t h[8], p[4];
+          for (int piece = 0; piece < 3; ++piece) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int at_z = cb * 16 + 2 * e, r = half * 32 + at_z;
-              const float w0 = fast_exp2(__uint_as_float(z[at_z])), w1 = fast_exp2(__uint_as_float(z[at_z + 1]));
-              l2[r / 2] = fma2(f2pack(w0, w1), c2, l2[r / 2]);
-              h[e] = pack2<__half>(w0, w1);
-            }
-            // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
-#pragma unroll
-            for (int piece = 0; piece < 3; ++piece) {
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
-                p[e / 2] = __byte_perm(u, v, 0x7531);
-                if (piece < 2) {
-                  const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
-                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(hu));
-                  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e + 1]) : "r"(hv));
-                }
+            for (int e = 0; e < 8; e += 2) {
+              const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
+              p[e / 2] = __byte_perm(u, v, 0x7531);
+              if (piece < 2) {
+                const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
+                asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(hu));
+                asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e + 1]) : "r"(hv));
               }
-              *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + (half * 2 + cb) * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
             }
+            *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + cb * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
           }
         }
-        if (!ok) break;
         if (edge) {
           // the tile reaches past the committed tokens: rows of V past the last
           // token become 0 (they may hold anything), and so do NaN of new tokens,
@@ -506,7 +537,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         for (int e = 0; e < 16; ++e) f2unpack(l2[r0 / 2 + e], v[2 * e], v[2 * e + 1]);
         sums[warp * 64 + r0 + lane] = transposed_sum(v);
       }
-      if (!(ok = group_sync())) break;
+      if (!(ok = group_sync(s))) break;
       const bool whole = w.flags & kWhole8, base = w.flags & kBase8;
       const int kind = own ? 0 : 1;
       if (tid < w.rows) {
@@ -528,7 +559,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           to[tid] = reinterpret_cast<char *>(k.w.o_c + cont * D);
         }
       }
-      if (!(ok = group_sync())) break;
+      if (!(ok = group_sync(s))) break;
       const bool bad = *reinterpret_cast<volatile unsigned *>(&s->nonfinite) == seg;
 #pragma unroll 1
       for (int cb = 0; cb < chunks; ++cb) {
@@ -564,7 +595,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       if (k.join_inside && !whole) {
         // the CTA that stores a cut unit's last part joins them, in their order
         const int owner = w.join & 0xffff, more = w.join >> 16;
-        if (!(ok = group_sync())) break;
+        if (!(ok = group_sync(s))) break;
         if (tid == 0) {
           __threadfence();  // what the CTA stored, ahead of the count
           const bool all = atomicAdd(&k.w.tickets[owner], 1u) == static_cast<unsigned>(more);
@@ -572,7 +603,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           s->joins = all;
           __threadfence();
         }
-        if (!(ok = group_sync())) break;
+        if (!(ok = group_sync(s))) break;
         if (s->joins) {
           for (int slot = warp; slot < w.rows; slot += 4) {
             const int token = slot / heads.n, qh = heads.first + slot - token * heads.n;
@@ -582,8 +613,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
         __syncwarp();
       }
-      // (the next segment's first weights are written behind a turn of `group`, and so behind all of this)
+      // (the next segment's first weights are written behind a turn of the barrier, and so behind all of this)
     }
+    if (s->abort) leave_group();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 4) {

@@ -61,7 +61,7 @@ struct Kernel8Args : WorkArgs {
 };
 
 constexpr float kTop = 15.f;      // weights are at most 2^kTop ...
-constexpr float kTopFresh = 11.f; // ... and the largest one 2^kTopFresh when the maximum is taken
+constexpr float kTopFresh = 9.f; // ... and the largest one 2^kTopFresh when the maximum is taken
 constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 
@@ -96,7 +96,9 @@ struct Tail8 {
   Seg8 seg[kSegs8];
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
-  int top[64];        // maxima of a tile, then factors
+  alignas(16) int top[64];  // maxima of a tile, then factors
+  float move[64];     // what a tile's scores move by
+  int unset;          // a row has seen nothing yet
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
   uint32_t tmem;
   volatile int abort;
@@ -174,6 +176,19 @@ __device__ __forceinline__ bool group_sync(Tail8 *s) {
   return !s->abort;
 }
 __device__ __forceinline__ void leave_group() { asm volatile("barrier.cta.arrive 1, 128;" ::: "memory"); }
+
+// Of a scale.  (Where log2's last bit is off, both a token's weight and what
+// its weight adds to the sum are by the same factor: a score off by 2^-22 of it.)
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // The order of floats in that of ints (and back: its own inverse).
 __device__ __forceinline__ int ordered(int bits) { return bits ^ (bits >> 31 & 0x7fffffff); }
@@ -338,6 +353,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
       }
       ++seg;
+      if (tid == 64) s->unset = 0;
       if (!(ok = group_sync(s))) break;
       warp_arrive(&s->q_taken, lane);
       unsigned long long l2[kPad / 2];  // sums of w / s_v, this thread's tokens
@@ -348,7 +364,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const uint32_t buf = tile & 1u, t_sb = t_s + buf * 64;
         const float sk = scale_of(ks), sv = scale_of(vs);
         const unsigned long long a2 = f2dup(k.sc * sk);
-        const float b = log2f(sv), c = kSumScale / sv;
+        const float b = fast_log2(sv), c = kSumScale * fast_rcp(sv);
         if (i + 1 < w.n) {
           from = scale_at(next);
           ks = ks_of[from];
@@ -370,8 +386,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           for (int cb = 0; cb < kChunks; ++cb) {
             if (cb < chunks) tmem_ld16(t_sb + cb * 16, z + cb * 16);
           }
+          float4 col[4];  // read ahead of their use
+#pragma unroll
+          for (int e = 0; e < 4; ++e) col[e] = s->col[e];
           tmem_wait_all();
-          hi = -INFINITY;
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int cb = 0; cb < kChunks; ++cb) {
             if (cb >= chunks) break;
@@ -379,10 +398,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const int r = cb * 16 + e;
-              const float4 col = s->col[r / 2];
               unsigned long long y = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])),
-                                          mul2(a2, f2pack(col.x, col.y)), b2);
-              if (past) y = add2(y, f2pack(col.z, col.w));  // (behind the same rounding as the maximum's)
+                                          mul2(a2, f2pack(col[e / 2 & 3].x, col[e / 2 & 3].y)), b2);
+              // (behind the same rounding as the maximum's)
+              if (past) y = add2(y, f2pack(col[e / 2 & 3].z, col[e / 2 & 3].w));
+              if (r + 8 < kRows) col[e / 2 & 3] = s->col[r / 2 + 4];
               float y0, y1;
               f2unpack(y, y0, y1);
               z[r] = __float_as_uint(y0);
@@ -397,9 +417,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             }
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              hi = fmaxf(fmaxf(hi, __uint_as_float(z[cb * 16 + e])), __uint_as_float(z[cb * 16 + e + 1]));
+              float &t = top[e / 2 & 3];
+              t = fmaxf(fmaxf(t, __uint_as_float(z[cb * 16 + e])), __uint_as_float(z[cb * 16 + e + 1]));
             }
           }
+          hi = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         };
         bool rise = i == 0;
         if (!rise) {
@@ -408,11 +430,17 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           if (!ok) break;
         }
         if (rise) {
-          // new maxima: of every row whose weights would pass 2^kTopFresh, while at it
+          // New maxima: of every row whose weights would pass 2^kTopFresh, while at it.  The tile's scores are moved
+          // by what `less` moves by; as long as a row is unset they are taken anew, without it.
+          const bool raw = i == 0 || *reinterpret_cast<volatile int *>(&s->unset);
+          if (!(ok = group_sync(s))) break;
           if (tid < 64) s->top[tid] = INT32_MIN;
+          if (tid == 64) s->unset = 0;
+          if (raw) {
 #pragma unroll
-          for (int r = 0; r < kPad; ++r) z[r] = 0xff800000u;
-          scores(false);
+            for (int r = 0; r < kPad; ++r) z[r] = 0xff800000u;
+            scores(false);
+          }
           if (!(ok = group_sync(s))) break;
 #pragma unroll
           for (int half = 0; half < kPad; half += 32) {
@@ -420,22 +448,35 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           }
           if (!(ok = group_sync(s))) break;
           if (tid < 64) {
-            float f = 1.f;
+            float f = 1.f, move = 0.f;
             if (tid < w.rows) {
               const float top = __int_as_float(ordered(s->top[tid]));
               float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);
-              if (top > -INFINITY && top + *less > kTopFresh) {
-                f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
-                const float fresh = kTopFresh - top;
-                *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
+              const float old = *less, base = raw ? 0.f : old, now = top + (raw ? old : 0.f);  // now: as a weight's exponent
+              float to = old;
+              if (top > -INFINITY && now > kTopFresh) {
+                to = base + (kTopFresh - top);
+                if (top + (to - base) > kTop) to = base - top;  // where a step of fp32 is more than kTop - kTopFresh
+                f = old == kUnset ? 0.f : fast_exp2(to - old);
+                *less = to;
               }
+              if (to == kUnset) s->unset = 1;
+              move = to - base;
             }
             s->top[tid] = __float_as_int(f);
+            s->move[tid] = move;
           }
           if (!(ok = group_sync(s))) break;
 #pragma unroll
-          for (int r = 0; r < kRows; r += 2) {
-            l2[r / 2] = mul2(l2[r / 2], f2pack(__int_as_float(s->top[r]), __int_as_float(s->top[r + 1])));
+          for (int r = 0; r < kRows; r += 4) {
+            const float4 move = *reinterpret_cast<const float4 *>(&s->move[r]);
+            const float4 f = *reinterpret_cast<const float4 *>(&s->top[r]);
+            l2[r / 2] = mul2(l2[r / 2], f2pack(f.x, f.y));
+            l2[r / 2 + 1] = mul2(l2[r / 2 + 1], f2pack(f.z, f.w));
+            z[r] = __float_as_uint(__uint_as_float(z[r]) + move.x);
+            z[r + 1] = __float_as_uint(__uint_as_float(z[r + 1]) + move.y);
+            z[r + 2] = __float_as_uint(__uint_as_float(z[r + 2]) + move.z);
+            z[r + 3] = __float_as_uint(__uint_as_float(z[r + 3]) + move.w);
           }
           if (i > 0) {  // the last product is in the accumulator
             if (!(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
@@ -455,7 +496,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             }
             tmem_wait_st();
           }
-          scores(true);
         }
         tc_fence_before();
         warp_arrive(&s->s_free[buf], lane);

@@ -60,7 +60,8 @@ struct Kernel8Args : WorkArgs {
   ScaleArgs sc8;
 };
 
-constexpr float kTop = 15.f;      // weights are at most 2^kTop ...
+constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: kTopHalf) ...
+constexpr uint32_t kTopHalf = 0x7800;
 constexpr float kTopFresh = 9.f; // ... and the largest one 2^kTopFresh when the maximum is taken
 constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
@@ -97,8 +98,6 @@ struct Tail8 {
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
   alignas(16) int top[64];  // maxima of a tile, then factors
-  float move[64];     // what a tile's scores move by
-  int unset;          // a row has seen nothing yet
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
   uint32_t tmem;
   volatile int abort;
@@ -248,16 +247,12 @@ __device__ __forceinline__ float transposed_sum(float *v) {
   return v[0];
 }
 
-// Their maximum likewise, NaN as -inf.
-__device__ __forceinline__ float transposed_max(const uint32_t *z) {
+// The maximum of v[0..15] over the warp's lanes, NaN as -inf; lane l gets that of v[l % 16].
+__device__ __forceinline__ float transposed_max(const uint32_t *x) {
   const int lane = threadIdx.x & 31;
   float v[16];
-  const bool up = lane & 16;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t send = up ? z[j] : z[j + 16], keep = up ? z[j + 16] : z[j];
-    v[j] = fmaxf(fmaxf(__uint_as_float(keep), __uint_as_float(__shfl_xor_sync(0xffffffffu, send, 16))), -INFINITY);
-  }
+  for (int j = 0; j < 16; ++j) v[j] = fmaxf(__uint_as_float(x[j]), -INFINITY);
 #pragma unroll
   for (int s = 8; s > 0; s >>= 1) {
     const bool up = lane & s;
@@ -267,7 +262,33 @@ __device__ __forceinline__ float transposed_max(const uint32_t *z) {
       v[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, s));
     }
   }
-  return v[0];
+  return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
+// A token's 128 bytes of a V tile: all become 0, or (not `all`) those that are
+// NaN, of which it says whether there were any.
+__device__ __forceinline__ bool clear_row8(char *row, bool all) {
+  bool found = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint4 *x16 = reinterpret_cast<uint4 *>(row) + ((e + threadIdx.x) & 7);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    bool change = all;
+    if (!all) {
+      x = *x16;
+      uint32_t *words = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t bad = __vcmpeq4(words[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (bad) {
+          words[j] &= ~bad;
+          change = found = true;
+        }
+      }
+    }
+    if (change) *x16 = x;
+  }
+  return found;
 }
 
 template <typename T, bool kTma>
@@ -290,9 +311,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->v_full[i], 1);
       mbar_init(&s->v_empty[i], 1);
       mbar_init(&s->s_full[i], 1);
-      mbar_init(&s->s_free[i], 4);
+      mbar_init(&s->s_free[i], 1);
     }
-    mbar_init(&s->p_full, 4);
+    mbar_init(&s->p_full, 1);
     mbar_init(&s->pv_done, 1);
     mbar_init(&s->q_full, 2);
     mbar_init(&s->q_free, 1);
@@ -353,7 +374,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
       }
       ++seg;
-      if (tid == 64) s->unset = 0;
       if (!(ok = group_sync(s))) break;
       warp_arrive(&s->q_taken, lane);
       unsigned long long l2[kPad / 2];  // sums of w / s_v, this thread's tokens
@@ -377,110 +397,129 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
         tc_fence_after();
         const unsigned long long b2 = f2dup(b), c2 = f2dup(c);
-        uint32_t z[kPad];
-        float hi;
-        // the rows' z + log2 s_v, less (with `past`) M and plus kTopFresh
-        auto scores = [&](bool past) {
-          __syncwarp();
+        // Weights are taken on trust that none passes 2^kTop, and written ahead of the vote that says so: the products
+        // start behind it.  Where a maximum has risen the tile is taken again.
+        uint32_t z[kRows];
+        for (bool known = i > 0;; known = true) {
+          if (known) {
+            __syncwarp();
 #pragma unroll
-          for (int cb = 0; cb < kChunks; ++cb) {
-            if (cb < chunks) tmem_ld16(t_sb + cb * 16, z + cb * 16);
-          }
-          float4 col[4];  // read ahead of their use
-#pragma unroll
-          for (int e = 0; e < 4; ++e) col[e] = s->col[e];
-          tmem_wait_all();
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int cb = 0; cb < kChunks; ++cb) {
-            if (cb >= chunks) break;
-            tmem_tie16(z + cb * 16);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int r = cb * 16 + e;
-              unsigned long long y = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])),
-                                          mul2(a2, f2pack(col[e / 2 & 3].x, col[e / 2 & 3].y)), b2);
-              // (behind the same rounding as the maximum's)
-              if (past) y = add2(y, f2pack(col[e / 2 & 3].z, col[e / 2 & 3].w));
-              if (r + 8 < kRows) col[e / 2 & 3] = s->col[r / 2 + 4];
-              float y0, y1;
-              f2unpack(y, y0, y1);
-              z[r] = __float_as_uint(y0);
-              z[r + 1] = __float_as_uint(y1);
+            for (int cb = 0; cb < kChunks; ++cb) {
+              if (cb < chunks) tmem_ld16(t_sb + cb * 16, z + cb * 16);
             }
-            if (edge) {
-              const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
+            float4 col[4];  // read ahead of their use
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (!(some >> e & 1)) z[cb * 16 + e] = 0xff800000u;
+            for (int e = 0; e < 4; ++e) col[e] = s->col[e];
+            // the weights' slots are free when the last product is done
+            if (tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+            tmem_wait_all();
+            uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
+#pragma unroll
+            for (int cb = 0; cb < kChunks; ++cb) {
+              if (cb >= chunks) break;
+              tmem_tie16(z + cb * 16);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const int r = cb * 16 + e;
+                unsigned long long y = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])),
+                                            mul2(a2, f2pack(col[e / 2 & 3].x, col[e / 2 & 3].y)), b2);
+                y = add2(y, f2pack(col[e / 2 & 3].z, col[e / 2 & 3].w));  // (behind the maximum's own rounding)
+                if (r + 8 < kRows) col[e / 2 & 3] = s->col[r / 2 + 4];
+                float y0, y1;
+                f2unpack(y, y0, y1);
+                z[r] = __float_as_uint(y0);
+                z[r + 1] = __float_as_uint(y1);
+              }
+              if (edge) {
+                const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  if (!(some >> e & 1)) z[cb * 16 + e] = 0xff800000u;
+                }
+              }
+              uint32_t h[8], p[4];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int r = cb * 16 + 2 * e;
+                const float w0 = fast_exp2(__uint_as_float(z[r])), w1 = fast_exp2(__uint_as_float(z[r + 1]));
+                z[r] = __float_as_uint(w0);
+                z[r + 1] = __float_as_uint(w1);
+                h[e] = pack2<__half>(w0, w1);
+                asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[e]));
+              }
+              // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
+#pragma unroll
+              for (int piece = 0; piece < 3; ++piece) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                  const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
+                  p[e / 2] = __byte_perm(u, v, 0x7531);
+                  if (piece < 2) {
+                    const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
+                    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(hu));
+                    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e + 1]) : "r"(hv));
+                  }
+                }
+                *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + cb * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
               }
             }
+            if (edge) {
+              // the tile reaches past the committed tokens: rows of V past the last
+              // token become 0 (they may hold anything), and so do NaN of new tokens,
+              // which patch_nan8 puts back
+              if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
+              if (at >= w.ctx && clear_row8(v_tile + buf * kTileBytes8 + tid * 128, at >= w.kv1)) s->nonfinite = seg;
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            const bool over = (most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf;
+            if (!group_any(s, over, &ok) || !ok) break;
+            tc_fence_after();
+          }
+          // New maxima, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest z + log2 s_v.
+          if (tid < 64) s->top[tid] = INT32_MIN;
+          if (!(ok = group_sync(s))) break;
+#pragma unroll 1
+          for (int cb = 0; cb < chunks; ++cb) {
+            uint32_t x[16];
+            __syncwarp();
+            tmem_ld16(t_sb + cb * 16, x);
+            tmem_wait_all();
+            tmem_tie16(x);
+            const uint32_t some = edge ? static_cast<uint32_t>(see >> (cb * 16)) : 0xffffu;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              float &t = top[e / 2 & 3];
-              t = fmaxf(fmaxf(t, __uint_as_float(z[cb * 16 + e])), __uint_as_float(z[cb * 16 + e + 1]));
+              const float4 col = s->col[cb * 8 + e / 2];
+              float y0, y1;
+              f2unpack(fma2(f2pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2(a2, f2pack(col.x, col.y)), b2), y0, y1);
+              x[e] = some >> e & 1 ? __float_as_uint(y0) : 0xff800000u;
+              x[e + 1] = some >> (e + 1) & 1 ? __float_as_uint(y1) : 0xff800000u;
             }
-          }
-          hi = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        };
-        bool rise = i == 0;
-        if (!rise) {
-          scores(true);
-          rise = group_any(s, hi > kTop, &ok);
-          if (!ok) break;
-        }
-        if (rise) {
-          // New maxima: of every row whose weights would pass 2^kTopFresh, while at it.  The tile's scores are moved
-          // by what `less` moves by; as long as a row is unset they are taken anew, without it.
-          const bool raw = i == 0 || *reinterpret_cast<volatile int *>(&s->unset);
-          if (!(ok = group_sync(s))) break;
-          if (tid < 64) s->top[tid] = INT32_MIN;
-          if (tid == 64) s->unset = 0;
-          if (raw) {
-#pragma unroll
-            for (int r = 0; r < kPad; ++r) z[r] = 0xff800000u;
-            scores(false);
-          }
-          if (!(ok = group_sync(s))) break;
-#pragma unroll
-          for (int half = 0; half < kPad; half += 32) {
-            if (half < w.rows) atomicMax(&s->top[half + lane], ordered(__float_as_int(transposed_max(z + half))));
+            const float top = transposed_max(x);
+            if (lane < 16) atomicMax(&s->top[cb * 16 + lane], ordered(__float_as_int(top)));
           }
           if (!(ok = group_sync(s))) break;
           if (tid < 64) {
-            float f = 1.f, move = 0.f;
+            float f = 1.f;
             if (tid < w.rows) {
               const float top = __int_as_float(ordered(s->top[tid]));
               float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);
-              const float old = *less, base = raw ? 0.f : old, now = top + (raw ? old : 0.f);  // now: as a weight's exponent
-              float to = old;
-              if (top > -INFINITY && now > kTopFresh) {
-                to = base + (kTopFresh - top);
-                if (top + (to - base) > kTop) to = base - top;  // where a step of fp32 is more than kTop - kTopFresh
-                f = old == kUnset ? 0.f : fast_exp2(to - old);
-                *less = to;
+              if (top > -INFINITY && top + *less > kTopFresh) {
+                f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
+                const float fresh = kTopFresh - top;
+                *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
               }
-              if (to == kUnset) s->unset = 1;
-              move = to - base;
             }
             s->top[tid] = __float_as_int(f);
-            s->move[tid] = move;
           }
           if (!(ok = group_sync(s))) break;
 #pragma unroll
           for (int r = 0; r < kRows; r += 4) {
-            const float4 move = *reinterpret_cast<const float4 *>(&s->move[r]);
             const float4 f = *reinterpret_cast<const float4 *>(&s->top[r]);
             l2[r / 2] = mul2(l2[r / 2], f2pack(f.x, f.y));
             l2[r / 2 + 1] = mul2(l2[r / 2 + 1], f2pack(f.z, f.w));
-            z[r] = __float_as_uint(__uint_as_float(z[r]) + move.x);
-            z[r + 1] = __float_as_uint(__uint_as_float(z[r + 1]) + move.y);
-            z[r + 2] = __float_as_uint(__uint_as_float(z[r + 2]) + move.z);
-            z[r + 3] = __float_as_uint(__uint_as_float(z[r + 3]) + move.w);
           }
-          if (i > 0) {  // the last product is in the accumulator
-            if (!(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
-            tc_fence_after();
+          if (i > 0) {  // the last product is in the accumulator, the weights' slots having been free
 #pragma unroll 1
             for (int cb = 0; cb < chunks; ++cb) {
               uint32_t o[16];
@@ -497,70 +536,21 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             tmem_wait_st();
           }
         }
-        tc_fence_before();
-        warp_arrive(&s->s_free[buf], lane);
-        // the weights' slots are free when the last product is done
-        if (tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+        if (!ok) break;
+        if (tid == 0) {  // behind the vote, for all
+          mbar_arrive(&s->p_full);
+          mbar_arrive(&s->s_free[buf]);
+        }
+        __syncwarp();
 #pragma unroll
         for (int cb = 0; cb < kChunks; ++cb) {
           if (cb >= chunks) break;
-          uint32_t h[8], p[4];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int r = cb * 16 + 2 * e;
-            const float w0 = fast_exp2(__uint_as_float(z[r])), w1 = fast_exp2(__uint_as_float(z[r + 1]));
-            l2[r / 2] = fma2(f2pack(w0, w1), c2, l2[r / 2]);
-            h[e] = pack2<__half>(w0, w1);
-          }
-          // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
-#pragma unroll
-          for (int piece = 0; piece < 3; ++piece) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
-              p[e / 2] = __byte_perm(u, v, 0x7531);
-              if (piece < 2) {
-                const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
-                asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(hu));
-                asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[e + 1]) : "r"(hv));
-              }
-            }
-            *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + cb * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
+            l2[r / 2] = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])), c2, l2[r / 2]);
           }
         }
-        if (edge) {
-          // the tile reaches past the committed tokens: rows of V past the last
-          // token become 0 (they may hold anything), and so do NaN of new tokens,
-          // which patch_nan8 puts back
-          if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
-          if (at >= w.ctx) {
-            uint4 *row = reinterpret_cast<uint4 *>(v_tile + buf * kTileBytes8 + tid * 128);
-            bool found = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint4 *x16 = row + ((e + lane) & 7);
-              uint4 x = make_uint4(0, 0, 0, 0);
-              bool change = at >= w.kv1;
-              if (!change) {
-                x = *x16;
-                uint32_t *words = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t bad = __vcmpeq4(words[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  if (bad) {
-                    words[j] &= ~bad;
-                    change = found = true;
-                  }
-                }
-              }
-              if (change) *x16 = x;
-            }
-            if (found) s->nonfinite = seg;
-          }
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        warp_arrive(&s->p_full, lane);
       }
       if (!ok) break;
       // ---- the unit's result --------------------------------------------------

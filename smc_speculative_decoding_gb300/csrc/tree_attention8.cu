@@ -35,7 +35,8 @@ namespace smcsd {
 constexpr int kTile8 = 128;    // tokens per tile
 constexpr int kMaxCtas8 = 384; // slots for continuations
 constexpr int kCtasPerSm = 2;
-constexpr int kThreads8 = 256;
+constexpr int kThreads8 = 384;
+constexpr int kSoftmax8 = 256;  // the first ones
 constexpr int kSegs8 = 4;      // segments found ahead
 constexpr int kTileBytes8 = kTile8 * 128;
 
@@ -67,14 +68,21 @@ constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in plac
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 
 // ---------------------------------------------------------------------------
-// attention8_kernel.  Two CTAs to a multiprocessor, each: warps 0-3 the softmax
-// (thread = token of a tile), warp 4 issues the matrix products, warp 5 finds
-// the CTA's segments (parts of units) and copies K and V, warps 6 and 7 cut the
-// next segment's rows of q into pieces.  Shared memory: two slots each of K and
-// V tiles, q's pieces, the weights' pieces.  Tensor memory: two tiles' scores
-// and the accumulator, 64 columns each.
-//   The scores of a tile are computed beside the softmax of the one before; one
-// CTA's waits are covered by the other's work.
+// attention8_kernel.  Two CTAs to a multiprocessor, each: warps 0-7 the softmax
+// (thread = token of a tile; warps w and w + 4 take the even and the odd chunks of
+// 16 rows), warp 8 issues the matrix products, warp 9 finds the CTA's segments
+// (parts of units) and copies K and V, warps 10 and 11 cut the next segment's
+// rows of q into pieces.  Shared memory: two slots each of K and V tiles, q's
+// pieces, the weights' pieces.  Tensor memory, 64 columns each: a tile's scores,
+// the accumulator, the sums of w / s_v (a token's share each) of the tile at hand
+// and of the one before.
+//   A softmax thread's loop takes 16 rows at a time and keeps nothing of them in
+// registers: the code is short (with 64 rows unrolled, and the sums in registers,
+// a tile took 5200 cycles, half of them without an instruction at hand) and 16
+// warps fit on a multiprocessor.  Weights are taken on trust that none passes
+// 2^kTop, and written ahead of the vote that says so; the products start behind
+// it.  Where a maximum has risen, the maxima are raised, what was summed up is
+// scaled, and the tile is taken again.
 //   Every wait is bounded, and on a barrier all of whose turns the waiting
 // thread follows.
 // ---------------------------------------------------------------------------
@@ -91,8 +99,8 @@ struct alignas(16) Seg8 {  // read and written in 16-byte words
 constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final result, first tiles, none left
 
 struct Tail8 {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_free[2];
-  uint64_t p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full, p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
   uint64_t seg_full[kSegs8], seg_empty[kSegs8];
   Seg8 seg[kSegs8];
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
@@ -153,7 +161,7 @@ __device__ __forceinline__ bool take_segment8(Tail8 *s, uint32_t seg, Seg8 *to, 
   return !(to->flags & kEnd8);
 }
 
-// The four softmax warps' barrier, and the vote on it.  A hardware barrier (30
+// The softmax warps' barrier, and the vote on it.  A hardware barrier (30
 // cycles against an mbarrier's 300) has no bound of its own; it is kept by this
 // rule: every warp looks at `abort` behind each turn and each wait, and one that
 // finds it set, or sets it, arrives once more (leave_group) and comes no more.
@@ -163,7 +171,7 @@ __device__ __forceinline__ bool group_any(Tail8 *s, bool mine, bool *ok) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
       : "r"(static_cast<uint32_t>(mine))
       : "memory");
@@ -171,10 +179,10 @@ __device__ __forceinline__ bool group_any(Tail8 *s, bool mine, bool *ok) {
   return any;
 }
 __device__ __forceinline__ bool group_sync(Tail8 *s) {
-  asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
   return !s->abort;
 }
-__device__ __forceinline__ void leave_group() { asm volatile("barrier.cta.arrive 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void leave_group() { asm volatile("barrier.cta.arrive 1, 256;" ::: "memory"); }
 
 // Of a scale.  (Where log2's last bit is off, both a token's weight and what
 // its weight adds to the sum are by the same factor: a score off by 2^-22 of it.)
@@ -232,11 +240,14 @@ __device__ __forceinline__ void patch_nan8(const WorkArgs &k, const Seg8 &w, con
   }
 }
 
-// Sums v[0..31] over the warp's lanes; lane l gets that of v[l].
-__device__ __forceinline__ float transposed_sum(float *v) {
+// Sums v[0..15] over the warp's lanes; lane l gets that of v[l % 16].
+__device__ __forceinline__ float transposed_sum(const uint32_t *x) {
   const int lane = threadIdx.x & 31;
+  float v[16];
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[j]);
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) {
     const bool up = lane & s;
 #pragma unroll
     for (int j = 0; j < s; ++j) {
@@ -244,7 +255,7 @@ __device__ __forceinline__ float transposed_sum(float *v) {
       v[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
     }
   }
-  return v[0];
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 // The maximum of v[0..15] over the warp's lanes, NaN as -inf; lane l gets that of v[l % 16].
@@ -265,13 +276,13 @@ __device__ __forceinline__ float transposed_max(const uint32_t *x) {
   return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// A token's 128 bytes of a V tile: all become 0, or (not `all`) those that are
-// NaN, of which it says whether there were any.
+// 64 of a token's 128 bytes of a V tile: all become 0, or (not `all`) those that
+// are NaN, of which it says whether there were any.
 __device__ __forceinline__ bool clear_row8(char *row, bool all) {
   bool found = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint4 *x16 = reinterpret_cast<uint4 *>(row) + ((e + threadIdx.x) & 7);
+  for (int e = 0; e < 4; ++e) {
+    uint4 *x16 = reinterpret_cast<uint4 *>(row) + ((e + threadIdx.x) & 3);
     uint4 x = make_uint4(0, 0, 0, 0);
     bool change = all;
     if (!all) {
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(kThreads8, kCtasPerSm)
 attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
   using M = Smem8<T>;
-  constexpr int kRows = Rows8<T>::kRows, kPieces = Rows8<T>::kPieces, kChunks = kRows / 16, kPad = (kRows + 31) / 32 * 32;
+  constexpr int kRows = Rows8<T>::kRows, kPieces = Rows8<T>::kPieces;
   extern __shared__ __align__(1024) char smem[];
   Tail8 *const s = reinterpret_cast<Tail8 *>(smem + M::kTail);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -310,27 +321,26 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->k_empty[i], 1);
       mbar_init(&s->v_full[i], 1);
       mbar_init(&s->v_empty[i], 1);
-      mbar_init(&s->s_full[i], 1);
-      mbar_init(&s->s_free[i], 1);
     }
+    mbar_init(&s->s_full, 1);
     mbar_init(&s->p_full, 1);
     mbar_init(&s->pv_done, 1);
     mbar_init(&s->q_full, 2);
     mbar_init(&s->q_free, 1);
-    mbar_init(&s->q_taken, 4);
+    mbar_init(&s->q_taken, 8);
     mbar_init(&s->o_full, 1);
-    mbar_init(&s->o_free, 4);
+    mbar_init(&s->o_free, 8);
     mbar_init(&s->drained, 1);
     for (int i = 0; i < kSegs8; ++i) {
       mbar_init(&s->seg_full[i], 1);
-      mbar_init(&s->seg_empty[i], 7);  // every warp but the one that fills it
+      mbar_init(&s->seg_empty[i], 11);  // every warp but the one that fills it
     }
     s->nonfinite = 0;
     s->abort = (smem_addr(smem) & 1023u) != 0;
     mbar_init_fence();
   }
-  if (warp == 4) tmem_alloc<256>(&s->tmem);
-  if (kTma && warp == 5 && elect_one()) {
+  if (warp == 8) tmem_alloc<256>(&s->tmem);
+  if (kTma && warp == 9 && elect_one()) {
     prefetch_map(&map_k);
     prefetch_map(&map_v);
   }
@@ -343,13 +353,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 
   if (s->abort) {
     if (tid == 0) raise_status(status, SMC_DEV_TIMEOUT);
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ---- softmax --------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t t_s = tmem + lanes, t_o = tmem + lanes + 128;
-    char *const p_at = smem + M::kP + (tid >> 3) * 128 + (tid & 7) * 16;
-    char *const v_tile = smem + M::kV;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int half = warp >> 2, token = tid & 127;  // chunks half, half + 2; token of a tile
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_s + 64;
+    uint32_t t_sum = t_s + 128, t_new = t_s + 192;  // sums before the tile at hand, and with it
+    char *const p_at = smem + M::kP + (token >> 3) * 128 + (token & 7) * 16;
     uint32_t seg = 0, tile = 0;
     bool ok = true;
     Seg8 w;
@@ -360,13 +370,21 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       const bool own = !(w.flags & kShared);
       const int t_end = min(w.t0 + w.n * kTile8, w.kv1);
       const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
-      // scales: of the tile at hand, of the next one the block (its table entry as it is read: looked at a tile later)
+      // scales: of the tile at hand, then of the next one, and of the one after it the block (its table entry as it
+      // is read: looked at a tile later)
       auto entry_at = [&](int t) { return t < t_end ? table[block_of(k, t)] : -1; };
-      auto scale_at = [&](int id) { return (id < 0 || id >= c8.blocks ? 0 : id) * k.sc8.block; };
-      const float *ks_of = k.sc8.k + heads.key * k.sc8.head, *vs_of = k.sc8.v + heads.key * k.sc8.head;
-      int at = w.t0 + tid, next = entry_at(at + kTile8);
+      auto scale_at = [&](int id) { return (id < 0 || id >= c8.blocks ? 0 : id) * k.sc8.block + heads.key * k.sc8.head; };
+      int at = w.t0 + token, next = entry_at(at + kTile8);
       int64_t from = scale_at(entry_at(at));
-      float ks = ks_of[from], vs = vs_of[from];
+      float ks = k.sc8.k[from], vs = k.sc8.v[from];
+      {
+        uint32_t zero[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero[e] = 0;
+        __syncwarp();
+        for (int cb = half; cb < chunks; cb += 2) tmem_st16(t_sum + cb * 16, zero);
+        tmem_wait_st();
+      }
       // the rows' scales and maxima
       if (!(ok = warp_wait8(s, &s->q_full, seg & 1u, status))) break;
       if (tid < 32) {
@@ -376,77 +394,68 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       ++seg;
       if (!(ok = group_sync(s))) break;
       warp_arrive(&s->q_taken, lane);
-      unsigned long long l2[kPad / 2];  // sums of w / s_v, this thread's tokens
-#pragma unroll
-      for (int i = 0; i < kPad / 2; ++i) l2[i] = 0;
 
       for (int i = 0; i < w.n; ++i, ++tile, at += kTile8) {
-        const uint32_t buf = tile & 1u, t_sb = t_s + buf * 64;
-        const float sk = scale_of(ks), sv = scale_of(vs);
-        const unsigned long long a2 = f2dup(k.sc * sk);
-        const float b = fast_log2(sv), c = kSumScale * fast_rcp(sv);
+        const float sv = scale_of(vs);
+        const unsigned long long a2 = f2dup(k.sc * scale_of(ks)), b2 = f2dup(fast_log2(sv)),
+                                 c2 = f2dup(kSumScale * fast_rcp(sv));
         if (i + 1 < w.n) {
           from = scale_at(next);
-          ks = ks_of[from];
-          vs = vs_of[from];
+          ks = k.sc8.k[from];
+          vs = k.sc8.v[from];
           next = entry_at(at + 2 * kTile8);
         }
-        const int t0 = w.t0 + i * kTile8;
-        const bool edge = own && t0 + kTile8 > w.ctx;
-        const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : 0;
-        if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
+        const bool edge = own && w.t0 + (i + 1) * kTile8 > w.ctx;
+        const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : ~0ull;
+        if (!(ok = warp_wait8(s, &s->s_full, tile & 1u, status))) break;
         tc_fence_after();
-        const unsigned long long b2 = f2dup(b), c2 = f2dup(c);
-        // Weights are taken on trust that none passes 2^kTop, and written ahead of the vote that says so: the products
-        // start behind it.  Where a maximum has risen the tile is taken again.
-        uint32_t z[kRows];
         for (bool known = i > 0;; known = true) {
           if (known) {
-            __syncwarp();
-#pragma unroll
-            for (int cb = 0; cb < kChunks; ++cb) {
-              if (cb < chunks) tmem_ld16(t_sb + cb * 16, z + cb * 16);
-            }
-            float4 col[4];  // read ahead of their use
-#pragma unroll
-            for (int e = 0; e < 4; ++e) col[e] = s->col[e];
             // the weights' slots are free when the last product is done
             if (tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
-            tmem_wait_all();
             uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
-#pragma unroll
-            for (int cb = 0; cb < kChunks; ++cb) {
-              if (cb >= chunks) break;
-              tmem_tie16(z + cb * 16);
+#pragma unroll 1
+            for (int cb = half; cb < chunks; cb += 2) {
+              uint32_t z[16], sum[16];
+              __syncwarp();
+              tmem_ld16(t_s + cb * 16, z);
+              tmem_ld16(t_sum + cb * 16, sum);
+              const float4 *col = s->col + cb * 8;
+              tmem_wait_all();
+              tmem_tie16(z);
+              tmem_tie16(sum);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                const int r = cb * 16 + e;
-                unsigned long long y = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])),
-                                            mul2(a2, f2pack(col[e / 2 & 3].x, col[e / 2 & 3].y)), b2);
-                y = add2(y, f2pack(col[e / 2 & 3].z, col[e / 2 & 3].w));  // (behind the maximum's own rounding)
-                if (r + 8 < kRows) col[e / 2 & 3] = s->col[r / 2 + 4];
+                const float4 c = col[e / 2];
+                unsigned long long y = fma2(f2pack(__uint_as_float(z[e]), __uint_as_float(z[e + 1])),
+                                            mul2(a2, f2pack(c.x, c.y)), b2);
+                y = add2(y, f2pack(c.z, c.w));  // (behind the maximum's own rounding)
                 float y0, y1;
                 f2unpack(y, y0, y1);
-                z[r] = __float_as_uint(y0);
-                z[r + 1] = __float_as_uint(y1);
+                z[e] = __float_as_uint(y0);
+                z[e + 1] = __float_as_uint(y1);
               }
               if (edge) {
                 const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  if (!(some >> e & 1)) z[cb * 16 + e] = 0xff800000u;
+                  if (!(some >> e & 1)) z[e] = 0xff800000u;
                 }
               }
               uint32_t h[8], p[4];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int r = cb * 16 + 2 * e;
-                const float w0 = fast_exp2(__uint_as_float(z[r])), w1 = fast_exp2(__uint_as_float(z[r + 1]));
-                z[r] = __float_as_uint(w0);
-                z[r + 1] = __float_as_uint(w1);
+                const float w0 = fast_exp2(__uint_as_float(z[2 * e])), w1 = fast_exp2(__uint_as_float(z[2 * e + 1]));
                 h[e] = pack2<__half>(w0, w1);
+                float s0, s1;
+                f2unpack(fma2(f2pack(w0, w1), c2, f2pack(__uint_as_float(sum[2 * e]), __uint_as_float(sum[2 * e + 1]))),
+                         s0, s1);
+                sum[2 * e] = __float_as_uint(s0);
+                sum[2 * e + 1] = __float_as_uint(s1);
                 asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[e]));
               }
+              __syncwarp();
+              tmem_st16(t_new + cb * 16, sum);
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
 #pragma unroll
               for (int piece = 0; piece < 3; ++piece) {
@@ -467,10 +476,15 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               // the tile reaches past the committed tokens: rows of V past the last
               // token become 0 (they may hold anything), and so do NaN of new tokens,
               // which patch_nan8 puts back
-              if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
-              if (at >= w.ctx && clear_row8(v_tile + buf * kTileBytes8 + tid * 128, at >= w.kv1)) s->nonfinite = seg;
+              const uint32_t slot = tile & 1u;
+              if (!(ok = warp_wait8(s, &s->v_full[slot], tile >> 1 & 1u, status))) break;
+              if (at >= w.ctx && clear_row8(smem + M::kV + slot * kTileBytes8 + token * 128 + half * 64, at >= w.kv1)) {
+                s->nonfinite = seg;
+              }
             }
             fence_proxy_async_smem();
+            __syncwarp();
+            tmem_wait_st();
             tc_fence_before();
             const bool over = (most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf;
             if (!group_any(s, over, &ok) || !ok) break;
@@ -480,18 +494,18 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           if (tid < 64) s->top[tid] = INT32_MIN;
           if (!(ok = group_sync(s))) break;
 #pragma unroll 1
-          for (int cb = 0; cb < chunks; ++cb) {
+          for (int cb = half; cb < chunks; cb += 2) {
             uint32_t x[16];
             __syncwarp();
-            tmem_ld16(t_sb + cb * 16, x);
+            tmem_ld16(t_s + cb * 16, x);
             tmem_wait_all();
             tmem_tie16(x);
-            const uint32_t some = edge ? static_cast<uint32_t>(see >> (cb * 16)) : 0xffffu;
+            const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float4 col = s->col[cb * 8 + e / 2];
+              const float4 c = s->col[cb * 8 + e / 2];
               float y0, y1;
-              f2unpack(fma2(f2pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2(a2, f2pack(col.x, col.y)), b2), y0, y1);
+              f2unpack(fma2(f2pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2(a2, f2pack(c.x, c.y)), b2), y0, y1);
               x[e] = some >> e & 1 ? __float_as_uint(y0) : 0xff800000u;
               x[e + 1] = some >> (e + 1) & 1 ? __float_as_uint(y1) : 0xff800000u;
             }
@@ -513,44 +527,34 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             s->top[tid] = __float_as_int(f);
           }
           if (!(ok = group_sync(s))) break;
-#pragma unroll
-          for (int r = 0; r < kRows; r += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(&s->top[r]);
-            l2[r / 2] = mul2(l2[r / 2], f2pack(f.x, f.y));
-            l2[r / 2 + 1] = mul2(l2[r / 2 + 1], f2pack(f.z, f.w));
-          }
-          if (i > 0) {  // the last product is in the accumulator, the weights' slots having been free
+          if (i > 0) {  // (the last product is in the accumulator: the weights' slots were free)
 #pragma unroll 1
-            for (int cb = 0; cb < chunks; ++cb) {
-              uint32_t o[16];
+            for (int cb = half; cb < chunks; cb += 2) {
+              uint32_t o[16], sum[16];
               __syncwarp();
               tmem_ld16(t_o + cb * 16, o);
+              tmem_ld16(t_sum + cb * 16, sum);
               tmem_wait_all();
               tmem_tie16(o);
+              tmem_tie16(sum);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * __int_as_float(s->top[cb * 16 + e]));
+                const float f = __int_as_float(s->top[cb * 16 + e]);
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                sum[e] = __float_as_uint(__uint_as_float(sum[e]) * f);
               }
               tmem_st16(t_o + cb * 16, o);
+              tmem_st16(t_sum + cb * 16, sum);
             }
             tmem_wait_st();
           }
         }
         if (!ok) break;
-        if (tid == 0) {  // behind the vote, for all
-          mbar_arrive(&s->p_full);
-          mbar_arrive(&s->s_free[buf]);
-        }
+        if (tid == 0) mbar_arrive(&s->p_full);  // behind the vote, for all: the scores have been read, too
         __syncwarp();
-#pragma unroll
-        for (int cb = 0; cb < kChunks; ++cb) {
-          if (cb >= chunks) break;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = cb * 16 + 2 * e;
-            l2[r / 2] = fma2(f2pack(__uint_as_float(z[r]), __uint_as_float(z[r + 1])), c2, l2[r / 2]);
-          }
-        }
+        const uint32_t before = t_sum;
+        t_sum = t_new;
+        t_new = before;
       }
       if (!ok) break;
       // ---- the unit's result --------------------------------------------------
@@ -559,20 +563,22 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       // (the weights' slots are free: the sums of four warps, factors and rows' addresses)
       float *const sums = reinterpret_cast<float *>(smem + M::kP), *const inverse = sums + 4 * 64;
       char **const to = reinterpret_cast<char **>(inverse + 64);
-#pragma unroll
-      for (int r0 = 0; r0 < kRows; r0 += 32) {
-        if (r0 >= w.rows) break;
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) f2unpack(l2[r0 / 2 + e], v[2 * e], v[2 * e + 1]);
-        sums[warp * 64 + r0 + lane] = transposed_sum(v);
+#pragma unroll 1
+      for (int cb = half; cb < chunks; cb += 2) {
+        uint32_t x[16];
+        __syncwarp();
+        tmem_ld16(t_sum + cb * 16, x);
+        tmem_wait_all();
+        tmem_tie16(x);
+        const float sum = transposed_sum(x);
+        if (lane < 16) sums[(warp & 3) * 64 + cb * 16 + lane] = sum;
       }
       if (!(ok = group_sync(s))) break;
       const bool whole = w.flags & kWhole8, base = w.flags & kBase8;
       const int kind = own ? 0 : 1;
       if (tid < w.rows) {
         const float l = (sums[tid] + sums[64 + tid]) + (sums[128 + tid] + sums[192 + tid]);
-        const int token = tid / heads.n, row = w.row0 + token, qh = heads.first + tid - token * heads.n;
+        const int in = tid / heads.n, row = w.row0 + in, qh = heads.first + tid - in * heads.n;
         const int64_t rh = static_cast<int64_t>(row) * k.a.q_heads + qh;
         const int64_t cont = static_cast<int64_t>(blockIdx.x) * kRows + tid;
         const float less = *(reinterpret_cast<const float *>(&s->col[tid >> 1]) + 2 + (tid & 1));
@@ -592,34 +598,35 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       if (!(ok = group_sync(s))) break;
       const bool bad = *reinterpret_cast<volatile unsigned *>(&s->nonfinite) == seg;
 #pragma unroll 1
-      for (int cb = 0; cb < chunks; ++cb) {
+      for (int cb = half; cb < chunks; cb += 2) {
         uint32_t o[16];
         __syncwarp();
         tmem_ld16(t_o + cb * 16, o);
         tmem_wait_all();
         tmem_tie16(o);
-        if (cb + 1 == chunks) {  // the accumulator may be written again
-          tc_fence_before();
-          warp_arrive(&s->o_free, lane);
-        }
-        if (tid < D) {
+        if (token < D) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int r = cb * 16 + e;
             if (r < w.rows) {
-              const float x = inverse[r] == 0.f ? 0.f : __uint_as_float(o[e]) * inverse[r];
+              const float f = inverse[r], x = f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
               if (whole) {
-                reinterpret_cast<T *>(to[r])[tid] = from_f32<T>(x);
+                reinterpret_cast<T *>(to[r])[token] = from_f32<T>(x);
               } else {
-                reinterpret_cast<float *>(to[r])[tid] = x;
+                reinterpret_cast<float *>(to[r])[token] = x;
               }
             }
           }
         }
       }
-      if (bad && tid < D) {
-        if (whole) patch_nan8<T>(k, w, heads, tid, to);
-        else patch_nan8<float>(k, w, heads, tid, to);
+      tc_fence_before();
+      warp_arrive(&s->o_free, lane);  // the accumulator may be written again
+      if (bad) {
+        if (!(ok = group_sync(s))) break;  // both halves' rows are written
+        if (tid < D) {
+          if (whole) patch_nan8<T>(k, w, heads, tid, to);
+          else patch_nan8<float>(k, w, heads, tid, to);
+        }
       }
       __syncwarp();
       if (k.join_inside && !whole) {
@@ -635,10 +642,10 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
         if (!(ok = group_sync(s))) break;
         if (s->joins) {
-          for (int slot = warp; slot < w.rows; slot += 4) {
-            const int token = slot / heads.n, qh = heads.first + slot - token * heads.n;
-            const int64_t rh = static_cast<int64_t>(w.row0 + token) * k.a.q_heads + qh;
-            write_row<T>(k, rh, w.row0 + token, qh, join_parts<Units8<T>>(k, 0, rh, owner, more, slot));
+          for (int slot = warp; slot < w.rows; slot += 8) {
+            const int in = slot / heads.n, qh = heads.first + slot - in * heads.n;
+            const int64_t rh = static_cast<int64_t>(w.row0 + in) * k.a.q_heads + qh;
+            write_row<T>(k, rh, w.row0 + in, qh, join_parts<Units8<T>>(k, 0, rh, owner, more, slot));
           }
         }
         __syncwarp();
@@ -647,8 +654,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     }
     if (s->abort) leave_group();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 8) {
       // ---- matrix products ----------------------------------------------------
       const int k_steps = (D + 31) / 32;
       const uint32_t k0 = smem_desc(smem_addr(smem + M::kK), 16), v0 = smem_desc(smem_addr(smem + M::kV), 16);
@@ -664,12 +671,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const int n = w.n, columns = (w.rows + 15) & ~15;
         const uint32_t id_s = instr_desc8(columns, false, false, false), id_o = instr_desc8(columns, true, true, true);
         if (elect_one()) {
-          auto scores = [&](int i) {
+          auto scores = [&](int i) {  // the last ones have been read
             const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
-            // (the first turn of a fresh barrier passes for the one before it)
-            if (!wait8(s, &s->s_free[at], turn ^ 1u, status) || !wait8(s, &s->k_full[at], turn, status)) {
-              return false;
-            }
+            if (!wait8(s, &s->k_full[at], turn, status)) return false;
             tc_fence_after();
             const uint32_t ka = k0 + at * (kTileBytes8 >> 4);
 #pragma unroll
@@ -677,33 +681,31 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 if (c < k_steps) {
-                  mma8_ss(tmem + at * 64, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
+                  mma8_ss(tmem, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
                           piece > 0 || c > 0);
                 }
               }
             }
-            tc_commit(&s->s_full[at]);
+            tc_commit(&s->s_full);
             tc_commit(&s->k_empty[at]);
             if (i + 1 == n) tc_commit(&s->q_free);
             return true;
           };
           ok = wait8(s, &s->q_full, seg & 1u, status) && scores(0);
           for (int i = 0; ok && i < n; ++i) {
+            if (!(ok = wait8(s, &s->p_full, (tile + i) & 1u, status))) break;
             if (i + 1 < n && !(ok = scores(i + 1))) break;
             // the last segment's result has been read
             if (i == 0 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
             const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
-            if (!(ok = wait8(s, &s->v_full[at], turn, status) &&
-                       wait8(s, &s->p_full, (tile + i) & 1u, status))) {
-              break;
-            }
+            if (!(ok = wait8(s, &s->v_full[at], turn, status))) break;
             tc_fence_after();
             const uint32_t va = v0 + at * (kTileBytes8 >> 4);
 #pragma unroll
             for (int piece = 0; piece < 3; ++piece) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                mma8_ss(tmem + 128, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
+                mma8_ss(tmem + 64, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
                         i > 0 || piece > 0 || c > 0);
               }
             }
@@ -721,7 +723,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(status, SMC_DEV_TIMEOUT);
       }
       __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 9) {
       // ---- segments, K and V ----------------------------------------------------
       Walk<Units8<T>> walk;
       walk.start(k);
@@ -847,65 +849,73 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       if (bits) raise_status(status, bits);
     } else {
       // ---- q's pieces -----------------------------------------------------------
-      const int r = tid - 192;  // row of the unit
+      // four lanes to a row, 32 dims each; 16 rows at a time, and the next ones' loads under way
+      const int part = tid & 3, r_in = (tid - 320) >> 2;
       uint32_t seg = 0;
       bool ok = true;
       Seg8 w;
       while (ok && take_segment8(s, seg, &w, status)) {
         warp_arrive(&s->seg_empty[seg % kSegs8], lane);
         const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
-        const bool live = r < w.rows;
-        const int token = live ? r / heads.n : 0, qh = heads.first + (live ? r - token * heads.n : 0);
-        const uint4 *q = reinterpret_cast<const uint4 *>(
-            k.a.q + ((w.row0 + token) * k.a.q_row + qh * k.a.q_head) * static_cast<int64_t>(sizeof(T)));
-        float top = 0.f;
-        if (live) {
-#pragma unroll 4
-          for (int e = 0; e < D / 8; ++e) {
-            const uint4 v = q[e];
-            const T *x = reinterpret_cast<const T *>(&v);
+        uint4 v[4];
+        auto fetch = [&](int r) {
+          const int in = r / heads.n, qh = heads.first + r - in * heads.n;
+          const uint4 *q = reinterpret_cast<const uint4 *>(
+              k.a.q + ((w.row0 + in) * k.a.q_row + qh * k.a.q_head) * static_cast<int64_t>(sizeof(T)));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float a = fabsf(to_f32(x[j]));
-              if (a < INFINITY) top = fmaxf(top, a);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const bool has = r < w.rows && part * 4 + e < D / 8;
+            v[e] = has ? q[part * 4 + e] : make_uint4(0, 0, 0, 0);
           }
-        }
-        const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
+        };
+        fetch(r_in);
         // the rows before have been read: their scales, and their pieces by the last scores
         if (seg > 0 && !(ok = warp_wait8(s, &s->q_taken, (seg - 1) & 1u, status) &&
                               warp_wait8(s, &s->q_free, (seg - 1) & 1u, status))) {
           break;
         }
-        if (r < ((w.rows + 15) & ~15)) {
-          char *to = smem + M::kQ + r * 128;
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {
+#pragma unroll 1
+        for (int r = r_in; r < 64; r += 16) {
+          if (r - r_in >= w.rows) {  // (for the whole warp)
+            if (part == 0) s->q_scale[r] = 0.f;
+            continue;
+          }
+          const uint4 now[4] = {v[0], v[1], v[2], v[3]};
+          if (r - r_in + 16 < w.rows) fetch(r + 16);
+          const T *x = reinterpret_cast<const T *>(now);
+          float top = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float a = fabsf(to_f32(x[j]));
+            if (a < INFINITY) top = fmaxf(top, a);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
+          char *const to = smem + M::kQ + r * 128;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             uint32_t words[kPieces][4] = {};
-            if (live && c * 16 < D) {
-              const uint4 v[2] = {q[2 * c], q[2 * c + 1]};
-              const T *x = reinterpret_cast<const T *>(v);
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float a = finite_or_nan(to_f32(x[j])) * inv, b = finite_or_nan(to_f32(x[j + 1])) * inv;
+            for (int j = 0; j < 16; j += 2) {
+              float a = finite_or_nan(to_f32(x[c * 16 + j])) * inv, b = finite_or_nan(to_f32(x[c * 16 + j + 1])) * inv;
 #pragma unroll
-                for (int piece = 0; piece < kPieces; ++piece) {
-                  const uint32_t e = to_e4m3x2(a, b), h = from_e4m3x2(e);
-                  words[piece][j / 4] |= e << (j & 2) * 8;
-                  const float2 taken = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                  a -= taken.x;
-                  b -= taken.y;
-                }
+              for (int piece = 0; piece < kPieces; ++piece) {
+                const uint32_t e = to_e4m3x2(a, b), h = from_e4m3x2(e);
+                words[piece][j / 4] |= e << (j & 2) * 8;
+                const float2 taken = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                a -= taken.x;
+                b -= taken.y;
               }
             }
 #pragma unroll
             for (int piece = 0; piece < kPieces; ++piece) {
-              *reinterpret_cast<uint4 *>(to + piece * M::kPiece + ((c ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4 *>(to + piece * M::kPiece + (((part * 2 + c) ^ (r & 7)) << 4)) =
                   make_uint4(words[piece][0], words[piece][1], words[piece][2], words[piece][3]);
             }
           }
+          if (part == 0) s->q_scale[r] = r < w.rows ? scale : 0.f;
         }
-        s->q_scale[r] = live ? scale : 0.f;
         fence_proxy_async_smem();
         warp_arrive(&s->q_full, lane);
         ++seg;
@@ -913,7 +923,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     }
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_free<256>(tmem);
   }

@@ -73,16 +73,15 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // 16 rows), warp 8 issues the matrix products, warp 9 finds the CTA's segments
 // (parts of units) and copies K and V, warps 10 and 11 cut the next segment's
 // rows of q into pieces.  Shared memory: two slots each of K and V tiles, q's
-// pieces, the weights' pieces.  Tensor memory, 64 columns each: a tile's scores,
-// the accumulator, the sums of w / s_v (a token's share each) of the tile at hand
-// and of the one before.
+// pieces, the weights' pieces.  Tensor memory, 64 columns each: two tiles'
+// scores, the accumulator, the sums of w / s_v (each lane's tokens').
 //   A softmax thread's loop takes 16 rows at a time and keeps nothing of them in
 // registers: the code is short (with 64 rows unrolled, and the sums in registers,
 // a tile took 5200 cycles, half of them without an instruction at hand) and 16
 // warps fit on a multiprocessor.  Weights are taken on trust that none passes
 // 2^kTop, and written ahead of the vote that says so; the products start behind
-// it.  Where a maximum has risen, the maxima are raised, what was summed up is
-// scaled, and the tile is taken again.
+// it.  Where a maximum has risen, what the tile added to the sums is taken off
+// again, maxima, sums and accumulator are brought up, and the tile is taken anew.
 //   Every wait is bounded, and on a barrier all of whose turns the waiting
 // thread follows.
 // ---------------------------------------------------------------------------
@@ -100,7 +99,7 @@ constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final resul
 
 struct Tail8 {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full, p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
+  uint64_t s_full[2], p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
   uint64_t seg_full[kSegs8], seg_empty[kSegs8];
   Seg8 seg[kSegs8];
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
@@ -321,8 +320,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->k_empty[i], 1);
       mbar_init(&s->v_full[i], 1);
       mbar_init(&s->v_empty[i], 1);
+      mbar_init(&s->s_full[i], 1);
     }
-    mbar_init(&s->s_full, 1);
     mbar_init(&s->p_full, 1);
     mbar_init(&s->pv_done, 1);
     mbar_init(&s->q_full, 2);
@@ -357,8 +356,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     // ---- softmax --------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int half = warp >> 2, token = tid & 127;  // chunks half, half + 2; token of a tile
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_s + 64;
-    uint32_t t_sum = t_s + 128, t_new = t_s + 192;  // sums before the tile at hand, and with it
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_lane + 128, t_sum = t_lane + 192;
     char *const p_at = smem + M::kP + (token >> 3) * 128 + (token & 7) * 16;
     uint32_t seg = 0, tile = 0;
     bool ok = true;
@@ -407,12 +405,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
         const bool edge = own && w.t0 + (i + 1) * kTile8 > w.ctx;
         const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : ~0ull;
-        if (!(ok = warp_wait8(s, &s->s_full, tile & 1u, status))) break;
+        const uint32_t t_s = t_lane + (tile & 1u) * 64;
+        if (!(ok = warp_wait8(s, &s->s_full[tile & 1u], tile >> 1 & 1u, status))) break;
         tc_fence_after();
         for (bool known = i > 0;; known = true) {
           if (known) {
-            // the weights' slots are free when the last product is done
-            if (tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
             uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
@@ -455,7 +452,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[e]));
               }
               __syncwarp();
-              tmem_st16(t_new + cb * 16, sum);
+              tmem_st16(t_sum + cb * 16, sum);
+              // the weights' slots are free when the last product is done
+              if (cb == half && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
 #pragma unroll
               for (int piece = 0; piece < 3; ++piece) {
@@ -472,6 +471,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + cb * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
               }
             }
+            if (!ok) break;
             if (edge) {
               // the tile reaches past the committed tokens: rows of V past the last
               // token become 0 (they may hold anything), and so do NaN of new tokens,
@@ -491,27 +491,41 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             tc_fence_after();
           }
           // New maxima, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest z + log2 s_v.
+          // What the tile added to the sums is taken off again; where that was so much (2^60 and more) that nothing
+          // before it counts beside the row's largest weight, 0 is left.
           if (tid < 64) s->top[tid] = INT32_MIN;
           if (!(ok = group_sync(s))) break;
 #pragma unroll 1
           for (int cb = half; cb < chunks; cb += 2) {
-            uint32_t x[16];
+            uint32_t x[16], sum[16];
             __syncwarp();
             tmem_ld16(t_s + cb * 16, x);
+            tmem_ld16(t_sum + cb * 16, sum);
             tmem_wait_all();
             tmem_tie16(x);
+            tmem_tie16(sum);
             const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const float4 c = s->col[cb * 8 + e / 2];
-              float y0, y1;
-              f2unpack(fma2(f2pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2(a2, f2pack(c.x, c.y)), b2), y0, y1);
+              const unsigned long long y =
+                  fma2(f2pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2(a2, f2pack(c.x, c.y)), b2);
+              float y0, y1, w0, w1, s0, s1;
+              f2unpack(y, y0, y1);
+              f2unpack(add2(y, f2pack(c.z, c.w)), w0, w1);
               x[e] = some >> e & 1 ? __float_as_uint(y0) : 0xff800000u;
               x[e + 1] = some >> (e + 1) & 1 ? __float_as_uint(y1) : 0xff800000u;
+              w0 = some >> e & 1 ? fast_exp2(w0) : 0.f;
+              w1 = some >> (e + 1) & 1 ? fast_exp2(w1) : 0.f;
+              f2unpack(fma2(f2pack(-w0, -w1), c2, f2pack(__uint_as_float(sum[e]), __uint_as_float(sum[e + 1]))), s0, s1);
+              sum[e] = w0 > 0x1p60f ? 0u : __float_as_uint(s0);
+              sum[e + 1] = w1 > 0x1p60f ? 0u : __float_as_uint(s1);
             }
+            if (known) tmem_st16(t_sum + cb * 16, sum);
             const float top = transposed_max(x);
             if (lane < 16) atomicMax(&s->top[cb * 16 + lane], ordered(__float_as_int(top)));
           }
+          tmem_wait_st();
           if (!(ok = group_sync(s))) break;
           if (tid < 64) {
             float f = 1.f;
@@ -552,9 +566,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         if (!ok) break;
         if (tid == 0) mbar_arrive(&s->p_full);  // behind the vote, for all: the scores have been read, too
         __syncwarp();
-        const uint32_t before = t_sum;
-        t_sum = t_new;
-        t_new = before;
       }
       if (!ok) break;
       // ---- the unit's result --------------------------------------------------
@@ -671,7 +682,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const int n = w.n, columns = (w.rows + 15) & ~15;
         const uint32_t id_s = instr_desc8(columns, false, false, false), id_o = instr_desc8(columns, true, true, true);
         if (elect_one()) {
-          auto scores = [&](int i) {  // the last ones have been read
+          auto scores = [&](int i) {  // the last ones of its buffer have been read
             const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
             if (!wait8(s, &s->k_full[at], turn, status)) return false;
             tc_fence_after();
@@ -681,20 +692,19 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 if (c < k_steps) {
-                  mma8_ss(tmem, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
+                  mma8_ss(tmem + at * 64, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
                           piece > 0 || c > 0);
                 }
               }
             }
-            tc_commit(&s->s_full);
+            tc_commit(&s->s_full[at]);
             tc_commit(&s->k_empty[at]);
             if (i + 1 == n) tc_commit(&s->q_free);
             return true;
           };
-          ok = wait8(s, &s->q_full, seg & 1u, status) && scores(0);
+          ok = wait8(s, &s->q_full, seg & 1u, status) && scores(0) && (n == 1 || scores(1));
           for (int i = 0; ok && i < n; ++i) {
             if (!(ok = wait8(s, &s->p_full, (tile + i) & 1u, status))) break;
-            if (i + 1 < n && !(ok = scores(i + 1))) break;
             // the last segment's result has been read
             if (i == 0 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
             const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
@@ -705,12 +715,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             for (int piece = 0; piece < 3; ++piece) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                mma8_ss(tmem + 64, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
+                mma8_ss(tmem + 128, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
                         i > 0 || piece > 0 || c > 0);
               }
             }
             tc_commit(&s->v_empty[at]);
             tc_commit(&s->pv_done);
+            if (i + 2 < n && !(ok = scores(i + 2))) break;
           }
           if (ok) tc_commit(&s->o_full);
         }

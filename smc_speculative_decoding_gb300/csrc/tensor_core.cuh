@@ -141,6 +141,34 @@ __device__ __forceinline__ void tmem_tie(uint32_t *r) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// The same as pairs, two times 16 columns, there when it returns.  In one
+// statement and in 64 bits: packed arithmetic takes the pairs where the loads put
+// them, while pairs made of loads that are waited for apart were moved first
+// (a third of a softmax loop's instructions).
+#define SMC_L8(r) "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7])
+__device__ __forceinline__ void tmem_get16x2(uint32_t a, uint32_t b, unsigned long long *x, unsigned long long *y) {
+  asm volatile(
+      "{\n\t.reg .b32 a<16>, b<16>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {b0, b1, b2, b3, b4, b5, b6, b7, b8, b9, b10, b11, b12, b13, b14, b15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {a0, a1};\n\tmov.b64 %1, {a2, a3};\n\tmov.b64 %2, {a4, a5};\n\tmov.b64 %3, {a6, a7};\n\t"
+      "mov.b64 %4, {a8, a9};\n\tmov.b64 %5, {a10, a11};\n\tmov.b64 %6, {a12, a13};\n\tmov.b64 %7, {a14, a15};\n\t"
+      "mov.b64 %8, {b0, b1};\n\tmov.b64 %9, {b2, b3};\n\tmov.b64 %10, {b4, b5};\n\tmov.b64 %11, {b6, b7};\n\t"
+      "mov.b64 %12, {b8, b9};\n\tmov.b64 %13, {b10, b11};\n\tmov.b64 %14, {b12, b13};\n\tmov.b64 %15, {b14, b15};\n\t}"
+      : SMC_L8(x), SMC_L8(y)
+      : "r"(a), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t addr, const unsigned long long *x) {
+  asm volatile(
+      "{\n\t.reg .b32 a<16>;\n\t"
+      "mov.b64 {a0, a1}, %1;\n\tmov.b64 {a2, a3}, %2;\n\tmov.b64 {a4, a5}, %3;\n\tmov.b64 {a6, a7}, %4;\n\t"
+      "mov.b64 {a8, a9}, %5;\n\tmov.b64 {a10, a11}, %6;\n\tmov.b64 {a12, a13}, %7;\n\tmov.b64 {a14, a15}, %8;\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15};\n\t}" ::"r"(addr),
+      "l"(x[0]), "l"(x[1]), "l"(x[2]), "l"(x[3]), "l"(x[4]), "l"(x[5]), "l"(x[6]), "l"(x[7])
+      : "memory");
+}
 // kind::f16 with 128 rows, n columns, fp32 accumulators; b_mn: B is stored
 // with its n axis contiguous.
 __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn) {

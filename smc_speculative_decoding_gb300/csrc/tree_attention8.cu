@@ -135,6 +135,7 @@ __device__ __forceinline__ void give_up(Tail8 *s, unsigned *status) {
   raise_status(status, SMC_DEV_TIMEOUT);
 }
 __device__ __forceinline__ bool wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (s->abort) return false;
@@ -144,6 +145,7 @@ __device__ __forceinline__ bool wait8(Tail8 *s, uint64_t *bar, uint32_t parity, 
 }
 // A whole warp, in step.
 __device__ __forceinline__ bool warp_wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, s->abort)) return false;
@@ -413,46 +415,38 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
-              uint32_t z[16], sum[16];
+              unsigned long long z[8], sum[8];
               __syncwarp();
-              tmem_ld16(t_s + cb * 16, z);
-              tmem_ld16(t_sum + cb * 16, sum);
+              tmem_get16x2(t_s + cb * 16, t_sum + cb * 16, z, sum);
               const float4 *col = s->col + cb * 8;
-              tmem_wait_all();
-              tmem_tie16(z);
-              tmem_tie16(sum);
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float4 c = col[e / 2];
-                unsigned long long y = fma2(f2pack(__uint_as_float(z[e]), __uint_as_float(z[e + 1])),
-                                            mul2(a2, f2pack(c.x, c.y)), b2);
-                y = add2(y, f2pack(c.z, c.w));  // (behind the maximum's own rounding)
-                float y0, y1;
-                f2unpack(y, y0, y1);
-                z[e] = __float_as_uint(y0);
-                z[e + 1] = __float_as_uint(y1);
+              for (int e = 0; e < 8; ++e) {
+                const float4 c = col[e];
+                // (less M behind the maximum's own rounding)
+                z[e] = add2(fma2(z[e], mul2(a2, f2pack(c.x, c.y)), b2), f2pack(c.z, c.w));
               }
               if (edge) {
                 const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  if (!(some >> e & 1)) z[e] = 0xff800000u;
+                for (int e = 0; e < 8; ++e) {
+                  float y0, y1;
+                  f2unpack(z[e], y0, y1);
+                  z[e] = f2pack(some >> 2 * e & 1 ? y0 : -INFINITY, some >> (2 * e + 1) & 1 ? y1 : -INFINITY);
                 }
               }
               uint32_t h[8], p[4];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float w0 = fast_exp2(__uint_as_float(z[2 * e])), w1 = fast_exp2(__uint_as_float(z[2 * e + 1]));
+                float w0, w1;
+                f2unpack(z[e], w0, w1);
+                w0 = fast_exp2(w0);
+                w1 = fast_exp2(w1);
                 h[e] = pack2<__half>(w0, w1);
-                float s0, s1;
-                f2unpack(fma2(f2pack(w0, w1), c2, f2pack(__uint_as_float(sum[2 * e]), __uint_as_float(sum[2 * e + 1]))),
-                         s0, s1);
-                sum[2 * e] = __float_as_uint(s0);
-                sum[2 * e + 1] = __float_as_uint(s1);
+                sum[e] = fma2(f2pack(w0, w1), c2, sum[e]);
                 asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[e]));
               }
               __syncwarp();
-              tmem_st16(t_sum + cb * 16, sum);
+              tmem_put16(t_sum + cb * 16, sum);
               // the weights' slots are free when the last product is done
               if (cb == half && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step

@@ -98,10 +98,11 @@ struct alignas(16) Seg8 {  // read and written in 16-byte words
 constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final result, first tiles, none left
 
 struct Tail8 {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], scales_full[2];
   uint64_t s_full[2], p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
   uint64_t seg_full[kSegs8], seg_empty[kSegs8];
   Seg8 seg[kSegs8];
+  float4 token[2][kTile8];  // of a tile's tokens: scale * log2 e * s_k, log2 s_v, kSumScale / s_v
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
   alignas(16) int top[64];  // maxima of a tile, then factors
@@ -322,6 +323,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->k_empty[i], 1);
       mbar_init(&s->v_full[i], 1);
       mbar_init(&s->v_empty[i], 1);
+      mbar_init(&s->scales_full[i], 1);
       mbar_init(&s->s_full[i], 1);
     }
     mbar_init(&s->p_full, 1);
@@ -368,15 +370,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
       const int chunks = (w.rows + 15) >> 4;
       const bool own = !(w.flags & kShared);
-      const int t_end = min(w.t0 + w.n * kTile8, w.kv1);
-      const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
-      // scales: of the tile at hand, then of the next one, and of the one after it the block (its table entry as it
-      // is read: looked at a tile later)
-      auto entry_at = [&](int t) { return t < t_end ? table[block_of(k, t)] : -1; };
-      auto scale_at = [&](int id) { return (id < 0 || id >= c8.blocks ? 0 : id) * k.sc8.block + heads.key * k.sc8.head; };
-      int at = w.t0 + token, next = entry_at(at + kTile8);
-      int64_t from = scale_at(entry_at(at));
-      float ks = k.sc8.k[from], vs = k.sc8.v[from];
+      int at = w.t0 + token;
       {
         uint32_t zero[16];
 #pragma unroll
@@ -396,19 +390,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       warp_arrive(&s->q_taken, lane);
 
       for (int i = 0; i < w.n; ++i, ++tile, at += kTile8) {
-        const float sv = scale_of(vs);
-        const unsigned long long a2 = f2dup(k.sc * scale_of(ks)), b2 = f2dup(fast_log2(sv)),
-                                 c2 = f2dup(kSumScale * fast_rcp(sv));
-        if (i + 1 < w.n) {
-          from = scale_at(next);
-          ks = k.sc8.k[from];
-          vs = k.sc8.v[from];
-          next = entry_at(at + 2 * kTile8);
-        }
         const bool edge = own && w.t0 + (i + 1) * kTile8 > w.ctx;
         const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : ~0ull;
-        const uint32_t t_s = t_lane + (tile & 1u) * 64;
-        if (!(ok = warp_wait8(s, &s->s_full[tile & 1u], tile >> 1 & 1u, status))) break;
+        const uint32_t buf = tile & 1u, t_s = t_lane + buf * 64;
+        if (!(ok = warp_wait8(s, &s->scales_full[buf], tile >> 1 & 1u, status))) break;
+        const float4 scales = s->token[buf][token];
+        const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
+        if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
         tc_fence_after();
         for (bool known = i > 0;; known = true) {
           if (known) {
@@ -470,9 +458,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               // the tile reaches past the committed tokens: rows of V past the last
               // token become 0 (they may hold anything), and so do NaN of new tokens,
               // which patch_nan8 puts back
-              const uint32_t slot = tile & 1u;
-              if (!(ok = warp_wait8(s, &s->v_full[slot], tile >> 1 & 1u, status))) break;
-              if (at >= w.ctx && clear_row8(smem + M::kV + slot * kTileBytes8 + token * 128 + half * 64, at >= w.kv1)) {
+              if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
+              if (at >= w.ctx && clear_row8(smem + M::kV + buf * kTileBytes8 + token * 128 + half * 64, at >= w.kv1)) {
                 s->nonfinite = seg;
               }
             }
@@ -774,7 +761,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           return make_int2(id, t - slot * c8.block_size);
         };
         // places of 32 boxes, a lane each, and of the 32 after them
-        const int per_tile = kTile8 / k.box;
+        const int box_log2 = 31 - __clz(k.box), per_tile = kTile8 >> box_log2;
         int2 here = make_int2(0, 0), ahead = make_int2(0, 0);
         int from = -32;
         if constexpr (kTma) {
@@ -784,6 +771,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           const uint32_t slot = tile & 1u, turn = tile >> 1 & 1u;
           const int t0 = w.t0 + i * kTile8, t1 = min(t0 + kTile8, t_end);
           char *const to_k = smem + M::kK + slot * kTileBytes8, *const to_v = smem + M::kV + slot * kTileBytes8;
+          // scales of tokens lane, lane + 32, ...: on their way while slots are waited for
+          float ks[4], vs[4];
+          auto scales_of = [&](int e, int block) {
+            const int64_t from = block * k.sc8.block + head * k.sc8.head;
+            ks[e] = k.sc8.k[from];
+            vs[e] = k.sc8.v[from];
+          };
           if constexpr (kTma) {
             if ((i + 1) * per_tile > from + 32) {
               from = i * per_tile;
@@ -793,6 +787,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             }
             const int boxes = (t1 - t0 + k.box - 1) / k.box, mine = i * per_tile - from + lane;
             const int block = __shfl_sync(0xffffffffu, here.x, mine & 31), token = __shfl_sync(0xffffffffu, here.y, mine & 31);
+            // (a token past the last one has its box's block, or the one of some box before: a block of the cache)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              scales_of(e, __shfl_sync(0xffffffffu, here.x, (i * per_tile - from + ((lane + 32 * e) >> box_log2)) & 31));
+            }
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
               uint64_t *full = which ? &s->v_full[slot] : &s->k_full[slot];
@@ -809,8 +808,10 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             int64_t off[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (t0 + lane + 32 * e < t1) {
-                const int2 p = place(t0 + lane + 32 * e);
+              const bool in = t0 + lane + 32 * e < t1;
+              const int2 p = in ? place(t0 + lane + 32 * e) : make_int2(0, 0);
+              scales_of(e, p.x);
+              if (in) {
                 off[e] = p.x * c8.block_stride + p.y * c8.token_stride + head * c8.head_stride;
               }
             }
@@ -843,6 +844,13 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
           }
           if (!ok) break;
+          // (V's slot is free when all of the softmax has read the scales of its last tile)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float sv = scale_of(vs[e]);
+            s->token[slot][lane + 32 * e] = make_float4(k.sc * scale_of(ks[e]), fast_log2(sv), kSumScale * fast_rcp(sv), 0.f);
+          }
+          warp_arrive(&s->scales_full[slot], lane);
         }
       }
       if (kTma && s->abort) {  // copies that may be under way

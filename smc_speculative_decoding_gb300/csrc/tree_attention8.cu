@@ -63,7 +63,7 @@ struct Kernel8Args : WorkArgs {
 
 constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: kTopHalf) ...
 constexpr uint32_t kTopHalf = 0x7800;
-constexpr float kTopFresh = 9.f; // ... and the largest one 2^kTopFresh when the maximum is taken
+constexpr float kTopFresh = 7.f; // ... and the largest one 2^kTopFresh when the maximum is taken
 constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 
@@ -98,14 +98,15 @@ struct alignas(16) Seg8 {  // read and written in 16-byte words
 constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final result, first tiles, none left
 
 struct Tail8 {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], scales_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
-  uint64_t seg_full[kSegs8], seg_empty[kSegs8];
+  uint64_t seg_full[kSegs8], seg_empty[kSegs8], group;
   Seg8 seg[kSegs8];
   float4 token[2][kTile8];  // of a tile's tokens: scale * log2 e * s_k, log2 s_v, kSumScale / s_v
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
   alignas(16) int top[64];  // maxima of a tile, then factors
+  uint32_t rise[2];   // the last vote (from 1) that said yes, of even and of odd ones
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
   uint32_t tmem;
   volatile int abort;
@@ -163,29 +164,6 @@ __device__ __forceinline__ bool take_segment8(Tail8 *s, uint32_t seg, Seg8 *to, 
   return !(to->flags & kEnd8);
 }
 
-// The softmax warps' barrier, and the vote on it.  A hardware barrier (30
-// cycles against an mbarrier's 300) has no bound of its own; it is kept by this
-// rule: every warp looks at `abort` behind each turn and each wait, and one that
-// finds it set, or sets it, arrives once more (leave_group) and comes no more.
-// A warp that saw nothing behind turn n so finds the others' arrivals at turn
-// n + 1; they are behind the flag, so it leaves there, and no one waits at n + 2.
-__device__ __forceinline__ bool group_any(Tail8 *s, bool mine, bool *ok) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(static_cast<uint32_t>(mine))
-      : "memory");
-  *ok = !s->abort;
-  return any;
-}
-__device__ __forceinline__ bool group_sync(Tail8 *s) {
-  asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
-  return !s->abort;
-}
-__device__ __forceinline__ void leave_group() { asm volatile("barrier.cta.arrive 1, 256;" ::: "memory"); }
-
 // Of a scale.  (Where log2's last bit is off, both a token's weight and what
 // its weight adds to the sum are by the same factor: a score off by 2^-22 of it.)
 __device__ __forceinline__ float fast_log2(float x) {
@@ -204,13 +182,16 @@ __device__ __forceinline__ int ordered(int bits) { return bits ^ (bits >> 31 & 0
 
 // Which rows of a unit see token `at` (at or past w.ctx): bits [i * heads, (i + 1)
 // * heads) for new token w.i0 + i.
-__device__ __forceinline__ uint64_t rows_that_see(const WorkArgs &k, const Seg8 &w, int heads, int at) {
+template <typename T>
+__device__ __forceinline__ uint64_t rows_that_see(const WorkArgs &k, const Seg8 &w, int at) {
   if (at < w.ctx) return ~0ull;
   if (at >= w.kv1) return 0;
+  const int heads = unit_heads<Units8<T>>(k, w.head).n;
   const int j = at - w.ctx, tokens = w.rows / heads, word = j >> 5;
   const uint64_t one = heads >= 64 ? ~0ull : (1ull << heads) - 1;
   uint64_t see = 0;
   if (!k.a.mask) {  // a chain: new tokens j and later
+#pragma unroll 1
     for (int i = max(j - w.i0, 0); i < tokens; ++i) see |= one << (i * heads);
     return see;
   }
@@ -225,19 +206,25 @@ __device__ __forceinline__ uint64_t rows_that_see(const WorkArgs &k, const Seg8 
 
 // Rows that see a new token whose element d of v is NaN get NaN there: the
 // products met it as 0.
-template <typename Out>
-__device__ __forceinline__ void patch_nan8(const WorkArgs &k, const Seg8 &w, const UnitHeads &heads, int d, char *const *to) {
+template <typename T>
+__device__ __forceinline__ void patch_nan8(const WorkArgs &k, const Seg8 &w, const UnitHeads &heads, int d, char *const *to,
+                                           bool whole) {
   const int32_t *table = k.a.b.tables + static_cast<int64_t>(w.seq) * k.a.b.T;
   const int t1 = min(w.t0 + w.n * kTile8, w.kv1);
+#pragma unroll 1
   for (int at = max(w.t0, w.ctx); at < t1; ++at) {
     const int block = table[block_of(k, at)];
     if (block < 0 || block >= k.a.c.blocks) continue;
     const char *v = k.a.c.v + block * k.a.c.block_stride + (at % k.a.c.block_size) * k.a.c.token_stride +
                     heads.key * k.a.c.head_stride;
     if ((v[d] & 0x7f) != 0x7f) continue;
-    const uint64_t see = rows_that_see(k, w, heads.n, at);
+    const uint64_t see = rows_that_see<T>(k, w, at);
+#pragma unroll 1
     for (int r = 0; r < w.rows; ++r) {
-      if (see >> r & 1) reinterpret_cast<Out *>(to[r])[d] = from_f32<Out>(__uint_as_float(0x7fffffffu));
+      if (!(see >> r & 1)) continue;
+      const float nan = __uint_as_float(0x7fffffffu);
+      if (whole) reinterpret_cast<T *>(to[r])[d] = from_f32<T>(nan);
+      else reinterpret_cast<float *>(to[r])[d] = nan;
     }
   }
 }
@@ -323,8 +310,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       mbar_init(&s->k_empty[i], 1);
       mbar_init(&s->v_full[i], 1);
       mbar_init(&s->v_empty[i], 1);
-      mbar_init(&s->scales_full[i], 1);
-      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->s_full[i], 2);  // the products, and the tokens' scales
     }
     mbar_init(&s->p_full, 1);
     mbar_init(&s->pv_done, 1);
@@ -334,6 +320,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     mbar_init(&s->o_full, 1);
     mbar_init(&s->o_free, 8);
     mbar_init(&s->drained, 1);
+    mbar_init(&s->group, 8);
+    s->rise[0] = s->rise[1] = 0;
     for (int i = 0; i < kSegs8; ++i) {
       mbar_init(&s->seg_full[i], 1);
       mbar_init(&s->seg_empty[i], 11);  // every warp but the one that fills it
@@ -362,14 +350,27 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     const int half = warp >> 2, token = tid & 127;  // chunks half, half + 2; token of a tile
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_lane + 128, t_sum = t_lane + 192;
     char *const p_at = smem + M::kP + (token >> 3) * 128 + (token & 7) * 16;
-    uint32_t seg = 0, tile = 0;
+    uint32_t seg = 0, tile = 0, turns = 0;
     bool ok = true;
-    Seg8 w;
-    while (ok && take_segment8(s, seg, &w, status)) {
-      warp_arrive(&s->seg_empty[seg % kSegs8], lane);
-      const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
+    // all softmax warps, and whether any of them says so
+    auto group_any = [&](bool mine) {
+      volatile uint32_t *const rise = &s->rise[turns & 1u];
+      ++turns;
+      if (__any_sync(0xffffffffu, mine) && lane == 0) *rise = turns;
+      warp_arrive(&s->group, lane);
+      ok = warp_wait8(s, &s->group, (turns - 1) & 1u, status);
+      return *rise == turns;
+    };
+    auto group_sync = [&] {
+      warp_arrive(&s->group, lane);
+      ++turns;
+      return warp_wait8(s, &s->group, (turns - 1) & 1u, status);
+    };
+    while (ok && warp_wait8(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) {
+      const Seg8 &w = s->seg[seg % kSegs8];  // (released behind the segment: what is rarely looked at stays there)
+      if (w.flags & kEnd8) break;
+      const int tiles = w.n, ctx = w.flags & kShared ? INT32_MAX : w.ctx, kv1 = w.kv1;
       const int chunks = (w.rows + 15) >> 4;
-      const bool own = !(w.flags & kShared);
       int at = w.t0 + token;
       {
         uint32_t zero[16];
@@ -386,18 +387,18 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
       }
       ++seg;
-      if (!(ok = group_sync(s))) break;
+      if (!(ok = group_sync())) break;
       warp_arrive(&s->q_taken, lane);
 
-      for (int i = 0; i < w.n; ++i, ++tile, at += kTile8) {
-        const bool edge = own && w.t0 + (i + 1) * kTile8 > w.ctx;
-        const uint64_t see = edge ? rows_that_see(k, w, heads.n, at) : ~0ull;
+      for (int i = 0; i < tiles; ++i, ++tile, at += kTile8) {
+        const bool edge = at - token + kTile8 > ctx;
+        const uint64_t see = edge ? rows_that_see<T>(k, w, at) : ~0ull;
         const uint32_t buf = tile & 1u, t_s = t_lane + buf * 64;
-        if (!(ok = warp_wait8(s, &s->scales_full[buf], tile >> 1 & 1u, status))) break;
-        const float4 scales = s->token[buf][token];
-        const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
         if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
         tc_fence_after();
+        const float4 scales = s->token[buf][token];
+        const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
+        bool again = false;  // at most once
         for (bool known = i > 0;; known = true) {
           if (known) {
             uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
@@ -414,6 +415,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 z[e] = add2(fma2(z[e], mul2(a2, f2pack(c.x, c.y)), b2), f2pack(c.z, c.w));
               }
               if (edge) {
+                asm volatile("" ::: "memory");  // a branch: as selects it took every tile a third more instructions
                 const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -459,7 +461,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               // token become 0 (they may hold anything), and so do NaN of new tokens,
               // which patch_nan8 puts back
               if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
-              if (at >= w.ctx && clear_row8(smem + M::kV + buf * kTileBytes8 + token * 128 + half * 64, at >= w.kv1)) {
+              if (at >= ctx && clear_row8(smem + M::kV + buf * kTileBytes8 + token * 128 + half * 64, at >= kv1)) {
                 s->nonfinite = seg;
               }
             }
@@ -468,14 +470,15 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             tmem_wait_st();
             tc_fence_before();
             const bool over = (most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf;
-            if (!group_any(s, over, &ok) || !ok) break;
+            if (!group_any(over && !again) || !ok) break;
             tc_fence_after();
+            again = true;
           }
           // New maxima, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest z + log2 s_v.
           // What the tile added to the sums is taken off again; where that was so much (2^60 and more) that nothing
           // before it counts beside the row's largest weight, 0 is left.
           if (tid < 64) s->top[tid] = INT32_MIN;
-          if (!(ok = group_sync(s))) break;
+          if (!(ok = group_sync())) break;
 #pragma unroll 1
           for (int cb = half; cb < chunks; cb += 2) {
             uint32_t x[16], sum[16];
@@ -507,7 +510,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             if (lane < 16) atomicMax(&s->top[cb * 16 + lane], ordered(__float_as_int(top)));
           }
           tmem_wait_st();
-          if (!(ok = group_sync(s))) break;
+          if (!(ok = group_sync())) break;
           if (tid < 64) {
             float f = 1.f;
             if (tid < w.rows) {
@@ -521,7 +524,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             }
             s->top[tid] = __float_as_int(f);
           }
-          if (!(ok = group_sync(s))) break;
+          if (!(ok = group_sync())) break;
           if (i > 0) {  // (the last product is in the accumulator: the weights' slots were free)
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
@@ -565,9 +568,10 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const float sum = transposed_sum(x);
         if (lane < 16) sums[(warp & 3) * 64 + cb * 16 + lane] = sum;
       }
-      if (!(ok = group_sync(s))) break;
+      if (!(ok = group_sync())) break;
+      const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
       const bool whole = w.flags & kWhole8, base = w.flags & kBase8;
-      const int kind = own ? 0 : 1;
+      const int kind = w.flags & kShared ? 1 : 0;
       if (tid < w.rows) {
         const float l = (sums[tid] + sums[64 + tid]) + (sums[128 + tid] + sums[192 + tid]);
         const int in = tid / heads.n, row = w.row0 + in, qh = heads.first + tid - in * heads.n;
@@ -587,7 +591,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           to[tid] = reinterpret_cast<char *>(k.w.o_c + cont * D);
         }
       }
-      if (!(ok = group_sync(s))) break;
+      if (!(ok = group_sync())) break;
       const bool bad = *reinterpret_cast<volatile unsigned *>(&s->nonfinite) == seg;
 #pragma unroll 1
       for (int cb = half; cb < chunks; cb += 2) {
@@ -614,17 +618,14 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       tc_fence_before();
       warp_arrive(&s->o_free, lane);  // the accumulator may be written again
       if (bad) {
-        if (!(ok = group_sync(s))) break;  // both halves' rows are written
-        if (tid < D) {
-          if (whole) patch_nan8<T>(k, w, heads, tid, to);
-          else patch_nan8<float>(k, w, heads, tid, to);
-        }
+        if (!(ok = group_sync())) break;  // both halves' rows are written
+        if (tid < D) patch_nan8<T>(k, w, heads, tid, to, whole);
       }
       __syncwarp();
       if (k.join_inside && !whole) {
         // the CTA that stores a cut unit's last part joins them, in their order
         const int owner = w.join & 0xffff, more = w.join >> 16;
-        if (!(ok = group_sync(s))) break;
+        if (!(ok = group_sync())) break;
         if (tid == 0) {
           __threadfence();  // what the CTA stored, ahead of the count
           const bool all = atomicAdd(&k.w.tickets[owner], 1u) == static_cast<unsigned>(more);
@@ -632,7 +633,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           s->joins = all;
           __threadfence();
         }
-        if (!(ok = group_sync(s))) break;
+        if (!(ok = group_sync())) break;
         if (s->joins) {
           for (int slot = warp; slot < w.rows; slot += 8) {
             const int in = slot / heads.n, qh = heads.first + slot - in * heads.n;
@@ -642,9 +643,12 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
         __syncwarp();
       }
-      // (the next segment's first weights are written behind a turn of the barrier, and so behind all of this)
+      // (the next segment's first weights are written behind a turn of `group`, and so behind all of this)
+      warp_arrive(&s->seg_empty[(seg - 1) % kSegs8], lane);
     }
-    if (s->abort) leave_group();
+    __syncwarp();
+    tmem_wait_all();  // (a warp that gave up may have left some under way)
+    tmem_wait_st();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8) {
@@ -663,46 +667,45 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const int n = w.n, columns = (w.rows + 15) & ~15;
         const uint32_t id_s = instr_desc8(columns, false, false, false), id_o = instr_desc8(columns, true, true, true);
         if (elect_one()) {
-          auto scores = [&](int i) {  // the last ones of its buffer have been read
-            const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
-            if (!wait8(s, &s->k_full[at], turn, status)) return false;
-            tc_fence_after();
-            const uint32_t ka = k0 + at * (kTileBytes8 >> 4);
+          // the scores of tile i, then the product with V of the tile before
+          ok = wait8(s, &s->q_full, seg & 1u, status);
+          for (int i = 0; ok && i <= n; ++i) {
+            if (i < n) {  // (their buffer's last ones have been read: the weights of two tiles ago were there)
+              const uint32_t at = (tile + i) & 1u;
+              if (!(ok = wait8(s, &s->k_full[at], (tile + i) >> 1 & 1u, status))) break;
+              tc_fence_after();
+              const uint32_t ka = k0 + at * (kTileBytes8 >> 4);
+#pragma unroll 1
+              for (int piece = 0; piece < kPieces; ++piece) {
 #pragma unroll
-            for (int piece = 0; piece < kPieces; ++piece) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if (c < k_steps) {
-                  mma8_ss(tmem + at * 64, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
-                          piece > 0 || c > 0);
+                for (int c = 0; c < 4; ++c) {
+                  if (c < k_steps) {
+                    mma8_ss(tmem + at * 64, ka + c * 32 / 16, q0 + (piece * M::kPiece + c * 32) / 16, kDescHigh, id_s,
+                            piece > 0 || c > 0);
+                  }
                 }
               }
+              tc_commit(&s->s_full[at]);
+              tc_commit(&s->k_empty[at]);
+              if (i + 1 == n) tc_commit(&s->q_free);
             }
-            tc_commit(&s->s_full[at]);
-            tc_commit(&s->k_empty[at]);
-            if (i + 1 == n) tc_commit(&s->q_free);
-            return true;
-          };
-          ok = wait8(s, &s->q_full, seg & 1u, status) && scores(0) && (n == 1 || scores(1));
-          for (int i = 0; ok && i < n; ++i) {
-            if (!(ok = wait8(s, &s->p_full, (tile + i) & 1u, status))) break;
+            if (i == 0) continue;
+            const uint32_t last = tile + i - 1, at = last & 1u;
             // the last segment's result has been read
-            if (i == 0 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
-            const uint32_t at = (tile + i) & 1u, turn = (tile + i) >> 1 & 1u;
-            if (!(ok = wait8(s, &s->v_full[at], turn, status))) break;
+            if (i == 1 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
+            if (!(ok = wait8(s, &s->v_full[at], last >> 1 & 1u, status) && wait8(s, &s->p_full, last & 1u, status))) break;
             tc_fence_after();
             const uint32_t va = v0 + at * (kTileBytes8 >> 4);
-#pragma unroll
+#pragma unroll 1
             for (int piece = 0; piece < 3; ++piece) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 mma8_ss(tmem + 128, va + c * 4096 / 16, p0 + (piece * M::kPiece + c * 512) / 16, kHighP, id_o,
-                        i > 0 || piece > 0 || c > 0);
+                        i > 1 || piece > 0 || c > 0);
               }
             }
             tc_commit(&s->v_empty[at]);
             tc_commit(&s->pv_done);
-            if (i + 2 < n && !(ok = scores(i + 2))) break;
           }
           if (ok) tc_commit(&s->o_full);
         }
@@ -850,7 +853,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             const float sv = scale_of(vs[e]);
             s->token[slot][lane + 32 * e] = make_float4(k.sc * scale_of(ks[e]), fast_log2(sv), kSumScale * fast_rcp(sv), 0.f);
           }
-          warp_arrive(&s->scales_full[slot], lane);
+          warp_arrive(&s->s_full[slot], lane);
         }
       }
       if (kTma && s->abort) {  // copies that may be under way

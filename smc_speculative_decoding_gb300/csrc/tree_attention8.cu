@@ -106,7 +106,7 @@ struct Tail8 {
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
   float q_scale[64];  // of the next segment's rows
   alignas(16) int top[64];  // maxima of a tile, then factors
-  uint32_t rise[2];   // the last vote (from 1) that said yes, of even and of odd ones
+  uint32_t rise[3];   // chunks of 16 rows in which a weight passed 2^kTop, of three votes
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
   uint32_t tmem;
   volatile int abort;
@@ -321,7 +321,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     mbar_init(&s->o_free, 8);
     mbar_init(&s->drained, 1);
     mbar_init(&s->group, 8);
-    s->rise[0] = s->rise[1] = 0;
+    s->rise[0] = s->rise[1] = s->rise[2] = 0;
     for (int i = 0; i < kSegs8; ++i) {
       mbar_init(&s->seg_full[i], 1);
       mbar_init(&s->seg_empty[i], 11);  // every warp but the one that fills it
@@ -350,16 +350,20 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     const int half = warp >> 2, token = tid & 127;  // chunks half, half + 2; token of a tile
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_lane + 128, t_sum = t_lane + 192;
     char *const p_at = smem + M::kP + (token >> 3) * 128 + (token & 7) * 16;
-    uint32_t seg = 0, tile = 0, turns = 0;
+    uint32_t seg = 0, tile = 0, turns = 0, votes = 0;
     bool ok = true;
-    // all softmax warps, and whether any of them says so
-    auto group_any = [&](bool mine) {
-      volatile uint32_t *const rise = &s->rise[turns & 1u];
-      ++turns;
-      if (__any_sync(0xffffffffu, mine) && lane == 0) *rise = turns;
+    // all softmax warps, and the bits that any of them names.  Vote v goes into word v % 3, which was cleared behind
+    // vote v - 2: all had read it then, and no one writes it before the one who clears it has come to vote v - 1.
+    auto group_or = [&](uint32_t mine) {
+      uint32_t *const word = s->rise + votes;
+      if (mine) atomicOr(word, mine);
       warp_arrive(&s->group, lane);
+      ++turns;
       ok = warp_wait8(s, &s->group, (turns - 1) & 1u, status);
-      return *rise == turns;
+      const uint32_t all = *reinterpret_cast<volatile uint32_t *>(word);
+      votes = votes == 2 ? 0 : votes + 1;
+      if (tid == 0) s->rise[votes == 2 ? 0 : votes + 1] = 0;  // word v + 2 = v - 1
+      return all;
     };
     auto group_sync = [&] {
       warp_arrive(&s->group, lane);
@@ -398,12 +402,14 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         tc_fence_after();
         const float4 scales = s->token[buf][token];
         const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
-        bool again = false;  // at most once
-        for (bool known = i > 0;; known = true) {
+        uint32_t todo = ~0u;  // chunks to take; at first all, then those with a new maximum (once)
+        for (bool known = i > 0, again = false;; known = true) {
           if (known) {
-            uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
+            uint32_t over = 0;
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
+              if (!(todo >> cb & 1)) continue;
+              uint32_t most = 0;  // the largest weights, fp16, of even and of odd rows
               unsigned long long z[8], sum[8];
               __syncwarp();
               tmem_get16x2(t_s + cb * 16, t_sum + cb * 16, z, sum);
@@ -437,6 +443,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               }
               __syncwarp();
               tmem_put16(t_sum + cb * 16, sum);
+              if ((most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf) over |= 1u << cb;
               // the weights' slots are free when the last product is done
               if (cb == half && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
@@ -469,18 +476,20 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             __syncwarp();
             tmem_wait_st();
             tc_fence_before();
-            const bool over = (most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf;
-            if (!group_any(over && !again) || !ok) break;
+            todo = group_or(again ? 0 : over);
+            if (!ok || !todo) break;
             tc_fence_after();
             again = true;
           }
-          // New maxima, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest z + log2 s_v.
+          // New maxima in these chunks, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest
+          // z + log2 s_v.
           // What the tile added to the sums is taken off again; where that was so much (2^60 and more) that nothing
           // before it counts beside the row's largest weight, 0 is left.
           if (tid < 64) s->top[tid] = INT32_MIN;
           if (!(ok = group_sync())) break;
 #pragma unroll 1
           for (int cb = half; cb < chunks; cb += 2) {
+            if (!(todo >> cb & 1)) continue;
             uint32_t x[16], sum[16];
             __syncwarp();
             tmem_ld16(t_s + cb * 16, x);
@@ -513,7 +522,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           if (!(ok = group_sync())) break;
           if (tid < 64) {
             float f = 1.f;
-            if (tid < w.rows) {
+            if (tid < w.rows && todo >> (tid >> 4) & 1) {
               const float top = __int_as_float(ordered(s->top[tid]));
               float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);
               if (top > -INFINITY && top + *less > kTopFresh) {
@@ -528,6 +537,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           if (i > 0) {  // (the last product is in the accumulator: the weights' slots were free)
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
+              if (!(todo >> cb & 1)) continue;
               uint32_t o[16], sum[16];
               __syncwarp();
               tmem_ld16(t_o + cb * 16, o);

@@ -35,8 +35,7 @@ namespace smcsd {
 constexpr int kTile8 = 128;    // tokens per tile
 constexpr int kMaxCtas8 = 384; // slots for continuations
 constexpr int kCtasPerSm = 2;
-constexpr int kThreads8 = 384;
-constexpr int kSoftmax8 = 256;  // the first ones
+constexpr int kThreads8 = 320;
 constexpr int kSegs8 = 4;      // segments found ahead
 constexpr int kTileBytes8 = kTile8 * 128;
 
@@ -70,9 +69,9 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // ---------------------------------------------------------------------------
 // attention8_kernel.  Two CTAs to a multiprocessor, each: warps 0-7 the softmax
 // (thread = token of a tile; warps w and w + 4 take the even and the odd chunks of
-// 16 rows), warp 8 issues the matrix products, warp 9 finds the CTA's segments
-// (parts of units) and copies K and V, warps 10 and 11 cut the next segment's
-// rows of q into pieces.  Shared memory: two slots each of K and V tiles, q's
+// 16 rows; ahead of a segment they cut its rows of q into pieces, four threads a
+// row), warp 8 issues the matrix products, warp 9 finds the CTA's segments (parts
+// of units), copies K and V and prepares their scales.  Shared memory: two slots each of K and V tiles, q's
 // pieces, the weights' pieces.  Tensor memory, 64 columns each: two tiles'
 // scores, the accumulator, the sums of w / s_v (each lane's tokens').
 //   A softmax thread's loop takes 16 rows at a time and keeps nothing of them in
@@ -99,12 +98,11 @@ constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final resul
 
 struct Tail8 {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full, pv_done, q_full, q_free, q_taken, o_full, o_free, drained;
+  uint64_t s_full[2], p_full, pv_done, q_full, o_full, o_free, drained;
   uint64_t seg_full[kSegs8], seg_empty[kSegs8], group;
   Seg8 seg[kSegs8];
   float4 token[2][kTile8];  // of a tile's tokens: scale * log2 e * s_k, log2 s_v, kSumScale / s_v
   float4 col[32];     // of two rows each: scale of q, and kTopFresh - M
-  float q_scale[64];  // of the next segment's rows
   alignas(16) int top[64];  // maxima of a tile, then factors
   uint32_t rise[3];   // chunks of 16 rows in which a weight passed 2^kTop, of three votes
   unsigned nonfinite; // the last segment (from 1) with a new token whose NaN were zeroed
@@ -129,9 +127,7 @@ static_assert(Smem8<__nv_bfloat16>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "s
 static_assert(Smem8<__half>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "shared memory");
 static_assert(Smem8<__half>::kPiece % 1024 == 0, "the swizzle counts from 1 KB boundaries");
 
-// Waits, bounded as those of tensor_core.cuh, but without a call: the registers
-// of the warps that take more than the launch gave them (setmaxnreg) cannot be
-// saved around one.
+// Waits, bounded as those of tensor_core.cuh; in place, as a softmax loop has few of them.
 __device__ __forceinline__ void give_up(Tail8 *s, unsigned *status) {
   s->abort = 1;
   raise_status(status, SMC_DEV_TIMEOUT);
@@ -314,9 +310,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     }
     mbar_init(&s->p_full, 1);
     mbar_init(&s->pv_done, 1);
-    mbar_init(&s->q_full, 2);
-    mbar_init(&s->q_free, 1);
-    mbar_init(&s->q_taken, 8);
+    mbar_init(&s->q_full, 8);
     mbar_init(&s->o_full, 1);
     mbar_init(&s->o_free, 8);
     mbar_init(&s->drained, 1);
@@ -324,7 +318,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     s->rise[0] = s->rise[1] = s->rise[2] = 0;
     for (int i = 0; i < kSegs8; ++i) {
       mbar_init(&s->seg_full[i], 1);
-      mbar_init(&s->seg_empty[i], 11);  // every warp but the one that fills it
+      mbar_init(&s->seg_empty[i], 9);  // every warp but the one that fills it
     }
     s->nonfinite = 0;
     s->abort = (smem_addr(smem) & 1023u) != 0;
@@ -346,7 +340,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     if (tid == 0) raise_status(status, SMC_DEV_TIMEOUT);
   } else if (warp < 8) {
     // ---- softmax --------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int half = warp >> 2, token = tid & 127;  // chunks half, half + 2; token of a tile
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21), t_o = t_lane + 128, t_sum = t_lane + 192;
     char *const p_at = smem + M::kP + (token >> 3) * 128 + (token & 7) * 16;
@@ -384,15 +377,61 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         for (int cb = half; cb < chunks; cb += 2) tmem_st16(t_sum + cb * 16, zero);
         tmem_wait_st();
       }
-      // the rows' scales and maxima
-      if (!(ok = warp_wait8(s, &s->q_full, seg & 1u, status))) break;
-      if (tid < 32) {
-        const float unset[2] = {2 * tid < w.rows ? kUnset : -INFINITY, 2 * tid + 1 < w.rows ? kUnset : -INFINITY};
-        s->col[tid] = make_float4(s->q_scale[2 * tid], s->q_scale[2 * tid + 1], unset[0], unset[1]);
+      // the rows' pieces and scales, maxima not set (the products of the last segment are done)
+      {
+        const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
+        const int r = tid >> 2, part = tid & 3, in = r / heads.n, rows = w.rows;  // 32 dims each
+        const uint4 *q = reinterpret_cast<const uint4 *>(
+            k.a.q + ((w.row0 + in) * k.a.q_row + (heads.first + r - in * heads.n) * k.a.q_head) * static_cast<int64_t>(sizeof(T)));
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = r < rows && part * 4 + e < D / 8 ? q[part * 4 + e] : make_uint4(0, 0, 0, 0);
+        }
+        const T *x = reinterpret_cast<const T *>(v);
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float a = fabsf(to_f32(x[j]));
+          if (a < INFINITY) top = fmaxf(top, a);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
+        if (r < 16 * chunks) {
+          char *const to = smem + M::kQ + r * 128;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t words[kPieces][4] = {};
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float a = finite_or_nan(to_f32(x[c * 16 + j])) * inv, b = finite_or_nan(to_f32(x[c * 16 + j + 1])) * inv;
+#pragma unroll
+              for (int piece = 0; piece < kPieces; ++piece) {
+                const uint32_t e = to_e4m3x2(a, b), h = from_e4m3x2(e);
+                words[piece][j / 4] |= e << (j & 2) * 8;
+                const float2 taken = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                a -= taken.x;
+                b -= taken.y;
+              }
+            }
+#pragma unroll
+            for (int piece = 0; piece < kPieces; ++piece) {
+              *reinterpret_cast<uint4 *>(to + piece * M::kPiece + (((part * 2 + c) ^ (r & 7)) << 4)) =
+                  make_uint4(words[piece][0], words[piece][1], words[piece][2], words[piece][3]);
+            }
+          }
+        }
+        if (part == 0) {
+          float *const col = reinterpret_cast<float *>(&s->col[r >> 1]) + (r & 1);
+          col[0] = r < rows ? scale : 0.f;
+          col[2] = r < rows ? kUnset : -INFINITY;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&s->q_full, lane);
       }
       ++seg;
-      if (!(ok = group_sync())) break;
-      warp_arrive(&s->q_taken, lane);
+      if (!(ok = group_sync())) break;  // (every row's scale)
 
       for (int i = 0; i < tiles; ++i, ++tile, at += kTile8) {
         const bool edge = at - token + kTile8 > ctx;
@@ -603,6 +642,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       }
       if (!(ok = group_sync())) break;
       const bool bad = *reinterpret_cast<volatile unsigned *>(&s->nonfinite) == seg;
+      const int rows = w.rows;
 #pragma unroll 1
       for (int cb = half; cb < chunks; cb += 2) {
         uint32_t o[16];
@@ -611,16 +651,20 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         tmem_wait_all();
         tmem_tie16(o);
         if (token < D) {
+          const int some = min(rows - cb * 16, 16);
+          auto value = [&](int e) {
+            const float f = inverse[cb * 16 + e];
+            return f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+          };
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int r = cb * 16 + e;
-            if (r < w.rows) {
-              const float f = inverse[r], x = f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
-              if (whole) {
-                reinterpret_cast<T *>(to[r])[token] = from_f32<T>(x);
-              } else {
-                reinterpret_cast<float *>(to[r])[token] = x;
-              }
+            for (int e = 0; e < 16; ++e) {
+              if (e < some) reinterpret_cast<T *>(to[cb * 16 + e])[token] = from_f32<T>(value(e));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (e < some) reinterpret_cast<float *>(to[cb * 16 + e])[token] = value(e);
             }
           }
         }
@@ -660,7 +704,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     tmem_wait_all();  // (a warp that gave up may have left some under way)
     tmem_wait_st();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8) {
       // ---- matrix products ----------------------------------------------------
       const int k_steps = (D + 31) / 32;
@@ -697,7 +740,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               }
               tc_commit(&s->s_full[at]);
               tc_commit(&s->k_empty[at]);
-              if (i + 1 == n) tc_commit(&s->q_free);
             }
             if (i == 0) continue;
             const uint32_t last = tile + i - 1, at = last & 1u;
@@ -728,7 +770,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         if (!mbar_wait(&s->drained, 0, kWaitPolls)) raise_status(status, SMC_DEV_TIMEOUT);
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else {
       // ---- segments, K and V ----------------------------------------------------
       Walk<Units8<T>> walk;
       walk.start(k);
@@ -873,79 +915,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
       }
       if (bits) raise_status(status, bits);
-    } else {
-      // ---- q's pieces -----------------------------------------------------------
-      // four lanes to a row, 32 dims each; 16 rows at a time, and the next ones' loads under way
-      const int part = tid & 3, r_in = (tid - 320) >> 2;
-      uint32_t seg = 0;
-      bool ok = true;
-      Seg8 w;
-      while (ok && take_segment8(s, seg, &w, status)) {
-        warp_arrive(&s->seg_empty[seg % kSegs8], lane);
-        const UnitHeads heads = unit_heads<Units8<T>>(k, w.head);
-        uint4 v[4];
-        auto fetch = [&](int r) {
-          const int in = r / heads.n, qh = heads.first + r - in * heads.n;
-          const uint4 *q = reinterpret_cast<const uint4 *>(
-              k.a.q + ((w.row0 + in) * k.a.q_row + qh * k.a.q_head) * static_cast<int64_t>(sizeof(T)));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool has = r < w.rows && part * 4 + e < D / 8;
-            v[e] = has ? q[part * 4 + e] : make_uint4(0, 0, 0, 0);
-          }
-        };
-        fetch(r_in);
-        // the rows before have been read: their scales, and their pieces by the last scores
-        if (seg > 0 && !(ok = warp_wait8(s, &s->q_taken, (seg - 1) & 1u, status) &&
-                              warp_wait8(s, &s->q_free, (seg - 1) & 1u, status))) {
-          break;
-        }
-#pragma unroll 1
-        for (int r = r_in; r < 64; r += 16) {
-          if (r - r_in >= w.rows) {  // (for the whole warp)
-            if (part == 0) s->q_scale[r] = 0.f;
-            continue;
-          }
-          const uint4 now[4] = {v[0], v[1], v[2], v[3]};
-          if (r - r_in + 16 < w.rows) fetch(r + 16);
-          const T *x = reinterpret_cast<const T *>(now);
-          float top = 0.f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float a = fabsf(to_f32(x[j]));
-            if (a < INFINITY) top = fmaxf(top, a);
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
-          char *const to = smem + M::kQ + r * 128;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t words[kPieces][4] = {};
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float a = finite_or_nan(to_f32(x[c * 16 + j])) * inv, b = finite_or_nan(to_f32(x[c * 16 + j + 1])) * inv;
-#pragma unroll
-              for (int piece = 0; piece < kPieces; ++piece) {
-                const uint32_t e = to_e4m3x2(a, b), h = from_e4m3x2(e);
-                words[piece][j / 4] |= e << (j & 2) * 8;
-                const float2 taken = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                a -= taken.x;
-                b -= taken.y;
-              }
-            }
-#pragma unroll
-            for (int piece = 0; piece < kPieces; ++piece) {
-              *reinterpret_cast<uint4 *>(to + piece * M::kPiece + (((part * 2 + c) ^ (r & 7)) << 4)) =
-                  make_uint4(words[piece][0], words[piece][1], words[piece][2], words[piece][3]);
-            }
-          }
-          if (part == 0) s->q_scale[r] = r < w.rows ? scale : 0.f;
-        }
-        fence_proxy_async_smem();
-        warp_arrive(&s->q_full, lane);
-        ++seg;
-      }
     }
   }
   __syncthreads();

@@ -127,33 +127,8 @@ static_assert(Smem8<__nv_bfloat16>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "s
 static_assert(Smem8<__half>::kBytes <= 228 * 1024 / kCtasPerSm - 1024, "shared memory");
 static_assert(Smem8<__half>::kPiece % 1024 == 0, "the swizzle counts from 1 KB boundaries");
 
-// Waits, bounded as those of tensor_core.cuh; in place, as a softmax loop has few of them.
-__device__ __forceinline__ void give_up(Tail8 *s, unsigned *status) {
-  s->abort = 1;
-  raise_status(status, SMC_DEV_TIMEOUT);
-}
-__device__ __forceinline__ bool wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (s->abort) return false;
-  }
-  give_up(s, status);
-  return false;
-}
-// A whole warp, in step.
-__device__ __forceinline__ bool warp_wait8(Tail8 *s, uint64_t *bar, uint32_t parity, unsigned *status) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, s->abort)) return false;
-  }
-  give_up(s, status);
-  return false;
-}
-
 __device__ __forceinline__ bool take_segment8(Tail8 *s, uint32_t seg, Seg8 *to, unsigned *status) {
-  if (!warp_wait8(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) return false;
+  if (!warp_wait(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) return false;
   const int4 *from = reinterpret_cast<const int4 *>(&s->seg[seg % kSegs8]);
   const int4 a = from[0], b = from[1], c = from[2];
   *to = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
@@ -352,7 +327,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       if (mine) atomicOr(word, mine);
       warp_arrive(&s->group, lane);
       ++turns;
-      ok = warp_wait8(s, &s->group, (turns - 1) & 1u, status);
+      ok = warp_wait(s, &s->group, (turns - 1) & 1u, status);
       const uint32_t all = *reinterpret_cast<volatile uint32_t *>(word);
       votes = votes == 2 ? 0 : votes + 1;
       if (tid == 0) s->rise[votes == 2 ? 0 : votes + 1] = 0;  // word v + 2 = v - 1
@@ -361,9 +336,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
     auto group_sync = [&] {
       warp_arrive(&s->group, lane);
       ++turns;
-      return warp_wait8(s, &s->group, (turns - 1) & 1u, status);
+      return warp_wait(s, &s->group, (turns - 1) & 1u, status);
     };
-    while (ok && warp_wait8(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) {
+    while (ok && warp_wait(s, &s->seg_full[seg % kSegs8], seg / kSegs8 & 1u, status)) {
       const Seg8 &w = s->seg[seg % kSegs8];  // (released behind the segment: what is rarely looked at stays there)
       if (w.flags & kEnd8) break;
       const int tiles = w.n, ctx = w.flags & kShared ? INT32_MAX : w.ctx, kv1 = w.kv1;
@@ -437,7 +412,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const bool edge = at - token + kTile8 > ctx;
         const uint64_t see = edge ? rows_that_see<T>(k, w, at) : ~0ull;
         const uint32_t buf = tile & 1u, t_s = t_lane + buf * 64;
-        if (!(ok = warp_wait8(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
+        if (!(ok = warp_wait(s, &s->s_full[buf], tile >> 1 & 1u, status))) break;
         tc_fence_after();
         const float4 scales = s->token[buf][token];
         const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
@@ -484,7 +459,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               tmem_put16(t_sum + cb * 16, sum);
               if ((most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf) over |= 1u << cb;
               // the weights' slots are free when the last product is done
-              if (cb == half && tile > 0 && !(ok = warp_wait8(s, &s->pv_done, (tile - 1) & 1u, status))) break;
+              if (cb == half && tile > 0 && !(ok = warp_wait(s, &s->pv_done, (tile - 1) & 1u, status))) break;
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
 #pragma unroll
               for (int piece = 0; piece < 3; ++piece) {
@@ -506,7 +481,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               // the tile reaches past the committed tokens: rows of V past the last
               // token become 0 (they may hold anything), and so do NaN of new tokens,
               // which patch_nan8 puts back
-              if (!(ok = warp_wait8(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
+              if (!(ok = warp_wait(s, &s->v_full[buf], tile >> 1 & 1u, status))) break;
               if (at >= ctx && clear_row8(smem + M::kV + buf * kTileBytes8 + token * 128 + half * 64, at >= kv1)) {
                 s->nonfinite = seg;
               }
@@ -602,7 +577,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       }
       if (!ok) break;
       // ---- the unit's result --------------------------------------------------
-      if (!(ok = warp_wait8(s, &s->o_full, (seg - 1) & 1u, status))) break;
+      if (!(ok = warp_wait(s, &s->o_full, (seg - 1) & 1u, status))) break;
       tc_fence_after();
       // (the weights' slots are free: the sums of four warps, factors and rows' addresses)
       float *const sums = reinterpret_cast<float *>(smem + M::kP), *const inverse = sums + 4 * 64;
@@ -721,11 +696,11 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const uint32_t id_s = instr_desc8(columns, false, false, false), id_o = instr_desc8(columns, true, true, true);
         if (elect_one()) {
           // the scores of tile i, then the product with V of the tile before
-          ok = wait8(s, &s->q_full, seg & 1u, status);
+          ok = guarded_wait(s, &s->q_full, seg & 1u, status);
           for (int i = 0; ok && i <= n; ++i) {
             if (i < n) {  // (their buffer's last ones have been read: the weights of two tiles ago were there)
               const uint32_t at = (tile + i) & 1u;
-              if (!(ok = wait8(s, &s->k_full[at], (tile + i) >> 1 & 1u, status))) break;
+              if (!(ok = guarded_wait(s, &s->k_full[at], (tile + i) >> 1 & 1u, status))) break;
               tc_fence_after();
               const uint32_t ka = k0 + at * (kTileBytes8 >> 4);
 #pragma unroll 1
@@ -744,8 +719,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             if (i == 0) continue;
             const uint32_t last = tile + i - 1, at = last & 1u;
             // the last segment's result has been read
-            if (i == 1 && seg > 0 && !(ok = wait8(s, &s->o_free, (seg - 1) & 1u, status))) break;
-            if (!(ok = wait8(s, &s->v_full[at], last >> 1 & 1u, status) && wait8(s, &s->p_full, last & 1u, status))) break;
+            if (i == 1 && seg > 0 && !(ok = guarded_wait(s, &s->o_free, (seg - 1) & 1u, status))) break;
+            if (!(ok = guarded_wait(s, &s->v_full[at], last >> 1 & 1u, status) && guarded_wait(s, &s->p_full, last & 1u, status))) break;
             tc_fence_after();
             const uint32_t va = v0 + at * (kTileBytes8 >> 4);
 #pragma unroll 1
@@ -778,7 +753,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
       uint32_t tile = 0;
       bool ok = true, begun = false;
       for (uint32_t seg = 0; ok; ++seg) {
-        if (seg >= kSegs8 && !(ok = warp_wait8(s, &s->seg_empty[seg % kSegs8], (seg / kSegs8 - 1) & 1u, status))) break;
+        if (seg >= kSegs8 && !(ok = warp_wait(s, &s->seg_empty[seg % kSegs8], (seg / kSegs8 - 1) & 1u, status))) break;
         const bool more = walk.next(k);
         if (!begun && lane == 0 && !k.join_inside) {
           const bool cut = more && walk.first_cut;
@@ -850,7 +825,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
               uint64_t *full = which ? &s->v_full[slot] : &s->k_full[slot];
-              if (!(ok = warp_wait8(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
+              if (!(ok = warp_wait(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
               if (lane == 0) mbar_arrive_expect_tx(full, boxes * k.box * 128);
               __syncwarp();
               if (lane < boxes) {
@@ -874,7 +849,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             const bool take = chunk * 16 < D;
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
-              if (!(ok = warp_wait8(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
+              if (!(ok = warp_wait(s, which ? &s->v_empty[slot] : &s->k_empty[slot], turn ^ 1u, status))) break;
               const char *column = (which ? c8.v : c8.k) + (take ? chunk * 16 : 0);
               const uint32_t to = smem_addr(which ? to_v : to_k);
 #pragma unroll

@@ -1,6 +1,6 @@
 // Per-head RMS norms of queries and keys, the position rotation, and the write
 // of keys and values into an 8-bit cache (smc_qk_norm_rope8 in smcsd.h).
-#include "cache_common.cuh"
+#include "qk_turn.cuh"
 
 namespace smcsd {
 
@@ -16,25 +16,48 @@ struct Run {
   int seq, at;     // the first one's place in its table
 };
 
-// The first run that begins at row `r` or later and before `end`; n = 0: none.
-__device__ __forceinline__ Run next_run(const QkArgs &a, int r, int end) {
-  const int bs = a.c.block_size;
-  while (r < end) {
-    const int s = seq_of_row(a.b, r);
-    if (s < 0 || s >= a.b.S) break;  // rows past the last sequence
-    const SeqInfo si = seq_info(a.b, bs, s);
-    const int i = r - si.row0;
-    if (i < 0 || i >= si.n) {
-      if (si.bits && blockIdx.y == 0 && threadIdx.x == 0) raise_status(a.status, si.bits);
-      ++r;
-      continue;
-    }
-    const int at = si.len - si.n + i, off = at % bs, n = min(bs - off, si.n - i);
-    if (i == 0 || off == 0) return {r, n, s, at};
-    r += n;
+// The first sequence whose rows end behind row r (S: none): a warp probes 32
+// places at a time, so that 1024 sequences take two dependent loads.
+__device__ __forceinline__ int find_seq(const BatchArgs &b, int r) {
+  if (!b.row_start) return min(r / b.max_new, b.S);
+  int lo = 0, hi = b.S;  // in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 32) / 32, at = lo + (static_cast<int>(threadIdx.x & 31) + 1) * step - 1;
+    const unsigned past = __ballot_sync(0xffffffffu, at >= hi || b.row_start[at + 1] > r);
+    const int first = __ffs(past) - 1;  // (at least the last lane's is)
+    hi = min(hi, lo + (first + 1) * step - 1);
+    lo += first * step;
+    if (step == 1) break;
   }
-  return {0, 0, 0, 0};
+  return lo;
 }
+
+// The runs that begin in rows [r, end), one after the other.
+struct Runs {
+  int s, r, end;
+  __device__ __forceinline__ Runs(const QkArgs &a, int r0, int r1) : s(find_seq(a.b, r0)), r(r0), end(r1) {}
+  __device__ __forceinline__ Run next(const QkArgs &a) {
+    const int bs = a.c.block_size;
+    while (r < end && s < a.b.S) {
+      const SeqInfo si = seq_info(a.b, bs, s);
+      const int i = r - si.row0;
+      if (si.bits || i >= si.n) {  // the next sequence
+        if (si.bits && blockIdx.y == 0 && threadIdx.x == 0) raise_status(a.status, si.bits);
+        ++s;
+        continue;
+      }
+      if (i < 0) {  // (rows of a sequence that is out of order)
+        r = min(end, si.row0);
+        continue;
+      }
+      const int at = si.len - si.n + i, off = at % bs, n = min(bs - off, si.n - i);
+      const Run run{r, n, s, at};
+      r += n;
+      if (i == 0 || off == 0) return run;
+    }
+    return {0, 0, 0, 0};
+  }
+};
 
 // Element d of a vector after norm (r = rsqrt of the mean square) and rotation.
 template <typename T>
@@ -76,8 +99,9 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
   const int bs = a.c.block_size, D = a.c.head_dim;
   wait_for_stream();
-  const int r0 = blockIdx.x * per, end = min(r0 + per, a.b.rows);
-  for (Run run = next_run(a, r0, end); run.n > 0; run = next_run(a, run.row + run.n, end)) {
+  const int r0 = blockIdx.x * per;
+  Runs runs(a, r0, min(r0 + per, a.b.rows));
+  for (Run run = runs.next(a); run.n > 0; run = runs.next(a)) {
     const int block = a.b.tables[static_cast<int64_t>(run.seq) * a.b.T + run.at / bs], off = run.at % bs;
     if (block < 0 || block >= a.c.blocks) {
       if (h == 0 && tid == 0) raise_status(a.status, SMC_DEV_BAD_BLOCK);
@@ -160,10 +184,237 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
   }
 }
 
+// ---------------------------------------------------------------------------
+// The same with 16-byte accesses: a vector per group of kLanes lanes.  A run's
+// keys and values are dealt to the groups, computed once, and stay in registers
+// while the largest of them is found (kKept vectors a group; what is more is
+// computed again); the queries, which need no scale, are worked on before the
+// CTA waits for it.
+//   Keys are rounded step by step, x r, then w, then the rotation's products, as
+// plain fp32 does: where the largest one lies beside a power of two, its last bit
+// decides the scale.
+// ---------------------------------------------------------------------------
+constexpr int kKept = 2;
+
+template <typename T, int kLanes, bool kInter>
+__global__ void __launch_bounds__(kThreads8, 2)
+append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleArgs sc, int per) {
+  constexpr int E = 16 / sizeof(T);
+  __shared__ int s_top[2];
+  __shared__ float s_old[2], s_new[2];
+  const int tid = threadIdx.x, h = blockIdx.y, vec = tid % kLanes, group = tid / kLanes, groups = blockDim.x / kLanes;
+  const int bs = a.c.block_size, d0 = vec * E, half = a.rot / 2;
+  Turn<T, kLanes, kInter> turn;
+  turn.place(a);
+  const bool has = turn.has;
+  const float inv_dim = 1.f / a.c.head_dim;
+  const int nq = h < a.q_heads ? (a.q_heads - h + a.c.kv_heads - 1) / a.c.kv_heads : 0;  // query heads h, h + kv_heads, ...
+  wait_for_stream();
+  const int r0 = blockIdx.x * per;
+  Runs runs(a, r0, min(r0 + per, a.b.rows));
+  for (Run run = runs.next(a); run.n > 0; run = runs.next(a)) {
+    const int block = a.b.tables[static_cast<int64_t>(run.seq) * a.b.T + run.at / bs], off = run.at % bs, n = run.n;
+    if (block < 0 || block >= a.c.blocks) {
+      if (h == 0 && tid == 0) raise_status(a.status, SMC_DEV_BAD_BLOCK);
+      continue;
+    }
+    auto position = [&](int i) {  // a row's, -1 out of range
+      const int p = a.positions ? a.positions[run.row + i] : run.at + i;
+      return p >= 0 && p < a.max_pos ? p : -1;
+    };
+    auto table_of = [&](int pos) { return a.rope + static_cast<int64_t>(pos) * a.rot; };
+    auto fetch = [&](const char *base, int64_t row_stride, int64_t head_stride, int i, int head) {
+      return has ? *reinterpret_cast<const uint4 *>(base + ((run.row + i) * row_stride + head * head_stride) *
+                                                               static_cast<int64_t>(sizeof(T)) + vec * 16)
+                 : make_uint4(0, 0, 0, 0);
+    };
+    // item j < n: key of row j; j < 2n: value of row j - n.  All lanes of a warp call it.
+    auto item = [&](int j, float *z) {
+      const bool key = j < n;
+      const int i = key ? j : j - n;
+      const bool in = j < 2 * n;
+      const uint4 raw = in ? (key ? fetch(a.k, a.k_row, a.k_head, i, h) : fetch(a.v, a.v_row, a.v_head, i, h)) : make_uint4(0, 0, 0, 0);
+      const int pos = in ? position(i) : -1;
+      float x[E], y[E];
+      unpack16<T>(raw, x);
+      if (a.kw) {
+        float sum = 0.f, w[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, kLanes);
+        const float r = rsqrtf(fmaf(sum, inv_dim, a.eps));
+        if (has) unpack16<T>(reinterpret_cast<const uint4 *>(a.kw)[vec], w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (key && has) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e] + a.w0);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = kInter ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], turn.other);
+#pragma unroll
+      for (int e = 0; e < E; ++e) z[e] = x[e];
+      if (key && pos >= 0 && turn.turns) {
+        const float *cs = table_of(pos) + (kInter ? d0 / 2 : turn.second ? d0 - half : d0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float c = cs[kInter ? e / 2 : e], sn = cs[half + (kInter ? e / 2 : e)];
+          const bool second = kInter ? e & 1 : turn.second;
+          const float p = __fmul_rn(x[e], c), q = __fmul_rn(y[e], sn);
+          z[e] = second ? __fadd_rn(q, p) : __fsub_rn(p, q);
+        }
+      }
+      return has && pos >= 0;
+    };
+    auto largest = [&](const float *z) {
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float v = fabsf(z[e]);
+        if (v < INFINITY) top = fmaxf(top, v);
+      }
+      return top;
+    };
+    __syncthreads();
+    if (tid < 2) s_top[tid] = 0;
+    if (tid < n && h == 0 && position(tid) < 0) raise_status(a.status, SMC_DEV_BAD_ROWS);
+    for (int i = tid + blockDim.x; i < n; i += blockDim.x) {
+      if (h == 0 && position(i) < 0) raise_status(a.status, SMC_DEV_BAD_ROWS);
+    }
+    float kept[kKept][E];
+    bool live[kKept];
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < kKept; ++t) {
+      const int j = group + t * groups;
+      live[t] = item(j, kept[t]);
+      const float m = live[t] ? largest(kept[t]) : 0.f;
+      if (j < n) top[0] = fmaxf(top[0], m); else top[1] = fmaxf(top[1], m);
+    }
+    for (int j0 = kKept * groups; j0 < 2 * n; j0 += groups) {
+      float z[E];
+      const int j = j0 + group;
+      const float m = item(j, z) ? largest(z) : 0.f;
+      if (j < n) top[0] = fmaxf(top[0], m); else top[1] = fmaxf(top[1], m);
+    }
+    __syncthreads();  // s_top is clear
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int m = __reduce_max_sync(0xffffffffu, __float_as_int(top[w]));  // of positive numbers: their bits' order
+      if ((tid & 31) == 0 && m) atomicMax(&s_top[w], m);
+    }
+    // the queries, row by row as far as a group goes
+    int last = -1;
+    for (int j0 = 0; j0 < n * nq; j0 += groups) {
+      const int j = j0 + group, i = j % n, g = h + j / n * a.c.kv_heads;
+      const bool in = j < n * nq;
+      const int pos = in ? position(i) : -1;
+      const uint4 raw = in ? fetch(a.q, a.q_row, a.q_head, i, g) : make_uint4(0, 0, 0, 0);
+      if (pos >= 0 && i != last) {
+        turn.load(a, table_of(pos), a.qw);
+        last = i;
+      }
+      const uint4 z = turn.apply(raw, a.qw != nullptr, inv_dim, a.eps);
+      if (pos >= 0 && has) {
+        *reinterpret_cast<uint4 *>(a.out + ((run.row + i) * a.o_row + g * a.o_head) * static_cast<int64_t>(sizeof(T)) + vec * 16) = z;
+      }
+    }
+    __syncthreads();
+    if (tid < 2) {
+      float *at = (tid ? sc.v : sc.k) + block * sc.block + h * sc.head;
+      const float need = least_scale(__int_as_float(s_top[tid]));
+      s_old[tid] = off ? scale_of(*at) : need;
+      s_new[tid] = fmaxf(need, s_old[tid]);
+      *at = s_new[tid];
+    }
+    __syncthreads();
+    char *const to[2] = {a.c.k + block * a.c.block_stride + h * a.c.head_stride,
+                         a.c.v + block * a.c.block_stride + h * a.c.head_stride};
+    auto store = [&](int j, const float *z) {
+      const int which = j >= n;
+      const float scale = s_new[which];
+      uint32_t words[E / 4];
+      // a power of two's reciprocal is exact
+      const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+      const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        float v[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[f] = power ? finite_or_nan(z[e + f]) * inv : finite_or_nan(z[e + f]) / scale;
+        words[e / 4] = to_e4m3x2(v[0], v[1]) | to_e4m3x2(v[2], v[3]) << 16;
+      }
+      char *dst = to[which] + (off + (which ? j - n : j)) * a.c.token_stride + d0;
+      if constexpr (E == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(words[0], words[1]);
+      else *reinterpret_cast<uint32_t *>(dst) = words[0];
+    };
+#pragma unroll
+    for (int t = 0; t < kKept; ++t) {
+      if (live[t]) store(group + t * groups, kept[t]);
+    }
+    for (int j0 = kKept * groups; j0 < 2 * n; j0 += groups) {
+      float z[E];
+      if (item(j0 + group, z)) store(j0 + group, z);
+    }
+    for (int which = 0; which < 2; ++which) {  // tokens ahead of the new ones
+      const float f = s_old[which] / s_new[which];
+      if (f == 1.f || !has) continue;
+      for (int t = group; t < off; t += groups) {
+        uint32_t *x = reinterpret_cast<uint32_t *>(to[which] + t * a.c.token_stride + d0);
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) x[e] = rescale_e4m3x4(x[e], f);
+      }
+    }
+  }
+}
+
+// Whether rows and weights are 16-byte vectors that turn as a whole, and the
+// cache's are aligned to what becomes of one.
+static bool vectors8_ok(const QkArgs &a, int dtype) {
+  const int esz = dtype_bytes(dtype), E = 16 / esz;
+  uint64_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
+                 reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out) |
+                 reinterpret_cast<uintptr_t>(a.qw) | reinterpret_cast<uintptr_t>(a.kw) |
+                 reinterpret_cast<uintptr_t>(a.rope);
+  uint64_t cache = reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v);
+  const int rows = a.b.rows, Hk = a.c.kv_heads;
+  auto stride = [&](int64_t s, int n) { if (n > 1) all |= static_cast<uint64_t>(s) * esz; };
+  stride(a.q_row, rows); stride(a.k_row, rows); stride(a.v_row, rows); stride(a.o_row, rows);
+  stride(a.q_head, a.q_heads); stride(a.o_head, a.q_heads);
+  stride(a.k_head, Hk); stride(a.v_head, Hk);
+  cache |= static_cast<uint64_t>(a.c.head_stride) | static_cast<uint64_t>(a.c.token_stride) |
+           static_cast<uint64_t>(a.c.block_stride);
+  return all % 16 == 0 && cache % E == 0 && a.c.head_dim % E == 0 && a.c.head_dim <= 32 * E && a.rot % E == 0 &&
+         (a.interleaved || a.rot / 2 % E == 0);
+}
+
+template <typename T, bool kInter>
+static const void *vectors8_fn(int lanes) {
+  return lanes == 8    ? reinterpret_cast<const void *>(append8_vectors_kernel<T, 8, kInter>)
+         : lanes == 16 ? reinterpret_cast<const void *>(append8_vectors_kernel<T, 16, kInter>)
+                       : reinterpret_cast<const void *>(append8_vectors_kernel<T, 32, kInter>);
+}
+
+template <typename T>
+static const void *vectors8_fn(const QkArgs &a, int lanes) {
+  return a.interleaved ? vectors8_fn<T, true>(lanes) : vectors8_fn<T, false>(lanes);
+}
+
 cudaError_t launch_qk_norm_rope8(const QkArgs &a, const ScaleArgs &s, int dtype, cudaStream_t st) {
   if (a.b.rows == 0) return cudaSuccess;
   int per = a.c.block_size < a.b.max_new ? a.c.block_size : a.b.max_new;
   ScaleArgs scales = s;
+  if (vectors8_ok(a, dtype)) {
+    const int vectors = a.c.head_dim * dtype_bytes(dtype) / 16, lanes = vectors <= 8 ? 8 : vectors <= 16 ? 16 : 32;
+    const void *fn = dtype == SMC_F32    ? vectors8_fn<float>(a, lanes)
+                     : dtype == SMC_BF16 ? vectors8_fn<__nv_bfloat16>(a, lanes)
+                                         : vectors8_fn<__half>(a, lanes);
+    // no more threads than vectors of a run
+    const int64_t most = static_cast<int64_t>(per) * (2 + (a.q_heads + a.c.kv_heads - 1) / a.c.kv_heads) * lanes;
+    const int threads = most >= kThreads8 ? kThreads8 : static_cast<int>((most + 31) / 32 * 32);
+    void *args[] = {const_cast<QkArgs *>(&a), &scales, &per};
+    return launch_early(fn, dim3((a.b.rows + per - 1) / per, a.c.kv_heads), threads, 0, args, st);
+  }
   const void *fn = dtype == SMC_F32    ? reinterpret_cast<const void *>(append8_kernel<float>)
                    : dtype == SMC_BF16 ? reinterpret_cast<const void *>(append8_kernel<__nv_bfloat16>)
                                        : reinterpret_cast<const void *>(append8_kernel<__half>);

@@ -19,7 +19,6 @@ struct Run {
 // The first sequence whose rows end behind row r (S: none): a warp probes 32
 // places at a time, so that 1024 sequences take two dependent loads.
 __device__ __forceinline__ int find_seq(const BatchArgs &b, int r) {
-  if (!b.row_start) return min(r / b.max_new, b.S);
   int lo = 0, hi = b.S;  // in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 32) / 32, at = lo + (static_cast<int>(threadIdx.x & 31) + 1) * step - 1;
@@ -35,7 +34,11 @@ __device__ __forceinline__ int find_seq(const BatchArgs &b, int r) {
 // The runs that begin in rows [r, end), one after the other.
 struct Runs {
   int s, r, end;
-  __device__ __forceinline__ Runs(const QkArgs &a, int r0, int r1) : s(find_seq(a.b, r0)), r(r0), end(r1) {}
+  __device__ __forceinline__ Runs(const QkArgs &a, int r0, int r1) : s(min(r0 / a.b.max_new, a.b.S - 1)), r(r0), end(r1) {
+    // (the guess is right where every sequence has max_new rows)
+    if (!a.b.row_start) s = r0 / a.b.max_new;
+    else if (!(a.b.row_start[s] <= r0 && r0 < a.b.row_start[s + 1])) s = find_seq(a.b, r0);
+  }
   __device__ __forceinline__ Run next(const QkArgs &a) {
     const int bs = a.c.block_size;
     while (r < end && s < a.b.S) {
@@ -195,6 +198,7 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
 // decides the scale.
 // ---------------------------------------------------------------------------
 constexpr int kKept = 2;
+constexpr int kAhead8 = 4;  // queries of a group whose loads are under way at once
 
 template <typename T, int kLanes, bool kInter>
 __global__ void __launch_bounds__(kThreads8, 2)
@@ -228,6 +232,9 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
                                                                static_cast<int64_t>(sizeof(T)) + vec * 16)
                  : make_uint4(0, 0, 0, 0);
     };
+    // (read early: its use is at the end of a chain of loads)
+    float *const scale_at = (tid == 1 ? sc.v : sc.k) + block * sc.block + h * sc.head;
+    const float before = tid < 2 && off ? *scale_at : 0.f;
     // item j < n: key of row j; j < 2n: value of row j - n.  All lanes of a warp call it.
     auto item = [&](int j, float *z) {
       const bool key = j < n;
@@ -237,31 +244,47 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
       const int pos = in ? position(i) : -1;
       float x[E], y[E];
       unpack16<T>(raw, x);
-      if (a.kw) {
-        float sum = 0.f, w[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, kLanes);
-        const float r = rsqrtf(fmaf(sum, inv_dim, a.eps));
-        if (has) unpack16<T>(reinterpret_cast<const uint4 *>(a.kw)[vec], w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (key && has) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e] + a.w0);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = kInter ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], turn.other);
 #pragma unroll
       for (int e = 0; e < E; ++e) z[e] = x[e];
-      if (key && pos >= 0 && turn.turns) {
-        const float *cs = table_of(pos) + (kInter ? d0 / 2 : turn.second ? d0 - half : d0);
+      if (__any_sync(0xffffffffu, key)) {
+        if (a.kw) {
+          float sum = 0.f, w[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float c = cs[kInter ? e / 2 : e], sn = cs[half + (kInter ? e / 2 : e)];
-          const bool second = kInter ? e & 1 : turn.second;
-          const float p = __fmul_rn(x[e], c), q = __fmul_rn(y[e], sn);
-          z[e] = second ? __fadd_rn(q, p) : __fsub_rn(p, q);
+          for (int e = 0; e < E; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, kLanes);
+          const float r = rsqrtf(fmaf(sum, inv_dim, a.eps));
+          if (has) unpack16<T>(reinterpret_cast<const uint4 *>(a.kw)[vec], w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (key && has) z[e] = x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e] + a.w0);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = kInter ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], turn.other);
+        if (key && pos >= 0 && turn.turns) {
+          const float *cs = table_of(pos) + (kInter ? d0 / 2 : turn.second ? d0 - half : d0);
+          constexpr int kAngles = kInter ? E / 2 : E;
+          alignas(16) float c[kAngles], sn[kAngles];
+          if constexpr (kAngles % 4 == 0) {
+#pragma unroll
+            for (int e = 0; e < kAngles; e += 4) {
+              *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(cs + e);
+              *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(cs + half + e);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kAngles; ++e) {
+              c[e] = cs[e];
+              sn[e] = cs[half + e];
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const bool second = kInter ? e & 1 : turn.second;
+            const float p = __fmul_rn(x[e], c[kInter ? e / 2 : e]), q = __fmul_rn(y[e], sn[kInter ? e / 2 : e]);
+            z[e] = second ? __fadd_rn(q, p) : __fsub_rn(p, q);
+          }
         }
       }
       return has && pos >= 0;
@@ -275,6 +298,24 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
       }
       return top;
     };
+    // Queries: a group takes rows group, group + groups, ..., and with fewer rows than groups, as many groups share a row's heads.
+    const int share = n < groups ? groups / n : 1, phase = n < groups ? group / n : 0;
+    const int q_row0 = n < groups ? group - phase * n : group, q_step = groups;
+    const int64_t head_step = static_cast<int64_t>(share) * a.c.kv_heads * a.q_head * static_cast<int64_t>(sizeof(T)),
+                  out_step = static_cast<int64_t>(share) * a.c.kv_heads * a.o_head * static_cast<int64_t>(sizeof(T));
+    const bool any_q = phase < share && has;
+    auto query_at = [&](int i) {
+      return a.q + ((run.row + i) * a.q_row + (h + phase * a.c.kv_heads) * a.q_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
+    };
+    // the first ones are on their way while keys and values are worked on
+    uint4 rq[kAhead8];
+    {
+      const char *q = query_at(q_row0);
+#pragma unroll
+      for (int t = 0; t < kAhead8; ++t, q += head_step) {
+        rq[t] = any_q && q_row0 < n && phase + t * share < nq ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
+      }
+    }
     __syncthreads();
     if (tid < 2) s_top[tid] = 0;
     if (tid < n && h == 0 && position(tid) < 0) raise_status(a.status, SMC_DEV_BAD_ROWS);
@@ -286,6 +327,8 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
     float top[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < kKept; ++t) {
+      live[t] = false;
+      if (t * groups >= 2 * n) break;  // for the whole CTA
       const int j = group + t * groups;
       live[t] = item(j, kept[t]);
       const float m = live[t] ? largest(kept[t]) : 0.f;
@@ -303,29 +346,37 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
       const int m = __reduce_max_sync(0xffffffffu, __float_as_int(top[w]));  // of positive numbers: their bits' order
       if ((tid & 31) == 0 && m) atomicMax(&s_top[w], m);
     }
-    // the queries, row by row as far as a group goes
-    int last = -1;
-    for (int j0 = 0; j0 < n * nq; j0 += groups) {
-      const int j = j0 + group, i = j % n, g = h + j / n * a.c.kv_heads;
-      const bool in = j < n * nq;
-      const int pos = in ? position(i) : -1;
-      const uint4 raw = in ? fetch(a.q, a.q_row, a.q_head, i, g) : make_uint4(0, 0, 0, 0);
-      if (pos >= 0 && i != last) {
-        turn.load(a, table_of(pos), a.qw);
-        last = i;
-      }
-      const uint4 z = turn.apply(raw, a.qw != nullptr, inv_dim, a.eps);
-      if (pos >= 0 && has) {
-        *reinterpret_cast<uint4 *>(a.out + ((run.row + i) * a.o_row + g * a.o_head) * static_cast<int64_t>(sizeof(T)) + vec * 16) = z;
+    // the queries
+    for (int i0 = 0; i0 < n; i0 += q_step) {
+      const int i = i0 + q_row0, pos = i < n ? position(i) : -1;
+      const bool writes = any_q && pos >= 0;
+      if (pos >= 0) turn.load(a, table_of(pos), a.qw);
+      char *out = a.out + ((run.row + i) * a.o_row + (h + phase * a.c.kv_heads) * a.o_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
+      const char *q = query_at(i);
+      for (int g0 = 0; g0 < nq; g0 += kAhead8 * share) {  // (of phase 0: the same number of turns for all lanes)
+        if (i0 > 0 || g0 > 0) {
+#pragma unroll
+          for (int t = 0; t < kAhead8; ++t) {
+            rq[t] = any_q && i < n && g0 + phase + t * share < nq ? *reinterpret_cast<const uint4 *>(q + t * head_step)
+                                                                   : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kAhead8; ++t) {
+          if (g0 + t * share >= nq) break;  // for the whole CTA
+          const uint4 z = turn.apply(rq[t], a.qw != nullptr, inv_dim, a.eps);
+          if (writes && g0 + phase + t * share < nq) *reinterpret_cast<uint4 *>(out + t * out_step) = z;
+        }
+        q += kAhead8 * head_step;
+        out += kAhead8 * out_step;
       }
     }
     __syncthreads();
     if (tid < 2) {
-      float *at = (tid ? sc.v : sc.k) + block * sc.block + h * sc.head;
       const float need = least_scale(__int_as_float(s_top[tid]));
-      s_old[tid] = off ? scale_of(*at) : need;
+      s_old[tid] = off ? scale_of(before) : need;
       s_new[tid] = fmaxf(need, s_old[tid]);
-      *at = s_new[tid];
+      *scale_at = s_new[tid];
     }
     __syncthreads();
     char *const to[2] = {a.c.k + block * a.c.block_stride + h * a.c.head_stride,
@@ -409,9 +460,10 @@ cudaError_t launch_qk_norm_rope8(const QkArgs &a, const ScaleArgs &s, int dtype,
     const void *fn = dtype == SMC_F32    ? vectors8_fn<float>(a, lanes)
                      : dtype == SMC_BF16 ? vectors8_fn<__nv_bfloat16>(a, lanes)
                                          : vectors8_fn<__half>(a, lanes);
-    // no more threads than vectors of a run
-    const int64_t most = static_cast<int64_t>(per) * (2 + (a.q_heads + a.c.kv_heads - 1) / a.c.kv_heads) * lanes;
-    const int threads = most >= kThreads8 ? kThreads8 : static_cast<int>((most + 31) / 32 * 32);
+    // a group of lanes for every row, whose key and value it keeps: with few rows a CTA is a small one, so that more
+    // of their chains of dependent loads run side by side
+    const int64_t most = static_cast<int64_t>(per) * lanes;
+    const int threads = most >= kThreads8 ? kThreads8 : most <= 64 ? 64 : static_cast<int>((most + 31) / 32 * 32);
     void *args[] = {const_cast<QkArgs *>(&a), &scales, &per};
     return launch_early(fn, dim3((a.b.rows + per - 1) / per, a.c.kv_heads), threads, 0, args, st);
   }

@@ -33,7 +33,7 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
   __shared__ int s_block[kMoves8], s_token[kMoves8];  // where a place's token comes from; block -1: it stays
   __shared__ int s_top[kThreads8];                    // new scales of the heads, as their bits
   __shared__ int s_warp[kThreads8 / 32], s_last, s_any;
-  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
   wait_for_stream();
   const SeqInfo si = seq_info(b, c.block_size, s);
   const int n = n_path[s];
@@ -55,7 +55,7 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
     const int off0 = (first + i0) % bs;
     const int i1 = min(n, i0 + (off0 + kMoves8) / bs * bs - off0);
     __syncthreads();  // s_last is set; the last places have been read
-    for (int r = i0; r < i1; r += kThreads8) {
+    for (int r = i0; r < i1; r += threads) {
       const int i = r + tid;
       // an index counts when it is in range, past every one in range before it
       // and not ahead of its place
@@ -74,7 +74,7 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
       before = max(before, s_last);
       for (int w = 0; w < (tid >> 5); ++w) before = max(before, s_warp[w]);
       __syncthreads();
-      if (tid == kThreads8 - 1) s_last = max(before, in ? mine : -1);
+      if (tid == threads - 1) s_last = max(before, in ? mine : -1);
       if (i < i1) {
         const bool good = in && mine > before && mine >= i;
         unsigned bits = good ? 0 : SMC_DEV_BAD_ROWS;
@@ -102,11 +102,11 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
       if (block < 0 || block >= c.blocks) continue;  // raised above where a token moves
       __syncthreads();
       if (tid == 0) s_any = 0;
-      for (int h = tid; h < here; h += kThreads8) {
+      for (int h = tid; h < here; h += threads) {
         s_top[h] = __float_as_int(scale_of(scale[block * sc.block + h * sc.head]));
       }
       __syncthreads();
-      for (int e = tid; e < moves * here; e += kThreads8) {
+      for (int e = tid; e < moves * here; e += threads) {
         const int j = e / here, h = e - j * here, src = s_block[at + j];
         if (src >= 0) {
           s_any = 1;
@@ -116,7 +116,7 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
       __syncthreads();
       if (!s_any) continue;
       char *const dst = base + block * c.block_stride;
-      for (int col = tid; col < cols; col += kThreads8) {
+      for (int col = tid; col < cols; col += threads) {
         const int h = col / per_head;
         const int64_t column = h * c.head_stride + (col - h * per_head) * static_cast<int64_t>(sizeof(U));
         const float now = __int_as_float(s_top[h]);
@@ -149,7 +149,7 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
         }
       }
       __syncthreads();  // every thread has read the block's old scales
-      for (int h = tid; h < here; h += kThreads8) scale[block * sc.block + h * sc.head] = __int_as_float(s_top[h]);
+      for (int h = tid; h < here; h += threads) scale[block * sc.block + h * sc.head] = __int_as_float(s_top[h]);
     }
     i0 = i1;
   }
@@ -177,7 +177,9 @@ cudaError_t launch_compact_tokens8(const CacheArgs &c, const ScaleArgs &s, const
                    : width == 4 ? reinterpret_cast<const void *>(compact_tokens8_kernel<uint32_t>)
                                 : reinterpret_cast<const void *>(compact_tokens8_kernel<uint8_t>);
   void *args[] = {&cache, &scales, &batch, &path, &n_path, &max_path, &heads, &status};
-  return launch_early(fn, dim3(b.S, 2 * c.layers, (c.kv_heads + heads - 1) / heads), kThreads8, 0, args, st);
+  // a thread per column, as far as a CTA goes; at least two warps, which find the places
+  const int cols = per_head * heads, threads = cols >= kThreads8 ? kThreads8 : cols <= 64 ? 64 : (cols + 31) / 32 * 32;
+  return launch_early(fn, dim3(b.S, 2 * c.layers, (c.kv_heads + heads - 1) / heads), threads, 0, args, st);
 }
 
 }  // namespace smcsd

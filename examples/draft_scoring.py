@@ -15,7 +15,10 @@ Shows how the entry points fit together around one decoding step:
                   the accepted path moved to the front (kv_compact_tokens), the
                   rest of the room given back (kv_truncate).
 
-    python examples/draft_scoring.py [--prompts 4] [--particles 8] [--steps 6]
+    python examples/draft_scoring.py [--prompts 4] [--particles 8] [--steps 6] [--bits 8]
+
+With --bits 8 the cache is one of 8-bit numbers with a scale per block and key
+head: the same calls with an 8 behind their names.
 
 The model's weights are random and its logits mean nothing; a real one puts its
 projections where `Model` has two matrix products.
@@ -30,6 +33,26 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import smc_speculative_decoding_gb300 as smcsd  # noqa: E402
 from smc_speculative_decoding_gb300.workloads import make_kv_state  # noqa: E402
+
+
+class Cache:
+    """A zero-filled paged cache of `bits` bits an element, and its entry points."""
+
+    def __init__(self, model, blocks, block_size, bits=16, device="cuda"):
+        shape = (len(model.qkv), blocks, block_size, model.kv_heads, model.dim)
+        if bits == 8:
+            self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+            self.k_scale, self.v_scale = (torch.ones((shape[0], blocks, model.kv_heads), device=device) for _ in range(2))
+            self.args = smcsd.make_cache8(self.k, self.v, self.k_scale, self.v_scale)
+            self.alloc_workspace, self.copy_blocks = smcsd.alloc_cache8_workspace, smcsd.kv_copy_blocks8
+            self.qk_norm_rope, self.attention = smcsd.smc_qk_norm_rope8, smcsd.smc_tree_attention8
+            self.compact_tokens = smcsd.kv_compact_tokens8
+        else:
+            self.k, self.v = (torch.zeros(shape, dtype=model.dtype, device=device) for _ in range(2))
+            self.args = smcsd.make_cache(self.k, self.v)
+            self.alloc_workspace, self.copy_blocks = smcsd.alloc_cache_workspace, smcsd.kv_copy_blocks
+            self.qk_norm_rope, self.attention = smcsd.smc_qk_norm_rope, smcsd.smc_tree_attention
+            self.compact_tokens = smcsd.kv_compact_tokens
 
 
 class Model:
@@ -61,22 +84,17 @@ class Model:
         for i in range(len(self.qkv)):
             q, k, v = (t.unflatten(1, (-1, d)) for t in (x @ self.qkv[i]).split([h * d, kv * d, kv * d], dim=1))
             turned = torch.empty((x.shape[0], h, d), dtype=self.dtype, device=x.device)
-            smcsd.smc_qk_norm_rope(cache, i, batch, q, k, v, self.rope, turned, workspace, positions=positions,
-                                   q_weight=self.q_weight[i], k_weight=self.k_weight[i])
+            cache.qk_norm_rope(cache.args, i, batch, q, k, v, self.rope, turned, workspace, positions=positions,
+                               q_weight=self.q_weight[i], k_weight=self.k_weight[i])
             o = torch.empty_like(turned)
-            smcsd.smc_tree_attention(cache, i, batch, turned, o, workspace, mask=mask)
+            cache.attention(cache.args, i, batch, turned, o, workspace, mask=mask)
             if seen is not None:
                 seen.append((turned, o))
             x = x + o.flatten(1) @ self.out[i]
         return (x @ self.embedding.T).float() * x.shape[1] ** -0.5
 
 
-def make_cache_tensors(model, blocks, block_size, device="cuda"):
-    shape = (len(model.qkv), blocks, block_size, model.kv_heads, model.dim)
-    return tuple(torch.zeros(shape, dtype=model.dtype, device=device) for _ in range(2))
-
-
-def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16, seed=0, observe=None):
+def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16, seed=0, observe=None, bits=16):
     """Runs `steps` SMC steps; returns the tokens that each particle emitted
     [B, N, steps * (K + 1)] and the share of blocks that sharing saves.
     observe(step, state) sees the state after each forward pass."""
@@ -85,8 +103,8 @@ def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16,
     slots = -(-(prefix + (steps + 2) * T) // block_size) + 1
     pool = n * slots + 1
     kv = make_kv_state(prompts, n, prefix, block_size, slots, pool, device=dev)
-    k, v = make_cache_tensors(model, prompts * pool, block_size)
-    cache = smcsd.make_cache(k, v)
+    cache = Cache(model, prompts * pool, block_size, bits)
+    k, v = cache.k, cache.v
     params = smcsd.make_params(prompts, n, K, vocab, "f32", ess_frac=0.6, seed=seed)
     kvs = smcsd.make_kv(params, kv, block_size)
     step_ws = smcsd.alloc_workspace(params, kvs)
@@ -95,7 +113,7 @@ def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16,
     # the prompt: its keys and values once, by the first particle of each prompt
     first = smcsd.make_batch(kv["tables"][:, :1].reshape(prompts, -1).contiguous(),
                              kv["seq_len"][:, :1].reshape(-1).contiguous(), prefix)
-    ws0 = smcsd.alloc_cache_workspace(cache, first, model.heads)
+    ws0 = cache.alloc_workspace(cache.args, first, model.heads)
     prompt_tokens = torch.randint(0, vocab, (prompts * prefix,), generator=g, device=dev)
     model.forward(prompt_tokens, cache, first, ws0)
 
@@ -105,8 +123,8 @@ def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16,
     resampled = torch.zeros(prompts, dtype=torch.int32, device=dev)
     smcsd.kv_blocktable_remap(params, kvs, ancestors, resampled, T, step_ws)
     batch = smcsd.make_batch(kv["tables"], kv["seq_len"], T, group=n)
-    ws = smcsd.alloc_cache_workspace(cache, batch, model.heads)
-    smcsd.kv_copy_blocks(cache, kv["cow_pairs"], kv["n_cow"], ws)
+    ws = cache.alloc_workspace(cache.args, batch, model.heads)
+    cache.copy_blocks(cache.args, kv["cow_pairs"], kv["n_cow"], ws)
     last = torch.randint(0, vocab, (prompts, n, 1), generator=g, device=dev, dtype=torch.int32)
     emitted = []
     ess = torch.empty(prompts, device=dev)
@@ -121,11 +139,11 @@ def particles(prompts=4, n=8, K=4, vocab=512, steps=6, prefix=40, block_size=16,
         logits = model.forward(new.reshape(-1), cache, batch, ws, seen=seen)
         target = (draft.mean() + logits).view(prompts, n, T, vocab).contiguous()
         if observe:
-            observe(step, dict(kv=kv, k=k, v=v, seen=seen, new=new, block_size=block_size, model=model))
+            observe(step, dict(kv=kv, k=k, v=v, seen=seen, new=new, block_size=block_size, model=model, cache=cache))
         params.step = step
         smcsd.smc_step(params, target, draft, drafted, log_weights, tokens_out, ancestors, ess, resampled, kv=kvs,
                        workspace=step_ws)
-        smcsd.kv_copy_blocks(cache, kv["cow_pairs"], kv["n_cow"], ws)
+        cache.copy_blocks(cache.args, kv["cow_pairs"], kv["n_cow"], ws)
         if observe:
             observe(step, dict(ancestors=ancestors.view(prompts, n), resampled=resampled))
         last = tokens_out[:, :, K:].clone()
@@ -157,24 +175,24 @@ def ancestor_masks(parents):
     return torch.where(m >= 1 << 31, m - (1 << 32), m).to(torch.int32).cuda(), torch.tensor(depths, dtype=torch.int32).cuda()
 
 
-def tree(prompts=3, M=12, vocab=512, prefix=37, rounds=4, block_size=16, seed=0, observe=None):
+def tree(prompts=3, M=12, vocab=512, prefix=37, rounds=4, block_size=16, seed=0, observe=None, bits=16):
     """Verifies `rounds` drafted trees of M tokens per prompt by greedy
     decoding; returns the token counts [prompts] at the end."""
     dev = "cuda"
     model = Model(vocab, seed=seed)
     slots = -(-(prefix + rounds * M + M) // block_size) + 1
     kv = make_kv_state(prompts, 1, prefix, block_size, slots, slots + 1, device=dev)
-    k, v = make_cache_tensors(model, prompts * (slots + 1), block_size)
-    cache = smcsd.make_cache(k, v)
+    cache = Cache(model, prompts * (slots + 1), block_size, bits)
+    k, v = cache.k, cache.v
     params = smcsd.make_params(prompts, 1, 1, vocab, "f32")
     kvs = smcsd.make_kv(params, kv, block_size)
     step_ws = smcsd.alloc_workspace(params, kvs)
     g = torch.Generator(device=dev).manual_seed(seed + 1)
     batch = smcsd.make_batch(kv["tables"], kv["seq_len"], prefix)
-    ws = smcsd.alloc_cache_workspace(cache, batch, model.heads)
+    ws = cache.alloc_workspace(cache.args, batch, model.heads)
     model.forward(torch.randint(0, vocab, (prompts * prefix,), generator=g, device=dev), cache, batch, ws)
     batch = smcsd.make_batch(kv["tables"], kv["seq_len"], M)
-    ws = smcsd.alloc_cache_workspace(cache, batch, model.heads)
+    ws = cache.alloc_workspace(cache.args, batch, model.heads)
     nobody = torch.zeros(prompts, dtype=torch.int32, device=dev)
     for round_ in range(rounds):
         # a drafted tree: token i continues a random earlier one
@@ -201,11 +219,13 @@ def tree(prompts=3, M=12, vocab=512, prefix=37, rounds=4, block_size=16, seed=0,
             path[s, :len(taken)], n_path[s] = torch.tensor(taken, dtype=torch.int32), len(taken)
         path, n_path = path.to(dev), n_path.to(dev)
         if observe:
-            observe(round_, dict(kv=kv, k=k, v=v, committed=committed, path=path, n_path=n_path, block_size=block_size))
-        smcsd.kv_compact_tokens(cache, batch, path, n_path, ws)
+            observe(round_, dict(kv=kv, k=k, v=v, committed=committed, path=path, n_path=n_path, block_size=block_size,
+                                 cache=cache))
+        cache.compact_tokens(cache.args, batch, path, n_path, ws)
         smcsd.kv_truncate(params, kvs, committed + n_path, step_ws)
         if observe:
-            observe(round_, dict(kv=kv, k=k, v=v, committed=committed, n_path=n_path, block_size=block_size, after=True))
+            observe(round_, dict(kv=kv, k=k, v=v, committed=committed, n_path=n_path, block_size=block_size, cache=cache,
+                                 after=True))
     for w in (step_ws, ws):
         if bits := smcsd.smc_device_status(w):
             raise RuntimeError(f"device status {smcsd.status_names(bits)}")
@@ -217,11 +237,12 @@ def main():
     ap.add_argument("--prompts", type=int, default=4)
     ap.add_argument("--particles", type=int, default=8)
     ap.add_argument("--steps", type=int, default=6)
+    ap.add_argument("--bits", type=int, default=16, choices=(8, 16))
     a = ap.parse_args()
-    tokens, saved = particles(a.prompts, a.particles, steps=a.steps)
+    tokens, saved = particles(a.prompts, a.particles, steps=a.steps, bits=a.bits)
     print(f"{a.prompts} prompts x {a.particles} particles: {tokens.shape[2]} tokens each, "
           f"{100 * saved:.0f} % fewer cache blocks than unshared copies")
-    print("tokens held after four drafted trees:", tree(a.prompts).tolist())
+    print("tokens held after four drafted trees:", tree(a.prompts, bits=a.bits).tolist())
 
 
 if __name__ == "__main__":

@@ -606,9 +606,11 @@ size_t smc_cache8_workspace_bytes(const smc_cache8 *cache, const smc_batch *batc
  * q and out have `dtype`, SMC_BF16 or SMC_F16; arguments and rows that see
  * nothing are otherwise as there.  head_dim a multiple of 16, at most 128;
  * pointers and the cache's strides in multiples of 16 bytes, those of q and out
- * in multiples of 8 elements.  Scores, statistics and sums are fp32; a row of q
- * keeps what is above 2^-18 of its largest element, and a weight what is above
- * 2^-28 of the row's largest weight times scale.  Equal inputs give equal bits. */
+ * in multiples of 8 elements.  Scores, statistics and sums are fp32.  Rounded are: a row
+ * of q, to what is above 2^-18 of its largest element; the weights times the
+ * scales of v, to fp16's eleven bits, and to nothing below 2^-24 of the row's
+ * largest one.  The scales of v that a row meets lie within a factor of 2^100 of
+ * one another.  Equal inputs give equal bits. */
 int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, int32_t layer,
                             const smc_batch *batch, int32_t dtype, const void *q,
                             const uint32_t *mask, void *out, float *lse, void *workspace,

@@ -6,9 +6,11 @@ Tolerances count roundings, with the terms of cache_cases.py and these:
    is left over is at most half of e4m3's smallest subnormal, 2^-10, where the
    row's largest element is over 224, so 2^-17.8 of that element.  A score is
    off by that times scale * s_k * sum |k8| more;
- - a weight goes into the product with v as an fp16 number in e5m2 pieces: half
-   a step of fp16 and what the third piece leaves, 2^-11 each, and nothing below
-   2^-28 of the row's largest weight times scale of v;
+ - a weight times its scale of v goes into the product with v as an fp16 number
+   in e5m2 pieces: half a step of fp16 and what the third piece leaves, 2^-11
+   each, and nothing below half of e5m2's least number, 2^-17, where the row's
+   largest is 2^7 at least (2^7 when its maximum is taken, 2^15 before it is
+   taken again): 2^-24 of that one;
  - an element of the cache is off by half a step of e4m3, 2^-4 of it, or half of
    the smallest subnormal, 2^-10 times its scale.
 """
@@ -22,7 +24,7 @@ from cache_cases import E32, CacheCase, half_step, half_subnormal
 E4M3 = torch.float8_e4m3fn
 Q_LEFT = 2.0 ** -17.8
 WEIGHT = 2.0 ** -10
-WEIGHT_FLOOR = 2.0 ** -28
+WEIGHT_FLOOR = 2.0 ** -24
 
 
 def least_scale(top):

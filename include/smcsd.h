@@ -609,8 +609,9 @@ size_t smc_cache8_workspace_bytes(const smc_cache8 *cache, const smc_batch *batc
  * in multiples of 8 elements.  Scores, statistics and sums are fp32.  Rounded are: a row
  * of q, to what is above 2^-18 of its largest element; the weights times the
  * scales of v, to fp16's eleven bits, and to nothing below 2^-24 of the row's
- * largest one.  The scales of v that a row meets lie within a factor of 2^100 of
- * one another.  Equal inputs give equal bits. */
+ * largest one.  The scales of v that a row meets lie within a factor of 2^108 of
+ * one another (a block of zeros has the least one, 2^-100).  Equal inputs give
+ * equal bits. */
 int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, int32_t layer,
                             const smc_batch *batch, int32_t dtype, const void *q,
                             const uint32_t *mask, void *out, float *lse, void *workspace,
@@ -626,7 +627,8 @@ int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, i
  *           the first new one, else need;
  *   x     = y / scale, rounded to e4m3 (to nearest, ties to even; past 448: 448).
  * Tokens ahead of the new ones are rounded again under a scale that has grown.
- * A row that is skipped (its position out of range) leaves its slot's bytes. */
+ * A row that is skipped (its position out of range) leaves its slot's bytes.
+ * Blocks that hold new tokens are one sequence's alone, as there. */
 int32_t smc_qk_norm_rope8(const smc_qk_params *p, const smc_cache8 *cache, int32_t layer,
                           const smc_batch *batch, int32_t dtype, const void *q, const void *k,
                           const void *v, const void *q_weight, const void *k_weight,

@@ -141,10 +141,7 @@ __device__ __forceinline__ void tmem_tie(uint32_t *r) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// The same as pairs, two times 16 columns, there when it returns.  In one
-// statement and in 64 bits: packed arithmetic takes the pairs where the loads put
-// them, while pairs made of loads that are waited for apart were moved first
-// (a third of a softmax loop's instructions).
+// The same as pairs, two times 16 columns, there when it returns.
 #define SMC_L8(r) "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7])
 __device__ __forceinline__ void tmem_get16x2(uint32_t a, uint32_t b, unsigned long long *x, unsigned long long *y) {
   asm volatile(

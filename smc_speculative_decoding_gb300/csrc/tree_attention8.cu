@@ -16,7 +16,7 @@
 //    2^8, tokens of 2^-18 and less of the largest weight would be lost, and a
 //    long context has many.)
 // The scales of k go to the scores.  Those of v go into the weights' exponents,
-//   w_j = 2^(z_j + log2 s_v(j) - M + 11),  out = sum w_j v8_j / sum w_j / s_v(j),
+//   w_j = 2^(z_j + log2 s_v(j) - M + 7),  out = sum w_j v8_j / sum w_j / s_v(j),
 // with M a running maximum of z + log2 s_v, so that weights stay in range
 // whatever the scales.
 //   The products are the transposed ones, S^T = K Q^T and O^T = V^T P^T: a tile's
@@ -60,8 +60,8 @@ struct Kernel8Args : WorkArgs {
   ScaleArgs sc8;
 };
 
-constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: kTopHalf) ...
-constexpr uint32_t kTopHalf = 0x7800;
+constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: 0x7800) ...
+constexpr uint32_t kPastTop = 0x07ff07ff;  // adds up to 0x8000 with what is more, as fp16
 constexpr float kTopFresh = 7.f; // ... and the largest one 2^kTopFresh when the maximum is taken
 constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
@@ -71,16 +71,27 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // (thread = token of a tile; warps w and w + 4 take the even and the odd chunks of
 // 16 rows; ahead of a segment they cut its rows of q into pieces, four threads a
 // row), warp 8 issues the matrix products, warp 9 finds the CTA's segments (parts
-// of units), copies K and V and prepares their scales.  Shared memory: two slots each of K and V tiles, q's
-// pieces, the weights' pieces.  Tensor memory, 64 columns each: two tiles'
-// scores, the accumulator, the sums of w / s_v (each lane's tokens').
+// of units), copies K and V and prepares their scales.  Shared memory: two slots
+// each of K and V tiles, q's pieces, the weights' pieces.  Tensor memory, 64
+// columns each: two tiles' scores, the accumulator, the sums of w / s_v (each
+// lane's tokens).
 //   A softmax thread's loop takes 16 rows at a time and keeps nothing of them in
-// registers: the code is short (with 64 rows unrolled, and the sums in registers,
-// a tile took 5200 cycles, half of them without an instruction at hand) and 16
-// warps fit on a multiprocessor.  Weights are taken on trust that none passes
-// 2^kTop, and written ahead of the vote that says so; the products start behind
-// it.  Where a maximum has risen, what the tile added to the sums is taken off
-// again, maxima, sums and accumulator are brought up, and the tile is taken anew.
+// registers.  64 trees of 16 tokens over up to 8192: 64 rows unrolled with the
+// sums in registers, 4 warps a CTA, 391 us; so, with 8 warps, 291; with the rows'
+// pieces cut by the same warps and so 96 registers each, 256.  Other ways since:
+// chunks of 8 rows 289, two chunks unrolled 320, the next chunk's scores loaded
+// ahead 274, 4 warps 277.
+//   Weights are taken on trust that none passes 2^kTop, and written ahead of the
+// vote that says so; the products start behind it.  Where a maximum has risen, what
+// the tile added to the sums of those chunks is taken off again, maxima, sums and
+// accumulator are brought up, and the chunks are taken anew (once: they cannot pass
+// again).  A timing copy whose maxima never rise took 262 us where this took 322.
+//   What bounds it: the softmax threads' instructions.  A tile's products keep the
+// tensor cores for 980 cycles (a product of 64 columns is bound by its operands'
+// way from shared memory, 49 cycles), its bytes the memory for 1400; a
+// multiprocessor takes 2500 cycles a tile.
+//   Measured: those 64 trees, 812 MB, 256 us, 3.2 TB/s; 131072 tokens of one
+// sequence, 269 MB, 101 us, of which 14 us start it; one token over 4096, 12 us.
 //   Every wait is bounded, and on a barrier all of whose turns the waiting
 // thread follows.
 // ---------------------------------------------------------------------------
@@ -417,9 +428,9 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         const float4 scales = s->token[buf][token];
         const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
         uint32_t todo = ~0u;  // chunks to take; at first all, then those with a new maximum (once)
+        uint32_t over = 0;    // of this warp: those where one of its weights passed 2^kTop
         for (bool known = i > 0, again = false;; known = true) {
           if (known) {
-            uint32_t over = 0;
 #pragma unroll 1
             for (int cb = half; cb < chunks; cb += 2) {
               if (!(todo >> cb & 1)) continue;
@@ -435,7 +446,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 z[e] = add2(fma2(z[e], mul2(a2, f2pack(c.x, c.y)), b2), f2pack(c.z, c.w));
               }
               if (edge) {
-                asm volatile("" ::: "memory");  // a branch: as selects it took every tile a third more instructions
                 const uint32_t some = static_cast<uint32_t>(see >> (cb * 16));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -455,9 +465,6 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 sum[e] = fma2(f2pack(w0, w1), c2, sum[e]);
                 asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(h[e]));
               }
-              __syncwarp();
-              tmem_put16(t_sum + cb * 16, sum);
-              if ((most & 0xffffu) > kTopHalf || most >> 16 > kTopHalf) over |= 1u << cb;
               // the weights' slots are free when the last product is done
               if (cb == half && tile > 0 && !(ok = warp_wait(s, &s->pv_done, (tile - 1) & 1u, status))) break;
               // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
@@ -475,6 +482,14 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
                 }
                 *reinterpret_cast<uint4 *>(p_at + piece * M::kPiece + cb * 2048) = make_uint4(p[0], p[1], p[2], p[3]);
               }
+              const bool past = __any_sync(0xffffffffu, (most + kPastTop) & 0x80008000u);
+              // (the sums go without weights that may be of any size; the second time none is)
+              if (again || !past) {
+                __syncwarp();
+                tmem_put16(t_sum + cb * 16, sum);
+              } else {
+                over |= 1u << cb;
+              }
             }
             if (!ok) break;
             if (edge) {
@@ -490,20 +505,20 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             __syncwarp();
             tmem_wait_st();
             tc_fence_before();
-            todo = group_or(again ? 0 : over);
+            todo = group_or(again || lane ? 0 : over);
             if (!ok || !todo) break;
             tc_fence_after();
             again = true;
           }
           // New maxima in these chunks, of every row whose weights would pass 2^kTopFresh while at it: a tile's largest
-          // z + log2 s_v.
-          // What the tile added to the sums is taken off again; where that was so much (2^60 and more) that nothing
-          // before it counts beside the row's largest weight, 0 is left.
+          // z + log2 s_v.  What the warp added to the sums is taken off again; it counts once more under the new
+          // maximum, so that its rounding here is small beside the sum.
           if (tid < 64) s->top[tid] = INT32_MIN;
           if (!(ok = group_sync())) break;
 #pragma unroll 1
           for (int cb = half; cb < chunks; cb += 2) {
             if (!(todo >> cb & 1)) continue;
+            const bool added = known && !(over >> cb & 1);
             uint32_t x[16], sum[16];
             __syncwarp();
             tmem_ld16(t_s + cb * 16, x);
@@ -525,22 +540,22 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               w0 = some >> e & 1 ? fast_exp2(w0) : 0.f;
               w1 = some >> (e + 1) & 1 ? fast_exp2(w1) : 0.f;
               f2unpack(fma2(f2pack(-w0, -w1), c2, f2pack(__uint_as_float(sum[e]), __uint_as_float(sum[e + 1]))), s0, s1);
-              sum[e] = w0 > 0x1p60f ? 0u : __float_as_uint(s0);
-              sum[e + 1] = w1 > 0x1p60f ? 0u : __float_as_uint(s1);
+              sum[e] = __float_as_uint(s0);
+              sum[e + 1] = __float_as_uint(s1);
             }
-            if (known) tmem_st16(t_sum + cb * 16, sum);
+            if (added) tmem_st16(t_sum + cb * 16, sum);
             const float top = transposed_max(x);
             if (lane < 16) atomicMax(&s->top[cb * 16 + lane], ordered(__float_as_int(top)));
           }
           tmem_wait_st();
           if (!(ok = group_sync())) break;
           if (tid < 64) {
-            float f = 1.f;
+            float f = 1.f;  // the factor's root: a factor itself may be less than fp32 holds, beside a sum of 2^75
             if (tid < w.rows && todo >> (tid >> 4) & 1) {
               const float top = __int_as_float(ordered(s->top[tid]));
               float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);
               if (top > -INFINITY && top + *less > kTopFresh) {
-                f = *less == kUnset ? 0.f : fast_exp2(kTopFresh - top - *less);
+                f = *less == kUnset ? 0.f : fast_exp2(0.5f * (kTopFresh - top - *less));
                 const float fresh = kTopFresh - top;
                 *less = top + fresh > kTop ? -top : fresh;  // where a step of fp32 is more than kTop - kTopFresh
               }
@@ -562,8 +577,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const float f = __int_as_float(s->top[cb * 16 + e]);
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                sum[e] = __float_as_uint(__uint_as_float(sum[e]) * f);
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * f * f);
+                sum[e] = __float_as_uint(__uint_as_float(sum[e]) * f * f);
               }
               tmem_st16(t_o + cb * 16, o);
               tmem_st16(t_sum + cb * 16, sum);
@@ -795,7 +810,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         int2 here = make_int2(0, 0), ahead = make_int2(0, 0);
         int from = -32;
         if constexpr (kTma) {
-          if (w.t0 + lane * k.box < t_end) ahead = place(w.t0 + lane * k.box);
+          if (lane * k.box < t_end - w.t0) ahead = place(w.t0 + lane * k.box);
         }
         for (int i = 0; i < w.n; ++i, ++tile) {
           const uint32_t slot = tile & 1u, turn = tile >> 1 & 1u;
@@ -812,8 +827,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
             if ((i + 1) * per_tile > from + 32) {
               from = i * per_tile;
               here = ahead;
-              const int t = t0 + (32 + lane) * k.box;
-              if (t < t_end) ahead = place(t);
+              const int on = (32 + lane) * k.box;  // (t0 + on may be past what 32 bits count)
+              if (on < t_end - t0) ahead = place(t0 + on);
             }
             const int boxes = (t1 - t0 + k.box - 1) / k.box, mine = i * per_tile - from + lane;
             const int block = __shfl_sync(0xffffffffu, here.x, mine & 31), token = __shfl_sync(0xffffffffu, here.y, mine & 31);
@@ -956,7 +971,7 @@ static cudaError_t launch8(const AttnArgs &a, const ScaleArgs &s, void *workspac
   Kernel8Args k{};
   k.a = a;
   k.sc8 = s;
-  // as for 16 bits: shared blocks are read once where reading them again is not the L2 cache's work
+  // as for 16 bits: shared blocks are read once where reading them again would not be the L2 cache's work
   const double table_bytes = static_cast<double>(a.b.S) * a.b.T * a.c.block_size * a.c.kv_heads * a.c.head_dim * 2;
   if (table_bytes < 96e6) k.a.b.group = 1;
   carve(a.c, k.a.b, a.q_heads, kMaxCtas8, 64, static_cast<char *>(workspace), &k.w);

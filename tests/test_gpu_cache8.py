@@ -234,6 +234,20 @@ def test_attention_of_scales_beyond_the_range():
         _check_attention(c, *_attend(c), want=want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("ctx,first,size", [(300, 8, 0), (300, 9, 8), (640, 24, 8), (3000, 8, 0), (3000, 160, 3)])
+def test_attention_of_zeros_ahead_of_values(ctx, first, size, dtype):
+    """Whole tiles of values that are zero, under the least scale, weigh as much as what follows them."""
+    c = Cache8Case([ctx, 20], [5, 5], heads=8, kv_heads=2, mask="tree", dtype=dtype)
+    size = min(size, 7) if dtype == torch.float16 else size  # (448 * 2^8 is out of fp16's range)
+    c.vs *= 2.0 ** size / c.vs.max().item()
+    for i in range(first):
+        b = c.tables[0, i]
+        bits(c.v)[0, b] = 0
+        c.vs[0, b] = 2.0 ** -100
+    _check_attention(c, *_attend(c))
+
+
 def test_attention_rows_past_the_last_sequence_are_untouched():
     c = Cache8Case([100, 50], [3, 2])
     rows = c.rows + 4

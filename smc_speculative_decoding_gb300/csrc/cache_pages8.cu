@@ -26,6 +26,9 @@ __device__ __forceinline__ U rescaled(U x, float f) {
 // is as it was: per block, first its new scales from those of the sources, then
 // the moves in their order (a place that is written is no later source, as the
 // path ascends), then, where a scale has grown, the tokens that stayed.
+//   Bytes bound it where there are many: 64 paths in 32 layers, 76 MB, 26 us, 2.9
+// TB/s, in three dependent round trips (places, scales, elements); with a CTA for
+// each block, and its threads over tokens and columns, 68.
 template <typename U>
 __global__ void __launch_bounds__(kThreads8)
 compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *path, const int32_t *n_path,

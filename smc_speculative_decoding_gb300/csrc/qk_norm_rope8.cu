@@ -94,6 +94,8 @@ __device__ __forceinline__ float norm_of(const QkArgs &a, const T *src, const T 
 
 // Any sizes, strides and alignment: a warp per vector, each lane elements lane,
 // lane + 32, ...; keys are computed for the block's scale and again to be stored.
+// (1280 rows of 32 + 8 + 8 heads of 128 107 us, 12535 rows 716 us; with the
+// vectors below 24 and 185.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads8)
 append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleArgs sc, int per) {
@@ -196,6 +198,11 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
 //   Keys are rounded step by step, x r, then w, then the rotation's products, as
 // plain fp32 does: where the largest one lies beside a power of two, its last bit
 // decides the scale.
+//   12535 rows of 32 + 8 + 8 heads, 300 MB: 185 us, 1.6 TB/s, bound by issue slots
+// (16 warps a multiprocessor at 128 registers); with a warp per vector and a
+// vector's loads apart 245.  1280 rows, 29 MB: 24 us, a chain of dependent loads
+// (offsets, lengths, table, rows, the block's scale) for which each of many small
+// CTAs waits by itself; with CTAs of 256 threads throughout 46.
 // ---------------------------------------------------------------------------
 constexpr int kKept = 2;
 constexpr int kAhead8 = 4;  // queries of a group whose loads are under way at once

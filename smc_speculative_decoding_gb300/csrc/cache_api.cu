@@ -319,8 +319,8 @@ int32_t smc_qk_norm_rope8(const smc_qk_params *p, const smc_cache8 *cache, int32
   if (!p || !cache) return SMC_ERR_ARG;
   if (cache->data.dtype != SMC_E4M3 || !dtype_ok(dtype)) return SMC_ERR_DTYPE;
   QkArgs a;
-  // (a CTA takes a key head, on the grid's second axis)
-  if (!cache8_ok(cache) || cache->data.kv_heads > 65535 ||
+  // (a CTA takes a key head, one more the queries, on the grid's second axis)
+  if (!cache8_ok(cache) || cache->data.kv_heads > 65534 ||
       !qk_args(p, &cache->data, layer, batch, dtype, q, k, v, q_weight, k_weight, positions, rope, q_out,
                workspace, &a)) {
     return SMC_ERR_ARG;

@@ -10,7 +10,8 @@ constexpr int kWarps8 = kThreads8 / 32;
 // Work: a *run* is the new tokens of one sequence that lie in one block; its
 // keys and values of one head share a scale.  CTA (x, h) takes the runs that
 // begin in rows [x * per, (x + 1) * per): for each, key head h's keys and
-// values, and the query heads h, h + kv_heads, ...
+// values, and query heads (the scalar kernel's) or, in CTAs of their own past
+// those of the key heads, query heads alone (the vectors').
 struct Run {
   int row, n;      // rows [row, row + n)
   int seq, at;     // the first one's place in its table
@@ -95,7 +96,7 @@ __device__ __forceinline__ float norm_of(const QkArgs &a, const T *src, const T 
 // Any sizes, strides and alignment: a warp per vector, each lane elements lane,
 // lane + 32, ...; keys are computed for the block's scale and again to be stored.
 // (1280 rows of 32 + 8 + 8 heads of 128 107 us, 12535 rows 716 us; with the
-// vectors below 24 and 185.)
+// vectors below 21 and 135.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads8)
 append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleArgs sc, int per) {
@@ -193,22 +194,24 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
 // The same with 16-byte accesses: a vector per group of kLanes lanes.  A run's
 // keys and values are dealt to the groups, computed once, and stay in registers
 // while the largest of them is found (kKept vectors a group; what is more is
-// computed again); the queries, which need no scale, are worked on before the
-// CTA waits for it.
+// computed again).  The queries, which need no scale, are other CTAs' work, where
+// a row's angles and weights serve several heads.
 //   Keys are rounded step by step, x r, then w, then the rotation's products, as
 // plain fp32 does: where the largest one lies beside a power of two, its last bit
 // decides the scale.
-//   12535 rows of 32 + 8 + 8 heads, 300 MB: 185 us, 1.6 TB/s, bound by issue slots
-// (16 warps a multiprocessor at 128 registers); with a warp per vector and a
-// vector's loads apart 245.  1280 rows, 29 MB: 24 us, a chain of dependent loads
-// (offsets, lengths, table, rows, the block's scale) for which each of many small
-// CTAs waits by itself; with CTAs of 256 threads throughout 46.
+//   A run is a chain of dependent loads (offsets, lengths, table, rows, the block's
+// scale), and what hides one is other runs: the registers are bound to what 32
+// warps a multiprocessor have, though some go to local memory.  12535 rows of 32 +
+// 8 + 8 heads, 300 MB: 135 us, 2.2 TB/s (24 warps 156, 16 without a spill 195; keys,
+// values and queries in one CTA, 16 warps, 185; CTAs of 512 threads 135).  1280
+// rows, 29 MB: 21 us, with CTAs of 256 threads throughout 46.
 // ---------------------------------------------------------------------------
 constexpr int kKept = 2;
+constexpr int kQueryCtas = 912;  // (with 24 warps: half as many 22.9 and 156 us, these 20.3 and 156, four times as many 21.6 and 162)
 constexpr int kAhead8 = 4;  // queries of a group whose loads are under way at once
 
 template <typename T, int kLanes, bool kInter>
-__global__ void __launch_bounds__(kThreads8, 2)
+__global__ void __launch_bounds__(kThreads8, 4)
 append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleArgs sc, int per) {
   constexpr int E = 16 / sizeof(T);
   __shared__ int s_top[2];
@@ -219,7 +222,9 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
   turn.place(a);
   const bool has = turn.has;
   const float inv_dim = 1.f / a.c.head_dim;
-  const int nq = h < a.q_heads ? (a.q_heads - h + a.c.kv_heads - 1) / a.c.kv_heads : 0;  // query heads h, h + kv_heads, ...
+  // CTAs past those of the key heads take query heads h0, h0 + parts, ...
+  const bool queries = h >= a.c.kv_heads;
+  const int parts = gridDim.y - a.c.kv_heads, h0 = h - a.c.kv_heads, nq = (a.q_heads - h0 + parts - 1) / parts;
   wait_for_stream();
   const int r0 = blockIdx.x * per;
   Runs runs(a, r0, min(r0 + per, a.b.rows));
@@ -239,6 +244,41 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
                                                                static_cast<int64_t>(sizeof(T)) + vec * 16)
                  : make_uint4(0, 0, 0, 0);
     };
+    if (queries) {
+      // Queries: a group takes rows group, group + groups, ..., and with fewer rows than groups, as many groups share a row's heads.
+      const int share = n < groups ? groups / n : 1, phase = n < groups ? group / n : 0;
+      const int q_row0 = n < groups ? group - phase * n : group, q_step = groups;
+      const int64_t head_step = static_cast<int64_t>(share) * parts * a.q_head * static_cast<int64_t>(sizeof(T)),
+                    out_step = static_cast<int64_t>(share) * parts * a.o_head * static_cast<int64_t>(sizeof(T));
+      const bool any_q = phase < share && has;
+      auto query_at = [&](int i) {
+        return a.q + ((run.row + i) * a.q_row + (h0 + phase * parts) * a.q_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
+      };
+      for (int i0 = 0; i0 < n; i0 += q_step) {
+        const int i = i0 + q_row0, pos = i < n ? position(i) : -1;
+        const bool writes = any_q && pos >= 0;
+        char *out = a.out + ((run.row + i) * a.o_row + (h0 + phase * parts) * a.o_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
+        const char *q = query_at(i);
+        for (int g0 = 0; g0 < nq; g0 += kAhead8 * share) {  // (of phase 0: the same number of turns for all lanes)
+          uint4 rq[kAhead8];
+#pragma unroll
+          for (int t = 0; t < kAhead8; ++t) {
+            rq[t] = any_q && i < n && g0 + phase + t * share < nq ? *reinterpret_cast<const uint4 *>(q + t * head_step)
+                                                                   : make_uint4(0, 0, 0, 0);
+          }
+          if (g0 == 0 && pos >= 0) turn.load(a, table_of(pos), a.qw);
+#pragma unroll
+          for (int t = 0; t < kAhead8; ++t) {
+            if (g0 + t * share >= nq) break;  // for the whole CTA
+            const uint4 z = turn.apply(rq[t], a.qw != nullptr, inv_dim, a.eps);
+            if (writes && g0 + phase + t * share < nq) *reinterpret_cast<uint4 *>(out + t * out_step) = z;
+          }
+          q += kAhead8 * head_step;
+          out += kAhead8 * out_step;
+        }
+      }
+      continue;
+    }
     // (read early: its use is at the end of a chain of loads)
     float *const scale_at = (tid == 1 ? sc.v : sc.k) + block * sc.block + h * sc.head;
     const float before = tid < 2 && off ? *scale_at : 0.f;
@@ -305,24 +345,6 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
       }
       return top;
     };
-    // Queries: a group takes rows group, group + groups, ..., and with fewer rows than groups, as many groups share a row's heads.
-    const int share = n < groups ? groups / n : 1, phase = n < groups ? group / n : 0;
-    const int q_row0 = n < groups ? group - phase * n : group, q_step = groups;
-    const int64_t head_step = static_cast<int64_t>(share) * a.c.kv_heads * a.q_head * static_cast<int64_t>(sizeof(T)),
-                  out_step = static_cast<int64_t>(share) * a.c.kv_heads * a.o_head * static_cast<int64_t>(sizeof(T));
-    const bool any_q = phase < share && has;
-    auto query_at = [&](int i) {
-      return a.q + ((run.row + i) * a.q_row + (h + phase * a.c.kv_heads) * a.q_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
-    };
-    // the first ones are on their way while keys and values are worked on
-    uint4 rq[kAhead8];
-    {
-      const char *q = query_at(q_row0);
-#pragma unroll
-      for (int t = 0; t < kAhead8; ++t, q += head_step) {
-        rq[t] = any_q && q_row0 < n && phase + t * share < nq ? *reinterpret_cast<const uint4 *>(q) : make_uint4(0, 0, 0, 0);
-      }
-    }
     __syncthreads();
     if (tid < 2) s_top[tid] = 0;
     if (tid < n && h == 0 && position(tid) < 0) raise_status(a.status, SMC_DEV_BAD_ROWS);
@@ -352,31 +374,6 @@ append8_vectors_kernel(const __grid_constant__ QkArgs a, const __grid_constant__
     for (int w = 0; w < 2; ++w) {
       const int m = __reduce_max_sync(0xffffffffu, __float_as_int(top[w]));  // of positive numbers: their bits' order
       if ((tid & 31) == 0 && m) atomicMax(&s_top[w], m);
-    }
-    // the queries
-    for (int i0 = 0; i0 < n; i0 += q_step) {
-      const int i = i0 + q_row0, pos = i < n ? position(i) : -1;
-      const bool writes = any_q && pos >= 0;
-      if (pos >= 0) turn.load(a, table_of(pos), a.qw);
-      char *out = a.out + ((run.row + i) * a.o_row + (h + phase * a.c.kv_heads) * a.o_head) * static_cast<int64_t>(sizeof(T)) + vec * 16;
-      const char *q = query_at(i);
-      for (int g0 = 0; g0 < nq; g0 += kAhead8 * share) {  // (of phase 0: the same number of turns for all lanes)
-        if (i0 > 0 || g0 > 0) {
-#pragma unroll
-          for (int t = 0; t < kAhead8; ++t) {
-            rq[t] = any_q && i < n && g0 + phase + t * share < nq ? *reinterpret_cast<const uint4 *>(q + t * head_step)
-                                                                   : make_uint4(0, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < kAhead8; ++t) {
-          if (g0 + t * share >= nq) break;  // for the whole CTA
-          const uint4 z = turn.apply(rq[t], a.qw != nullptr, inv_dim, a.eps);
-          if (writes && g0 + phase + t * share < nq) *reinterpret_cast<uint4 *>(out + t * out_step) = z;
-        }
-        q += kAhead8 * head_step;
-        out += kAhead8 * out_step;
-      }
     }
     __syncthreads();
     if (tid < 2) {
@@ -471,8 +468,13 @@ cudaError_t launch_qk_norm_rope8(const QkArgs &a, const ScaleArgs &s, int dtype,
     // of their chains of dependent loads run side by side
     const int64_t most = static_cast<int64_t>(per) * lanes;
     const int threads = most >= kThreads8 ? kThreads8 : most <= 64 ? 64 : static_cast<int>((most + 31) / 32 * 32);
+    // queries: CTAs to fill the multiprocessors, and no more: a row's angles and weights serve all heads of a CTA
+    const int groups = (a.b.rows + per - 1) / per, most_parts = a.q_heads < a.c.kv_heads ? a.q_heads : a.c.kv_heads;
+    int parts = (kQueryCtas + groups - 1) / groups;
+    parts = parts > most_parts ? most_parts : parts;
+    parts = parts > 65535 - a.c.kv_heads ? 65535 - a.c.kv_heads : parts;  // (the grid's second axis)
     void *args[] = {const_cast<QkArgs *>(&a), &scales, &per};
-    return launch_early(fn, dim3((a.b.rows + per - 1) / per, a.c.kv_heads), threads, 0, args, st);
+    return launch_early(fn, dim3(groups, a.c.kv_heads + parts), threads, 0, args, st);
   }
   const void *fn = dtype == SMC_F32    ? reinterpret_cast<const void *>(append8_kernel<float>)
                    : dtype == SMC_BF16 ? reinterpret_cast<const void *>(append8_kernel<__nv_bfloat16>)

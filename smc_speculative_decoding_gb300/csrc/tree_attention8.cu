@@ -86,7 +86,8 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // the tile added to the sums of those chunks is taken off again, maxima, sums and
 // accumulator are brought up, and the chunks are taken anew (once: they cannot pass
 // again).  A timing copy whose maxima never rise took 262 us where this took 322.
-//   What bounds it: the softmax threads' instructions.  A tile's products keep the
+//   What bounds it: the softmax, half of the issue slots and waits for tensor
+// memory, exponentials and the vote between them.  A tile's products keep the
 // tensor cores for 980 cycles (a product of 64 columns is bound by its operands'
 // way from shared memory, 49 cycles), its bytes the memory for 1400; a
 // multiprocessor takes 2500 cycles a tile.

@@ -1,6 +1,7 @@
 // An accepted path of an 8-bit cache moved to the front of its sequence's new
 // tokens (kv_compact_tokens8 in smcsd.h).
 #include "cache_common.cuh"
+#include "path_places.h"
 
 namespace smcsd {
 
@@ -52,11 +53,10 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
   float *scale = ((blockIdx.y & 1) ? sc.v : sc.k) + layer * sc.layer + head0 * sc.head;
   const int bs = c.block_size, first = si.len - si.n, per_head = c.head_dim / static_cast<int>(sizeof(U));
   const int cols = per_head * here;
+  const PathPlaces places{first, si.n, n, bs};
   if (tid == 0) s_last = -1;
   for (int i0 = 0; i0 < n;) {
-    // whole blocks, as many as the places have room for
-    const int off0 = (first + i0) % bs;
-    const int i1 = min(n, i0 + (off0 + kMoves8) / bs * bs - off0);
+    const int i1 = places.end(i0, kMoves8);
     __syncthreads();  // s_last is set; the last places have been read
     for (int r = i0; r < i1; r += threads) {
       const int i = r + tid;
@@ -81,10 +81,11 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
       if (i < i1) {
         const bool good = in && mine > before && mine >= i;
         unsigned bits = good ? 0 : SMC_DEV_BAD_ROWS;
-        int block = -1;
+        int block = -1, token = 0;
         if (good && mine != i) {
           const int to = table[(first + i) / bs];
           block = table[(first + mine) / bs];
+          token = (first + mine) % bs;
           if (to < 0 || to >= c.blocks || block < 0 || block >= c.blocks) {
             bits |= SMC_DEV_BAD_BLOCK;
             block = -1;
@@ -92,13 +93,13 @@ compact_tokens8_kernel(CacheArgs c, ScaleArgs sc, BatchArgs b, const int32_t *pa
         }
         if (bits && reports) raise_status(status, bits);
         s_block[i - i0] = block;
-        s_token[i - i0] = (first + max(mine, 0)) % bs;
+        s_token[i - i0] = token;
       }
       __syncthreads();
     }
     // the blocks that tokens move into
-    for (int from = i0; from < i1;) {
-      const int slot = (first + from) / bs, to = min(i1, (slot + 1) * bs - first), off = first + from - slot * bs;
+    for (int from = i0, last = places.moves_end(i1); from < last;) {
+      const int slot = places.slot(from), to = places.slot_end(from, last), off = first + from - slot * bs;
       const int moves = to - from, at = from - i0;
       const int block = table[slot];
       from = to;

@@ -608,8 +608,10 @@ size_t smc_cache8_workspace_bytes(const smc_cache8 *cache, const smc_batch *batc
  * pointers and the cache's strides in multiples of 16 bytes, those of q and out
  * in multiples of 8 elements.  Scores, statistics and sums are fp32.  Rounded are: a row
  * of q, to what is above 2^-18 of its largest element; the weights times the
- * scales of v, to fp16's eleven bits, and to nothing below 2^-24 of the row's
- * largest one.  The scales of v that a row meets lie within a factor of 2^108 of
+ * scales of v, to fp16's eleven bits, below 2^-14 of the row's largest one to a
+ * multiple of 2^-24 of that, up or down by the token's place so that many small
+ * ones keep their sum, and to nothing below 2^-33 (of n tokens, n * 2^-33 of the
+ * largest one is what can be missing).  The scales of v that a row meets lie within a factor of 2^108 of
  * one another (a block of zeros has the least one, 2^-100).  Equal inputs give
  * equal bits. */
 int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, int32_t layer,

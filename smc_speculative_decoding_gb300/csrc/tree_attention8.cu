@@ -11,12 +11,17 @@
 //    so two hold bf16's eight and three fp16's eleven (down to 2^-10 beside a
 //    largest element of 224 to 448);
 //  - a weight w <= 2^15, as fp16, into three e5m2 pieces: three significant bits
-//    and a sign each, 2^-11 of w left over, and half of 2^-16 where w is small.
+//    and a sign each hold fp16's eleven down to w = 2^-6.  The least piece is
+//    2^-16; what a smaller weight has below that is rounded up or down by the
+//    token's place (small_part), so that many tokens of one small weight come to
+//    their sum.  (Rounded to nearest, all of them would be off to the same side:
+//    20000 tokens of 2^-21.6 of the largest weight by 17 %, of 2^-24.5 by all that
+//    they add.)  What fp16 drops is 2^-25, 2^-33 of a largest weight of 2^8.
 //    (e4m3 has two bits more in two pieces, but ends at 2^-9: beside a weight of
 //    2^8, tokens of 2^-18 and less of the largest weight would be lost, and a
 //    long context has many.)
 // The scales of k go to the scores.  Those of v go into the weights' exponents,
-//   w_j = 2^(z_j + log2 s_v(j) - M + 7),  out = sum w_j v8_j / sum w_j / s_v(j),
+//   w_j = 2^(z_j + log2 s_v(j) - M + 8),  out = sum w_j v8_j / sum w_j / s_v(j),
 // with M a running maximum of z + log2 s_v, so that weights stay in range
 // whatever the scales.
 //   The products are the transposed ones, S^T = K Q^T and O^T = V^T P^T: a tile's
@@ -62,7 +67,7 @@ struct Kernel8Args : WorkArgs {
 
 constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: 0x7800) ...
 constexpr uint32_t kPastTop = 0x07ff07ff;  // adds up to 0x8000 with what is more, as fp16
-constexpr float kTopFresh = 7.f; // ... and the largest one 2^kTopFresh when the maximum is taken
+constexpr float kTopFresh = 8.f; // ... and the largest one 2^kTopFresh when the maximum is taken
 constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 
@@ -158,6 +163,14 @@ __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// What is added to a weight's last fp16 part (twice) before its lower byte is
+// dropped, so that it is rounded to e5m2: 0 to 255 by a token's place, the
+// golden ratio's multiples, which any run of places covers evenly.  A part that
+// e5m2 holds has a lower byte of 0 and stays as it is.
+__device__ __forceinline__ uint32_t small_part(int place) {
+  return (static_cast<uint32_t>(place) * 40503u >> 8 & 0xffu) * 0x00010001u;
 }
 
 // The order of floats in that of ints (and back: its own inverse).
@@ -428,6 +441,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         tc_fence_after();
         const float4 scales = s->token[buf][token];
         const unsigned long long a2 = f2dup(scales.x), b2 = f2dup(scales.y), c2 = f2dup(scales.z);
+        const uint32_t last = small_part(at);
         uint32_t todo = ~0u;  // chunks to take; at first all, then those with a new maximum (once)
         uint32_t over = 0;    // of this warp: those where one of its weights passed 2^kTop
         for (bool known = i > 0, again = false;; known = true) {
@@ -468,12 +482,12 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
               }
               // the weights' slots are free when the last product is done
               if (cb == half && tile > 0 && !(ok = warp_wait(s, &s->pv_done, (tile - 1) & 1u, status))) break;
-              // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step
+              // pieces: e5m2 is fp16's upper byte, rounded by adding half of its step (the last one: see small_part)
 #pragma unroll
               for (int piece = 0; piece < 3; ++piece) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                  const uint32_t u = h[e] + 0x00800080u, v = h[e + 1] + 0x00800080u;
+                  const uint32_t u = h[e] + (piece < 2 ? 0x00800080u : last), v = h[e + 1] + (piece < 2 ? 0x00800080u : last);
                   p[e / 2] = __byte_perm(u, v, 0x7531);
                   if (piece < 2) {
                     const uint32_t hu = u & 0xff00ff00u, hv = v & 0xff00ff00u;
@@ -551,7 +565,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           tmem_wait_st();
           if (!(ok = group_sync())) break;
           if (tid < 64) {
-            float f = 1.f;  // the factor's root: a factor itself may be less than fp32 holds, beside a sum of 2^75
+            float f = 1.f;  // the factor's root: a factor itself may be less than fp32 holds, beside a sum of 2^76
             if (tid < w.rows && todo >> (tid >> 4) & 1) {
               const float top = __int_as_float(ordered(s->top[tid]));
               float *less = reinterpret_cast<float *>(&s->col[tid >> 1]) + 2 + (tid & 1);

@@ -1,11 +1,14 @@
 """The 8-bit paged cache's operators at the edges of what their calls may say,
 against 64-bit references."""
+import math
+
 import pytest
 import torch
 
 import smc_speculative_decoding_gb300 as smcsd
 
-from cache8_cases import Cache8Case, compacted
+from cache8_cases import E4M3, WEIGHT, Cache8Case, bits, compacted
+from cache_cases import E32, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +42,71 @@ def test_compact_of_a_path_longer_than_its_new_tokens(block, new, n):
     for name, x, s in (("k", c.k, c.ks), ("v", c.v, c.vs)):
         data, scale = want[name]
         assert torch.equal(s.double(), scale) and torch.equal(x.double(), data)
+
+
+# ---- attention ------------------------------------------------------------------
+
+def _beside_a_heavy_token(n, gap, dtype, noise=0.0, sequences=304, dim=64):
+    """`sequences` sequences of one new token over the same n + 1 tokens: the first of them `gap` nats over the others
+    and of no value, the others' scores alike (or spread by `noise`), their values positive and alike in each dim.  So
+    many sequences that a multiprocessor takes whole ones: every weight has the first token's beside it."""
+    g = torch.Generator().manual_seed(n)
+    block, blocks = 16, -(-(n + 1) // 16)
+    k, v = torch.zeros((1, blocks, block, 1, dim)), torch.zeros((1, blocks, block, 1, dim))
+    k[0, 0, 0, 0, 0] = 448
+    k[..., 1] = torch.randn((1, blocks, block, 1), generator=g) * 64 if noise else 0
+    k[0, 0, 0, 0, 1] = 0
+    grid = torch.arange(0x38, 0x38 + 46, dtype=torch.uint8).view(E4M3).float()  # 1 to 52
+    v[:] = grid[torch.arange(dim) % 46]
+    v[0, 0, 0] = 0
+    # blocks' scales: one for all, or powers of two with the heavy token's the least of them
+    size = torch.exp2(torch.randint(-3, 4, (1, blocks, 1), generator=g).float()) if noise else torch.full((1, blocks, 1), 0.25)
+    size[0, 0, 0] = size.min()
+    v = (v / size[..., None, None]).to(E4M3)
+    k = k.to(E4M3)
+    c = dict(k=k.cuda(), v=v.cuda(), ks=torch.ones_like(size).cuda(), vs=size.cuda())
+    scale = 2.0 ** -12
+    q = torch.zeros((sequences, 1, dim), dtype=dtype)
+    q[..., 0] = gap / (448 * scale)
+    q[..., 1] = noise / (64 * scale)
+    table = torch.arange(blocks, dtype=torch.int32).expand(sequences, -1).contiguous()
+    c.update(q=q.cuda(), scale=scale, tables=table.cuda(), seq_len=torch.full((sequences,), n + 1, dtype=torch.int32).cuda())
+    kk = k.double().reshape(-1, dim)[:n + 1]
+    vv = (v.double() * size.double()[..., None, None]).reshape(-1, dim)[:n + 1]
+    z = scale * (kk @ q[0, 0].double())
+    w = torch.exp(z - z[0])
+    c.update(want=(w[1:] @ vv[1:] / w.sum()).cuda(), lse=(z[0] + w.sum().log()).item(), w=w)
+    return c
+
+
+# 131072 tokens are a gap of 11.8 nats' mass beside the heavy one
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,gap,noise", [(20000, 11.0, 0), (20000, 14.0, 0), (20000, 15.0, 0), (20000, 16.5, 0),
+                                         (20000, 17.0, 0), (20000, 18.0, 0), (20000, 20.0, 0), (20000, 17.0, 0.5),
+                                         (3000, 16.5, 0), (3000, 15.0, 1.0)])
+def test_many_small_weights_beside_a_heavy_token(n, gap, noise, dtype):
+    """What falls to the many keeps its size, however small each one's share.
+
+    The output is the small weights' sum alone.  A weight is off by half of fp16's step: 2^-11 of it, or half of
+    2^-24 where the heavy one is 2^8; by WEIGHT for its pieces while it is over 2^-6 there.  Less of it is a multiple
+    of 2^-16, up or down by the token's place: over consecutive places these are off by a few steps in all (a golden
+    ratio's multiples: at most two for each of the 26 Fibonacci numbers below 131072, so 52), not by half a step each."""
+    c = _beside_a_heavy_token(n, gap, dtype, noise)
+    w = c["w"][1:] * 2.0 ** 8
+    small = w.clamp(max=2.0 ** -6)
+    half = torch.maximum(2.0 ** -11 * w, torch.full_like(w, 2.0 ** -25)).sum() / w.sum()
+    steps = 52 * 2.0 ** -16 / w.sum() if small.min() < 2.0 ** -6 else 0.0
+    if noise:  # (weights of all sizes: their steps are as good as independent, 6 standard deviations of half a step)
+        steps = 6 * 0.5 * 2.0 ** -16 * math.sqrt(n) / w.sum()
+    score = 2 * (66 * E32 + 2.0 ** -17.8) * gap * 1.01 + 2.0 ** -19 + 2 * n * E32
+    rel = (half + steps + WEIGHT + score + half_step(dtype)).item() * 1.01
+    assert rel < 0.5  # an output without the small weights is off by 1
+    cache = smcsd.make_cache8(c["k"], c["v"], c["ks"], c["vs"])
+    batch = smcsd.make_batch(c["tables"], c["seq_len"], 1)
+    ws = smcsd.alloc_cache8_workspace(cache, batch, 1)
+    out, lse = torch.empty_like(c["q"]), torch.empty(c["q"].shape[:2], device="cuda")
+    smcsd.smc_tree_attention8(cache, 0, batch, c["q"], out, ws, lse=lse, scale=c["scale"])
+    assert smcsd.smc_device_status(ws) == 0
+    off = ((out.double() - c["want"]) / c["want"]).abs().max().item()
+    assert off <= rel, (off, rel)
+    assert (lse.double() - c["lse"]).abs().max().item() <= score + 4 * E32 * (1 + c["lse"])

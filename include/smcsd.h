@@ -584,7 +584,8 @@ int32_t kv_truncate(const smc_params *p, const smc_kv *kv, const int32_t *new_le
  * Conventions, batches, status bits and the order behind the kernels ahead are
  * those of the entry points above.  One workspace of
  * smc_cache8_workspace_bytes() for the largest batch, zero-filled once, serves
- * all of them on one stream. */
+ * all of them on one stream; of the larger of that and
+ * smc_cache_workspace_bytes(), those above too, in any order. */
 
 /* An 8-bit cache: data.dtype SMC_E4M3 (strides in elements, that is in bytes);
  * element (layer, block, head) of k_scale, and of v_scale, is at

@@ -22,6 +22,10 @@ namespace smcsd {
 // segment) and stores it in its own slot.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+// Most CTAs of either kernel.  What has to be zero between calls (the header and
+// the tickets) lies alike in every layout, so that calls of other shapes, and of
+// the other cache's width, may follow one another in a workspace.
+constexpr int kMostCtas = 384;
 
 struct Entry {
   int row0;    // first row
@@ -47,7 +51,7 @@ struct PlanHeader {
 
 struct AttnWorkspace {
   PlanHeader *head;
-  unsigned *tickets;  // [ctas] parts stored of the unit that a CTA's end cuts; return to zero
+  unsigned *tickets;  // [kMostCtas] parts stored of the unit that a CTA's end cuts; return to zero
   int *common;     // [groups] shared tokens
   int *ref;        // [groups] the sequence by whose table they are read
   int *tile0;      // [entries + 1]
@@ -75,7 +79,7 @@ inline size_t carve(const CacheArgs &c, const BatchArgs &b, int q_heads, int cta
   t.n_entries = b.S + t.groups;
   take(kCacheStatusBytes);
   t.head = reinterpret_cast<PlanHeader *>(take(sizeof(PlanHeader)));
-  t.tickets = reinterpret_cast<unsigned *>(take(sizeof(unsigned) * ctas));
+  t.tickets = reinterpret_cast<unsigned *>(take(sizeof(unsigned) * kMostCtas));
   t.common = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
   t.ref = reinterpret_cast<int *>(take(sizeof(int) * t.groups));
   t.tile0 = reinterpret_cast<int *>(take(sizeof(int) * (static_cast<size_t>(t.n_entries) + 1)));

@@ -25,6 +25,7 @@ constexpr int kTile = 64;         // tokens per tile
 constexpr int kRows = 128;        // rows of a tensor-core tile
 constexpr int kUnitRows = 256;    // most rows of a unit: two tensor-core tiles of 128
 constexpr int kMaxCtas = 192;     // slots for continuations
+static_assert(kMaxCtas <= kMostCtas, "tickets");
 
 size_t attention_workspace_bytes(const CacheArgs &c, const BatchArgs &b, int q_heads) {
   return carve(c, b, q_heads, kMaxCtas, kUnitRows, nullptr, nullptr);

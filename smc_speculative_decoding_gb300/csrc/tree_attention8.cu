@@ -39,6 +39,7 @@ namespace smcsd {
 
 constexpr int kTile8 = 128;    // tokens per tile
 constexpr int kMaxCtas8 = 384; // slots for continuations
+static_assert(kMaxCtas8 <= kMostCtas, "tickets");
 constexpr int kCtasPerSm = 2;
 constexpr int kThreads8 = 320;
 constexpr int kSegs8 = 4;      // segments found ahead

@@ -8,7 +8,7 @@ import torch
 import smc_speculative_decoding_gb300 as smcsd
 
 from cache8_cases import E4M3, WEIGHT, Cache8Case, bits, compacted
-from cache_cases import E32, half_step
+from cache_cases import E32, CacheCase, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +110,29 @@ def test_many_small_weights_beside_a_heavy_token(n, gap, noise, dtype):
     off = ((out.double() - c["want"]) / c["want"]).abs().max().item()
     assert off <= rel, (off, rel)
     assert (lse.double() - c["lse"]).abs().max().item() <= score + 4 * E32 * (1 + c["lse"])
+
+
+@pytest.mark.parametrize("group,sequences", [(1, 300), (4, 320)])
+def test_calls_on_caches_of_both_widths_share_a_workspace(group, sequences):
+    """A draft in 16 bits and a target in 8, by turns, in one workspace: each call's parts are joined whatever the
+    calls before it left there."""
+    wide = CacheCase([150] * sequences, [1] * sequences, heads=8, kv_heads=2, group=group,
+                     shared=128 if group > 1 else 0, slots=2000 if group > 1 else 0)
+    long16 = CacheCase([20000], [1], heads=8, kv_heads=8, dim=64)
+    long8 = Cache8Case([20000], [1], heads=8, kv_heads=8, dim=64)
+    wide8 = Cache8Case([150] * sequences, [1] * sequences, heads=8, kv_heads=2, group=group,
+                       shared=128 if group > 1 else 0, slots=4000 if group > 1 else 0)
+    calls = []
+    for c, eight in ((wide, False), (long8, True), (long16, False), (wide8, True), (long8, True), (wide, False)):
+        sizes, call = (smcsd.smc_cache8_workspace_bytes, smcsd.smc_tree_attention8) if eight else \
+            (smcsd.smc_cache_workspace_bytes, smcsd.smc_tree_attention)
+        cache, batch = c.cache(smcsd), c.batch(smcsd)
+        out = torch.full((c.rows, c.heads, c.dim), 7.0, dtype=c.dtype, device="cuda")
+        calls.append((c, call, cache, batch, out, sizes(cache, batch, c.heads)))
+    ws = torch.zeros(max(call[-1] for call in calls), dtype=torch.uint8, device="cuda")
+    for c, call, cache, batch, out, _ in calls:
+        call(cache, 0, batch, c.q, out, ws, scale=c.scale)
+    assert smcsd.smc_device_status(ws) == 0
+    for c, _, _, _, out, _ in calls:
+        ref, _, tol, _ = c.reference()
+        assert ((out.double() - ref).abs() <= tol).all()

@@ -63,12 +63,18 @@ struct Runs {
   }
 };
 
+// Keys are rounded step by step, x r, then w, then the rotation's products, as
+// plain fp32 does, and the sum of a norm is taken in one order (eight or four
+// neighbours each lane, then across the lanes) by both kernels below: where a
+// block's largest key lies beside a power of two, its last bit decides the scale,
+// and neither alignment nor strides have a say in it.
+
 // Element d of a vector after norm (r = rsqrt of the mean square) and rotation.
 template <typename T>
 __device__ __forceinline__ float turned(const QkArgs &a, const T *src, const T *w, float r, const float *cs, int d) {
   auto normed = [&](int e) {
-    const float x = to_f32(src[e]) * r;
-    return w ? x * (to_f32(w[e]) + a.w0) : x;
+    const float x = to_f32(src[e]);
+    return w ? __fmul_rn(__fmul_rn(x, r), to_f32(w[e]) + a.w0) : x;
   };
   const float y = normed(d);
   if (d >= a.rot) return y;
@@ -76,21 +82,26 @@ __device__ __forceinline__ float turned(const QkArgs &a, const T *src, const T *
   const bool second = a.interleaved ? (d & 1) : d >= half;
   const int j = a.interleaved ? d >> 1 : (second ? d - half : d);
   const float z = normed(a.interleaved ? d ^ 1 : (second ? d - half : d + half));
-  return second ? fmaf(z, cs[half + j], y * cs[j]) : fmaf(-z, cs[half + j], y * cs[j]);
+  const float p = __fmul_rn(y, cs[j]), q = __fmul_rn(z, cs[half + j]);
+  return second ? __fadd_rn(q, p) : __fsub_rn(p, q);
 }
 
 // rsqrt(mean(x^2) + eps) of a vector, or 1 without weights: a warp's lanes.
 template <typename T>
 __device__ __forceinline__ float norm_of(const QkArgs &a, const T *src, const T *w) {
   if (!w) return 1.f;
+  constexpr int E = 16 / sizeof(T);
   float sum = 0.f;
-  for (int d = threadIdx.x & 31; d < a.c.head_dim; d += 32) {
-    const float x = to_f32(src[d]);
-    sum = fmaf(x, x, sum);
+  for (int d0 = static_cast<int>(threadIdx.x & 31) * E; d0 < a.c.head_dim; d0 += 32 * E) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float x = d0 + e < a.c.head_dim ? to_f32(src[d0 + e]) : 0.f;
+      sum = fmaf(x, x, sum);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return rsqrtf(sum / a.c.head_dim + a.eps);
+  return rsqrtf(fmaf(sum, 1.f / a.c.head_dim, a.eps));
 }
 
 // Any sizes, strides and alignment: a warp per vector, each lane elements lane,
@@ -196,9 +207,6 @@ append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleAr
 // while the largest of them is found (kKept vectors a group; what is more is
 // computed again).  The queries, which need no scale, are other CTAs' work, where
 // a row's angles and weights serve several heads.
-//   Keys are rounded step by step, x r, then w, then the rotation's products, as
-// plain fp32 does: where the largest one lies beside a power of two, its last bit
-// decides the scale.
 //   A run is a chain of dependent loads (offsets, lengths, table, rows, the block's
 // scale), and what hides one is other runs: the registers are bound to what 32
 // warps a multiprocessor have, though some go to local memory.  12535 rows of 32 +

@@ -2,13 +2,14 @@
 against 64-bit references."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import smc_speculative_decoding_gb300 as smcsd
 
 from cache8_cases import E4M3, WEIGHT, Cache8Case, bits, compacted
-from cache_cases import E32, CacheCase, half_step
+from cache_cases import E32, CacheCase, half_step, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +137,72 @@ def test_calls_on_caches_of_both_widths_share_a_workspace(group, sequences):
     for c, _, _, _, out, _ in calls:
         ref, _, tol, _ = c.reference()
         assert ((out.double() - ref).abs() <= tol).all()
+
+
+# ---- norms, rotation, quantised cache write ------------------------------------
+
+def _append(c, q, k, v, table, aligned=True, **kw):
+    """The case's cache after a call, its rows' addresses a vector's multiples or one element past them."""
+    def place(t):
+        wide = torch.empty((*t.shape[:2], t.shape[2] + 16 // t.element_size()), dtype=t.dtype, device="cuda")
+        at = wide[..., :t.shape[2]] if aligned else wide[..., 1:t.shape[2] + 1]
+        return at.copy_(t)
+    cache, batch = c.cache(smcsd), c.batch(smcsd)
+    ws = smcsd.alloc_cache8_workspace(cache)
+    out = torch.empty_like(q)
+    kept = [t.clone() for t in (bits(c.k), bits(c.v), c.ks, c.vs)]
+    smcsd.smc_qk_norm_rope8(cache, 0, batch, place(q), place(k), place(v), table, out, ws, **kw)
+    assert smcsd.smc_device_status(ws) == 0
+    got = [t.clone() for t in (bits(c.k), bits(c.v), c.ks, c.vs)]
+    for t, old in zip((bits(c.k), bits(c.v), c.ks, c.vs), kept):
+        t.copy_(old)
+    return got
+
+
+@pytest.mark.parametrize("dtype,dim,rot,interleaved,norm", [
+    (torch.bfloat16, 128, 128, False, True), (torch.bfloat16, 64, 64, True, True), (torch.float16, 96, 64, True, True),
+    (torch.float16, 256, 128, False, True), (torch.float32, 128, 128, False, True), (torch.float32, 80, 40, False, False),
+    (torch.bfloat16, 128, 128, False, False), (torch.float32, 64, 64, True, False)])
+def test_append_stores_the_same_whatever_the_alignment(dtype, dim, rot, interleaved, norm):
+    c = Cache8Case([37, 0, 90], [900, 700, 1100], heads=8, kv_heads=8, dim=dim, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    q, k, v = (torch.randn((c.rows, 8, dim), generator=g, device="cuda").to(dtype) for _ in range(3))
+    w = (1 + 0.2 * torch.randn(dim, generator=g, device="cuda")).to(dtype) if norm else None
+    kw = dict(q_weight=w, k_weight=w, interleaved=interleaved)
+    table = rope_table(1300, rot)
+    for a, b in zip(_append(c, q, k, v, table, **kw), _append(c, q, k, v, table, aligned=False, **kw)):
+        assert torch.equal(a, b)
+
+
+def _beside_a_scale(count):
+    """(a, b, cos, sin) in fp32 with a cos - b sin within a step of 448, on the one side rounded product by product and
+    on the other with the second product left whole."""
+    rng = np.random.default_rng(3)
+    found = []
+    while len(found) < count:
+        angle = rng.uniform(0.3, 1.2, 4000)
+        c, s = np.cos(angle).astype(np.float32), np.sin(angle).astype(np.float32)
+        b = rng.uniform(-450, -150, 4000).astype(np.float32)
+        a = ((448 + b.astype(np.float64) * s) / c).astype(np.float32)
+        stepwise = a * c - b * s
+        whole = ((a * c).astype(np.float64) - b.astype(np.float64) * s).astype(np.float32)
+        other = a * s + b * c  # the other of the pair
+        for i in np.nonzero(((stepwise <= 448) != (whole <= 448)) & (np.abs(other) < 440))[0]:
+            found.append((a[i], b[i], c[i], s[i], stepwise[i]))
+    return np.array(found[:count], dtype=np.float32)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+def test_append_of_a_largest_key_beside_a_scale(aligned):
+    """Its products are rounded one by one, whatever the alignment: the scale is the rounded difference's."""
+    found = _beside_a_scale(60)
+    c = Cache8Case([0], [60], heads=1, kv_heads=1, dim=16, dtype=torch.float32, block=1)
+    k = torch.zeros((60, 1, 16))
+    k[:, 0, 0], k[:, 0, 8] = torch.from_numpy(found[:, 0].copy()), torch.from_numpy(found[:, 1].copy())
+    table = torch.zeros((60, 16))
+    table[:, :8] = 1
+    table[:, 0], table[:, 8] = torch.from_numpy(found[:, 2].copy()), torch.from_numpy(found[:, 3].copy())
+    k = k.cuda()
+    _, _, ks, _ = _append(c, k, k, torch.zeros_like(k), table.cuda(), aligned)
+    got = ks[0, c.tables[0, :60].long(), 0].cpu().numpy()
+    assert (got == np.where(found[:, 4] <= 448, 1.0, 2.0)).all()

@@ -59,11 +59,12 @@ constexpr float kLeastScale = 0x1p-100f, kMostScale = 0x1p100f;
 // A stored scale as it counts: within [2^-100, 2^100], NaN as the least.
 __device__ __forceinline__ float scale_of(float s) { return fminf(fmaxf(s, kLeastScale), kMostScale); }
 
-// The least 2^t in that range with top <= 448 * 2^t = 1.75 * 2^(t + 8); top >= 0.
+// The least 2^t with top <= 448 * 2^t = 1.75 * 2^(t + 8), t within [-kRange, kRange]; top >= 0.
+template <int kRange = 100>
 __device__ __forceinline__ float least_scale(float top) {
   const uint32_t bits = __float_as_uint(top);
   const int t = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
-  return __uint_as_float(static_cast<uint32_t>(min(max(t, -100), 100) + 127) << 23);
+  return __uint_as_float(static_cast<uint32_t>(min(max(t, -kRange), kRange) + 127) << 23);
 }
 // Two numbers to e4m3, a in the low byte: to nearest, ties to even; past 448
 // to 448, NaN to NaN.

@@ -398,7 +398,8 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float scale = least_scale(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
+        // (a row of bf16 may be of any size: the range is that of 2^t and 2^-t both)
+        const float scale = least_scale<126>(top), inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / 2^t
         if (r < 16 * chunks) {
           char *const to = smem + M::kQ + r * 128;
 #pragma unroll

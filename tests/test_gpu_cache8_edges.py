@@ -139,6 +139,25 @@ def test_calls_on_caches_of_both_widths_share_a_workspace(group, sequences):
         assert ((out.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("q,k,scale", [(110, -90, -20), (-110, 90, 20), (118, -90, -28), (0, 60, -60)])
+def test_attention_of_rows_of_any_size(q, k, scale):
+    """Rows of q, scales of k and the scores' scale by powers of two that make up for one another."""
+    c = Cache8Case([300, 40], [5, 9], mask="tree", spread=0)
+    want = c.reference()
+    c.q = c.q * 2.0 ** q
+    c.ks *= 2.0 ** k
+    c.scale *= 2.0 ** scale
+    assert torch.isfinite(c.q).all() and c.ks.max() < 2.0 ** 100 and c.ks.min() > 2.0 ** -100
+    cache, batch = c.cache(smcsd), c.batch(smcsd)
+    ws = smcsd.alloc_cache8_workspace(cache, batch, c.heads)
+    out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    smcsd.smc_tree_attention8(cache, 0, batch, c.q, out, ws, mask=c.mask, lse=lse, scale=c.scale)
+    assert smcsd.smc_device_status(ws) == 0
+    ref, ref_lse, tol, tol_lse = want
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert ((lse.double() - ref_lse).abs() <= tol_lse).all()
+
+
 # ---- norms, rotation, quantised cache write ------------------------------------
 
 def _append(c, q, k, v, table, aligned=True, **kw):

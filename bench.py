@@ -18,7 +18,8 @@ more than the 129 MB L2, from a ring of two distinct step inputs, so no step
 finds its logits in L2.  The KV state and weights are reset every 128 steps
 (the workload's episode length), outside the timed region.
 
-Besides the headline line's own numbers, the JSON carries:
+Standard output is one JSON line, the headline.  A second JSON line, on standard
+error, carries the details, which are ten times as long:
   * ``extensions``: the draft sampler, smc_step_ex (temperature, potentials,
     top-p), sps_verify on the serving rows with sampled and with argmax
     drafts, and the KV-cache saving over a 128-step serving episode;
@@ -26,8 +27,8 @@ Besides the headline line's own numbers, the JSON carries:
     sampling, the serving draft-noise sweep, the single-prompt latency case,
     the batch-32 (N, K) sweep), each timed the same way, with its row-pass and
     whole-step roofline fractions and the oracle timed on a sample of it;
-  * ``parity_sample``: the headline's first steps checked against the CPU
-    oracle (part of the oracle leg), with flagged and mismatched draw counts.
+The headline holds ``parity_sample``: its first steps checked against the CPU
+oracle (part of the oracle leg), with flagged and mismatched draw counts.
 """
 import argparse
 import hashlib
@@ -922,6 +923,16 @@ def run_reference(args, world, rank):
                     "d2h_bytes_per_step": 0}}
 
 
+DETAILS = ("extensions", "workloads")
+
+
+def split_line(out):
+    """The headline, short enough for a reader that takes a few kilobytes of a
+    line, and the details that go beside it."""
+    return ({k: v for k, v in out.items() if k not in DETAILS},
+            {k: out[k] for k in DETAILS if k in out})
+
+
 def main():
     args = parse_args()
     if args.impl == "reference":
@@ -938,7 +949,10 @@ def main():
         if not args.no_cpu_baseline:
             out["cpu_baseline"] = cpu_baseline(workload(args), args.cpu_seconds, samples)
             out["parity_sample"] = out["cpu_baseline"].pop("parity_sample", None)
-        print(json.dumps(out), flush=True)
+        headline, details = split_line(out)
+        if details:
+            print(json.dumps(details), file=sys.stderr, flush=True)
+        print(json.dumps(headline), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()

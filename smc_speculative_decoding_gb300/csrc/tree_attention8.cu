@@ -91,7 +91,8 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // vote that says so; the products start behind it.  Where a maximum has risen, what
 // the tile added to the sums of those chunks is taken off again, maxima, sums and
 // accumulator are brought up, and the chunks are taken anew (once: they cannot pass
-// again).  A timing copy whose maxima never rise took 262 us where this took 322.
+// again).  (Of an earlier form that took 322 us, a timing copy whose maxima never
+// rose took 262.)
 //   What bounds it: the softmax, half of the issue slots and waits for tensor
 // memory, exponentials and the vote between them.  A tile's products keep the
 // tensor cores for 980 cycles (a product of 64 columns is bound by its operands'
@@ -108,9 +109,9 @@ struct alignas(16) Seg8 {  // read and written in 16-byte words
   int seq, head;   // head unit
   int t0, n;       // first token, tiles
   int ctx, kv1;    // tokens before ctx are seen by all; end of the entry's tokens
-  int n_new;       // new tokens of the sequence (own parts)
   int flags;
   int join;        // of a cut unit: the owner CTA, and continuations << 16
+  int pad;
 };
 constexpr int kWhole8 = 4, kBase8 = 8, kEnd8 = 16;  // with kShared: final result, first tiles, none left
 
@@ -798,7 +799,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
         w.flags = kEnd8;
         if (more) {
           w = {walk.t.row0 + walk.tokens0, walk.rows, walk.tokens0, walk.t.seq, walk.head, walk.t.kv0 + walk.i0 * kTile8,
-               walk.n, walk.t.ctx, walk.t.kv1, walk.t.tokens, 0, walk.owner | walk.more << 16};
+               walk.n, walk.t.ctx, walk.t.kv1, 0, walk.owner | walk.more << 16, 0};
           w.flags = (walk.t.flags & kShared) | ((walk.t.flags & kSolo) && walk.n == walk.t.tiles ? kWhole8 : 0) |
                     (walk.i0 == 0 ? kBase8 : 0);
         }
@@ -806,7 +807,7 @@ attention8_kernel(const __grid_constant__ Kernel8Args k, const __grid_constant__
           int4 *to = reinterpret_cast<int4 *>(&s->seg[seg % kSegs8]);
           to[0] = make_int4(w.row0, w.rows, w.i0, w.seq);
           to[1] = make_int4(w.head, w.t0, w.n, w.ctx);
-          to[2] = make_int4(w.kv1, w.n_new, w.flags, w.join);
+          to[2] = make_int4(w.kv1, w.flags, w.join, 0);
         }
         warp_arrive(&s->seg_full[seg % kSegs8], lane);
         if (!more) break;

@@ -225,3 +225,111 @@ def test_append_of_a_largest_key_beside_a_scale(aligned):
     _, _, ks, _ = _append(c, k, k, torch.zeros_like(k), table.cuda(), aligned)
     got = ks[0, c.tables[0, :60].long(), 0].cpu().numpy()
     assert (got == np.where(found[:, 4] <= 448, 1.0, 2.0)).all()
+
+
+# ---- the calls together ---------------------------------------------------------
+
+def _step(c, cache, batch, ws, q, k, v, table, out, path, n_path, pairs, counts):
+    """Drafted tokens stored and attended to, the accepted path moved, a block copied."""
+    turned = torch.empty_like(q)
+    smcsd.smc_qk_norm_rope8(cache, 0, batch, q, k, v, table, turned, ws)
+    smcsd.smc_tree_attention8(cache, 0, batch, turned, out, ws, mask=c.mask, scale=c.scale)
+    smcsd.kv_compact_tokens8(cache, batch, path, n_path, ws)
+    smcsd.kv_copy_blocks8(cache, pairs, counts, ws)
+
+
+def test_a_step_captured_and_replayed_is_the_step():
+    c = Cache8Case([70, 33, 900], [9, 5, 12], mask="tree", spread=2)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = rope_table(1000, 128)
+    make = lambda: [torch.randn((c.rows, n, 128), generator=g, device="cuda").to(c.dtype) for n in (8, 2, 2)]  # noqa: E731
+    rows = make()
+    path = torch.tensor([[0, 3, 8], [1, 4, -1], [5, 6, 11]], dtype=torch.int32, device="cuda")
+    n_path = torch.tensor([3, 2, 3], dtype=torch.int32, device="cuda")
+    free = sorted(set(range(c.blocks)) - set(c.tables.flatten().tolist()))
+    pairs = torch.tensor([[[int(c.tables[0, 4]), free[0]], [int(c.tables[2, 56]), free[1]]]], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([2], dtype=torch.int32, device="cuda")
+    cache, batch = c.cache(smcsd), c.batch(smcsd)
+    ws = smcsd.alloc_cache8_workspace(cache, batch, c.heads)
+    out = torch.empty_like(c.q)
+    held = (bits(c.k), bits(c.v), c.ks, c.vs)
+    start = [t.clone() for t in held]
+
+    def put_back():
+        for t, old in zip(held, start):
+            t.copy_(old)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        _step(c, cache, batch, ws, *rows, table, out, path, n_path, pairs, counts)
+    for turn in range(3):
+        for t, new in zip(rows, make()):
+            t.copy_(new)
+        n_path.copy_(torch.tensor([3 - turn, 2, 3 - turn]))
+        put_back()
+        _step(c, cache, batch, ws, *rows, table, out, path, n_path, pairs, counts)
+        want = [t.clone() for t in (*held, out)]
+        put_back()
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (*held, out)))
+        assert not torch.equal(want[0], start[0])
+    assert smcsd.smc_device_status(ws) == 0
+
+
+def test_two_streams_at_once_with_a_workspace_each():
+    """Calls that run beside one another, on caches and workspaces of their own, do not meet."""
+    cases = [Cache8Case([20000, 30], [8, 3], heads=16, kv_heads=4, seed=i, mask="tree") for i in range(2)]
+    calls, streams = [], [torch.cuda.Stream() for _ in cases]
+    for c in cases:
+        cache, batch = c.cache(smcsd), c.batch(smcsd)
+        ws = smcsd.alloc_cache8_workspace(cache, batch, c.heads)
+        out = torch.empty_like(c.q)
+        smcsd.smc_tree_attention8(cache, 0, batch, c.q, out, ws, mask=c.mask, scale=c.scale)
+        calls.append((c, cache, batch, ws, out.clone(), torch.empty_like(out)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (c, cache, batch, ws, want, out) in zip(streams, calls):
+            out.record_stream(st)
+            smcsd.smc_tree_attention8(cache, 0, batch, c.q, out, ws, mask=c.mask, scale=c.scale, stream=st)
+        torch.cuda.synchronize()
+        for c, _, _, ws, want, out in calls:
+            assert torch.equal(out, want) and smcsd.smc_device_status(ws) == 0
+            out.fill_(7)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("block", [16, 20])
+def test_blocks_past_what_32_bits_count(block):
+    """A pool of more than 2^32 bytes, of which a call's blocks are the last ones: every entry point finds them."""
+    blocks, kv_heads, dim = (1 << 32) // (block * 8 * 128) + 3000, 8, 128
+    small = Cache8Case([333, 60], [7, 9], heads=8, kv_heads=kv_heads, dim=dim, block=block, spread=2)
+    # the same call in a small pool and in the large one, whose last blocks stand for the small one's
+    shift = blocks - small.blocks
+    big_k, big_v = (torch.zeros((1, blocks, block, kv_heads, dim), dtype=torch.uint8, device="cuda") for _ in range(2))
+    big_k[:, shift:], big_v[:, shift:] = bits(small.k), bits(small.v)
+    big_ks, big_vs = (torch.ones((1, blocks, kv_heads), device="cuda") for _ in range(2))
+    big_ks[:, shift:], big_vs[:, shift:] = small.ks, small.vs
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((small.rows, 8, dim), generator=g, device="cuda").to(small.dtype) for _ in range(3))
+    path = torch.tensor([[2, 5], [0, 7]], dtype=torch.int32, device="cuda")
+    n_path = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    free = sorted(set(range(small.blocks)) - set(small.tables.flatten().tolist()))
+    counts = torch.tensor([1], dtype=torch.int32, device="cuda")
+    table, outs = rope_table(400, dim), []
+    for cache, at in ((small.cache(smcsd), 0), (smcsd.make_cache8(big_k.view(E4M3), big_v.view(E4M3), big_ks, big_vs), shift)):
+        tables = torch.where(small.tables < 0, -1, small.tables + at).to(torch.int32)
+        batch = smcsd.make_batch(tables, small.seq_len, small.max_new, row_start=small.row_start, rows=small.rows)
+        pairs = torch.tensor([[[int(tables[0, 3]), free[0] + at]]], dtype=torch.int32, device="cuda")
+        ws = smcsd.alloc_cache8_workspace(cache, batch, 8)
+        out = torch.empty_like(q)
+        _step(small, cache, batch, ws, q, k, v, table, out, path, n_path, pairs, counts)
+        assert smcsd.smc_device_status(ws) == 0
+        outs.append(out)
+    assert torch.equal(*outs)
+    assert torch.equal(big_k[:, shift:], bits(small.k)) and torch.equal(big_v[:, shift:], bits(small.v))
+    assert torch.equal(big_ks[:, shift:], small.ks) and torch.equal(big_vs[:, shift:], small.vs)
+    assert not big_k[:, :shift].any() and torch.all(big_ks[:, :shift] == 1)

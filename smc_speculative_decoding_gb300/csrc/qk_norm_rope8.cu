@@ -106,8 +106,8 @@ __device__ __forceinline__ float norm_of(const QkArgs &a, const T *src, const T 
 
 // Any sizes, strides and alignment: a warp per vector, each lane elements lane,
 // lane + 32, ...; keys are computed for the block's scale and again to be stored.
-// (1280 rows of 32 + 8 + 8 heads of 128 107 us, 12535 rows 716 us; with the
-// vectors below 21 and 135.)
+// (1280 rows of 32 + 8 + 8 heads of 128 58 us, 12535 rows of 40 + 8 + 8 heads of 96
+// 358 us; with the vectors below 21 and 135.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads8)
 append8_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ ScaleArgs sc, int per) {

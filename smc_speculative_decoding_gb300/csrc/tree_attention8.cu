@@ -84,7 +84,8 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 //   A softmax thread's loop takes 16 rows at a time and keeps nothing of them in
 // registers.  64 trees of 16 tokens over up to 8192: 64 rows unrolled with the
 // sums in registers, 4 warps a CTA, 391 us; so, with 8 warps, 291; with the rows'
-// pieces cut by the same warps and so 96 registers each, 256.  Other ways since:
+// pieces cut by the same warps and so 96 registers each, 256 (a largest weight of
+// 2^8 and not 2^7 since, 261).  Other ways:
 // chunks of 8 rows 289, two chunks unrolled 320, the next chunk's scores loaded
 // ahead 274, 4 warps 277.
 //   Weights are taken on trust that none passes 2^kTop, and written ahead of the
@@ -98,8 +99,10 @@ constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 // tensor cores for 980 cycles (a product of 64 columns is bound by its operands'
 // way from shared memory, 49 cycles), its bytes the memory for 1400; a
 // multiprocessor takes 2500 cycles a tile.
-//   Measured: those 64 trees, 812 MB, 256 us, 3.2 TB/s; 131072 tokens of one
-// sequence, 269 MB, 101 us, of which 14 us start it; one token over 4096, 12 us.
+//   Measured: those 64 trees, 812 MB, 258 to 265 us, 3.1 TB/s; 131072 tokens of
+// one sequence, 269 MB, 102 to 108 us, of which 14 us start it; one token over 513,
+// 12.5 us.  DRAM reads 1.21 GB for the 64 trees: a head's token is 128 bytes, and
+// what comes with it to L2 is the next head's, which another CTA reads later.
 //   Every wait is bounded, and on a barrier all of whose turns the waiting
 // thread follows.
 // ---------------------------------------------------------------------------

@@ -36,6 +36,11 @@ static bool batch_ok(const smc_batch *b) {
   return true;
 }
 
+// (a path's places, and those of the threads past its end, are counted in 32 bits)
+static bool path_ok(const int32_t *path, const int32_t *n_path, int32_t max_path) {
+  return path && n_path && max_path >= 1 && max_path <= (1 << 30);
+}
+
 // The stride of an axis of length 1 is never used: it counts as an aligned one.
 static int64_t stride_of(int64_t stride, int32_t length) { return length > 1 ? stride : 128; }
 
@@ -268,7 +273,7 @@ int32_t kv_compact_tokens(const smc_cache *cache, const smc_batch *batch, const 
                           size_t ws_bytes, void *stream) {
   if (!cache) return SMC_ERR_ARG;
   if (!dtype_ok(cache->dtype)) return SMC_ERR_DTYPE;
-  if (!cache_ok(cache) || !batch_ok(batch) || !path || !n_path || max_path < 1) return SMC_ERR_ARG;
+  if (!cache_ok(cache) || !batch_ok(batch) || !path_ok(path, n_path, max_path)) return SMC_ERR_ARG;
   const int32_t rc = check_ws(workspace, ws_bytes, kCacheStatusBytes);
   if (rc != SMC_OK) return rc;
   return launch_compact_tokens(to_cache(cache, 0), to_batch(batch), path, n_path, max_path,
@@ -351,7 +356,7 @@ int32_t kv_compact_tokens8(const smc_cache8 *cache, const smc_batch *batch, cons
                            void *stream) {
   if (!cache) return SMC_ERR_ARG;
   if (cache->data.dtype != SMC_E4M3) return SMC_ERR_DTYPE;
-  if (!cache8_ok(cache) || !batch_ok(batch) || !path || !n_path || max_path < 1) return SMC_ERR_ARG;
+  if (!cache8_ok(cache) || !batch_ok(batch) || !path_ok(path, n_path, max_path)) return SMC_ERR_ARG;
   if (cache->data.block_size > kMostCompactBlock || cache->data.kv_heads > 65535) return SMC_ERR_ARG;
   const int32_t rc = check_ws(workspace, ws_bytes, kCacheStatusBytes);
   if (rc != SMC_OK) return rc;

@@ -631,6 +631,7 @@ int32_t smc_tree_attention8(const smc_attn_params *p, const smc_cache8 *cache, i
  *   x     = y / scale, rounded to e4m3 (to nearest, ties to even; past 448: 448).
  * Tokens ahead of the new ones are rounded again under a scale that has grown.
  * A row that is skipped (its position out of range) leaves its slot's bytes.
+ * At most 2^30 rows.
  * Blocks that hold new tokens are one sequence's alone, as there. */
 int32_t smc_qk_norm_rope8(const smc_qk_params *p, const smc_cache8 *cache, int32_t layer,
                           const smc_batch *batch, int32_t dtype, const void *q, const void *k,

@@ -324,8 +324,9 @@ int32_t smc_qk_norm_rope8(const smc_qk_params *p, const smc_cache8 *cache, int32
   if (!p || !cache) return SMC_ERR_ARG;
   if (cache->data.dtype != SMC_E4M3 || !dtype_ok(dtype)) return SMC_ERR_DTYPE;
   QkArgs a;
-  // (a CTA takes a key head, one more the queries, on the grid's second axis)
-  if (!cache8_ok(cache) || cache->data.kv_heads > 65534 ||
+  // (a CTA takes a key head, one more the queries, on the grid's second axis; rows are counted in 32 bits, as far as
+  // a CTA's last one past the arrays' end)
+  if (!cache8_ok(cache) || cache->data.kv_heads > 65534 || !batch || batch->rows > (1 << 30) ||
       !qk_args(p, &cache->data, layer, batch, dtype, q, k, v, q_weight, k_weight, positions, rope, q_out,
                workspace, &a)) {
     return SMC_ERR_ARG;

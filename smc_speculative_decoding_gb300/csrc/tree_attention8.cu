@@ -69,7 +69,7 @@ struct Kernel8Args : WorkArgs {
 constexpr float kTop = 15.f;      // weights are at most 2^kTop (as fp16: 0x7800) ...
 constexpr uint32_t kPastTop = 0x07ff07ff;  // adds up to 0x8000 with what is more, as fp16
 constexpr float kTopFresh = 8.f; // ... and the largest one 2^kTopFresh when the maximum is taken
-constexpr float kUnset = 1e30f;   // of a row that has seen nothing yet, in place of kTopFresh - M
+constexpr float kUnset = 3e38f;   // of a row that has seen nothing yet, in place of kTopFresh - M: past kTop with any score
 constexpr float kSumScale = 0x1p-32f;  // sums of w / s_v: centres their range
 
 // ---------------------------------------------------------------------------

@@ -158,6 +158,34 @@ def test_attention_of_rows_of_any_size(q, k, scale):
     assert ((lse.double() - ref_lse).abs() <= tol_lse).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("score", [-1.0, -1e20, -1e33, -1e37, 1e37])
+def test_attention_of_scores_of_any_size(score, dtype):
+    """Scores that are all alike, however far below or above zero: the mean of what a row sees.  Some rows see nothing
+    in the first 128 tokens."""
+    c = Cache8Case([0, 140], [200, 5], mask="tree", spread=0, dtype=dtype, heads=4, kv_heads=2, dim=64)
+    c.seen[150], c.seen[199] = [140, 150], [199]
+    c.mask = c._packed()
+    bits(c.k).zero_()
+    bits(c.k)[..., 0] = 0x38  # 1
+    c.ks.fill_(1.0)
+    c.vs.fill_(1.0)  # (what fp32 holds beside such a score is no scale of v's)
+    c.q.zero_()
+    zero = c.reference()
+    size = 2.0 ** 15 if dtype == torch.float16 else 2.0 ** 122  # of q: the rest is the scale's
+    c.q[..., 0] = math.copysign(min(abs(score), size), score)
+    c.scale = abs(score) / min(abs(score), size)
+    z = c.scale * c.q[0, 0, 0].item()
+    cache, batch = c.cache(smcsd), c.batch(smcsd)
+    ws = smcsd.alloc_cache8_workspace(cache, batch, c.heads)
+    out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    smcsd.smc_tree_attention8(cache, 0, batch, c.q, out, ws, mask=c.mask, lse=lse, scale=c.scale)
+    assert smcsd.smc_device_status(ws) == 0
+    ref, ref_lse, tol, tol_lse = zero  # (of scores 0: alike as well)
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert ((lse.double() - (ref_lse + z)).abs() <= tol_lse + 8 * E32 * abs(z)).all()
+
+
 # ---- norms, rotation, quantised cache write ------------------------------------
 
 def _append(c, q, k, v, table, aligned=True, **kw):
